@@ -23,6 +23,7 @@
 #include <vector>
 
 #include "../../include/dinfer.h"
+#include "../../include/dinfer_kv.h"
 #include "../../include/dinfer_ops.h"
 #include "attention.cuh"
 #include "attention_tc.cuh"
@@ -1878,3 +1879,5 @@ extern "C" dinfer_status dinfer_op_gemm_bf16_noalloc_status(void* stream) {
               "calls since the last check is not valid); first timeout: site 0x%x block 0x%x z/step 0x%x thread %u",
               word[0], word[1], word[2], word[3], word[4]);
 }
+
+#include "kv_api.cuh"

@@ -1,0 +1,348 @@
+// Host side of include/dinfer_kv.h: argument checks and launches.  Included at
+// the end of dinfer_api.cu, whose launch, error and workspace helpers it uses.
+#pragma once
+#include "kv_attention.cuh"
+#include "kv_pages.cuh"
+#include "window_attention.cuh"
+
+namespace {
+
+// Why the cache description is unusable, or NULL.
+const char* kv_bad(const dinfer_kv_cache* kc) {
+  if (!kc) return "cache is NULL";
+  if (!kc->k || !kc->v || !kc->table || !kc->lens || !kc->refs || !kc->state) return "cache: NULL buffer";
+  if (kc->dtype != DINFER_BF16 && kc->dtype != DINFER_FP32) return "cache: unknown dtype";
+  if (kc->head_dim != 64 && kc->head_dim != 128) return "cache: head_dim must be 64 or 128";
+  if (kc->n_layers < 1 || kc->num_pages < 1 || kc->kv_heads < 1 || kc->kv_heads > 1024 || kc->page_size < 1 ||
+      kc->page_size > 65536 || kc->max_seqs < 1 || kc->max_pages < 1)
+    return "cache: size out of range";
+  if ((int64_t)kc->max_pages * kc->page_size >= (1ll << 31)) return "cache: max_pages * page_size must be below 2^31";
+  if ((int64_t)kc->page_size * kc->kv_heads * kc->head_dim >= (1ll << 31)) return "cache: page too large";
+  if ((reinterpret_cast<uintptr_t>(kc->k) | reinterpret_cast<uintptr_t>(kc->v)) & 15)
+    return "cache: k and v must be 16-byte aligned";
+  if ((reinterpret_cast<uintptr_t>(kc->table) | reinterpret_cast<uintptr_t>(kc->lens) |
+       reinterpret_cast<uintptr_t>(kc->refs) | reinterpret_cast<uintptr_t>(kc->state)) & 3)
+    return "cache: misaligned table, lens, refs or state";
+  // no two elements share a place: smallest stride first, each steps over all that the ones before it reach
+  int64_t size[4] = {kc->n_layers, kc->num_pages, kc->page_size, kc->kv_heads};
+  int64_t stride[4] = {kc->layer_stride, kc->page_stride, kc->token_stride, kc->head_stride};
+  const int64_t per = kc->dtype == DINFER_BF16 ? 8 : 4;  // elements of 16 bytes
+  for (int i = 0; i < 4; ++i)
+    for (int j = i + 1; j < 4; ++j)
+      if (stride[j] < stride[i]) {
+        std::swap(stride[i], stride[j]);
+        std::swap(size[i], size[j]);
+      }
+  int64_t reach = kc->head_dim;
+  for (int i = 0; i < 4; ++i) {
+    if (size[i] == 1) continue;
+    if (stride[i] % per) return "cache: strides must be multiples of 16 bytes";
+    if (stride[i] < reach || stride[i] > (1ll << 56) / size[i]) return "cache: strides overlap or are out of range";
+    reach += (size[i] - 1) * stride[i];
+  }
+  return nullptr;
+}
+
+KvPages kv_pages(const dinfer_kv_cache& kc) {
+  const int64_t per = kc.dtype == DINFER_BF16 ? 8 : 4;
+  KvPages c{};
+  c.k = (uint4*)kc.k;
+  c.v = (uint4*)kc.v;
+  // the stride of a dimension of one entry is never multiplied by more than 0
+  c.layer_stride = kc.layer_stride / per;
+  c.page_stride = kc.page_stride / per;
+  c.token_stride = kc.token_stride / per;
+  c.head_stride = kc.head_stride / per;
+  c.table = kc.table;
+  c.lens = kc.lens;
+  c.refs = kc.refs;
+  c.state = kc.state;
+  c.n_layers = kc.n_layers;
+  c.num_pages = kc.num_pages;
+  c.page_size = kc.page_size;
+  c.kv_heads = kc.kv_heads;
+  c.head_vecs = (int)(kc.head_dim / per);
+  c.max_seqs = kc.max_seqs;
+  c.max_pages = kc.max_pages;
+  c.page_div = FastDiv::make((uint32_t)kc.page_size);
+  return c;
+}
+
+int log2_of(int x) {
+  int s = 0;
+  while ((1 << s) < x) ++s;
+  return s;
+}
+
+// Shared-memory limits and resident CTAs of this file's kernels, per device.
+struct KvSetup {
+  bool done = false;
+  int ka_ctas[2][2] = {};  // [dtype][head_dim == 128]: attention CTAs per SM
+};
+KvSetup g_kv_setup[kMaxDevices];
+
+template <typename T, int HD>
+bool kv_setup_one(int* ctas) {
+  if (cudaFuncSetAttribute(kv_attention_kernel<T, HD>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           KaCfg<T, HD>::kSmem) != cudaSuccess)
+    return false;
+  if (cudaFuncSetAttribute(window_simt_kernel<T, HD>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           WfCfg<HD>::kSmem) != cudaSuccess)
+    return false;
+  return cudaOccupancyMaxActiveBlocksPerMultiprocessor(ctas, kv_attention_kernel<T, HD>, kKaThreads,
+                                                       KaCfg<T, HD>::kSmem) == cudaSuccess &&
+         *ctas > 0;
+}
+
+const KvSetup* kv_setup() {
+  const int dev = current_device();
+  std::lock_guard<std::mutex> lk(g_setup_mutex);
+  KvSetup& s = g_kv_setup[dev];
+  if (!s.done) {
+    s.done = kv_setup_one<float, 64>(&s.ka_ctas[DINFER_FP32][0]) && kv_setup_one<float, 128>(&s.ka_ctas[DINFER_FP32][1]) &&
+             kv_setup_one<__nv_bfloat16, 64>(&s.ka_ctas[DINFER_BF16][0]) &&
+             kv_setup_one<__nv_bfloat16, 128>(&s.ka_ctas[DINFER_BF16][1]);
+    if (!s.done) {
+      cudaGetLastError();
+      return nullptr;
+    }
+  }
+  return &s;
+}
+
+KvMove kv_move(const dinfer_kv_cache& kc, const KvPages& c) {
+  KvMove m{};
+  m.vec_shift = log2_of(c.head_vecs);
+  const int64_t vecs = (int64_t)c.page_size * c.kv_heads * c.head_vecs;
+  m.parts = (int)((vecs + kKvPartVecs - 1) / kKvPartVecs);
+  m.heads = FastDiv::make((uint32_t)c.kv_heads);
+  m.head_major = kc.kv_heads > 1 && kc.head_stride > kc.token_stride;
+  return m;
+}
+
+// A packed-head-rows operand: aligned, its row stride a multiple of 16 bytes
+// and, where there is more than one row, no shorter than a row.
+bool rows_ok(const void* p, int64_t stride, int64_t rows, int64_t row, int64_t per) {
+  if (reinterpret_cast<uintptr_t>(p) & 15) return false;
+  return rows <= 1 || (stride % per == 0 && stride >= row && stride < (1ll << 36));
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t dinfer_kv_state_ints(int32_t num_pages, int32_t max_seqs) {
+  if (num_pages < 1 || max_seqs < 1) return 0;
+  return (size_t)kKvHead + max_seqs + kKvMaxEntries + 3 * (size_t)num_pages;
+}
+
+dinfer_status dinfer_kv_status(const dinfer_kv_cache* kc, uint32_t* bits, void* stream) {
+  dinfer_ctx* c = nullptr;
+  if (const char* why = kv_bad(kc)) return fail(c, DINFER_EINVAL, "%s", why);
+  const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  uint32_t word = 0;
+  CK(cudaMemcpyAsync(&word, kc->state, 4, cudaMemcpyDeviceToHost, s));
+  CK(cudaStreamSynchronize(s));
+  if (bits) *bits = word;
+  if (!word) return DINFER_OK;
+  CK(cudaMemsetAsync(kc->state, 0, 4, s));
+  return fail(c, DINFER_EDEVICE, "paged cache: status 0x%x:%s%s%s%s%s", word,
+              word & KV_BAD_SEQ ? " bad sequence number" : "", word & KV_NO_PAGES ? " out of pages" : "",
+              word & KV_BAD_PAGE ? " bad page number in a table" : "",
+              word & KV_SHARED ? " rows for a shared page" : "", word & KV_FULL ? " sequence too long" : "");
+}
+
+dinfer_status dinfer_kv_extend(const dinfer_kv_cache* kc, const int32_t* seqs, const int32_t* add, int32_t n,
+                               void* stream) {
+  dinfer_ctx* c = nullptr;
+  if (const char* why = kv_bad(kc)) return fail(c, DINFER_EINVAL, "%s", why);
+  if (n < 1 || n > kKvMaxEntries) return fail(c, DINFER_EINVAL, "n must be 1 .. %d", kKvMaxEntries);
+  CK(launchk(kv_extend_kernel, dim3(1), dim3(kKvPlanThreads), 0, reinterpret_cast<cudaStream_t>(stream), 1,
+             kv_pages(*kc), seqs, add, (int)n));
+  return DINFER_OK;
+}
+
+dinfer_status dinfer_kv_append(const dinfer_kv_cache* kc, int32_t layer, const int32_t* seqs, const int32_t* rows,
+                               int32_t n, const void* k, const void* v, int64_t k_stride, int64_t v_stride,
+                               int32_t total_rows, void* stream) {
+  dinfer_ctx* c = nullptr;
+  if (const char* why = kv_bad(kc)) return fail(c, DINFER_EINVAL, "%s", why);
+  if (!k || !v) return fail(c, DINFER_EINVAL, "NULL operand");
+  if (layer < 0 || layer >= kc->n_layers) return fail(c, DINFER_EINVAL, "no layer %d", layer);
+  if (n < 1 || total_rows < 1 || (!rows && total_rows != n)) return fail(c, DINFER_EINVAL, "bad number of rows or entries");
+  const int64_t per = kc->dtype == DINFER_BF16 ? 8 : 4, row = (int64_t)kc->kv_heads * kc->head_dim;
+  if (!rows_ok(k, k_stride, total_rows, row, per) || !rows_ok(v, v_stride, total_rows, row, per))
+    return fail(c, DINFER_EINVAL, "k, v: 16-byte aligned rows at least a row apart are needed");
+  const KvPages p = kv_pages(*kc);
+  KvAppend a{};
+  a.seqs = seqs;
+  a.rows = rows;
+  a.k = (const uint4*)k;
+  a.v = (const uint4*)v;
+  a.k_stride = k_stride / per;
+  a.v_stride = v_stride / per;
+  a.layer_off = layer * p.layer_stride;
+  a.n = n;
+  a.total_rows = total_rows;
+  a.vec_shift = log2_of(p.head_vecs);
+  const int64_t warps = 2 * (int64_t)total_rows;
+  const int grid = (int)std::min<int64_t>((warps + 7) / 8, (int64_t)num_sms() * 8);
+  CK(launchk(kv_append_kernel, dim3(grid), dim3(256), 0, reinterpret_cast<cudaStream_t>(stream), 1, p, a));
+  return DINFER_OK;
+}
+
+dinfer_status dinfer_kv_fork(const dinfer_kv_cache* kc, const int32_t* src, const int32_t* dst, int32_t n,
+                             int32_t share, void* stream) {
+  dinfer_ctx* c = nullptr;
+  if (const char* why = kv_bad(kc)) return fail(c, DINFER_EINVAL, "%s", why);
+  if (!src || !dst) return fail(c, DINFER_EINVAL, "NULL operand");
+  if (n < 1 || n > kKvMaxEntries) return fail(c, DINFER_EINVAL, "n must be 1 .. %d", kKvMaxEntries);
+  const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const KvPages p = kv_pages(*kc);
+  KvMove m = kv_move(*kc, p);
+  m.src = src;
+  m.dst = dst;
+  m.n = n;
+  m.share = share != 0;
+  CK(launchk(kv_fork_plan_kernel, dim3(1), dim3(kKvPlanThreads), 0, s, 1, p, src, dst, (int)n, m.share));
+  CK(launchk(kv_move_kernel<true>, dim3(num_sms() * 8), dim3(kKvMoveThreads), 0, s, 1, p, m));
+  return DINFER_OK;
+}
+
+dinfer_status dinfer_kv_free(const dinfer_kv_cache* kc, const int32_t* seqs, int32_t n, void* stream) {
+  dinfer_ctx* c = nullptr;
+  if (const char* why = kv_bad(kc)) return fail(c, DINFER_EINVAL, "%s", why);
+  if (!seqs) return fail(c, DINFER_EINVAL, "NULL operand");
+  if (n < 1) return fail(c, DINFER_EINVAL, "n must be positive");
+  CK(launchk(kv_free_kernel, dim3(n), dim3(128), 0, reinterpret_cast<cudaStream_t>(stream), 1, kv_pages(*kc), seqs));
+  return DINFER_OK;
+}
+
+dinfer_status dinfer_kv_compact(const dinfer_kv_cache* kc, int32_t* live, void* stream) {
+  dinfer_ctx* c = nullptr;
+  if (const char* why = kv_bad(kc)) return fail(c, DINFER_EINVAL, "%s", why);
+  const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const KvPages p = kv_pages(*kc);
+  CK(launchk(kv_compact_plan_kernel, dim3(1), dim3(kKvPlanThreads), 0, s, 1, p, live));
+  CK(launchk(kv_move_kernel<false>, dim3(num_sms() * 8), dim3(kKvMoveThreads), 0, s, 1, p, kv_move(*kc, p)));
+  return DINFER_OK;
+}
+
+dinfer_status dinfer_kv_attention(const dinfer_kv_cache* kc, int32_t layer, const int32_t* seqs, int32_t n,
+                                  const void* q, void* o, int64_t q_stride, int64_t o_stride, int32_t heads,
+                                  int32_t window, int32_t sinks, float scale, void* workspace, size_t workspace_bytes,
+                                  void* stream) {
+  dinfer_ctx* c = nullptr;
+  if (const char* why = kv_bad(kc)) return fail(c, DINFER_EINVAL, "%s", why);
+  if (!q || !o) return fail(c, DINFER_EINVAL, "NULL operand");
+  if (layer < 0 || layer >= kc->n_layers) return fail(c, DINFER_EINVAL, "no layer %d", layer);
+  if (n < 1 || n > kKvMaxEntries) return fail(c, DINFER_EINVAL, "n must be 1 .. %d", kKvMaxEntries);
+  if (heads < 1 || heads > 65536 || heads % kc->kv_heads) return fail(c, DINFER_EINVAL, "heads must be a multiple of kv_heads");
+  if (sinks < 0 || !std::isfinite(scale)) return fail(c, DINFER_EINVAL, "bad sinks or scale");
+  const int64_t per = kc->dtype == DINFER_BF16 ? 8 : 4, row = (int64_t)heads * kc->head_dim;
+  if (!rows_ok(q, q_stride, n, row, per) || !rows_ok(o, o_stride, n, row, per))
+    return fail(c, DINFER_EINVAL, "q, o: 16-byte aligned rows at least a row apart are needed");
+  OpWs w;
+  if (!op_ws(workspace, workspace_bytes, w)) return fail(c, DINFER_EINVAL, "workspace too small");
+  KaArgs a{};
+  a.c = kv_pages(*kc);
+  a.seqs = seqs;
+  a.q = q;
+  a.o = o;
+  a.q_stride = q_stride;
+  a.o_stride = o_stride;
+  a.layer_off = layer * a.c.layer_stride;
+  a.n = n;
+  a.group = heads / kc->kv_heads;
+  a.window = window < 0 ? -1 : window;
+  a.sinks = sinks;
+  a.min_units = 1;
+  a.scale_log2 = scale * 1.4426950408889634f;
+  a.partial = reinterpret_cast<float*>(w.data);
+  a.tickets = w.tickets;
+  const int rows = kc->dtype == DINFER_BF16 ? 16 : 8;
+  a.subgroups = (a.group + rows - 1) / rows;
+  const int64_t most = std::min<int64_t>((int64_t)kc->max_pages * kc->page_size,
+                                         window < 0 ? INT64_MAX : (int64_t)window + 1 + sinks);
+  if ((most + kKaUnit - 1) / kKaUnit * n * kc->kv_heads * a.subgroups >= (1ll << 31))
+    return fail(c, DINFER_EINVAL, "more than 2^31 units of keys in one call");
+  const KvSetup* setup = kv_setup();
+  if (!setup) return fail(c, DINFER_ECUDA, "kernel set-up failed");
+  const int hd128 = kc->head_dim == 128;
+  const int grid = num_sms() * setup->ka_ctas[kc->dtype][hd128];
+  const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  auto go = [&](auto kernel, int smem, int slot) -> cudaError_t {
+    if ((size_t)grid * 2 * slot * 4 > w.data_bytes) return cudaErrorInvalidValue;
+    return launchk(kernel, dim3(grid), dim3(kKaThreads), smem, s, 1, a);
+  };
+  cudaError_t e;
+  if (kc->dtype == DINFER_BF16)
+    e = hd128 ? go(kv_attention_kernel<__nv_bfloat16, 128>, KaCfg<__nv_bfloat16, 128>::kSmem, KaCfg<__nv_bfloat16, 128>::kSlotFloats)
+              : go(kv_attention_kernel<__nv_bfloat16, 64>, KaCfg<__nv_bfloat16, 64>::kSmem, KaCfg<__nv_bfloat16, 64>::kSlotFloats);
+  else
+    e = hd128 ? go(kv_attention_kernel<float, 128>, KaCfg<float, 128>::kSmem, KaCfg<float, 128>::kSlotFloats)
+              : go(kv_attention_kernel<float, 64>, KaCfg<float, 64>::kSmem, KaCfg<float, 64>::kSlotFloats);
+  if (e == cudaErrorInvalidValue) return fail(c, DINFER_EINVAL, "workspace too small");
+  CK(e);
+  return DINFER_OK;
+}
+
+dinfer_status dinfer_op_window_attention(const void* q, const void* k, const void* v, void* o, int32_t dtype,
+                                         int32_t batch, const int32_t* cu_q, const int32_t* cu_k, int32_t total_q,
+                                         int32_t total_k, int32_t heads, int32_t kv_heads, int32_t head_dim,
+                                         int64_t q_stride, int64_t k_stride, int64_t v_stride, int64_t o_stride,
+                                         int32_t left, int32_t right, int32_t sinks, float scale, void* workspace,
+                                         size_t workspace_bytes, void* stream) {
+  dinfer_ctx* c = nullptr;
+  if (!q || !k || !v || !o) return fail(c, DINFER_EINVAL, "NULL operand");
+  if (dtype != DINFER_BF16 && dtype != DINFER_FP32) return fail(c, DINFER_EINVAL, "unknown dtype");
+  if (head_dim != 64 && head_dim != 128) return fail(c, DINFER_EINVAL, "head_dim must be 64 or 128");
+  if (batch < 1 || batch > 1024 || !cu_q != !cu_k || (!cu_q && batch != 1))
+    return fail(c, DINFER_EINVAL, "batch must be 1 .. 1024, with cu_q and cu_k both given unless it is 1");
+  if (total_q < 1 || total_k < 1 || total_q > (1 << 30) || total_k > (1 << 30)) return fail(c, DINFER_EINVAL, "unsupported number of rows");
+  if (heads < 1 || heads > 65536 || kv_heads < 1 || heads % kv_heads) return fail(c, DINFER_EINVAL, "heads must be a multiple of kv_heads");
+  if (sinks < 0 || !std::isfinite(scale)) return fail(c, DINFER_EINVAL, "bad sinks or scale");
+  const int64_t per = dtype == DINFER_BF16 ? 8 : 4, qr = (int64_t)heads * head_dim, kr = (int64_t)kv_heads * head_dim;
+  if (!rows_ok(q, q_stride, total_q, qr, per) || !rows_ok(o, o_stride, total_q, qr, per) ||
+      !rows_ok(k, k_stride, total_k, kr, per) || !rows_ok(v, v_stride, total_k, kr, per))
+    return fail(c, DINFER_EINVAL, "16-byte aligned rows at least a row apart are needed");
+  OpWs w{};
+  if (workspace && !op_ws(workspace, workspace_bytes, w)) return fail(c, DINFER_EINVAL, "workspace too small");
+  if (!kv_setup()) return fail(c, DINFER_ECUDA, "kernel set-up failed");
+  WaArgs a{};
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.o = o;
+  a.cu_q = cu_q;
+  a.cu_k = cu_k;
+  a.q_stride = q_stride;
+  a.k_stride = k_stride;
+  a.v_stride = v_stride;
+  a.o_stride = o_stride;
+  a.batch = batch;
+  a.total_q = total_q;
+  a.total_k = total_k;
+  a.heads = heads;
+  a.kv_heads = kv_heads;
+  a.group = heads / kv_heads;
+  a.left = left < 0 ? -1 : left;
+  a.right = right < 0 ? -1 : right;
+  a.sinks = sinks;
+  a.scale_log2 = scale * 1.4426950408889634f;
+  a.status = w.st;
+  const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  // every sequence adds at most one partly filled tile
+  const int64_t ctas = (int64_t)(total_q / kWfRows + batch) * heads;
+  if (ctas >= (1ll << 31)) return fail(c, DINFER_EINVAL, "too many rows");
+  const dim3 grid((unsigned)ctas);
+  if (dtype == DINFER_BF16)
+    CK(head_dim == 128 ? launchk(window_simt_kernel<__nv_bfloat16, 128>, grid, dim3(kWfThreads), WfCfg<128>::kSmem, s, 1, a)
+                       : launchk(window_simt_kernel<__nv_bfloat16, 64>, grid, dim3(kWfThreads), WfCfg<64>::kSmem, s, 1, a));
+  else
+    CK(head_dim == 128 ? launchk(window_simt_kernel<float, 128>, grid, dim3(kWfThreads), WfCfg<128>::kSmem, s, 1, a)
+                       : launchk(window_simt_kernel<float, 64>, grid, dim3(kWfThreads), WfCfg<64>::kSmem, s, 1, a));
+  return DINFER_OK;
+}
+
+}  // extern "C"

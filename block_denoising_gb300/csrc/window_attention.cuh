@@ -1,0 +1,283 @@
+// Attention of many rows with a sliding window and sinks over ragged
+// sequences (include/dinfer_kv.h, dinfer_op_window_attention): what its
+// kernels share, and the fp32 kernel.
+//
+// Row i of a sequence with nq rows and nk keys stands at p = nk - nq + i and
+// sees key j if j <= p + right and (j >= p - left or j < sinks): one interval
+// [lo, hi] and the sinks in front of it.
+#pragma once
+#include "attention_tc.cuh"
+#include "kv_attention.cuh"
+
+namespace dinfer {
+
+struct WaArgs {
+  const void* q;
+  const void* k;
+  const void* v;
+  void* o;
+  const int32_t* cu_q;  // both NULL: one sequence of all rows
+  const int32_t* cu_k;
+  int64_t q_stride, k_stride, v_stride, o_stride;  // elements
+  int batch, total_q, total_k, heads, kv_heads, group;
+  int left, right, sinks;
+  float scale_log2;
+  DevState* status;
+};
+
+// One sequence's rows and keys; out-of-order or out-of-range cu entries give an empty one.
+struct WaSeq {
+  int q0, nq, k0, nk;
+};
+__device__ __forceinline__ int wa_rows_of(const WaArgs& a, int b, int* begin) {
+  const int x0 = a.cu_q ? a.cu_q[b] : 0, x1 = a.cu_q ? a.cu_q[b + 1] : a.total_q;
+  *begin = x0;
+  return (x0 < 0 || x1 > a.total_q) ? 0 : max(0, x1 - x0);
+}
+__device__ __forceinline__ WaSeq wa_seq(const WaArgs& a, int b) {
+  WaSeq s;
+  s.nq = wa_rows_of(a, b, &s.q0);
+  s.k0 = a.cu_k ? a.cu_k[b] : 0;
+  const int x1 = a.cu_k ? a.cu_k[b + 1] : a.total_k;
+  s.nk = (s.k0 < 0 || x1 > a.total_k) ? 0 : max(0, x1 - s.k0);
+  if (s.nk == 0) s.k0 = 0;
+  return s;
+}
+
+// Which sequence and which of its tiles of `tile_rows` rows is tile number x:
+// whole warps, 32 sequences a step.  Returns false behind the last tile.
+__device__ __forceinline__ bool wa_find_tile(const WaArgs& a, int x, int tile_rows, int* b, int* tile) {
+  const int lane = threadIdx.x & 31;
+  for (int b0 = 0; b0 < a.batch; b0 += 32) {
+    int begin, tiles = 0;
+    if (b0 + lane < a.batch) tiles = (wa_rows_of(a, b0 + lane, &begin) + tile_rows - 1) / tile_rows;
+    int inc = tiles;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int u = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += u;
+    }
+    const uint32_t past = __ballot_sync(0xffffffffu, inc > x);
+    if (past) {
+      const int l = __ffs(past) - 1;
+      *b = b0 + l;
+      *tile = x - __shfl_sync(0xffffffffu, inc - tiles, l);
+      return true;
+    }
+    x -= __shfl_sync(0xffffffffu, inc, 31);
+  }
+  return false;
+}
+
+// The keys row i sees: [lo, hi] and the first min(sinks, lo, hi + 1) ones.
+struct WaRange {
+  int lo, hi;
+};
+__device__ __forceinline__ WaRange wa_range(const WaArgs& a, const WaSeq& s, int i) {
+  const int64_t p = (int64_t)s.nk - s.nq + i;
+  WaRange r;
+  r.lo = a.left < 0 ? 0 : (int)max((int64_t)0, min((int64_t)s.nk, p - a.left));
+  r.hi = a.right < 0 ? s.nk - 1 : (int)max((int64_t)-1, min((int64_t)s.nk - 1, p + a.right));
+  return r;
+}
+__device__ __forceinline__ bool wa_sees(const WaRange& r, int sinks, int j) {
+  return j <= r.hi && (j >= r.lo || j < sinks);
+}
+
+template <typename T>
+__device__ __forceinline__ float wa_f32(T x) {
+  if constexpr (sizeof(T) == 2) return __bfloat162float(x); else return x;
+}
+
+// One row by the definition, one key after the other, by a warp; a lane owns
+// HD / 32 dimensions.  Only keys that the row sees are read, so nothing a
+// masked key holds can reach the result.  The tile kernels multiply masked
+// keys' values by a weight of 0, which is NaN for an infinite or NaN value; a
+// row that comes out not finite is done again here, and then holds what its own
+// keys give.  One warp, one key at a time: some microseconds a thousand keys,
+// paid only by such rows.
+template <typename T, int HD>
+__device__ __noinline__ void wa_row_exact(const WaArgs& a, const WaSeq& s, int i, int head) {
+  constexpr int kE = HD / 32;
+  const int lane = threadIdx.x & 31;
+  const WaRange r = wa_range(a, s, i);
+  const T* q = reinterpret_cast<const T*>(a.q) + (int64_t)(s.q0 + i) * a.q_stride + head * HD + lane * kE;
+  const T* k = reinterpret_cast<const T*>(a.k) + (int64_t)s.k0 * a.k_stride + (head / a.group) * HD + lane * kE;
+  const T* v = reinterpret_cast<const T*>(a.v) + (int64_t)s.k0 * a.v_stride + (head / a.group) * HD + lane * kE;
+  float qq[kE], o[kE] = {}, m = -INFINITY, l = 0.f;
+#pragma unroll
+  for (int e = 0; e < kE; ++e) qq[e] = wa_f32(q[e]);
+  const int front = min(a.sinks, min(r.lo, r.hi + 1));
+  const int seen = front + max(0, r.hi - r.lo + 1);
+  for (int x = 0; x < seen; ++x) {
+    const int j = x < front ? x : x - front + r.lo;
+    float d = 0.f;
+#pragma unroll
+    for (int e = 0; e < kE; ++e) d = fmaf(qq[e], wa_f32(k[(int64_t)j * a.k_stride + e]), d);
+    d = warp_sum(d) * a.scale_log2;
+    const float mn = fmaxf(m, d);
+    const float nm = mn == -INFINITY ? 0.f : mn;
+    const float alpha = m == -INFINITY ? 0.f : exp2f(m - nm), p = exp2f(d - nm);
+    m = mn;
+    l = l * alpha + p;
+#pragma unroll
+    for (int e = 0; e < kE; ++e) o[e] = o[e] * alpha + p * wa_f32(v[(int64_t)j * a.v_stride + e]);
+  }
+  T* out = reinterpret_cast<T*>(a.o) + (int64_t)(s.q0 + i) * a.o_stride + head * HD + lane * kE;
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+  for (int e = 0; e < kE; ++e) {
+    if constexpr (sizeof(T) == 2) out[e] = __float2bfloat16(o[e] * inv); else out[e] = o[e] * inv;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// fp32
+// ---------------------------------------------------------------------------
+// One CTA = 64 rows of one head, 256 threads; K and V in tiles of 32 keys.
+// Thread (ty, tx) of 16 x 16 computes the scores of rows 4 ty .. + 3 and keys
+// tx, tx + 16, and owns 4 rows x HD / 16 columns of the output.  Bound by the
+// fp32 FMA rate (there is no fp32 tensor product that keeps 24 bits).
+constexpr int kWfThreads = 256;
+constexpr int kWfRows = 64;
+constexpr int kWfKeys = 32;
+template <int HD>
+struct WfCfg {
+  static constexpr int kPad = HD + 4;  // rows of Q and K start 4 banks apart
+  static constexpr int kOffK = kWfRows * kPad * 4;
+  static constexpr int kOffV = kOffK + kWfKeys * kPad * 4;
+  static constexpr int kOffP = kOffV + kWfKeys * HD * 4;
+  static constexpr int kSmem = kOffP + kWfRows * (kWfKeys + 1) * 4;
+};
+
+template <typename T, int HD>
+__global__ void __launch_bounds__(kWfThreads) window_simt_kernel(const WaArgs a) {
+  using Cfg = WfCfg<HD>;
+  extern __shared__ __align__(16) float wf_sm[];
+  float* qs = wf_sm;
+  float* ks = wf_sm + Cfg::kOffK / 4;
+  float* vs = wf_sm + Cfg::kOffV / 4;
+  float* ps = wf_sm + Cfg::kOffP / 4;
+  pdl_wait();
+  int b, tile;
+  if (!wa_find_tile(a, blockIdx.x / a.heads, kWfRows, &b, &tile)) return;
+  const WaSeq s = wa_seq(a, b);
+  const int head = blockIdx.x % a.heads, i0 = tile * kWfRows, rows = min(kWfRows, s.nq - i0);
+  const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
+  const T* q = reinterpret_cast<const T*>(a.q) + (int64_t)(s.q0 + i0) * a.q_stride + head * HD;
+  const T* k = reinterpret_cast<const T*>(a.k) + (int64_t)s.k0 * a.k_stride + (head / a.group) * HD;
+  const T* v = reinterpret_cast<const T*>(a.v) + (int64_t)s.k0 * a.v_stride + (head / a.group) * HD;
+  for (int x = tid; x < kWfRows * HD; x += kWfThreads) {
+    const int r = x / HD, d = x % HD;
+    qs[r * Cfg::kPad + d] = r < rows ? wa_f32(q[(int64_t)r * a.q_stride + d]) : 0.f;
+  }
+  constexpr int kC = HD / 16;  // output columns of a thread: tx * 4 + 64 * (c / 4) + c % 4
+  float o[4][kC] = {}, m[4], l[4] = {};
+  WaRange rr[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    m[e] = -INFINITY;
+    rr[e] = wa_range(a, s, i0 + min(ty * 4 + e, rows - 1));
+  }
+  // keys some row of the tile sees: the sinks, then from the first row's lo to the last row's hi
+  const WaRange top = wa_range(a, s, i0), bottom = wa_range(a, s, i0 + rows - 1);
+  const int front = min(a.sinks, min(top.lo, bottom.hi + 1));
+  int j0 = front > 0 ? 0 : top.lo / kWfKeys * kWfKeys;
+  while (j0 <= bottom.hi) {
+    __syncthreads();
+    for (int x = tid; x < kWfKeys * HD; x += kWfThreads) {
+      const int r = x / HD, d = x % HD;
+      const bool in = j0 + r < s.nk;
+      ks[r * Cfg::kPad + d] = in ? wa_f32(k[(int64_t)(j0 + r) * a.k_stride + d]) : 0.f;
+      vs[r * HD + d] = in ? wa_f32(v[(int64_t)(j0 + r) * a.v_stride + d]) : 0.f;
+    }
+    __syncthreads();
+    float sc[4][2] = {};
+#pragma unroll 4
+    for (int d = 0; d < HD; d += 4) {
+      float4 kk[2];
+#pragma unroll
+      for (int u = 0; u < 2; ++u) kk[u] = *reinterpret_cast<const float4*>(ks + (tx + 16 * u) * Cfg::kPad + d);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float4 qq = *reinterpret_cast<const float4*>(qs + (ty * 4 + e) * Cfg::kPad + d);
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+          sc[e][u] = fmaf(qq.x, kk[u].x, fmaf(qq.y, kk[u].y, fmaf(qq.z, kk[u].z, fmaf(qq.w, kk[u].w, sc[e][u]))));
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      float mx = -INFINITY;
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        sc[e][u] = wa_sees(rr[e], a.sinks, j0 + tx + 16 * u) ? sc[e][u] * a.scale_log2 : -INFINITY;
+        mx = fmaxf(mx, sc[e][u]);
+      }
+#pragma unroll
+      for (int d = 8; d > 0; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+      const float mn = fmaxf(m[e], mx);
+      const float nm = mn == -INFINITY ? 0.f : mn;
+      const float alpha = m[e] == -INFINITY ? 0.f : ex2_approx(m[e] - nm);
+      m[e] = mn;
+      l[e] *= alpha;
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const float p = ex2_approx(sc[e][u] - nm);
+        l[e] += p;
+        ps[(ty * 4 + e) * (kWfKeys + 1) + tx + 16 * u] = p;
+      }
+#pragma unroll
+      for (int c = 0; c < kC; ++c) o[e][c] *= alpha;
+    }
+    __syncwarp();  // a row's 16 threads are half a warp
+#pragma unroll 4
+    for (int j = 0; j < kWfKeys; ++j) {
+      float vv[kC];
+#pragma unroll
+      for (int c = 0; c < kC; c += 4)
+        *reinterpret_cast<float4*>(vv + c) = *reinterpret_cast<const float4*>(vs + j * HD + tx * 4 + 16 * c);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float p = ps[(ty * 4 + e) * (kWfKeys + 1) + j];
+#pragma unroll
+        for (int c = 0; c < kC; ++c) o[e][c] = fmaf(p, vv[c], o[e][c]);
+      }
+    }
+    j0 += kWfKeys;
+    if (j0 >= front && j0 < top.lo) j0 = max(j0, top.lo / kWfKeys * kWfKeys);  // behind the sinks: on to the window
+  }
+  // sums over the 16 threads of a row, and whether all of it is finite
+  uint32_t redo = 0;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    float sum = l[e], worst = 0.f;
+#pragma unroll
+    for (int c = 0; c < kC; ++c) worst = fmaxf(worst, fabsf(o[e][c]) <= 3.0e38f ? 0.f : 1.f);
+#pragma unroll
+    for (int d = 8; d > 0; d >>= 1) {
+      sum += __shfl_xor_sync(0xffffffffu, sum, d);
+      worst = fmaxf(worst, __shfl_xor_sync(0xffffffffu, worst, d));
+    }
+    const int r = ty * 4 + e;
+    const bool bad = worst != 0.f || !(sum <= 3.0e38f);
+    const uint32_t bads = __ballot_sync(0xffffffffu, bad && r < rows);
+    redo |= ((bads & 0xffffu) ? 1u << e : 0u) | ((bads >> 16) ? 16u << e : 0u);
+    if (r < rows) {
+      const float inv = sum == 0.f ? 0.f : 1.f / sum;
+      T* out = reinterpret_cast<T*>(a.o) + (int64_t)(s.q0 + i0 + r) * a.o_stride + head * HD;
+#pragma unroll
+      for (int c = 0; c < kC; c += 4)
+        ka_store4(out + tx * 4 + 16 * c,
+                  make_float4(o[e][c] * inv, o[e][c + 1] * inv, o[e][c + 2] * inv, o[e][c + 3] * inv));
+    }
+  }
+  __syncwarp();
+  while (redo) {  // warp-uniform: bits 0-3 the rows of its lower half, 4-7 of its upper half
+    const int e = __ffs(redo) - 1;
+    redo &= redo - 1;
+    wa_row_exact<T, HD>(a, s, i0 + ((tid >> 5) * 2 + (e >> 2)) * 4 + (e & 3), head);
+  }
+}
+
+}  // namespace dinfer

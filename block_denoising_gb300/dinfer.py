@@ -40,6 +40,14 @@ class DinferError(RuntimeError):
         self.status = status
 
 
+class KvCache(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("k", "v")] + \
+               [(n, ctypes.c_int64) for n in ("layer_stride", "page_stride", "token_stride", "head_stride")] + \
+               [(n, ctypes.c_void_p) for n in ("table", "lens", "refs", "state")] + \
+               [(n, ctypes.c_int32) for n in ("n_layers", "num_pages", "page_size", "kv_heads", "head_dim", "dtype",
+                                              "max_seqs", "max_pages")]
+
+
 _lib = None
 
 
@@ -88,6 +96,26 @@ def lib() -> ctypes.CDLL:
     L.dinfer_op_attention_bf16.restype = i32
     L.dinfer_op_moe_ffn_bf16.argtypes = [vp, vp, vp, vp, i32, i32, i32, i32, i32, vp, vp, vp, vp, sz, vp]
     L.dinfer_op_moe_ffn_bf16.restype = i32
+    i64 = ctypes.c_int64
+    L.dinfer_kv_state_ints.argtypes = [i32, i32]
+    L.dinfer_kv_state_ints.restype = sz
+    L.dinfer_kv_status.argtypes = [vp, ctypes.POINTER(ctypes.c_uint32), vp]
+    L.dinfer_kv_status.restype = i32
+    L.dinfer_kv_extend.argtypes = [vp, vp, vp, i32, vp]
+    L.dinfer_kv_extend.restype = i32
+    L.dinfer_kv_append.argtypes = [vp, i32, vp, vp, i32, vp, vp, i64, i64, i32, vp]
+    L.dinfer_kv_append.restype = i32
+    L.dinfer_kv_fork.argtypes = [vp, vp, vp, i32, i32, vp]
+    L.dinfer_kv_fork.restype = i32
+    L.dinfer_kv_free.argtypes = [vp, vp, i32, vp]
+    L.dinfer_kv_free.restype = i32
+    L.dinfer_kv_compact.argtypes = [vp, vp, vp]
+    L.dinfer_kv_compact.restype = i32
+    L.dinfer_kv_attention.argtypes = [vp, i32, vp, i32, vp, vp, i64, i64, i32, i32, i32, f32, vp, sz, vp]
+    L.dinfer_kv_attention.restype = i32
+    L.dinfer_op_window_attention.argtypes = [vp, vp, vp, vp, i32, i32, vp, vp, i32, i32, i32, i32, i32, i64, i64, i64,
+                                             i64, i32, i32, i32, f32, vp, sz, vp]
+    L.dinfer_op_window_attention.restype = i32
     _lib = L
     return L
 
@@ -255,3 +283,168 @@ def op_moe_ffn_bf16(X: torch.Tensor, router: torch.Tensor, w13: torch.Tensor, w2
     _check(lib().dinfer_op_moe_ffn_bf16(_ptr(X), _ptr(router), _ptr(w13), _ptr(w2), M, d, E, top_k, two_fe // 2,
                                         _ptr(out), _ptr(ids), _ptr(w), _ptr(ws.buf), ws.nbytes, _stream_ptr()))
     return out, ids, w
+
+
+# ---------------------------------------------------------------------------
+# paged KV cache and windowed prompt attention (include/dinfer_kv.h)
+# ---------------------------------------------------------------------------
+_DTYPES = {torch.float32: FP32, torch.bfloat16: BF16}
+KV_BAD_SEQ, KV_NO_PAGES, KV_BAD_PAGE, KV_SHARED, KV_FULL = 1, 2, 4, 8, 16
+
+
+def _require(ok, what: str):
+    if not ok:
+        raise ValueError(what)
+
+
+def _rows_of(t: torch.Tensor, name: str, heads: Optional[int], head_dim: int, like: torch.Tensor):
+    """Checks [rows, heads, head_dim] with packed head rows, of like's type and device; returns the row stride."""
+    _require(t.dim() == 3 and t.shape[2] == head_dim and (heads is None or t.shape[1] == heads),
+             f"{name}: [rows, {'heads' if heads is None else heads}, {head_dim}] expected, got {list(t.shape)}")
+    _require(t.dtype == like.dtype and t.device == like.device, f"{name}: {like.dtype} on {like.device} expected")
+    s = t.stride()
+    _require(s[2] == 1 and (s[1] == head_dim or t.shape[1] == 1), f"{name}: the heads of a row must be packed")
+    return s[0]
+
+
+def _ints(t: Optional[torch.Tensor], name: str, device, n: Optional[int] = None):
+    """Address of a contiguous int32 vector on device (None: NULL)."""
+    if t is None:
+        return None
+    _require(t.dtype == torch.int32 and t.dim() == 1 and t.device == device and t.is_contiguous(),
+             f"{name}: a contiguous int32 vector on {device} expected")
+    _require(n is None or t.shape[0] == n, f"{name}: {n} entries expected, got {t.shape[0]}")
+    return t.data_ptr()
+
+
+class PagedKV:
+    """A paged KV cache over caller-owned tensors (dinfer_kv.h): k, v viewed as
+    [layers, pages, page_size, kv_heads, head_dim] in any non-overlapping order
+    with packed head rows; table [max_seqs, max_pages], lens [max_seqs] and refs
+    [pages] int32.  All calls run on torch's current stream of the tensors'
+    device."""
+
+    def __init__(self, k: torch.Tensor, v: torch.Tensor, table: torch.Tensor, lens: torch.Tensor, refs: torch.Tensor):
+        _require(k.dim() == 5 and k.shape == v.shape and k.stride() == v.stride() and k.dtype == v.dtype
+                 and k.device == v.device, "k, v: two [layers, pages, page_size, kv_heads, head_dim] views alike expected")
+        _require(k.dtype in _DTYPES and k.is_cuda, "k, v: float32 or bfloat16 on a GPU expected")
+        _require(k.stride(4) == 1, "k, v: the elements of a head must be packed")
+        dev = k.device
+        _require(table.dim() == 2 and table.dtype == torch.int32 and table.device == dev and table.is_contiguous(),
+                 f"table: contiguous int32 [max_seqs, max_pages] on {dev} expected")
+        self.max_seqs, self.max_pages = table.shape
+        layers, pages, page, heads, hd = k.shape
+        lens_p, refs_p = _ints(lens, "lens", dev, self.max_seqs), _ints(refs, "refs", dev, pages)
+        L = lib()
+        self.k, self.v, self.table, self.lens, self.refs = k, v, table, lens, refs
+        self.device, self.kv_heads, self.head_dim = dev, heads, hd
+        self.state = torch.zeros(L.dinfer_kv_state_ints(pages, self.max_seqs), dtype=torch.int32, device=dev)
+        st = k.stride()
+        self.desc = KvCache(k.data_ptr(), v.data_ptr(), st[0], st[1], st[2], st[3], table.data_ptr(), lens_p, refs_p,
+                            self.state.data_ptr(), layers, pages, page, heads, hd, _DTYPES[k.dtype], self.max_seqs,
+                            self.max_pages)
+        self._desc = ctypes.addressof(self.desc)
+
+    @classmethod
+    def empty(cls, layers: int, pages: int, page_size: int, kv_heads: int, head_dim: int, max_seqs: int,
+              max_pages: int, dtype=torch.bfloat16, device="cuda"):
+        """A new cache without sequences."""
+        k, v = (torch.empty((layers, pages, page_size, kv_heads, head_dim), dtype=dtype, device=device) for _ in range(2))
+        return cls(k, v, torch.full((max_seqs, max_pages), -1, dtype=torch.int32, device=device),
+                   torch.zeros(max_seqs, dtype=torch.int32, device=device),
+                   torch.zeros(pages, dtype=torch.int32, device=device))
+
+    def _call(self, fn, *args):
+        if self.device.index == torch.cuda.current_device():
+            return _check(fn(self._desc, *args, torch.cuda.current_stream().cuda_stream))
+        with torch.cuda.device(self.device):
+            _check(fn(self._desc, *args, torch.cuda.current_stream().cuda_stream))
+
+    def set_tables(self, table: torch.Tensor, lens: torch.Tensor, refs: torch.Tensor):
+        """Takes over another set of tables of the same sizes (a snapshot, a scheduler's own plan)."""
+        _require(table.shape == self.table.shape and lens.shape == self.lens.shape and refs.shape == self.refs.shape,
+                 "table, lens, refs: the cache's sizes expected")
+        self.table.copy_(table)
+        self.lens.copy_(lens)
+        self.refs.copy_(refs)
+        self.state.zero_()
+
+    def extend(self, add: Optional[torch.Tensor] = None, seqs: Optional[torch.Tensor] = None):
+        """Sequences seqs (default: the first ones, one per entry of add; all) grow by add tokens (default: one each)."""
+        n = len(seqs) if seqs is not None else len(add) if add is not None else self.max_seqs
+        _require(seqs is not None or n <= self.max_seqs, "add: more entries than sequences")
+        self._call(lib().dinfer_kv_extend, _ints(seqs, "seqs", self.device), _ints(add, "add", self.device, n), n)
+
+    def append(self, layer: int, k: torch.Tensor, v: torch.Tensor, rows: Optional[torch.Tensor] = None,
+               seqs: Optional[torch.Tensor] = None):
+        """Stores the last rows of each sequence: k, v [rows, kv_heads, head_dim]; rows [n + 1] the entries'
+        first rows (default: one row per sequence)."""
+        ks = _rows_of(k, "k", self.kv_heads, self.head_dim, self.k)
+        vs = _rows_of(v, "v", self.kv_heads, self.head_dim, self.k)
+        _require(k.shape[0] == v.shape[0], "k, v: as many rows expected")
+        n = len(rows) - 1 if rows is not None else k.shape[0]
+        _require(seqs is not None or n <= self.max_seqs, "more entries than sequences")
+        self._call(lib().dinfer_kv_append, layer, _ints(seqs, "seqs", self.device, n), _ints(rows, "rows", self.device), n,
+                   k.data_ptr(), v.data_ptr(), ks, vs, k.shape[0])
+
+    def fork(self, src: torch.Tensor, dst: torch.Tensor, share: bool = True):
+        """Sequences dst (not in use) become copies of src, sharing the full pages or copying all of them."""
+        self._call(lib().dinfer_kv_fork, _ints(src, "src", self.device), _ints(dst, "dst", self.device, len(src)), len(src),
+                   int(share))
+
+    def free(self, seqs: torch.Tensor):
+        self._call(lib().dinfer_kv_free, _ints(seqs, "seqs", self.device), len(seqs))
+
+    def compact(self, live: Optional[torch.Tensor] = None):
+        """Packs the pages in use to the front; live (optional, int32 [1]) receives how many there are."""
+        self._call(lib().dinfer_kv_compact, _ints(live, "live", self.device, 1))
+
+    def attention(self, layer: int, q: torch.Tensor, ws: OpWorkspace, window: int = -1, sinks: int = 0,
+                  scale: Optional[float] = None, seqs: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None):
+        """Attention of each sequence's last token: q [n, heads, head_dim] -> [n, heads, head_dim]."""
+        hd = self.head_dim
+        qs = _rows_of(q, "q", None, hd, self.k)
+        n, heads, _ = q.shape
+        _require(seqs is not None or n <= self.max_seqs, "q: more rows than sequences")
+        _require(ws.buf.device == self.device, f"ws: a workspace on {self.device} expected")
+        if out is None:
+            out = torch.empty((n, heads, hd), dtype=q.dtype, device=self.device)
+        os_ = _rows_of(out, "out", heads, hd, self.k)
+        _require(out.shape[0] == n, f"out: {n} rows expected")
+        self._call(lib().dinfer_kv_attention, layer, _ints(seqs, "seqs", self.device, n), n, q.data_ptr(), out.data_ptr(),
+                   qs, os_, heads, window, sinks, hd ** -0.5 if scale is None else scale, ws.buf.data_ptr(), ws.nbytes)
+        return out
+
+    def check(self):
+        """Raise if an entry of an earlier call was skipped (DinferError names why); clears the status."""
+        self._call(lib().dinfer_kv_status, None)
+
+
+def op_window_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, ws: OpWorkspace,
+                        cu_q: Optional[torch.Tensor] = None, cu_k: Optional[torch.Tensor] = None, left: int = -1,
+                        right: int = -1, sinks: int = 0, scale: Optional[float] = None,
+                        out: Optional[torch.Tensor] = None):
+    """Attention with a sliding window and sinks: q [rows, heads, head_dim], k, v [keys, kv_heads, head_dim];
+    cu_q, cu_k [batch + 1] the sequences' first rows and keys (default: one sequence of all)."""
+    _require(q.dim() == 3 and q.dtype in _DTYPES and q.is_cuda, "q: float32 or bfloat16 [rows, heads, head_dim] on a GPU expected")
+    rows, heads, hd = q.shape
+    qs = _rows_of(q, "q", None, hd, q)
+    ks = _rows_of(k, "k", None, hd, q)
+    vs = _rows_of(v, "v", k.shape[1], hd, q)
+    _require(k.shape[0] == v.shape[0], "k, v: as many keys expected")
+    dev = q.device
+    cq, ck = _ints(cu_q, "cu_q", dev), _ints(cu_k, "cu_k", dev, None if cu_q is None else len(cu_q))
+    _require(ws.buf.device == dev, f"ws: a workspace on {dev} expected")
+    if out is None:
+        out = torch.empty((rows, heads, hd), dtype=q.dtype, device=dev)
+    os_ = _rows_of(out, "out", heads, hd, q)
+    _require(out.shape[0] == rows, f"out: {rows} rows expected")
+    args = (q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), _DTYPES[q.dtype],
+            1 if cu_q is None else len(cu_q) - 1, cq, ck, rows, k.shape[0], heads, k.shape[1], hd, qs, ks, vs, os_, left,
+            right, sinks, hd ** -0.5 if scale is None else scale, ws.buf.data_ptr(), ws.nbytes)
+    if dev.index == torch.cuda.current_device():
+        _check(lib().dinfer_op_window_attention(*args, torch.cuda.current_stream().cuda_stream))
+    else:
+        with torch.cuda.device(dev):
+            _check(lib().dinfer_op_window_attention(*args, torch.cuda.current_stream().cuda_stream))
+    return out
