@@ -4,6 +4,7 @@
 #include "kv_attention.cuh"
 #include "kv_pages.cuh"
 #include "window_attention.cuh"
+#include "window_attention_tc.cuh"
 
 namespace {
 
@@ -86,12 +87,18 @@ bool kv_setup_one(int* ctas) {
   if (cudaFuncSetAttribute(kv_attention_kernel<T, HD>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            KaCfg<T, HD>::kSmem) != cudaSuccess)
     return false;
-  if (cudaFuncSetAttribute(window_simt_kernel<T, HD>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           WfCfg<HD>::kSmem) != cudaSuccess)
+  if (sizeof(T) == 4 && cudaFuncSetAttribute(window_f32_kernel<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             WfCfg<HD>::kSmem) != cudaSuccess)
     return false;
   return cudaOccupancyMaxActiveBlocksPerMultiprocessor(ctas, kv_attention_kernel<T, HD>, kKaThreads,
                                                        KaCfg<T, HD>::kSmem) == cudaSuccess &&
          *ctas > 0;
+}
+
+template <int HD>
+bool kv_setup_tc() {
+  return cudaFuncSetAttribute(window_tc_kernel<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize, WtCfg<HD>::kSmem) ==
+         cudaSuccess;
 }
 
 const KvSetup* kv_setup() {
@@ -101,7 +108,7 @@ const KvSetup* kv_setup() {
   if (!s.done) {
     s.done = kv_setup_one<float, 64>(&s.ka_ctas[DINFER_FP32][0]) && kv_setup_one<float, 128>(&s.ka_ctas[DINFER_FP32][1]) &&
              kv_setup_one<__nv_bfloat16, 64>(&s.ka_ctas[DINFER_BF16][0]) &&
-             kv_setup_one<__nv_bfloat16, 128>(&s.ka_ctas[DINFER_BF16][1]);
+             kv_setup_one<__nv_bfloat16, 128>(&s.ka_ctas[DINFER_BF16][1]) && kv_setup_tc<64>() && kv_setup_tc<128>();
     if (!s.done) {
       cudaGetLastError();
       return nullptr;
@@ -125,6 +132,20 @@ KvMove kv_move(const dinfer_kv_cache& kc, const KvPages& c) {
 bool rows_ok(const void* p, int64_t stride, int64_t rows, int64_t row, int64_t per) {
   if (reinterpret_cast<uintptr_t>(p) & 15) return false;
   return rows <= 1 || (stride % per == 0 && stride >= row && stride < (1ll << 36));
+}
+
+// bf16 rows [rows][heads][hd], `stride` elements apart: boxes of 128 rows x one
+// head x 64 elements with the 128-byte swizzle; rows behind the last read as zeros.
+bool make_map_rows(CUtensorMap* m, const void* base, int64_t rows, int64_t heads, int64_t hd, int64_t stride) {
+  EncodeTiledFn enc = get_encode_fn();
+  if (!enc) return false;
+  cuuint64_t dims[3] = {(cuuint64_t)hd, (cuuint64_t)heads, (cuuint64_t)rows};
+  cuuint64_t strides[2] = {(cuuint64_t)hd * 2, (cuuint64_t)(rows > 1 ? stride : heads * hd) * 2};
+  cuuint32_t box[3] = {64, 1, kWtRows};
+  cuuint32_t es[3] = {1, 1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, es,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 }  // namespace
@@ -238,7 +259,7 @@ dinfer_status dinfer_kv_attention(const dinfer_kv_cache* kc, int32_t layer, cons
   if (layer < 0 || layer >= kc->n_layers) return fail(c, DINFER_EINVAL, "no layer %d", layer);
   if (n < 1 || n > kKvMaxEntries) return fail(c, DINFER_EINVAL, "n must be 1 .. %d", kKvMaxEntries);
   if (heads < 1 || heads > 65536 || heads % kc->kv_heads) return fail(c, DINFER_EINVAL, "heads must be a multiple of kv_heads");
-  if (sinks < 0 || !std::isfinite(scale)) return fail(c, DINFER_EINVAL, "bad sinks or scale");
+  if (sinks < 0 || !(scale > 0.f) || !std::isfinite(scale * 1.4426950408889634f)) return fail(c, DINFER_EINVAL, "bad sinks or scale");
   const int64_t per = kc->dtype == DINFER_BF16 ? 8 : 4, row = (int64_t)heads * kc->head_dim;
   if (!rows_ok(q, q_stride, n, row, per) || !rows_ok(o, o_stride, n, row, per))
     return fail(c, DINFER_EINVAL, "q, o: 16-byte aligned rows at least a row apart are needed");
@@ -301,7 +322,7 @@ dinfer_status dinfer_op_window_attention(const void* q, const void* k, const voi
     return fail(c, DINFER_EINVAL, "batch must be 1 .. 1024, with cu_q and cu_k both given unless it is 1");
   if (total_q < 1 || total_k < 1 || total_q > (1 << 30) || total_k > (1 << 30)) return fail(c, DINFER_EINVAL, "unsupported number of rows");
   if (heads < 1 || heads > 65536 || kv_heads < 1 || heads % kv_heads) return fail(c, DINFER_EINVAL, "heads must be a multiple of kv_heads");
-  if (sinks < 0 || !std::isfinite(scale)) return fail(c, DINFER_EINVAL, "bad sinks or scale");
+  if (sinks < 0 || !(scale > 0.f) || !std::isfinite(scale * 1.4426950408889634f)) return fail(c, DINFER_EINVAL, "bad sinks or scale");
   const int64_t per = dtype == DINFER_BF16 ? 8 : 4, qr = (int64_t)heads * head_dim, kr = (int64_t)kv_heads * head_dim;
   if (!rows_ok(q, q_stride, total_q, qr, per) || !rows_ok(o, o_stride, total_q, qr, per) ||
       !rows_ok(k, k_stride, total_k, kr, per) || !rows_ok(v, v_stride, total_k, kr, per))
@@ -333,15 +354,24 @@ dinfer_status dinfer_op_window_attention(const void* q, const void* k, const voi
   a.status = w.st;
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   // every sequence adds at most one partly filled tile
-  const int64_t ctas = (int64_t)(total_q / kWfRows + batch) * heads;
+  const int pair = a.group % 2 == 0;
+  const int block_rows = dtype == DINFER_FP32 ? kWfRows : pair ? kWtRows : 2 * kWtRows;
+  const int blocks = total_q / block_rows + batch;
+  const int64_t ctas = (int64_t)blocks * (dtype == DINFER_BF16 && pair ? heads / 2 : heads);
   if (ctas >= (1ll << 31)) return fail(c, DINFER_EINVAL, "too many rows");
   const dim3 grid((unsigned)ctas);
-  if (dtype == DINFER_BF16)
-    CK(head_dim == 128 ? launchk(window_simt_kernel<__nv_bfloat16, 128>, grid, dim3(kWfThreads), WfCfg<128>::kSmem, s, 1, a)
-                       : launchk(window_simt_kernel<__nv_bfloat16, 64>, grid, dim3(kWfThreads), WfCfg<64>::kSmem, s, 1, a));
-  else
-    CK(head_dim == 128 ? launchk(window_simt_kernel<float, 128>, grid, dim3(kWfThreads), WfCfg<128>::kSmem, s, 1, a)
-                       : launchk(window_simt_kernel<float, 64>, grid, dim3(kWfThreads), WfCfg<64>::kSmem, s, 1, a));
+  if (dtype == DINFER_FP32) {
+    CK(head_dim == 128 ? launchk(window_f32_kernel<128>, grid, dim3(kWfThreads), WfCfg<128>::kSmem, s, 1, a)
+                       : launchk(window_f32_kernel<64>, grid, dim3(kWfThreads), WfCfg<64>::kSmem, s, 1, a));
+    return DINFER_OK;
+  }
+  WtMaps maps;
+  if (!make_map_rows(&maps.q, q, total_q, heads, head_dim, q_stride) ||
+      !make_map_rows(&maps.k, k, total_k, kv_heads, head_dim, k_stride) ||
+      !make_map_rows(&maps.v, v, total_k, kv_heads, head_dim, v_stride))
+    return fail(c, DINFER_EINVAL, "tensor map encoding failed");
+  CK(head_dim == 128 ? launchk(window_tc_kernel<128>, grid, dim3(kWtThreads), WtCfg<128>::kSmem, s, 1, maps, a, pair, blocks)
+                     : launchk(window_tc_kernel<64>, grid, dim3(kWtThreads), WtCfg<64>::kSmem, s, 1, maps, a, pair, blocks));
   return DINFER_OK;
 }
 

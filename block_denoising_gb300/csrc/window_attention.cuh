@@ -97,7 +97,7 @@ __device__ __forceinline__ float wa_f32(T x) {
 // keys give.  One warp, one key at a time: some microseconds a thousand keys,
 // paid only by such rows.
 template <typename T, int HD>
-__device__ __noinline__ void wa_row_exact(const WaArgs& a, const WaSeq& s, int i, int head) {
+__device__ __noinline__ void wa_row_exact(const WaArgs& a, const WaSeq s, int i, int head) {
   constexpr int kE = HD / 32;
   const int lane = threadIdx.x & 31;
   const WaRange r = wa_range(a, s, i);
@@ -150,8 +150,8 @@ struct WfCfg {
   static constexpr int kSmem = kOffP + kWfRows * (kWfKeys + 1) * 4;
 };
 
-template <typename T, int HD>
-__global__ void __launch_bounds__(kWfThreads) window_simt_kernel(const WaArgs a) {
+template <int HD>
+__global__ void __launch_bounds__(kWfThreads) window_f32_kernel(const __grid_constant__ WaArgs a) {
   using Cfg = WfCfg<HD>;
   extern __shared__ __align__(16) float wf_sm[];
   float* qs = wf_sm;
@@ -164,12 +164,12 @@ __global__ void __launch_bounds__(kWfThreads) window_simt_kernel(const WaArgs a)
   const WaSeq s = wa_seq(a, b);
   const int head = blockIdx.x % a.heads, i0 = tile * kWfRows, rows = min(kWfRows, s.nq - i0);
   const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
-  const T* q = reinterpret_cast<const T*>(a.q) + (int64_t)(s.q0 + i0) * a.q_stride + head * HD;
-  const T* k = reinterpret_cast<const T*>(a.k) + (int64_t)s.k0 * a.k_stride + (head / a.group) * HD;
-  const T* v = reinterpret_cast<const T*>(a.v) + (int64_t)s.k0 * a.v_stride + (head / a.group) * HD;
+  const float* q = reinterpret_cast<const float*>(a.q) + (int64_t)(s.q0 + i0) * a.q_stride + head * HD;
+  const float* k = reinterpret_cast<const float*>(a.k) + (int64_t)s.k0 * a.k_stride + (head / a.group) * HD;
+  const float* v = reinterpret_cast<const float*>(a.v) + (int64_t)s.k0 * a.v_stride + (head / a.group) * HD;
   for (int x = tid; x < kWfRows * HD; x += kWfThreads) {
     const int r = x / HD, d = x % HD;
-    qs[r * Cfg::kPad + d] = r < rows ? wa_f32(q[(int64_t)r * a.q_stride + d]) : 0.f;
+    qs[r * Cfg::kPad + d] = r < rows ? q[(int64_t)r * a.q_stride + d] : 0.f;
   }
   constexpr int kC = HD / 16;  // output columns of a thread: tx * 4 + 64 * (c / 4) + c % 4
   float o[4][kC] = {}, m[4], l[4] = {};
@@ -188,8 +188,8 @@ __global__ void __launch_bounds__(kWfThreads) window_simt_kernel(const WaArgs a)
     for (int x = tid; x < kWfKeys * HD; x += kWfThreads) {
       const int r = x / HD, d = x % HD;
       const bool in = j0 + r < s.nk;
-      ks[r * Cfg::kPad + d] = in ? wa_f32(k[(int64_t)(j0 + r) * a.k_stride + d]) : 0.f;
-      vs[r * HD + d] = in ? wa_f32(v[(int64_t)(j0 + r) * a.v_stride + d]) : 0.f;
+      ks[r * Cfg::kPad + d] = in ? k[(int64_t)(j0 + r) * a.k_stride + d] : 0.f;
+      vs[r * HD + d] = in ? v[(int64_t)(j0 + r) * a.v_stride + d] : 0.f;
     }
     __syncthreads();
     float sc[4][2] = {};
@@ -265,7 +265,7 @@ __global__ void __launch_bounds__(kWfThreads) window_simt_kernel(const WaArgs a)
     redo |= ((bads & 0xffffu) ? 1u << e : 0u) | ((bads >> 16) ? 16u << e : 0u);
     if (r < rows) {
       const float inv = sum == 0.f ? 0.f : 1.f / sum;
-      T* out = reinterpret_cast<T*>(a.o) + (int64_t)(s.q0 + i0 + r) * a.o_stride + head * HD;
+      float* out = reinterpret_cast<float*>(a.o) + (int64_t)(s.q0 + i0 + r) * a.o_stride + head * HD;
 #pragma unroll
       for (int c = 0; c < kC; c += 4)
         ka_store4(out + tx * 4 + 16 * c,
@@ -276,7 +276,7 @@ __global__ void __launch_bounds__(kWfThreads) window_simt_kernel(const WaArgs a)
   while (redo) {  // warp-uniform: bits 0-3 the rows of its lower half, 4-7 of its upper half
     const int e = __ffs(redo) - 1;
     redo &= redo - 1;
-    wa_row_exact<T, HD>(a, s, i0 + ((tid >> 5) * 2 + (e >> 2)) * 4 + (e & 3), head);
+    wa_row_exact<float, HD>(a, s, i0 + ((tid >> 5) * 2 + (e >> 2)) * 4 + (e & 3), head);
   }
 }
 

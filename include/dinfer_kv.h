@@ -125,7 +125,7 @@ dinfer_status dinfer_kv_compact(const dinfer_kv_cache* cache, int32_t* live, voi
  * head rows packed, rows q_stride / o_stride elements apart, 16-byte aligned.
  * A sequence without tokens, or whose scores are all -inf, gives zeros.  Keys
  * on a table entry that is no page are left out (DINFER_KV_BAD_PAGE).
- * heads % kv_heads == 0, 1 <= n <= 1024.  The keys are split over the GPU and
+ * heads % kv_heads == 0, 1 <= n <= 1024, scale > 0.  The keys are split over the GPU and
  * joined in a fixed order: the same call gives the same bits. */
 dinfer_status dinfer_kv_attention(const dinfer_kv_cache* cache, int32_t layer, const int32_t* seqs, int32_t n,
                                   const void* q, void* o, int64_t q_stride, int64_t o_stride, int32_t heads,
@@ -143,7 +143,8 @@ dinfer_status dinfer_kv_attention(const dinfer_kv_cache* cache, int32_t layer, c
  * DINFER_BF16 or DINFER_FP32, head rows packed, rows x_stride elements apart
  * (multiples of 16 bytes), 16-byte aligned.  cu_q, cu_k: int32 [batch + 1],
  * non-decreasing, or both NULL with batch 1 (all rows).  Rows of o outside
- * every sequence stay as they were.  1 <= batch <= 1024, head_dim 64 or 128.
+ * every sequence stay as they were.  1 <= batch <= 1024, head_dim 64 or 128,
+ * scale > 0; o must not overlap q, k or v.
  * bf16 runs on the tensor cores: probabilities are rounded to bf16 and summed
  * in fp32.  fp32 is computed in fp32.  Keys that a row does not see do not
  * touch it, whatever they hold.  The workspace may be NULL; when given, a wait

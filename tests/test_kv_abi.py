@@ -72,7 +72,7 @@ def test_bad_call_arguments_are_refused(L):
         assert L.dinfer_kv_append(*a) == dinfer.EINVAL, (i, v)
     ok = [c, 0, None, 4, P, P, 4096, 4096, 32, -1, 0, 0.1, P, 1 << 30, None]
     for i, v in ((1, 2), (3, 0), (3, 1025), (4, P + 4), (5, P + 4), (6, 4000), (7, 4095), (8, 0), (8, 31), (10, -1),
-                 (11, float("nan")), (11, float("inf")), (12, None), (13, 1000)):
+                 (11, float("nan")), (11, float("inf")), (11, 0.0), (11, -0.1), (12, None), (13, 1000)):
         a = list(ok)
         a[i] = v
         assert L.dinfer_kv_attention(*a) == dinfer.EINVAL, (i, v)
@@ -91,7 +91,7 @@ def test_window_attention_refuses_bad_arguments(L):
     ok = [P, P, P, P, dinfer.BF16, 2, P, P, 100, 100, 32, 8, 128, 4096, 1024, 1024, 4096, -1, 0, 0, 0.1, None, 0, None]
     for i, v in ((0, None), (3, None), (0, P + 8), (4, 3), (5, 0), (5, 1025), (6, None), (7, None), (8, 0), (9, 0),
                  (8, (1 << 30) + 1), (10, 0), (10, 30), (11, 0), (12, 80), (13, 4097), (14, 1020), (15, 512), (16, 0),
-                 (19, -1), (20, float("nan"))):
+                 (19, -1), (20, float("nan")), (20, 0.0), (20, -1.0)):
         a = list(ok)
         a[i] = v
         assert L.dinfer_op_window_attention(*a) == dinfer.EINVAL, (i, v)
