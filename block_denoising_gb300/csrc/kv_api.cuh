@@ -75,46 +75,56 @@ int log2_of(int x) {
   return s;
 }
 
-// Shared-memory limits and resident CTAs of this file's kernels, per device.
-struct KvSetup {
-  bool done = false;
-  int ka_ctas[2][2] = {};  // [dtype][head_dim == 128]: attention CTAs per SM
-};
-KvSetup g_kv_setup[kMaxDevices];
+// Shared-memory limits of this file's kernels, set once per device.
+bool g_kv_setup[kMaxDevices] = {};
 
-template <typename T, int HD>
-bool kv_setup_one(int* ctas) {
-  if (cudaFuncSetAttribute(kv_attention_kernel<T, HD>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           KaCfg<T, HD>::kSmem) != cudaSuccess)
-    return false;
-  if (sizeof(T) == 4 && cudaFuncSetAttribute(window_f32_kernel<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             WfCfg<HD>::kSmem) != cudaSuccess)
-    return false;
-  return cudaOccupancyMaxActiveBlocksPerMultiprocessor(ctas, kv_attention_kernel<T, HD>, kKaThreads,
-                                                       KaCfg<T, HD>::kSmem) == cudaSuccess &&
-         *ctas > 0;
+template <typename K>
+bool max_smem(K* kernel, int bytes) {
+  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) == cudaSuccess;
+}
+
+template <typename T, int HD, int R>
+bool kv_setup_attention() {
+  return max_smem(kv_attention_kernel<T, HD, R>, KaCfg<T, HD, R>::kSmem);
 }
 
 template <int HD>
-bool kv_setup_tc() {
-  return cudaFuncSetAttribute(window_tc_kernel<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize, WtCfg<HD>::kSmem) ==
-         cudaSuccess;
+bool kv_setup_hd() {
+  return kv_setup_attention<__nv_bfloat16, HD, 8>() && kv_setup_attention<__nv_bfloat16, HD, 16>() &&
+         kv_setup_attention<float, HD, 1>() && kv_setup_attention<float, HD, 2>() && kv_setup_attention<float, HD, 4>() &&
+         kv_setup_attention<float, HD, 8>() && max_smem(window_f32_kernel<HD>, WfCfg<HD>::kSmem) &&
+         max_smem(window_tc_kernel<HD>, WtCfg<HD>::kSmem);
 }
 
-const KvSetup* kv_setup() {
+bool kv_setup() {
   const int dev = current_device();
   std::lock_guard<std::mutex> lk(g_setup_mutex);
-  KvSetup& s = g_kv_setup[dev];
-  if (!s.done) {
-    s.done = kv_setup_one<float, 64>(&s.ka_ctas[DINFER_FP32][0]) && kv_setup_one<float, 128>(&s.ka_ctas[DINFER_FP32][1]) &&
-             kv_setup_one<__nv_bfloat16, 64>(&s.ka_ctas[DINFER_BF16][0]) &&
-             kv_setup_one<__nv_bfloat16, 128>(&s.ka_ctas[DINFER_BF16][1]) && kv_setup_tc<64>() && kv_setup_tc<128>();
-    if (!s.done) {
-      cudaGetLastError();
-      return nullptr;
-    }
+  if (!g_kv_setup[dev]) {
+    g_kv_setup[dev] = kv_setup_hd<64>() && kv_setup_hd<128>();
+    if (!g_kv_setup[dev]) cudaGetLastError();
   }
-  return &s;
+  return g_kv_setup[dev];
+}
+
+template <typename T, int HD, int R>
+cudaError_t launch_kv_attention_r(const KaArgs& a, cudaStream_t s) {
+  return launchk(kv_attention_kernel<T, HD, R>, dim3(num_sms()), dim3(kKaThreads), KaCfg<T, HD, R>::kSmem, s, 1, a);
+}
+// rows: the query heads a CTA takes at once (kv_rows)
+template <int HD>
+cudaError_t launch_kv_attention(const KaArgs& a, bool bf16, int rows, cudaStream_t s) {
+  if (bf16) return rows == 8 ? launch_kv_attention_r<__nv_bfloat16, HD, 8>(a, s) : launch_kv_attention_r<__nv_bfloat16, HD, 16>(a, s);
+  switch (rows) {
+    case 1: return launch_kv_attention_r<float, HD, 1>(a, s);
+    case 2: return launch_kv_attention_r<float, HD, 2>(a, s);
+    case 4: return launch_kv_attention_r<float, HD, 4>(a, s);
+    default: return launch_kv_attention_r<float, HD, 8>(a, s);
+  }
+}
+// bf16: 8 or 16 rows of the tensor product; fp32: the smallest power of two, up to 8, that takes the group
+int kv_rows(bool bf16, int group) {
+  if (bf16) return group <= 8 ? 8 : 16;
+  return group <= 1 ? 1 : group <= 2 ? 2 : group <= 4 ? 4 : 8;
 }
 
 KvMove kv_move(const dinfer_kv_cache& kc, const KvPages& c) {
@@ -265,6 +275,7 @@ dinfer_status dinfer_kv_attention(const dinfer_kv_cache* kc, int32_t layer, cons
     return fail(c, DINFER_EINVAL, "q, o: 16-byte aligned rows at least a row apart are needed");
   OpWs w;
   if (!op_ws(workspace, workspace_bytes, w)) return fail(c, DINFER_EINVAL, "workspace too small");
+  if (reinterpret_cast<uintptr_t>(workspace) & 15) return fail(c, DINFER_EINVAL, "workspace must be 16-byte aligned");
   KaArgs a{};
   a.c = kv_pages(*kc);
   a.seqs = seqs;
@@ -277,34 +288,23 @@ dinfer_status dinfer_kv_attention(const dinfer_kv_cache* kc, int32_t layer, cons
   a.group = heads / kc->kv_heads;
   a.window = window < 0 ? -1 : window;
   a.sinks = sinks;
-  a.min_units = 1;
+  a.min_steps = 8;
   a.scale_log2 = scale * 1.4426950408889634f;
   a.partial = reinterpret_cast<float*>(w.data);
   a.tickets = w.tickets;
-  const int rows = kc->dtype == DINFER_BF16 ? 16 : 8;
+  const bool bf16 = kc->dtype == DINFER_BF16;
+  const int rows = kv_rows(bf16, a.group);
   a.subgroups = (a.group + rows - 1) / rows;
   const int64_t most = std::min<int64_t>((int64_t)kc->max_pages * kc->page_size,
                                          window < 0 ? INT64_MAX : (int64_t)window + 1 + sinks);
-  if ((most + kKaUnit - 1) / kKaUnit * n * kc->kv_heads * a.subgroups >= (1ll << 31))
-    return fail(c, DINFER_EINVAL, "more than 2^31 units of keys in one call");
-  const KvSetup* setup = kv_setup();
-  if (!setup) return fail(c, DINFER_ECUDA, "kernel set-up failed");
-  const int hd128 = kc->head_dim == 128;
-  const int grid = num_sms() * setup->ka_ctas[kc->dtype][hd128];
+  const int keys = bf16 ? KaCfg<__nv_bfloat16, 128, 8>::kKeys : KaCfg<float, 128, 8>::kKeys;
+  if ((most / keys + kKaWarps + kKaPairCost) * n * kc->kv_heads * a.subgroups >= (1ll << 31))
+    return fail(c, DINFER_EINVAL, "more than 2^31 steps of keys in one call");
+  const size_t slot = (2 * rows + 3) / 4 * 4 + rows * kc->head_dim;  // KaCfg::kSlotFloats
+  if ((size_t)num_sms() * 2 * slot * 4 > w.data_bytes) return fail(c, DINFER_EINVAL, "workspace too small");
+  if (!kv_setup()) return fail(c, DINFER_ECUDA, "kernel set-up failed");
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  auto go = [&](auto kernel, int smem, int slot) -> cudaError_t {
-    if ((size_t)grid * 2 * slot * 4 > w.data_bytes) return cudaErrorInvalidValue;
-    return launchk(kernel, dim3(grid), dim3(kKaThreads), smem, s, 1, a);
-  };
-  cudaError_t e;
-  if (kc->dtype == DINFER_BF16)
-    e = hd128 ? go(kv_attention_kernel<__nv_bfloat16, 128>, KaCfg<__nv_bfloat16, 128>::kSmem, KaCfg<__nv_bfloat16, 128>::kSlotFloats)
-              : go(kv_attention_kernel<__nv_bfloat16, 64>, KaCfg<__nv_bfloat16, 64>::kSmem, KaCfg<__nv_bfloat16, 64>::kSlotFloats);
-  else
-    e = hd128 ? go(kv_attention_kernel<float, 128>, KaCfg<float, 128>::kSmem, KaCfg<float, 128>::kSlotFloats)
-              : go(kv_attention_kernel<float, 64>, KaCfg<float, 64>::kSmem, KaCfg<float, 64>::kSlotFloats);
-  if (e == cudaErrorInvalidValue) return fail(c, DINFER_EINVAL, "workspace too small");
-  CK(e);
+  CK(kc->head_dim == 128 ? launch_kv_attention<128>(a, bf16, rows, s) : launch_kv_attention<64>(a, bf16, rows, s));
   return DINFER_OK;
 }
 
@@ -329,6 +329,7 @@ dinfer_status dinfer_op_window_attention(const void* q, const void* k, const voi
     return fail(c, DINFER_EINVAL, "16-byte aligned rows at least a row apart are needed");
   OpWs w{};
   if (workspace && !op_ws(workspace, workspace_bytes, w)) return fail(c, DINFER_EINVAL, "workspace too small");
+  if (reinterpret_cast<uintptr_t>(workspace) & 15) return fail(c, DINFER_EINVAL, "workspace must be 16-byte aligned");
   if (!kv_setup()) return fail(c, DINFER_ECUDA, "kernel set-up failed");
   WaArgs a{};
   a.q = q;

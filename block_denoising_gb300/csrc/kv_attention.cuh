@@ -8,16 +8,18 @@
 // that stream:
 //
 //   - the visible keys of a sequence (the sinks, then the window) are numbered
-//     0 .. seen - 1 and cut into units of 64; the units of all (sequence, key
-//     head) pairs, end to end, are split evenly over the CTAs, whatever the
-//     sequences' lengths.  A pair that several CTAs share is joined by the last
-//     of them to finish, in CTA order, from fp32 partials in the workspace: one
-//     launch, and the same bits every time;
-//   - each of the 4 warps of a CTA takes 16 keys of a unit and streams its own
-//     rows through a private ring of cp.async stages, so no barrier stands
-//     between the loads and the products.  The ring runs ahead across pair
-//     boundaries.  Page numbers are looked up per key (any page size, any
-//     stride), one unit ahead of the copies that need them;
+//     0 .. seen - 1 and cut into steps of kKeys keys; the steps of all (sequence,
+//     key head) pairs, end to end, are split evenly over the CTAs,
+//     whatever the sequences' lengths.  A pair that several CTAs share is joined
+//     by the last of them to finish, in CTA order, from fp32 partials in the
+//     workspace: one launch, and the same bits every time.  The split counts a
+//     pair as kPairCost steps more than its keys, about what its beginning and
+//     its merge take: without it the CTAs that got many short sequences ran
+//     twice as long as the others (64 sequences of 1 .. 8192 tokens);
+//   - each warp streams its own keys' rows through a private ring of cp.async
+//     stages, so no barrier stands between the loads and the products.  The ring
+//     runs ahead across pair boundaries.  Page numbers are looked up per key (any
+//     page size, any stride), one step ahead of the copies that need them;
 //   - each warp keeps an online softmax of its own (running maximum, sum and
 //     output); the four meet in shared memory at the end of a pair.
 //
@@ -34,27 +36,35 @@ namespace dinfer {
 
 constexpr int kKaWarps = 4;
 constexpr int kKaThreads = kKaWarps * 32;
-constexpr int kKaWarpKeys = 16;
-constexpr int kKaUnit = kKaWarps * kKaWarpKeys;  // keys of a unit
-constexpr int kKaMergeRows = 4;                  // rows merged per round
+constexpr int kKaJoin = 16;      // partials read at once by a join
+constexpr int kKaPairCost = 3;   // a pair's beginning and merge, in steps
 
-template <typename T, int HD>
+template <typename T, int HD, int R>  // R: query heads a CTA takes at once
 struct KaCfg {
-  static constexpr int kRows = sizeof(T) == 2 ? 16 : 8;       // query heads a CTA takes at once
+  static constexpr int kKeys = sizeof(T) == 2 ? 32 : 16;      // keys of a warp's step
+  static constexpr int kRows = R;
   static constexpr int kRowBytes = HD * (int)sizeof(T);
   static constexpr int kVecs = kRowBytes / 16;                // 16-byte vectors of a head's row
-  static constexpr int kStageBytes = 2 * kKaWarpKeys * kRowBytes;  // K and V rows of one warp
-  static constexpr int kStages = kStageBytes >= 16384 ? 2 : (kStageBytes >= 8192 ? 3 : 6);
-  static constexpr int kRing = kKaWarps * kStages * kStageBytes;
-  static constexpr int kMerge = kKaWarps * kKaMergeRows * HD * 4;  // fp32 output rows of the 4 warps
+  static constexpr int kStageBytes = 2 * kKeys * kRowBytes;   // K and V rows of one step: 8 or 16 KB
+  static constexpr int kStages = kStageBytes == 16384 ? 3 : 6;
+  static constexpr int kRing = kKaWarps * kStages * kStageBytes;   // 192 KB: one CTA an SM
+  static constexpr int kMergeRows = R < 4 ? R : 4;             // rows merged per round
+  static constexpr int kMerge = kKaWarps * kMergeRows * HD * 4;  // fp32 output rows of the 4 warps
   static constexpr int kOffMerge = kRing;
   static constexpr int kOffMl = kOffMerge + kMerge;            // [4 warps][rows][m, l]
   static constexpr int kOffQ = kOffMl + kKaWarps * kRows * 8;  // fp32 only: the query rows
   static constexpr int kOffCum = kOffQ + (sizeof(T) == 4 ? kRows * HD * 4 : 0);
-  static constexpr int kOffMask = kOffCum + (kKvMaxEntries + 4) * 4;  // [warp][stage]: keys present
+  static constexpr int kOffLen = kOffCum + (kKvMaxEntries + 4) * 4;
+  static constexpr int kOffMask = kOffLen + kKvMaxEntries * 4;  // [warp][stage]: keys present
   static constexpr int kSmem = kOffMask + kKaWarps * kStages * 4;
-  static constexpr int kSlotFloats = kRows * (HD + 2);         // a partial: m, l [rows], O [rows][HD]
+  // a partial in the workspace: (m, l) [rows], padded so that O [rows][HD] begins at 16 bytes
+  static constexpr int kSlotO = (2 * R + 3) / 4 * 4;
+  static constexpr int kSlotFloats = kSlotO + R * HD;
+  static_assert(kSlotO % 4 == 0 && kSlotFloats % 4 == 0, "16-byte accesses to the partials");
+  static_assert(kOffMerge % 16 == 0 && kOffMl % 16 == 0 && kOffQ % 16 == 0 && kOffCum % 4 == 0, "shared-memory alignment");
+  static_assert(kStageBytes == 8192 || kStageBytes == 16384, "stage size");
 };
+static_assert(KaCfg<float, 128, 8>::kSmem <= 232448, "attention shared memory above 227 KB");
 
 struct KaArgs {
   KvPages c;
@@ -63,7 +73,8 @@ struct KaArgs {
   void* o;
   int64_t q_stride, o_stride, layer_off;  // elements; layer_off in 16-byte vectors
   int n, group, subgroups;                // query heads per key head; pieces of at most kRows of them
-  int window, sinks, min_units;
+  int window, sinks;
+  int min_steps;  // the least a CTA is given
   float scale_log2;
   float* partial;  // [CTA][2][kSlotFloats]
   int* tickets;    // [CTA], zero between calls
@@ -110,140 +121,198 @@ __device__ __forceinline__ void mma_m16n8k16(float (&d)[4], const uint32_t (&a)[
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// The units of the call, walked in order: entry (sequence of the call), head
-// piece, unit of that pair.
+__device__ __forceinline__ int ticket_acq_rel(int* p) {
+  int old;
+  asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], 1;" : "=r"(old) : "l"(p) : "memory");
+  return old;
+}
+
+// How the places [0, total) are dealt to CTAs 0 .. ctas - 1: as evenly as whole
+// places go, the longer ranges first.
+struct KaSplit {
+  int ctas, each, longer;  // CTAs 0 .. longer - 1 have each + 1 places
+  __device__ __forceinline__ void make(int total, int n) {
+    ctas = n;
+    each = (int)((unsigned)total / (unsigned)n);
+    longer = total - each * n;
+  }
+  __device__ __forceinline__ int begin(int cta) const { return cta * each + min(cta, longer); }
+  __device__ __forceinline__ int owner(int place) const {
+    const int head = longer * (each + 1);
+    return place < head ? (int)((unsigned)place / (unsigned)(each + 1)) : longer + (int)((unsigned)(place - head) / (unsigned)each);
+  }
+};
+
+// The part of the call's work that a CTA has, walked in order: entry (sequence
+// of the call), head piece, and a round of kKaWarps steps of that pair (a step
+// is kKeys keys, a warp's).  A pair of `steps` steps takes kKaPairCost + steps
+// places from `base` on; this CTA has those at [x0, x1): steps from .. to - 1.
 struct KaWalk {
-  int entry, piece, unit, units;  // units: of this entry
-  __device__ void start(int u, const int* cum, int n, int pieces) {
-    int lo = 0, hi = n;  // cum[lo] * pieces <= u < cum[hi] * pieces
+  int entry, piece, step;  // step: the round's first
+  int steps, base, to;     // of this pair
+  __device__ __forceinline__ void set_entry(int e, const int* cum, int pieces) {
+    entry = e;
+    steps = (int)((unsigned)(cum[e + 1] - cum[e]) / (unsigned)pieces) - kKaPairCost;
+  }
+  // entry == n: nothing is left
+  __device__ __forceinline__ void start(int x0, int x1, const int* cum, int n, int pieces) {
+    int lo = 0, hi = n;  // cum[lo] <= x0 < cum[hi]
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
-      if (cum[mid] * pieces <= u) lo = mid; else hi = mid;
+      if (cum[mid] <= x0) lo = mid; else hi = mid;
     }
-    entry = lo;
-    units = cum[lo + 1] - cum[lo];
-    const int r = u - cum[lo] * pieces;
-    piece = r / units;
-    unit = r - piece * units;
+    set_entry(lo, cum, pieces);
+    const unsigned size = steps + kKaPairCost;
+    piece = (int)((unsigned)(x0 - cum[lo]) / size);
+    base = cum[lo] + piece * (int)size;
+    step = max(0, x0 - base - kKaPairCost);
+    to = min(steps, x1 - base - kKaPairCost);
+    if (to <= 0) entry = n;  // the range ends in the pair's cost
   }
-  __device__ void next(const int* cum, int n, int pieces) {
-    if (++unit < units) return;
-    unit = 0;
-    if (++piece < pieces) return;
-    piece = 0;
-    do {
-      ++entry;
-      if (entry >= n) return;
-      units = cum[entry + 1] - cum[entry];
-    } while (units == 0);
+  __device__ __forceinline__ void next(int x1, const int* cum, int n, int pieces) {
+    step += kKaWarps;
+    if (step < to) return;
+    step = 0;
+    base += steps + kKaPairCost;
+    if (++piece == pieces) {
+      piece = 0;
+      int e = entry + 1;
+      while (e < n && cum[e + 1] == cum[e]) ++e;  // entries without a key
+      entry = e;
+      if (e < n) set_entry(e, cum, pieces);
+    }
+    to = min(steps, x1 - base - kKaPairCost);
+    if (to <= 0) entry = n;
   }
 };
 
 // ---------------------------------------------------------------------------
 // a warp's running state over its keys of one (sequence, head piece)
 // ---------------------------------------------------------------------------
-// Both forms offer reset(), a step over one ring stage, and store(row0, ...)
-// of kKaMergeRows output rows and of (m, l).
+// Both forms offer load_q() (the query rows of a pair, into registers, ahead of
+// its beginning), begin(), step() over one ring stage, and store_ml() and
+// store_rows() of kMergeRows output rows.
 
 // bf16.  Fragments of mma.m16n8k16: lane = 4 g + t holds rows g and g + 8.
-template <int HD>
+// R = 8: rows g + 8 are zeros and left out of the softmax.
+template <int HD, int R>
 struct KaStateBf16 {
-  static constexpr int kKs = HD / 16, kNt = HD / 8;
-  uint32_t q[kKs][4];
+  static constexpr int kKs = HD / 16, kNt = HD / 8, kKeys = 32, kHalves = R / 8, kMergeRows = 4;
+  uint32_t q[kKs][4], qn[kKs][2 * kHalves];
   float o[kNt][4];
-  float m[2], l[2];
+  float m[kHalves], l[kHalves];
 
-  __device__ void reset(const __nv_bfloat16* qrow, int rows, int lane, float*) {
+  __device__ __forceinline__ void load_q(const __nv_bfloat16* qrow, int rows, int lane) {
     // A fragment: a0 (g, 2t), a1 (g + 8, 2t), a2 (g, 2t + 8), a3 (g + 8, 2t + 8); absent heads are zeros
     const int g = lane >> 2, t = lane & 3;
 #pragma unroll
     for (int ks = 0; ks < kKs; ++ks)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int row = g + (e & 1) * 8, col = ks * 16 + 2 * t + (e >> 1) * 8;
-        q[ks][e] = row < rows ? *reinterpret_cast<const uint32_t*>(qrow + row * HD + col) : 0u;
-      }
+      for (int e = 0; e < 2; ++e)
+#pragma unroll
+        for (int h = 0; h < kHalves; ++h) {
+          const int row = g + h * 8, col = ks * 16 + 2 * t + e * 8;
+          qn[ks][e * kHalves + h] = row < rows ? *reinterpret_cast<const uint32_t*>(qrow + row * HD + col) : 0u;
+        }
+  }
+  __device__ __forceinline__ void begin(int, float*) {
+#pragma unroll
+    for (int ks = 0; ks < kKs; ++ks)
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) q[ks][2 * e + h] = h < kHalves ? qn[ks][e * kHalves + (h < kHalves ? h : 0)] : 0u;
 #pragma unroll
     for (int i = 0; i < kNt; ++i)
 #pragma unroll
       for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
-    m[0] = m[1] = -INFINITY;
-    l[0] = l[1] = 0.f;
+#pragma unroll
+    for (int h = 0; h < kHalves; ++h) {
+      m[h] = -INFINITY;
+      l[h] = 0.f;
+    }
   }
 
-  // stage: K rows [16][HD], V rows [16][HD], 16-byte vector x of row r at x ^ (r & 7); mask: bit r = key r is there
-  __device__ void step(uint32_t stage, uint32_t mask, float sc, int lane, const float*) {
+  // stage: K rows [32][HD], V rows [32][HD], 16-byte vector x of row r at x ^ (r & 7); mask: bit r = key r is there
+  __device__ __forceinline__ void step(const uint8_t*, uint32_t stage, uint32_t mask, float sc, int lane, const float*) {
     constexpr int kRowBytes = HD * 2;
     const int mi = lane >> 3, r8 = lane & 7;
-    float s[2][4] = {};
+    float s[4][4] = {};
     {
-      const int row = (mi >> 1) * 8 + r8;
-      const uint32_t base = stage + row * kRowBytes;
+      const uint32_t base = stage + ((mi >> 1) * 8 + r8) * kRowBytes;
 #pragma unroll
-      for (int ks = 0; ks < kKs; ++ks) {
-        uint32_t b[4];
-        ldmatrix_x4(base + (((ks * 2 + (mi & 1)) ^ r8) << 4), b);
-        mma_m16n8k16(s[0], q[ks], b[0], b[1]);
-        mma_m16n8k16(s[1], q[ks], b[2], b[3]);
-      }
+      for (int ks = 0; ks < kKs; ++ks)
+#pragma unroll
+        for (int kp = 0; kp < 2; ++kp) {  // 16 keys
+          uint32_t b[4];
+          ldmatrix_x4(base + kp * 16 * kRowBytes + (((ks * 2 + (mi & 1)) ^ r8) << 4), b);
+          mma_m16n8k16(s[2 * kp], q[ks], b[0], b[1]);
+          mma_m16n8k16(s[2 * kp + 1], q[ks], b[2], b[3]);
+        }
     }
     const int t2 = (lane & 3) * 2;
+    uint32_t p[2][4] = {};
 #pragma unroll
-    for (int nt = 0; nt < 2; ++nt)
+    for (int h = 0; h < kHalves; ++h) {  // rows g, g + 8
+      float x[8];
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        s[nt][e] = (mask >> (nt * 8 + t2 + (e & 1))) & 1u ? s[nt][e] * sc : -INFINITY;
-    uint32_t p[4];
+      for (int e = 0; e < 8; ++e) x[e] = s[e >> 1][2 * h + (e & 1)] * sc;
+      if (mask != 0xffffffffu)
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {  // rows g, g + 8
-      float mx = fmaxf(fmaxf(s[0][2 * h], s[0][2 * h + 1]), fmaxf(s[1][2 * h], s[1][2 * h + 1]));
+        for (int e = 0; e < 8; ++e)
+          if (!((mask >> ((e >> 1) * 8 + t2 + (e & 1))) & 1u)) x[e] = -INFINITY;
+      float mx = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-      const float mn = fmaxf(m[h], mx);
-      const float nm = mn == -INFINITY ? 0.f : mn;  // nothing seen yet: every weight is 2^-inf = 0
-      const float alpha = m[h] == -INFINITY ? 0.f : ex2_approx(m[h] - nm);
-      m[h] = mn;
-      const uint32_t p0 = pack_bf16x2(ex2_approx(s[0][2 * h] - nm), ex2_approx(s[0][2 * h + 1] - nm));
-      const uint32_t p1 = pack_bf16x2(ex2_approx(s[1][2 * h] - nm), ex2_approx(s[1][2 * h + 1] - nm));
-      p[h] = p0;      // a0 / a1: keys 2t, 2t + 1
-      p[2 + h] = p1;  // a2 / a3: keys 2t + 8, 2t + 9
-      // this lane's four keys; the lanes of a row are summed at the end
-      l[h] = l[h] * alpha + (__uint_as_float(p0 << 16) + __uint_as_float(p0 & 0xffff0000u)) +
-             (__uint_as_float(p1 << 16) + __uint_as_float(p1 & 0xffff0000u));
+      // the maximum is raised only when it grows by more than 8 in log2 (P stays <= 2^8):
+      // O / l is exact whatever maximum was used
+      const bool grow = mx > m[h] + kAtcLazy;
+      if (__any_sync(0xffffffffu, grow)) {
+        const float alpha = !grow ? 1.f : m[h] == -INFINITY ? 0.f : ex2_approx(m[h] - mx);
+        if (grow) m[h] = mx;
+        l[h] *= alpha;
 #pragma unroll
-      for (int i = 0; i < kNt; ++i) {
-        o[i][2 * h] *= alpha;
-        o[i][2 * h + 1] *= alpha;
+        for (int i = 0; i < kNt; ++i) {
+          o[i][2 * h] *= alpha;
+          o[i][2 * h + 1] *= alpha;
+        }
+      }
+      const float nm = m[h] == -INFINITY ? 0.f : m[h];  // nothing seen yet: every weight is 2^-inf = 0
+#pragma unroll
+      for (int e = 0; e < 8; e += 2) {
+        const uint32_t w = pack_bf16x2(ex2_approx(x[e] - nm), ex2_approx(x[e + 1] - nm));
+        p[e >> 2][((e >> 1) & 1) * 2 + h] = w;  // a0 / a1: keys 2t, 2t + 1; a2 / a3: keys 2t + 8, 2t + 9
+        // this lane's keys; the lanes of a row are summed at the end
+        l[h] += __uint_as_float(w << 16) + __uint_as_float(w & 0xffff0000u);
       }
     }
-    const uint32_t vbase = stage + kKaWarpKeys * kRowBytes + ((mi & 1) * 8 + r8) * kRowBytes;
+    const uint32_t vbase = stage + kKeys * kRowBytes + ((mi & 1) * 8 + r8) * kRowBytes;
 #pragma unroll
-    for (int i = 0; i < kNt; i += 2) {
-      uint32_t b[4];
-      ldmatrix_x4_trans(vbase + (((i + (mi >> 1)) ^ r8) << 4), b);
-      mma_m16n8k16(o[i], p, b[0], b[1]);
-      mma_m16n8k16(o[i + 1], p, b[2], b[3]);
-    }
+    for (int kp = 0; kp < 2; ++kp)
+#pragma unroll
+      for (int i = 0; i < kNt; i += 2) {
+        uint32_t b[4];
+        ldmatrix_x4_trans(vbase + kp * 16 * kRowBytes + (((i + (mi >> 1)) ^ r8) << 4), b);
+        mma_m16n8k16(o[i], p[kp], b[0], b[1]);
+        mma_m16n8k16(o[i + 1], p[kp], b[2], b[3]);
+      }
   }
 
-  __device__ void store_ml(float* ml, int lane) {
+  __device__ __forceinline__ void store_ml(float* ml, int lane) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
+    for (int h = 0; h < kHalves; ++h) {
       float s = l[h];
       s += __shfl_xor_sync(0xffffffffu, s, 1);
       s += __shfl_xor_sync(0xffffffffu, s, 2);
-      if ((lane & 3) == 0) {
-        ml[((lane >> 2) + 8 * h) * 2] = m[h];
-        ml[((lane >> 2) + 8 * h) * 2 + 1] = s;
-      }
+      if ((lane & 3) == 0) *reinterpret_cast<float2*>(ml + ((lane >> 2) + 8 * h) * 2) = make_float2(m[h], s);
     }
   }
-  __device__ void store_rows(float* buf, int row0, int lane) {
+  __device__ __forceinline__ void store_rows(float* buf, int row0, int lane) {
     const int g = lane >> 2, t2 = (lane & 3) * 2;
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
+    for (int h = 0; h < kHalves; ++h) {
       const int row = g + 8 * h - row0;
-      if (row >= 0 && row < kKaMergeRows)
+      if (row >= 0 && row < kMergeRows)
 #pragma unroll
         for (int i = 0; i < kNt; ++i)
           *reinterpret_cast<float2*>(buf + row * HD + i * 8 + t2) = make_float2(o[i][2 * h], o[i][2 * h + 1]);
@@ -253,15 +322,20 @@ struct KaStateBf16 {
 
 // fp32.  For the scores lane = 16 half + key takes half of the head's
 // dimensions of one key; for the output a lane owns HD / 32 dimensions.
-template <int HD>
+template <int HD, int R>
 struct KaStateF32 {
-  static constexpr int kRows = 8, kOut = HD / 32;
-  float o[kRows][kOut];
+  static constexpr int kRows = R, kOut = HD / 32, kKeys = 16, kQ = kRows * HD / 32, kMergeRows = R < 4 ? R : 4;
+  float o[kRows][kOut], qn[kQ];
   float m[kRows], l[kRows];
 
-  __device__ void reset(const float* qrow, int rows, int lane, float* qs) {
+  __device__ __forceinline__ void load_q(const float* qrow, int rows, int lane) {
+#pragma unroll
+    for (int x = 0; x < kQ; ++x) qn[x] = x * 32 + lane < rows * HD ? qrow[x * 32 + lane] : 0.f;
+  }
+  __device__ __forceinline__ void begin(int lane, float* qs) {
     // every warp writes the same values: no barrier between the warps is needed for its own reads
-    for (int x = lane; x < kRows * HD; x += 32) qs[x] = x < rows * HD ? qrow[x] : 0.f;
+#pragma unroll
+    for (int x = 0; x < kQ; ++x) qs[x * 32 + lane] = qn[x];
     __syncwarp();
 #pragma unroll
     for (int r = 0; r < kRows; ++r) {
@@ -272,7 +346,7 @@ struct KaStateF32 {
     }
   }
 
-  __device__ void step(const uint8_t* stage, uint32_t mask, float sc, int lane, const float* qs) {
+  __device__ __forceinline__ void step(const uint8_t* stage, uint32_t, uint32_t mask, float sc, int lane, const float* qs) {
     constexpr int kRowBytes = HD * 4;
     const int key = lane & 15, half = lane >> 4;
     float s[kRows] = {};
@@ -304,9 +378,9 @@ struct KaStateF32 {
 #pragma unroll
       for (int e = 0; e < kOut; ++e) o[r][e] *= alpha;
     }
-    const uint8_t* vrows = stage + kKaWarpKeys * kRowBytes;
+    const uint8_t* vrows = stage + kKeys * kRowBytes;
 #pragma unroll 4
-    for (int k = 0; k < kKaWarpKeys; ++k) {
+    for (int k = 0; k < kKeys; ++k) {
       const int byte = lane * kOut * 4, vec = byte >> 4;
       const float* vp = reinterpret_cast<const float*>(vrows + k * kRowBytes + ((vec ^ (k & 7)) << 4) + (byte & 15));
       float vv[kOut];
@@ -321,7 +395,7 @@ struct KaStateF32 {
     }
   }
 
-  __device__ void store_ml(float* ml, int lane) {
+  __device__ __forceinline__ void store_ml(float* ml, int lane) {
 #pragma unroll
     for (int r = 0; r < kRows; ++r) {
       const float s = warp_sum(l[r]);
@@ -331,62 +405,62 @@ struct KaStateF32 {
       }
     }
   }
-  __device__ void store_rows(float* buf, int row0, int lane) {
+  __device__ __forceinline__ void store_rows(float* buf, int row0, int lane) {
 #pragma unroll
     for (int r = 0; r < kRows; ++r)
-      if (r >= row0 && r < row0 + kKaMergeRows)
+      if (r >= row0 && r < row0 + kMergeRows)
 #pragma unroll
         for (int e = 0; e < kOut; ++e) buf[(r - row0) * HD + lane * kOut + e] = o[r][e];
   }
 };
 
-template <typename T, int HD>
+template <typename T, int HD, int R>
 struct KaState;
-template <int HD>
-struct KaState<__nv_bfloat16, HD> : KaStateBf16<HD> {};
-template <int HD>
-struct KaState<float, HD> : KaStateF32<HD> {};
+template <int HD, int R>
+struct KaState<__nv_bfloat16, HD, R> : KaStateBf16<HD, R> {};
+template <int HD, int R>
+struct KaState<float, HD, R> : KaStateF32<HD, R> {};
 
 __device__ __forceinline__ void ka_store4(__nv_bfloat16* p, float4 v) {
   *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
 }
 __device__ __forceinline__ void ka_store4(float* p, float4 v) { *reinterpret_cast<float4*>(p) = v; }
 
-template <typename T, int HD>
-__global__ void __launch_bounds__(kKaThreads) kv_attention_kernel(const KaArgs a) {
-  using Cfg = KaCfg<T, HD>;
-  constexpr int kRows = Cfg::kRows, kStages = Cfg::kStages;
+template <typename T, int HD, int R>
+__global__ void __launch_bounds__(kKaThreads, 1) kv_attention_kernel(const __grid_constant__ KaArgs a) {
+  using Cfg = KaCfg<T, HD, R>;
+  constexpr int kRows = R, kMergeRows = Cfg::kMergeRows, kStages = Cfg::kStages, kKeys = Cfg::kKeys;
   extern __shared__ __align__(128) uint8_t sm[];
-  int* cum = reinterpret_cast<int*>(sm + Cfg::kOffCum);  // units before each entry, for one head piece
+  int* cum = reinterpret_cast<int*>(sm + Cfg::kOffCum);  // places before each entry
+  int* lens = reinterpret_cast<int*>(sm + Cfg::kOffLen);  // tokens of each entry
   float* merge = reinterpret_cast<float*>(sm + Cfg::kOffMerge);
   float* ml = reinterpret_cast<float*>(sm + Cfg::kOffMl);
   float* qs = reinterpret_cast<float*>(sm + Cfg::kOffQ);
-  __shared__ int warp_units[kKaWarps], join_sh;
+  __shared__ int warp_places[kKaWarps], join_sh;
   const KvPages& c = a.c;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int pieces = c.kv_heads * a.subgroups;
   pdl_wait();
+  pdl_trigger();
 
   auto seq_of = [&](int e) { return a.seqs ? a.seqs[e] : e; };
-  auto len_of = [&](int e) {
-    const int s = seq_of(e);
-    if (s < 0 || s >= c.max_seqs) return 0;
-    const int len = c.lens[s];
-    return c.valid_len(len) ? len : 0;
-  };
-  // units before each entry: thread i sums the entries of its own stretch
+  // places before each entry: thread i sums the entries of its own stretch
   {
     const int per = (a.n + kKaThreads - 1) / kKaThreads;
     const int e0 = min(a.n, tid * per), e1 = min(a.n, e0 + per);
     int sum = 0;
     for (int e = e0; e < e1; ++e) {
-      const int u = (ka_seen(len_of(e), a.window, a.sinks).seen + kKaUnit - 1) / kKaUnit;
-      cum[e + 1] = u;
-      sum += u;
-      if (blockIdx.x == 0) {
-        const int s = seq_of(e);
-        if (s < 0 || s >= c.max_seqs || !c.valid_len(c.lens[s])) c.flag(KV_BAD_SEQ);
+      const int s = seq_of(e);
+      int len = s >= 0 && s < c.max_seqs ? c.lens[s] : -1;
+      if (!c.valid_len(len)) {
+        if (blockIdx.x == 0) c.flag(KV_BAD_SEQ);
+        len = 0;
       }
+      lens[e] = len;
+      const int seen = ka_seen(len, a.window, a.sinks).seen;
+      const int x = seen ? ((seen + kKeys * kKaWarps - 1) / (kKeys * kKaWarps) * kKaWarps + kKaPairCost) * pieces : 0;
+      cum[e + 1] = x;
+      sum += x;
     }
     int inc = sum;
 #pragma unroll
@@ -394,10 +468,10 @@ __global__ void __launch_bounds__(kKaThreads) kv_attention_kernel(const KaArgs a
       const int u = __shfl_up_sync(0xffffffffu, inc, o);
       if (lane >= o) inc += u;
     }
-    if (lane == 31) warp_units[warp] = inc;
+    if (lane == 31) warp_places[warp] = inc;
     __syncthreads();
     int run = inc - sum;
-    for (int w = 0; w < warp; ++w) run += warp_units[w];
+    for (int w = 0; w < warp; ++w) run += warp_places[w];
     if (tid == 0) cum[0] = 0;
     for (int e = e0; e < e1; ++e) {
       run += cum[e + 1];
@@ -412,104 +486,129 @@ __global__ void __launch_bounds__(kKaThreads) kv_attention_kernel(const KaArgs a
     const int vecs = c.kv_heads * a.group * Cfg::kVecs;
     for (int x = tid; x < vecs; x += kKaThreads) reinterpret_cast<uint4*>(orow)[x] = make_uint4(0, 0, 0, 0);
   }
-  // units of the call (the host bounds them below 2^31) and the CTAs that
-  // take them: at least min_units each, so that none is without
-  const int64_t total = (int64_t)cum[a.n] * pieces;
-  const int64_t G = min((int64_t)gridDim.x, max((int64_t)1, total / a.min_units));
-  if (total == 0 || blockIdx.x >= G) return;
-  const int64_t u0 = total * blockIdx.x / G, u1 = total * (blockIdx.x + 1) / G;
-  const int count = (int)(u1 - u0);
+  // the host bounds the places of the call below 2^31
+  const int total = cum[a.n];
+  KaSplit split;
+  split.make(total, max(1, min((int)gridDim.x, total / a.min_steps)));
+  if (total == 0 || blockIdx.x >= split.ctas) return;
+  const int x0 = split.begin(blockIdx.x), x1 = split.begin(blockIdx.x + 1);
+  KaWalk load;
+  load.start(x0, x1, cum, a.n, pieces);
+  if (load.entry >= a.n) return;
 
   uint8_t* ring = sm + warp * (kStages * Cfg::kStageBytes);
   const uint32_t ring_u32 = smem_u32(ring);
   uint32_t* masks = reinterpret_cast<uint32_t*>(sm + Cfg::kOffMask) + warp * kStages;
-  KaWalk load, use;
-  load.start((int)u0, cum, a.n, pieces);
-  use = load;
-  int load_entry = -1, load_seq = 0;
+  KaWalk use = load;
+  // Where key `lane` of this warp's step of a round lies: its page's number as
+  // the table has it (not looked at until the copies are issued, two rounds
+  // later, so that the load's latency is hidden) and the rest of its address in
+  // 16-byte vectors; -1: no such key.
+  struct Where {
+    int page;
+    int64_t off;
+  };
+  int load_entry = -1;
+  const int32_t* load_row = nullptr;
   KaSeen seen{};
-  // the address of key `lane & 15` of the unit at `load`, in 16-byte vectors of
-  // the layer, or -1 (no such key); kept one unit ahead of its copies
-  auto look_up = [&]() -> int64_t {
+  auto look_up = [&]() -> Where {
     if (load.entry != load_entry) {
       load_entry = load.entry;
-      load_seq = seq_of(load_entry);
-      seen = ka_seen(c.lens[load_seq], a.window, a.sinks);
+      load_row = c.table + (size_t)seq_of(load_entry) * c.max_pages;
+      seen = ka_seen(lens[load_entry], a.window, a.sinks);
     }
-    const int x = load.unit * kKaUnit + warp * kKaWarpKeys + (lane & 15);
-    if (x >= seen.seen) return -1;
+    const int x = (load.step + warp) * kKeys + lane % kKeys;
+    if (load.step + warp >= load.to || x >= seen.seen) return {0, -1};
     const int key = x < seen.sink ? x : x - seen.sink + seen.first;
     const int j = (int)c.page_div.div((uint32_t)key);
-    const int page = c.table[(size_t)load_seq * c.max_pages + j];
-    if (page < 0 || page >= c.num_pages) {
-      c.flag(KV_BAD_PAGE);
-      return -1;
-    }
-    return a.layer_off + page * c.page_stride + (key - j * c.page_size) * c.token_stride +
-           (load.piece / a.subgroups) * c.head_stride;
+    return {load_row[j], a.layer_off + (key - j * c.page_size) * c.token_stride + (load.piece / a.subgroups) * c.head_stride};
   };
-  int64_t at = look_up();
-  int issued = 0;
+  Where at = look_up(), at_next{0, -1};
+  int ahead_rounds = 1;  // looked up and not issued yet: at, at_next
+  auto advance = [&]() {
+    load.next(x1, cum, a.n, pieces);
+    if (load.entry < a.n) {
+      if (load.step == 0 && warp == 0) {  // a new pair: its query rows into L2 by the time they are wanted
+        const int sub = load.piece % a.subgroups, rows = min(kRows, a.group - sub * kRows);
+        const char* qp = reinterpret_cast<const char*>(reinterpret_cast<const T*>(a.q) + load.entry * a.q_stride +
+                                                       ((load.piece / a.subgroups) * a.group + sub * kRows) * HD);
+        for (int x = lane * 128; x < rows * Cfg::kRowBytes; x += 32 * 128)
+          asm volatile("prefetch.global.L2 [%0];" ::"l"(qp + x));
+      }
+      at_next = look_up();
+      ++ahead_rounds;
+    }
+  };
+  advance();
+  // Copies of one step: eight lanes take 128 bytes of a row at a time, so that
+  // each line is asked for once; an absent key's row is zeros.
   auto issue = [&](int stage) {
-    if (issued < count) {
-      const uint32_t mask = __ballot_sync(0xffffffffu, at >= 0) & 0xffffu;
+    if (ahead_rounds > 0) {
+      int64_t place = -1;
+      if (at.off >= 0) {
+        if (at.page >= 0 && at.page < c.num_pages) place = at.off + at.page * c.page_stride;
+        else c.flag(KV_BAD_PAGE);
+      }
+      const uint32_t mask = __ballot_sync(0xffffffffu, place >= 0) & (kKeys == 32 ? 0xffffffffu : 0xffffu);
       if (lane == 0) masks[stage] = mask;
-      constexpr int kPer = 32 / Cfg::kVecs > 0 ? 32 / Cfg::kVecs : 1;  // rows an instruction covers
-      const int x = lane % Cfg::kVecs;
+      if (mask) {
 #pragma unroll
-      for (int r0 = 0; r0 < kKaWarpKeys; r0 += kPer) {
-        const int r = r0 + lane / Cfg::kVecs;
-        const int64_t off = __shfl_sync(0xffffffffu, at, r);
-        const int bytes = off >= 0 ? 16 : 0;  // an absent key's row is zeros
-        const int64_t v = off >= 0 ? off + x : 0;
-        const uint32_t d = ring_u32 + stage * Cfg::kStageBytes + r * Cfg::kRowBytes + ((x ^ (r & 7)) << 4);
-        cp_async16(d, c.k + v, bytes);
-        cp_async16(d + kKaWarpKeys * Cfg::kRowBytes, c.v + v, bytes);
+        for (int j = 0; j < kKeys / 4; ++j) {
+          const int r = j * 4 + (lane >> 3);
+          const int64_t off = __shfl_sync(0xffffffffu, place, r);
+          const int bytes = off >= 0 ? 16 : 0;
+          const uint4* ks = c.k + (off >= 0 ? off : 0) + (lane & 7);
+          const uint4* vs = c.v + (off >= 0 ? off : 0) + (lane & 7);
+          const uint32_t d = ring_u32 + stage * Cfg::kStageBytes + r * Cfg::kRowBytes + (((lane & 7) ^ (r & 7)) << 4);
+#pragma unroll
+          for (int i = 0; i < Cfg::kVecs / 8; ++i) {
+            cp_async16(d + 128 * i, ks + 8 * i, bytes);
+            cp_async16(d + 128 * i + kKeys * Cfg::kRowBytes, vs + 8 * i, bytes);
+          }
+        }
       }
-      ++issued;
-      if (issued < count) {
-        load.next(cum, a.n, pieces);
-        at = look_up();
-      }
+      --ahead_rounds;
+      at = at_next;
+      if (ahead_rounds > 0) advance();
     }
     cp_async_commit();
   };
+  KaState<T, HD, R> state;
+  auto load_q = [&](const KaWalk& w) {
+    const int sub = w.piece % a.subgroups, head = (w.piece / a.subgroups) * a.group + sub * kRows;
+    state.load_q(reinterpret_cast<const T*>(a.q) + w.entry * a.q_stride + head * HD, min(kRows, a.group - sub * kRows), lane);
+  };
+  load_q(use);
   for (int s = 0; s < kStages - 1; ++s) issue(s);
+  state.begin(lane, qs);
 
-  KaState<T, HD> state;
-  int done = 0, stage = 0, seg_unit = use.unit;  // the pair's first unit in this CTA
-  while (done < count) {
-    if (done == 0 || use.unit == 0) {
-      const int sub = use.piece % a.subgroups, rows = min(kRows, a.group - sub * kRows);
-      const int head = (use.piece / a.subgroups) * a.group + sub * kRows;
-      state.reset(reinterpret_cast<const T*>(a.q) + use.entry * a.q_stride + head * HD, rows, lane, qs);
-      seg_unit = use.unit;
-    }
+  int stage = 0, seg_step = use.step;  // the pair's first step in this CTA
+  while (true) {
     issue(stage == 0 ? kStages - 1 : stage - 1);
     cp_async_wait<kStages - 1>();
     __syncwarp();
-    if constexpr (sizeof(T) == 2)
-      state.step(ring_u32 + stage * Cfg::kStageBytes, masks[stage], a.scale_log2, lane, qs);
-    else
-      state.step(ring + stage * Cfg::kStageBytes, masks[stage], a.scale_log2, lane, qs);
+    const uint32_t mask = masks[stage];
+    if (mask)
+      state.step(ring + stage * Cfg::kStageBytes, ring_u32 + stage * Cfg::kStageBytes, mask, a.scale_log2, lane, qs);
     __syncwarp();  // the stage is refilled next turn
     stage = stage + 1 == kStages ? 0 : stage + 1;
-    ++done;
-    const int seg_end = use.unit + 1;
-    const bool last_unit = seg_end == use.units;
-    if (last_unit || done == count) {
+    KaWalk ahead = use;
+    ahead.next(x1, cum, a.n, pieces);
+    const bool go = ahead.entry < a.n;
+    if (!go || ahead.base != use.base) {
       // the pair's keys of this CTA are done: merge the four warps
+      if (go) load_q(ahead);
       const int sub = use.piece % a.subgroups, rows = min(kRows, a.group - sub * kRows);
       const int head = (use.piece / a.subgroups) * a.group + sub * kRows;
-      const bool whole = last_unit && seg_unit == 0;
-      const int slot = seg_unit == 0 ? 1 : 0;  // 0: the pair began in an earlier CTA
+      const bool whole = use.to == use.steps && seg_step == 0;
+      const int slot = seg_step == 0 ? 1 : 0;  // 0: the pair began in an earlier CTA
       float* part = a.partial + ((int64_t)blockIdx.x * 2 + slot) * Cfg::kSlotFloats;
       state.store_ml(ml + warp * kRows * 2, lane);
       T* orow = reinterpret_cast<T*>(a.o) + use.entry * a.o_stride + head * HD;
-      for (int r0 = 0; r0 < rows; r0 += kKaMergeRows) {
-        state.store_rows(merge + warp * (kKaMergeRows * HD), r0, lane);
+      for (int r0 = 0; r0 < rows; r0 += kMergeRows) {
+        state.store_rows(merge + warp * (kMergeRows * HD), r0, lane);
         __syncthreads();
-        for (int x = tid; x < kKaMergeRows * HD / 4; x += kKaThreads) {
+        for (int x = tid; x < kMergeRows * HD / 4; x += kKaThreads) {
           const int row = r0 + x / (HD / 4), c4 = (x % (HD / 4)) * 4;
           if (row < rows) {
             float mm = -INFINITY;
@@ -522,7 +621,7 @@ __global__ void __launch_bounds__(kKaThreads) kv_attention_kernel(const KaArgs a
               const float mw = ml[(w * kRows + row) * 2];
               const float f = mw == -INFINITY ? 0.f : ex2_approx(mw - mm);
               const float4 v =
-                  *reinterpret_cast<const float4*>(merge + w * (kKaMergeRows * HD) + (row - r0) * HD + c4);
+                  *reinterpret_cast<const float4*>(merge + w * (kMergeRows * HD) + (row - r0) * HD + c4);
               ll = fmaf(f, ml[(w * kRows + row) * 2 + 1], ll);
               acc.x = fmaf(f, v.x, acc.x);
               acc.y = fmaf(f, v.y, acc.y);
@@ -533,7 +632,7 @@ __global__ void __launch_bounds__(kKaThreads) kv_attention_kernel(const KaArgs a
               const float inv = ll == 0.f ? 0.f : 1.f / ll;
               ka_store4(orow + row * HD + c4, make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
             } else {
-              __stcg(reinterpret_cast<float4*>(part + kRows * 2 + row * HD + c4), acc);
+              __stcg(reinterpret_cast<float4*>(part + Cfg::kSlotO + row * HD + c4), acc);
               if (c4 == 0) __stcg(reinterpret_cast<float2*>(part + row * 2), make_float2(mm, ll));
             }
           }
@@ -541,38 +640,50 @@ __global__ void __launch_bounds__(kKaThreads) kv_attention_kernel(const KaArgs a
         __syncthreads();
       }
       if (!whole) {
-        // units of the pair, and the CTAs that share it
-        const int64_t pair0 = (int64_t)cum[use.entry] * pieces + (int64_t)use.piece * use.units;
-        const int64_t pair1 = pair0 + use.units;
-        const int c_first = (int)(((pair0 + 1) * G - 1) / total), c_last = (int)((pair1 * G - 1) / total);
-        __threadfence();
+        const int c_first = split.owner(use.base + kKaPairCost), c_last = split.owner(use.base + kKaPairCost + use.steps - 1);
+        // the barrier orders the CTA's partials before the ticket, which is taken with
+        // release and acquire: the last CTA sees the partials of all before it
         __syncthreads();
-        if (tid == 0) join_sh = atomicAdd(a.tickets + c_first, 1) == c_last - c_first;
+        if (tid == 0) join_sh = ticket_acq_rel(a.tickets + c_first) == c_last - c_first;
         __syncthreads();
         if (join_sh) {
-          __threadfence();
           const int nc = c_last - c_first + 1;
-          auto slot_of = [&](int k) {
-            return a.partial + ((int64_t)(c_first + k) * 2 + (k == 0 ? 1 : 0)) * Cfg::kSlotFloats;
-          };
           for (int x = tid; x < rows * HD / 4; x += kKaThreads) {
             const int row = x / (HD / 4), c4 = (x % (HD / 4)) * 4;
-            float mm = -INFINITY;
-#pragma unroll 4
-            for (int k = 0; k < nc; ++k) mm = fmaxf(mm, __ldcg(slot_of(k) + row * 2));
-            float ll = 0.f;
+            float mm = -INFINITY, ll = 0.f;
             float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-            for (int k = 0; k < nc; ++k) {
-              const float* p = slot_of(k);
-              const float2 w = __ldcg(reinterpret_cast<const float2*>(p + row * 2));
-              const float4 v = __ldcg(reinterpret_cast<const float4*>(p + kRows * 2 + row * HD + c4));
-              const float f = w.x == -INFINITY ? 0.f : ex2_approx(w.x - mm);
-              ll = fmaf(f, w.y, ll);
-              acc.x = fmaf(f, v.x, acc.x);
-              acc.y = fmaf(f, v.y, acc.y);
-              acc.z = fmaf(f, v.z, acc.z);
-              acc.w = fmaf(f, v.w, acc.w);
+            for (int k0 = 0; k0 < nc; k0 += kKaJoin) {  // all loads of a round before the first use
+              float2 w[kKaJoin];
+              float4 v[kKaJoin];
+#pragma unroll
+              for (int k = 0; k < kKaJoin; ++k) {
+                w[k] = make_float2(-INFINITY, 0.f);
+                v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (k0 + k < nc) {
+                  const float* p = a.partial + ((int64_t)(c_first + k0 + k) * 2 + (k0 + k == 0 ? 1 : 0)) * Cfg::kSlotFloats;
+                  w[k] = __ldcg(reinterpret_cast<const float2*>(p + row * 2));
+                  v[k] = __ldcg(reinterpret_cast<const float4*>(p + Cfg::kSlotO + row * HD + c4));
+                }
+              }
+              float mn = mm;
+#pragma unroll
+              for (int k = 0; k < kKaJoin; ++k) mn = fmaxf(mn, w[k].x);
+              const float f0 = mm == -INFINITY ? 0.f : ex2_approx(mm - mn);
+              mm = mn;
+              ll *= f0;
+              acc.x *= f0;
+              acc.y *= f0;
+              acc.z *= f0;
+              acc.w *= f0;
+#pragma unroll
+              for (int k = 0; k < kKaJoin; ++k) {
+                const float f = w[k].x == -INFINITY ? 0.f : ex2_approx(w[k].x - mm);
+                ll = fmaf(f, w[k].y, ll);
+                acc.x = fmaf(f, v[k].x, acc.x);
+                acc.y = fmaf(f, v[k].y, acc.y);
+                acc.z = fmaf(f, v[k].z, acc.z);
+                acc.w = fmaf(f, v[k].w, acc.w);
+              }
             }
             const float inv = ll == 0.f ? 0.f : 1.f / ll;
             ka_store4(orow + row * HD + c4, make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
@@ -580,8 +691,11 @@ __global__ void __launch_bounds__(kKaThreads) kv_attention_kernel(const KaArgs a
           if (tid == 0) a.tickets[c_first] = 0;
         }
       }
+      if (!go) break;
+      state.begin(lane, qs);
+      seg_step = 0;
     }
-    use.next(cum, a.n, pieces);
+    use = ahead;
   }
   cp_async_wait<0>();
 }

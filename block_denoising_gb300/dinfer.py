@@ -299,22 +299,35 @@ def _require(ok, what: str):
 
 def _rows_of(t: torch.Tensor, name: str, heads: Optional[int], head_dim: int, like: torch.Tensor):
     """Checks [rows, heads, head_dim] with packed head rows, of like's type and device; returns the row stride."""
-    _require(t.dim() == 3 and t.shape[2] == head_dim and (heads is None or t.shape[1] == heads),
-             f"{name}: [rows, {'heads' if heads is None else heads}, {head_dim}] expected, got {list(t.shape)}")
-    _require(t.dtype == like.dtype and t.device == like.device, f"{name}: {like.dtype} on {like.device} expected")
-    s = t.stride()
-    _require(s[2] == 1 and (s[1] == head_dim or t.shape[1] == 1), f"{name}: the heads of a row must be packed")
-    return s[0]
+    shape, s = t.shape, t.stride()
+    if (len(shape) == 3 and shape[2] == head_dim and (heads is None or shape[1] == heads) and t.dtype is like.dtype
+            and t.device == like.device and s[2] == 1 and (s[1] == head_dim or shape[1] == 1)):
+        return s[0]
+    raise ValueError(f"{name}: [rows, {'heads' if heads is None else heads}, {head_dim}] {like.dtype} on {like.device} with "
+                     f"the heads of a row packed expected, got {list(shape)} {t.dtype} on {t.device} with strides {s}")
 
 
 def _ints(t: Optional[torch.Tensor], name: str, device, n: Optional[int] = None):
     """Address of a contiguous int32 vector on device (None: NULL)."""
     if t is None:
         return None
-    _require(t.dtype == torch.int32 and t.dim() == 1 and t.device == device and t.is_contiguous(),
-             f"{name}: a contiguous int32 vector on {device} expected")
-    _require(n is None or t.shape[0] == n, f"{name}: {n} entries expected, got {t.shape[0]}")
-    return t.data_ptr()
+    if (t.dtype is torch.int32 and t.dim() == 1 and t.device == device and t.is_contiguous()
+            and (n is None or t.shape[0] == n)):
+        return t.data_ptr()
+    raise ValueError(f"{name}: a contiguous int32 vector {'' if n is None else f'of {n} '}on {device} expected, got "
+                     f"{list(t.shape)} {t.dtype} on {t.device}")
+
+
+def _run_on(device, fn, *args):
+    """One library call on torch's current stream of the operands' device, which becomes the current one for it."""
+    i = device.index
+    if i == torch.cuda.current_device():
+        st = fn(*args, torch._C._cuda_getCurrentRawStream(i))
+    else:
+        with torch.cuda.device(i):
+            st = fn(*args, torch._C._cuda_getCurrentRawStream(i))
+    if st != OK:
+        _check(st)
 
 
 class PagedKV:
@@ -355,10 +368,7 @@ class PagedKV:
                    torch.zeros(pages, dtype=torch.int32, device=device))
 
     def _call(self, fn, *args):
-        if self.device.index == torch.cuda.current_device():
-            return _check(fn(self._desc, *args, torch.cuda.current_stream().cuda_stream))
-        with torch.cuda.device(self.device):
-            _check(fn(self._desc, *args, torch.cuda.current_stream().cuda_stream))
+        _run_on(self.device, fn, self._desc, *args)
 
     def set_tables(self, table: torch.Tensor, lens: torch.Tensor, refs: torch.Tensor):
         """Takes over another set of tables of the same sizes (a snapshot, a scheduler's own plan)."""
@@ -371,7 +381,7 @@ class PagedKV:
 
     def extend(self, add: Optional[torch.Tensor] = None, seqs: Optional[torch.Tensor] = None):
         """Sequences seqs (default: the first ones, one per entry of add; all) grow by add tokens (default: one each)."""
-        n = len(seqs) if seqs is not None else len(add) if add is not None else self.max_seqs
+        n = seqs.shape[0] if seqs is not None else add.shape[0] if add is not None else self.max_seqs
         _require(seqs is not None or n <= self.max_seqs, "add: more entries than sequences")
         self._call(lib().dinfer_kv_extend, _ints(seqs, "seqs", self.device), _ints(add, "add", self.device, n), n)
 
@@ -382,18 +392,18 @@ class PagedKV:
         ks = _rows_of(k, "k", self.kv_heads, self.head_dim, self.k)
         vs = _rows_of(v, "v", self.kv_heads, self.head_dim, self.k)
         _require(k.shape[0] == v.shape[0], "k, v: as many rows expected")
-        n = len(rows) - 1 if rows is not None else k.shape[0]
+        n = rows.shape[0] - 1 if rows is not None else k.shape[0]
         _require(seqs is not None or n <= self.max_seqs, "more entries than sequences")
         self._call(lib().dinfer_kv_append, layer, _ints(seqs, "seqs", self.device, n), _ints(rows, "rows", self.device), n,
                    k.data_ptr(), v.data_ptr(), ks, vs, k.shape[0])
 
     def fork(self, src: torch.Tensor, dst: torch.Tensor, share: bool = True):
         """Sequences dst (not in use) become copies of src, sharing the full pages or copying all of them."""
-        self._call(lib().dinfer_kv_fork, _ints(src, "src", self.device), _ints(dst, "dst", self.device, len(src)), len(src),
-                   int(share))
+        n = src.shape[0]
+        self._call(lib().dinfer_kv_fork, _ints(src, "src", self.device), _ints(dst, "dst", self.device, n), n, int(share))
 
     def free(self, seqs: torch.Tensor):
-        self._call(lib().dinfer_kv_free, _ints(seqs, "seqs", self.device), len(seqs))
+        self._call(lib().dinfer_kv_free, _ints(seqs, "seqs", self.device), seqs.shape[0])
 
     def compact(self, live: Optional[torch.Tensor] = None):
         """Packs the pages in use to the front; live (optional, int32 [1]) receives how many there are."""
@@ -406,11 +416,11 @@ class PagedKV:
         qs = _rows_of(q, "q", None, hd, self.k)
         n, heads, _ = q.shape
         _require(seqs is not None or n <= self.max_seqs, "q: more rows than sequences")
-        _require(ws.buf.device == self.device, f"ws: a workspace on {self.device} expected")
+        _require(ws.buf.device == self.device, "ws: a workspace on the cache's device expected")
         if out is None:
             out = torch.empty((n, heads, hd), dtype=q.dtype, device=self.device)
         os_ = _rows_of(out, "out", heads, hd, self.k)
-        _require(out.shape[0] == n, f"out: {n} rows expected")
+        _require(out.shape[0] == n, "out: as many rows as q expected")
         self._call(lib().dinfer_kv_attention, layer, _ints(seqs, "seqs", self.device, n), n, q.data_ptr(), out.data_ptr(),
                    qs, os_, heads, window, sinks, hd ** -0.5 if scale is None else scale, ws.buf.data_ptr(), ws.nbytes)
         return out
@@ -433,18 +443,14 @@ def op_window_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, ws: O
     vs = _rows_of(v, "v", k.shape[1], hd, q)
     _require(k.shape[0] == v.shape[0], "k, v: as many keys expected")
     dev = q.device
-    cq, ck = _ints(cu_q, "cu_q", dev), _ints(cu_k, "cu_k", dev, None if cu_q is None else len(cu_q))
-    _require(ws.buf.device == dev, f"ws: a workspace on {dev} expected")
+    batch = 1 if cu_q is None else cu_q.shape[0] - 1
+    cq, ck = _ints(cu_q, "cu_q", dev), _ints(cu_k, "cu_k", dev, None if cu_q is None else batch + 1)
+    _require(ws.buf.device == dev, "ws: a workspace on the operands' device expected")
     if out is None:
         out = torch.empty((rows, heads, hd), dtype=q.dtype, device=dev)
     os_ = _rows_of(out, "out", heads, hd, q)
-    _require(out.shape[0] == rows, f"out: {rows} rows expected")
-    args = (q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), _DTYPES[q.dtype],
-            1 if cu_q is None else len(cu_q) - 1, cq, ck, rows, k.shape[0], heads, k.shape[1], hd, qs, ks, vs, os_, left,
-            right, sinks, hd ** -0.5 if scale is None else scale, ws.buf.data_ptr(), ws.nbytes)
-    if dev.index == torch.cuda.current_device():
-        _check(lib().dinfer_op_window_attention(*args, torch.cuda.current_stream().cuda_stream))
-    else:
-        with torch.cuda.device(dev):
-            _check(lib().dinfer_op_window_attention(*args, torch.cuda.current_stream().cuda_stream))
+    _require(out.shape[0] == rows, "out: as many rows as q expected")
+    _run_on(dev, lib().dinfer_op_window_attention, q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), _DTYPES[q.dtype],
+            batch, cq, ck, rows, k.shape[0], heads, k.shape[1], hd, qs, ks, vs, os_, left, right, sinks,
+            hd ** -0.5 if scale is None else scale, ws.buf.data_ptr(), ws.nbytes)
     return out

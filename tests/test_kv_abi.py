@@ -72,7 +72,7 @@ def test_bad_call_arguments_are_refused(L):
         assert L.dinfer_kv_append(*a) == dinfer.EINVAL, (i, v)
     ok = [c, 0, None, 4, P, P, 4096, 4096, 32, -1, 0, 0.1, P, 1 << 30, None]
     for i, v in ((1, 2), (3, 0), (3, 1025), (4, P + 4), (5, P + 4), (6, 4000), (7, 4095), (8, 0), (8, 31), (10, -1),
-                 (11, float("nan")), (11, float("inf")), (11, 0.0), (11, -0.1), (12, None), (13, 1000)):
+                 (11, float("nan")), (11, float("inf")), (11, 0.0), (11, -0.1), (12, None), (12, P + 8), (13, 1000)):
         a = list(ok)
         a[i] = v
         assert L.dinfer_kv_attention(*a) == dinfer.EINVAL, (i, v)
@@ -99,7 +99,9 @@ def test_window_attention_refuses_bad_arguments(L):
     a[6] = a[7] = None  # two sequences need their bounds
     assert L.dinfer_op_window_attention(*a) == dinfer.EINVAL
     a = list(ok)
-    a[21], a[22] = P, 100  # a workspace that is too small
+    a[21], a[22] = P, 100  # a workspace that is too small, one that is not aligned
+    assert L.dinfer_op_window_attention(*a) == dinfer.EINVAL
+    a[21], a[22] = P + 8, 1 << 30
     assert L.dinfer_op_window_attention(*a) == dinfer.EINVAL
 
 
