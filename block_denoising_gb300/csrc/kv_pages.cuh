@@ -169,6 +169,7 @@ __global__ void __launch_bounds__(kKvPlanThreads) kv_extend_kernel(const KvPages
   __shared__ int prefix[kKvPlanThreads + 1];
   __shared__ int seq_of[kKvPlanThreads], held_of[kKvPlanThreads];
   pdl_wait();
+  pdl_trigger();
   const int i = threadIdx.x;
   int s = -1;
   if (i < n) {
@@ -214,6 +215,7 @@ __global__ void __launch_bounds__(kKvPlanThreads) kv_fork_plan_kernel(const KvPa
   __shared__ int prefix[kKvPlanThreads + 1];
   __shared__ int src_of[kKvPlanThreads], len_of[kKvPlanThreads];
   pdl_wait();
+  pdl_trigger();
   const int i = threadIdx.x;
   int s = -1, d = -1;
   if (i < n) {
@@ -263,6 +265,7 @@ __global__ void __launch_bounds__(kKvPlanThreads) kv_fork_plan_kernel(const KvPa
 // --------------------------------------------------------------------------
 __global__ void __launch_bounds__(kKvPlanThreads) kv_compact_plan_kernel(const KvPages c, int32_t* live_out) {
   pdl_wait();
+  pdl_trigger();
   int live = 0;
   for (int at = threadIdx.x * 4; at < c.num_pages; at += kKvPlanThreads * 4)
 #pragma unroll
@@ -327,6 +330,7 @@ __device__ __forceinline__ int64_t kv_vec_offset(const KvPages& c, const KvMove&
 template <bool kFork>
 __global__ void __launch_bounds__(kKvMoveThreads) kv_move_kernel(const KvPages c, const KvMove m) {
   pdl_wait();
+  pdl_trigger();
   const int64_t tid = (int64_t)blockIdx.x * blockDim.x + threadIdx.x, step = (int64_t)gridDim.x * blockDim.x;
   if (kFork) {
     // table rows: pages held by both, then the new ones
@@ -401,6 +405,7 @@ __global__ void __launch_bounds__(kKvMoveThreads) kv_move_kernel(const KvPages c
 __global__ void __launch_bounds__(128) kv_free_kernel(const KvPages c, const int32_t* seqs) {
   __shared__ int len_sh;
   pdl_wait();
+  pdl_trigger();
   const int s = seqs[blockIdx.x];
   if (s < 0 || s >= c.max_seqs) {
     if (threadIdx.x == 0) c.flag(KV_BAD_SEQ);
@@ -444,6 +449,7 @@ struct KvAppend {
 
 __global__ void __launch_bounds__(256) kv_append_kernel(const KvPages c, const KvAppend a) {
   pdl_wait();
+  pdl_trigger();
   const int lane = threadIdx.x & 31;
   const int64_t warps = ((int64_t)gridDim.x * blockDim.x) >> 5;
   const int row_vecs = c.kv_heads << a.vec_shift;

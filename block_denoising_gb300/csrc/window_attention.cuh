@@ -98,7 +98,7 @@ __device__ __forceinline__ float wa_f32(T x) {
 // paid only by such rows.
 template <typename T, int HD>
 __device__ __noinline__ void wa_row_exact(const WaArgs& a, const WaSeq s, int i, int head) {
-  constexpr int kE = HD / 32;
+  constexpr int kE = HD / 32, kU = 8;
   const int lane = threadIdx.x & 31;
   const WaRange r = wa_range(a, s, i);
   const T* q = reinterpret_cast<const T*>(a.q) + (int64_t)(s.q0 + i) * a.q_stride + head * HD + lane * kE;
@@ -109,19 +109,41 @@ __device__ __noinline__ void wa_row_exact(const WaArgs& a, const WaSeq s, int i,
   for (int e = 0; e < kE; ++e) qq[e] = wa_f32(q[e]);
   const int front = min(a.sinks, min(r.lo, r.hi + 1));
   const int seen = front + max(0, r.hi - r.lo + 1);
-  for (int x = 0; x < seen; ++x) {
-    const int j = x < front ? x : x - front + r.lo;
-    float d = 0.f;
+  for (int x0 = 0; x0 < seen; x0 += kU) {  // kU keys' loads and sums at once
+    float d[kU], vv[kU][kE];
 #pragma unroll
-    for (int e = 0; e < kE; ++e) d = fmaf(qq[e], wa_f32(k[(int64_t)j * a.k_stride + e]), d);
-    d = warp_sum(d) * a.scale_log2;
-    const float mn = fmaxf(m, d);
-    const float nm = mn == -INFINITY ? 0.f : mn;
-    const float alpha = m == -INFINITY ? 0.f : exp2f(m - nm), p = exp2f(d - nm);
+    for (int u = 0; u < kU; ++u) {
+      const int x = min(x0 + u, seen - 1), j = x < front ? x : x - front + r.lo;
+      d[u] = 0.f;
+#pragma unroll
+      for (int e = 0; e < kE; ++e) {
+        d[u] = fmaf(qq[e], wa_f32(k[(int64_t)j * a.k_stride + e]), d[u]);
+        vv[u][e] = wa_f32(v[(int64_t)j * a.v_stride + e]);
+      }
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1)
+#pragma unroll
+      for (int u = 0; u < kU; ++u) d[u] += __shfl_xor_sync(0xffffffffu, d[u], off);
+    float mn = m;
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+      d[u] *= a.scale_log2;
+      mn = fmaxf(mn, d[u]);
+    }
+    const float nm = mn == -INFINITY ? 0.f : mn, alpha = m == -INFINITY ? 0.f : exp2f(m - nm);
     m = mn;
-    l = l * alpha + p;
+    l *= alpha;
 #pragma unroll
-    for (int e = 0; e < kE; ++e) o[e] = o[e] * alpha + p * wa_f32(v[(int64_t)j * a.v_stride + e]);
+    for (int e = 0; e < kE; ++e) o[e] *= alpha;
+#pragma unroll
+    for (int u = 0; u < kU; ++u)
+      if (x0 + u < seen) {
+        const float p = exp2f(d[u] - nm);
+        l += p;
+#pragma unroll
+        for (int e = 0; e < kE; ++e) o[e] += p * vv[u][e];
+      }
   }
   T* out = reinterpret_cast<T*>(a.o) + (int64_t)(s.q0 + i) * a.o_stride + head * HD + lane * kE;
   const float inv = l == 0.f ? 0.f : 1.f / l;
@@ -159,6 +181,7 @@ __global__ void __launch_bounds__(kWfThreads) window_f32_kernel(const __grid_con
   float* vs = wf_sm + Cfg::kOffV / 4;
   float* ps = wf_sm + Cfg::kOffP / 4;
   pdl_wait();
+  pdl_trigger();
   int b, tile;
   if (!wa_find_tile(a, blockIdx.x / a.heads, kWfRows, &b, &tile)) return;
   const WaSeq s = wa_seq(a, b);
