@@ -108,7 +108,8 @@ bool kv_setup() {
 
 template <typename T, int HD, int R>
 cudaError_t launch_kv_attention_r(const KaArgs& a, cudaStream_t s) {
-  return launchk(kv_attention_kernel<T, HD, R>, dim3(num_sms()), dim3(kKaThreads), KaCfg<T, HD, R>::kSmem, s, 1, a);
+  using Cfg = KaCfg<T, HD, R>;
+  return launchk(kv_attention_kernel<T, HD, R>, dim3(num_sms()), dim3(Cfg::kThreads), Cfg::kSmem, s, 1, a);
 }
 // rows: the query heads a CTA takes at once (kv_rows)
 template <int HD>
@@ -298,7 +299,7 @@ dinfer_status dinfer_kv_attention(const dinfer_kv_cache* kc, int32_t layer, cons
   const int64_t most = std::min<int64_t>((int64_t)kc->max_pages * kc->page_size,
                                          window < 0 ? INT64_MAX : (int64_t)window + 1 + sinks);
   const int keys = bf16 ? KaCfg<__nv_bfloat16, 128, 8>::kKeys : KaCfg<float, 128, 8>::kKeys;
-  if ((most / keys + kKaWarps + kKaPairCost) * n * kc->kv_heads * a.subgroups >= (1ll << 31))
+  if ((most / keys + 8 + kKaPairCost) * n * kc->kv_heads * a.subgroups >= (1ll << 31))
     return fail(c, DINFER_EINVAL, "more than 2^31 steps of keys in one call");
   const size_t slot = (2 * rows + 3) / 4 * 4 + rows * kc->head_dim;  // KaCfg::kSlotFloats
   if ((size_t)num_sms() * 2 * slot * 4 > w.data_bytes) return fail(c, DINFER_EINVAL, "workspace too small");

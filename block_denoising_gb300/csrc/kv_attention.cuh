@@ -21,42 +21,45 @@
 //     runs ahead across pair boundaries.  Page numbers are looked up per key (any
 //     page size, any stride), one step ahead of the copies that need them;
 //   - each warp keeps an online softmax of its own (running maximum, sum and
-//     output); the four meet in shared memory at the end of a pair.
+//     output); they meet in shared memory at the end of a pair.
 //
 // bf16: S = Q K^T and O += P V on mma.sync m16n8k16 with the query heads of
 // the group as the 16 rows (one token has too few rows for a tcgen05 tile of
-// 128, and the products are far from the bound either way).  P is rounded to
-// bf16 for its product, l sums the rounded values, so O / l weights the keys
-// exactly in proportion; everything else is fp32.  fp32: plain FMAs.
+// 128, and the products are far from the bound either way).  P goes through its
+// product as two bf16 (rounded down, and the rounded rest, 16 bits together):
+// the products have the room, and the output's own rounding is then all that is
+// left.  Everything else is fp32.  fp32: plain FMAs.
 #pragma once
 #include "attention_tc.cuh"
 #include "kv_pages.cuh"
 
 namespace dinfer {
 
-constexpr int kKaWarps = 4;
-constexpr int kKaThreads = kKaWarps * 32;
 constexpr int kKaJoin = 16;      // partials read at once by a join
 constexpr int kKaPairCost = 3;   // a pair's beginning and merge, in steps
 
 template <typename T, int HD, int R>  // R: query heads a CTA takes at once
 struct KaCfg {
   static constexpr int kKeys = sizeof(T) == 2 ? 32 : 16;      // keys of a warp's step
+  // a step of 16 KB hides its own latencies; steps of 8 KB want a second warp a scheduler (16 sequences that see
+  // 4100 tokens, 64 heads of 64 on 8: 29 us with 8 warps, 36 with 4)
+  static constexpr int kWarps = HD == 64 ? 8 : 4;
+  static constexpr int kThreads = kWarps * 32;
   static constexpr int kRows = R;
   static constexpr int kRowBytes = HD * (int)sizeof(T);
   static constexpr int kVecs = kRowBytes / 16;                // 16-byte vectors of a head's row
   static constexpr int kStageBytes = 2 * kKeys * kRowBytes;   // K and V rows of one step: 8 or 16 KB
-  static constexpr int kStages = kStageBytes == 16384 ? 3 : 6;
-  static constexpr int kRing = kKaWarps * kStages * kStageBytes;   // 192 KB: one CTA an SM
+  static constexpr int kStages = 3;
+  static constexpr int kRing = kWarps * kStages * kStageBytes;   // 192 KB: one CTA an SM
   static constexpr int kMergeRows = R < 4 ? R : 4;             // rows merged per round
-  static constexpr int kMerge = kKaWarps * kMergeRows * HD * 4;  // fp32 output rows of the 4 warps
+  static constexpr int kMerge = kWarps * kMergeRows * HD * 4;  // fp32 output rows of the warps
   static constexpr int kOffMerge = kRing;
-  static constexpr int kOffMl = kOffMerge + kMerge;            // [4 warps][rows][m, l]
-  static constexpr int kOffQ = kOffMl + kKaWarps * kRows * 8;  // fp32 only: the query rows
+  static constexpr int kOffMl = kOffMerge + kMerge;            // [warps][rows][m, l]
+  static constexpr int kOffQ = kOffMl + kWarps * kRows * 8;  // fp32 only: the query rows
   static constexpr int kOffCum = kOffQ + (sizeof(T) == 4 ? kRows * HD * 4 : 0);
   static constexpr int kOffLen = kOffCum + (kKvMaxEntries + 4) * 4;
   static constexpr int kOffMask = kOffLen + kKvMaxEntries * 4;  // [warp][stage]: keys present
-  static constexpr int kSmem = kOffMask + kKaWarps * kStages * 4;
+  static constexpr int kSmem = kOffMask + kWarps * kStages * 4;
   // a partial in the workspace: (m, l) [rows], padded so that O [rows][HD] begins at 16 bytes
   static constexpr int kSlotO = (2 * R + 3) / 4 * 4;
   static constexpr int kSlotFloats = kSlotO + R * HD;
@@ -144,7 +147,7 @@ struct KaSplit {
 };
 
 // The part of the call's work that a CTA has, walked in order: entry (sequence
-// of the call), head piece, and a round of kKaWarps steps of that pair (a step
+// of the call), head piece, and a round of kWarps steps of that pair (a step
 // is kKeys keys, a warp's).  A pair of `steps` steps takes kKaPairCost + steps
 // places from `base` on; this CTA has those at [x0, x1): steps from .. to - 1.
 struct KaWalk {
@@ -169,8 +172,9 @@ struct KaWalk {
     to = min(steps, x1 - base - kKaPairCost);
     if (to <= 0) entry = n;  // the range ends in the pair's cost
   }
+  template <int kWarps>
   __device__ __forceinline__ void next(int x1, const int* cum, int n, int pieces) {
-    step += kKaWarps;
+    step += kWarps;
     if (step < to) return;
     step = 0;
     base += steps + kKaPairCost;
@@ -194,7 +198,10 @@ struct KaWalk {
 // store_rows() of kMergeRows output rows.
 
 // bf16.  Fragments of mma.m16n8k16: lane = 4 g + t holds rows g and g + 8.
-// R = 8: rows g + 8 are zeros and left out of the softmax.
+// R = 8: rows g + 8 are zeros in Q and left out of the softmax; in P they hold the
+// second parts of rows g, so that one product takes both parts and O is the sum
+// of rows g and g + 8 (64 sequences of 1 .. 8192 tokens, 32 heads on 8: 54.8 us,
+// with a product of their own 58).
 template <int HD, int R>
 struct KaStateBf16 {
   static constexpr int kKs = HD / 16, kNt = HD / 8, kKeys = 32, kHalves = R / 8, kMergeRows = 4;
@@ -251,7 +258,7 @@ struct KaStateBf16 {
         }
     }
     const int t2 = (lane & 3) * 2;
-    uint32_t p[2][4] = {};
+    uint32_t p[2][4], pl[2][4];  // R = 8: pl is part of p
 #pragma unroll
     for (int h = 0; h < kHalves; ++h) {  // rows g, g + 8
       float x[8];
@@ -272,18 +279,22 @@ struct KaStateBf16 {
         if (grow) m[h] = mx;
         l[h] *= alpha;
 #pragma unroll
-        for (int i = 0; i < kNt; ++i) {
-          o[i][2 * h] *= alpha;
-          o[i][2 * h + 1] *= alpha;
-        }
+        for (int i = 0; i < kNt; ++i)
+#pragma unroll
+          for (int e = 2 * h; e < (R == 8 ? 4 : 2 * h + 2); ++e) o[i][e] *= alpha;
       }
       const float nm = m[h] == -INFINITY ? 0.f : m[h];  // nothing seen yet: every weight is 2^-inf = 0
 #pragma unroll
       for (int e = 0; e < 8; e += 2) {
-        const uint32_t w = pack_bf16x2(ex2_approx(x[e] - nm), ex2_approx(x[e + 1] - nm));
-        p[e >> 2][((e >> 1) & 1) * 2 + h] = w;  // a0 / a1: keys 2t, 2t + 1; a2 / a3: keys 2t + 8, 2t + 9
-        // this lane's keys; the lanes of a row are summed at the end
-        l[h] += __uint_as_float(w << 16) + __uint_as_float(w & 0xffff0000u);
+        const float p0 = ex2_approx(x[e] - nm), p1 = ex2_approx(x[e + 1] - nm);
+        const uint32_t u0 = __float_as_uint(p0), u1 = __float_as_uint(p1);
+        const int at = ((e >> 1) & 1) * 2 + h;  // a0 / a1: keys 2t, 2t + 1; a2 / a3: keys 2t + 8, 2t + 9
+        p[e >> 2][at] = __byte_perm(u0, u1, 0x7632);  // the upper halves: p rounded down
+        // the rest, never 0 (2^-126 at least): an infinite value must not meet 0
+        const uint32_t rest = pack_bf16x2(fmaxf(p0 - __uint_as_float(u0 & 0xffff0000u), 1.17549435e-38f),
+                                          fmaxf(p1 - __uint_as_float(u1 & 0xffff0000u), 1.17549435e-38f));
+        if constexpr (R == 8) p[e >> 2][at + 1] = rest; else pl[e >> 2][at] = rest;
+        l[h] += p0 + p1;  // this lane's keys; the lanes of a row are summed at the end
       }
     }
     const uint32_t vbase = stage + kKeys * kRowBytes + ((mi & 1) * 8 + r8) * kRowBytes;
@@ -295,6 +306,10 @@ struct KaStateBf16 {
         ldmatrix_x4_trans(vbase + kp * 16 * kRowBytes + (((i + (mi >> 1)) ^ r8) << 4), b);
         mma_m16n8k16(o[i], p[kp], b[0], b[1]);
         mma_m16n8k16(o[i + 1], p[kp], b[2], b[3]);
+        if constexpr (R == 16) {
+          mma_m16n8k16(o[i], pl[kp], b[0], b[1]);
+          mma_m16n8k16(o[i + 1], pl[kp], b[2], b[3]);
+        }
       }
   }
 
@@ -315,7 +330,8 @@ struct KaStateBf16 {
       if (row >= 0 && row < kMergeRows)
 #pragma unroll
         for (int i = 0; i < kNt; ++i)
-          *reinterpret_cast<float2*>(buf + row * HD + i * 8 + t2) = make_float2(o[i][2 * h], o[i][2 * h + 1]);
+          *reinterpret_cast<float2*>(buf + row * HD + i * 8 + t2) =
+              R == 8 ? make_float2(o[i][0] + o[i][2], o[i][1] + o[i][3]) : make_float2(o[i][2 * h], o[i][2 * h + 1]);
     }
   }
 };
@@ -426,17 +442,22 @@ __device__ __forceinline__ void ka_store4(__nv_bfloat16* p, float4 v) {
 }
 __device__ __forceinline__ void ka_store4(float* p, float4 v) { *reinterpret_cast<float4*>(p) = v; }
 
+// O / l; zeros where no weight was seen (whatever the values of weight 0 were)
+__device__ __forceinline__ float4 ka_scaled(float4 o, float inv) {
+  return inv == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+}
+
 template <typename T, int HD, int R>
-__global__ void __launch_bounds__(kKaThreads, 1) kv_attention_kernel(const __grid_constant__ KaArgs a) {
+__global__ void __launch_bounds__(KaCfg<T, HD, R>::kThreads, 1) kv_attention_kernel(const __grid_constant__ KaArgs a) {
   using Cfg = KaCfg<T, HD, R>;
-  constexpr int kRows = R, kMergeRows = Cfg::kMergeRows, kStages = Cfg::kStages, kKeys = Cfg::kKeys;
+  constexpr int kRows = R, kMergeRows = Cfg::kMergeRows, kStages = Cfg::kStages, kKeys = Cfg::kKeys, kWarps = Cfg::kWarps, kThreads = Cfg::kThreads;
   extern __shared__ __align__(128) uint8_t sm[];
   int* cum = reinterpret_cast<int*>(sm + Cfg::kOffCum);  // places before each entry
   int* lens = reinterpret_cast<int*>(sm + Cfg::kOffLen);  // tokens of each entry
   float* merge = reinterpret_cast<float*>(sm + Cfg::kOffMerge);
   float* ml = reinterpret_cast<float*>(sm + Cfg::kOffMl);
   float* qs = reinterpret_cast<float*>(sm + Cfg::kOffQ);
-  __shared__ int warp_places[kKaWarps], join_sh;
+  __shared__ int warp_places[kWarps], join_sh;
   const KvPages& c = a.c;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int pieces = c.kv_heads * a.subgroups;
@@ -446,7 +467,7 @@ __global__ void __launch_bounds__(kKaThreads, 1) kv_attention_kernel(const __gri
   auto seq_of = [&](int e) { return a.seqs ? a.seqs[e] : e; };
   // places before each entry: thread i sums the entries of its own stretch
   {
-    const int per = (a.n + kKaThreads - 1) / kKaThreads;
+    const int per = (a.n + kThreads - 1) / kThreads;
     const int e0 = min(a.n, tid * per), e1 = min(a.n, e0 + per);
     int sum = 0;
     for (int e = e0; e < e1; ++e) {
@@ -458,7 +479,7 @@ __global__ void __launch_bounds__(kKaThreads, 1) kv_attention_kernel(const __gri
       }
       lens[e] = len;
       const int seen = ka_seen(len, a.window, a.sinks).seen;
-      const int x = seen ? ((seen + kKeys * kKaWarps - 1) / (kKeys * kKaWarps) * kKaWarps + kKaPairCost) * pieces : 0;
+      const int x = seen ? ((seen + kKeys * kWarps - 1) / (kKeys * kWarps) * kWarps + kKaPairCost) * pieces : 0;
       cum[e + 1] = x;
       sum += x;
     }
@@ -484,7 +505,7 @@ __global__ void __launch_bounds__(kKaThreads, 1) kv_attention_kernel(const __gri
     if (cum[e + 1] != cum[e]) continue;
     T* orow = reinterpret_cast<T*>(a.o) + e * a.o_stride;
     const int vecs = c.kv_heads * a.group * Cfg::kVecs;
-    for (int x = tid; x < vecs; x += kKaThreads) reinterpret_cast<uint4*>(orow)[x] = make_uint4(0, 0, 0, 0);
+    for (int x = tid; x < vecs; x += kThreads) reinterpret_cast<uint4*>(orow)[x] = make_uint4(0, 0, 0, 0);
   }
   // the host bounds the places of the call below 2^31
   const int total = cum[a.n];
@@ -526,7 +547,7 @@ __global__ void __launch_bounds__(kKaThreads, 1) kv_attention_kernel(const __gri
   Where at = look_up(), at_next{0, -1};
   int ahead_rounds = 1;  // looked up and not issued yet: at, at_next
   auto advance = [&]() {
-    load.next(x1, cum, a.n, pieces);
+    load.template next<kWarps>(x1, cum, a.n, pieces);
     if (load.entry < a.n) {
       if (load.step == 0 && warp == 0) {  // a new pair: its query rows into L2 by the time they are wanted
         const int sub = load.piece % a.subgroups, rows = min(kRows, a.group - sub * kRows);
@@ -593,10 +614,10 @@ __global__ void __launch_bounds__(kKaThreads, 1) kv_attention_kernel(const __gri
     __syncwarp();  // the stage is refilled next turn
     stage = stage + 1 == kStages ? 0 : stage + 1;
     KaWalk ahead = use;
-    ahead.next(x1, cum, a.n, pieces);
+    ahead.template next<kWarps>(x1, cum, a.n, pieces);
     const bool go = ahead.entry < a.n;
     if (!go || ahead.base != use.base) {
-      // the pair's keys of this CTA are done: merge the four warps
+      // the pair's keys of this CTA are done: merge the warps
       if (go) load_q(ahead);
       const int sub = use.piece % a.subgroups, rows = min(kRows, a.group - sub * kRows);
       const int head = (use.piece / a.subgroups) * a.group + sub * kRows;
@@ -608,16 +629,16 @@ __global__ void __launch_bounds__(kKaThreads, 1) kv_attention_kernel(const __gri
       for (int r0 = 0; r0 < rows; r0 += kMergeRows) {
         state.store_rows(merge + warp * (kMergeRows * HD), r0, lane);
         __syncthreads();
-        for (int x = tid; x < kMergeRows * HD / 4; x += kKaThreads) {
+        for (int x = tid; x < kMergeRows * HD / 4; x += kThreads) {
           const int row = r0 + x / (HD / 4), c4 = (x % (HD / 4)) * 4;
           if (row < rows) {
             float mm = -INFINITY;
 #pragma unroll
-            for (int w = 0; w < kKaWarps; ++w) mm = fmaxf(mm, ml[(w * kRows + row) * 2]);
+            for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, ml[(w * kRows + row) * 2]);
             float ll = 0.f;
             float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-            for (int w = 0; w < kKaWarps; ++w) {
+            for (int w = 0; w < kWarps; ++w) {
               const float mw = ml[(w * kRows + row) * 2];
               const float f = mw == -INFINITY ? 0.f : ex2_approx(mw - mm);
               const float4 v =
@@ -630,7 +651,7 @@ __global__ void __launch_bounds__(kKaThreads, 1) kv_attention_kernel(const __gri
             }
             if (whole) {
               const float inv = ll == 0.f ? 0.f : 1.f / ll;
-              ka_store4(orow + row * HD + c4, make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
+              ka_store4(orow + row * HD + c4, ka_scaled(acc, inv));
             } else {
               __stcg(reinterpret_cast<float4*>(part + Cfg::kSlotO + row * HD + c4), acc);
               if (c4 == 0) __stcg(reinterpret_cast<float2*>(part + row * 2), make_float2(mm, ll));
@@ -648,7 +669,7 @@ __global__ void __launch_bounds__(kKaThreads, 1) kv_attention_kernel(const __gri
         __syncthreads();
         if (join_sh) {
           const int nc = c_last - c_first + 1;
-          for (int x = tid; x < rows * HD / 4; x += kKaThreads) {
+          for (int x = tid; x < rows * HD / 4; x += kThreads) {
             const int row = x / (HD / 4), c4 = (x % (HD / 4)) * 4;
             float mm = -INFINITY, ll = 0.f;
             float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -686,7 +707,7 @@ __global__ void __launch_bounds__(kKaThreads, 1) kv_attention_kernel(const __gri
               }
             }
             const float inv = ll == 0.f ? 0.f : 1.f / ll;
-            ka_store4(orow + row * HD + c4, make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
+            ka_store4(orow + row * HD + c4, ka_scaled(acc, inv));
           }
           if (tid == 0) a.tickets[c_first] = 0;
         }

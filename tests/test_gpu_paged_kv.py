@@ -281,6 +281,23 @@ def test_attention_of_peaked_and_infinite_scores(D, ws):
         assert torch.isfinite(cache.attention(0, q, ws, window=100, sinks=53)[1]).all()
 
 
+def test_attention_of_infinite_values(D, ws):
+    # an infinite value that a token sees makes its column infinite, whatever its weight's bits; one behind the
+    # sequence's end, or outside the window, does not touch it
+    rng = np.random.default_rng(20)
+    for dtype in (torch.bfloat16, torch.float32):
+        cache, seqs = filled(D, rng, [200, 50], 16, 1, 128, dtype)
+        for j, c, x in ((10, 3, float("inf")), (150, 7, float("-inf"))):
+            cache.v[0, cache.table[0, j // 16], j % 16, 0, c] = x
+        q = values(rng, (2, 16, 128), dtype)[1]
+        o = cache.attention(0, q, ws)
+        assert (o[0, :, 3] == float("inf")).all() and (o[0, :, 7] == float("-inf")).all()
+        finite = torch.isfinite(o)
+        assert int((~finite).sum()) == 32 and finite[1].all()
+        o = cache.attention(0, q, ws, window=100, sinks=5)
+        assert (o[0, :, 7] == float("-inf")).all() and int((~torch.isfinite(o)).sum()) == 16
+
+
 def test_attention_bad_entries_are_flagged(D, ws):
     rng = np.random.default_rng(4)
     cache, seqs = filled(D, rng, [40, 40, 40], 16, 1, 64, torch.bfloat16)
