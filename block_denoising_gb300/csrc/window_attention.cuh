@@ -11,6 +11,34 @@
 
 namespace dinfer {
 
+// Two fp32 operations an instruction, on register pairs.
+__device__ __forceinline__ uint64_t f32x2(uint32_t lo, uint32_t hi) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(lo), "r"(hi));
+  return d;
+}
+__device__ __forceinline__ void f32x2_parts(uint64_t d, float& lo, float& hi) {
+  uint32_t a, b;
+  asm("mov.b64 {%0, %1}, %2;" : "=r"(a), "=r"(b) : "l"(d));
+  lo = __uint_as_float(a);
+  hi = __uint_as_float(b);
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+
 struct WaArgs {
   const void* q;
   const void* k;
@@ -22,6 +50,7 @@ struct WaArgs {
   int batch, total_q, total_k, heads, kv_heads, group;
   int left, right, sinks;
   float scale_log2;
+  int last_first;  // fp32: CTAs take the tiles from the last to the first
   DevState* status;
 };
 
@@ -156,86 +185,110 @@ __device__ __noinline__ void wa_row_exact(const WaArgs& a, const WaSeq s, int i,
 // ---------------------------------------------------------------------------
 // fp32
 // ---------------------------------------------------------------------------
-// One CTA = 64 rows of one head, 256 threads; K and V in tiles of 32 keys.
-// Thread (ty, tx) of 16 x 16 computes the scores of rows 4 ty .. + 3 and keys
-// tx, tx + 16, and owns 4 rows x HD / 16 columns of the output.  Bound by the
-// fp32 FMA rate (there is no fp32 tensor product that keeps 24 bits).
+// One CTA = 16 kE rows of one head, 256 threads; K and V in tiles of 32 keys, two
+// of them in shared memory, the next one copied in while the current one is
+// worked on.  Thread (ty, tx) of 16 x 16 computes the scores of rows kE ty ..
+// + kE - 1 and keys tx, tx + 16, and owns kE rows x HD / 16 columns of the
+// output; two FMAs an instruction.  Bound by the fp32 FMA rate (there is no
+// fp32 tensor product that keeps 24 bits).
+//
+// kE = 4 (64 rows) does the most products per shared-memory read: 41 TFLOP/s
+// (16 heads of 128, 4096 causal rows; peak 80).  kE = 1 gives short calls four
+// times the CTAs, each half as long: 96 rows, 4 heads of 64, a window of 31 on
+// both sides: 6.4 us, 9.7 with kE = 4; 16 rows: 3.2 us, 4.8 with kE = 4.
 constexpr int kWfThreads = 256;
-constexpr int kWfRows = 64;
 constexpr int kWfKeys = 32;
-template <int HD>
+template <int HD, int kE>
 struct WfCfg {
-  static constexpr int kPad = HD + 4;  // rows of Q and K start 4 banks apart
-  static constexpr int kOffK = kWfRows * kPad * 4;
-  static constexpr int kOffV = kOffK + kWfKeys * kPad * 4;
-  static constexpr int kOffP = kOffV + kWfKeys * HD * 4;
-  static constexpr int kSmem = kOffP + kWfRows * (kWfKeys + 1) * 4;
+  static constexpr int kRows = 16 * kE;
+  static constexpr int kPad = HD + 4;              // rows of Q and K start 4 banks apart
+  static constexpr int kPitchP = kWfKeys + 4;
+  static constexpr int kStage = kWfKeys * (kPad + HD);  // floats: K, then V
+  static constexpr int kOffKv = kRows * kPad;
+  static constexpr int kOffP = kOffKv + 2 * kStage;
+  static constexpr int kSmem = (kOffP + kRows * kPitchP) * 4;
 };
 
-template <int HD>
-__global__ void __launch_bounds__(kWfThreads) window_f32_kernel(const __grid_constant__ WaArgs a) {
-  using Cfg = WfCfg<HD>;
+template <int HD, int kE>
+__global__ void __launch_bounds__(kWfThreads, 2) window_f32_kernel(const __grid_constant__ WaArgs a) {
+  using Cfg = WfCfg<HD, kE>;
+  constexpr int kRows = Cfg::kRows, kVecs = HD / 4;
   extern __shared__ __align__(16) float wf_sm[];
   float* qs = wf_sm;
-  float* ks = wf_sm + Cfg::kOffK / 4;
-  float* vs = wf_sm + Cfg::kOffV / 4;
-  float* ps = wf_sm + Cfg::kOffP / 4;
+  float* ps = wf_sm + Cfg::kOffP;
   pdl_wait();
   pdl_trigger();
   int b, tile;
-  if (!wa_find_tile(a, blockIdx.x / a.heads, kWfRows, &b, &tile)) return;
+  if (!wa_find_tile(a, (a.last_first ? gridDim.x - 1 - blockIdx.x : blockIdx.x) / a.heads, kRows, &b, &tile)) return;
   const WaSeq s = wa_seq(a, b);
-  const int head = blockIdx.x % a.heads, i0 = tile * kWfRows, rows = min(kWfRows, s.nq - i0);
+  const int head = blockIdx.x % a.heads, i0 = tile * kRows, rows = min(kRows, s.nq - i0);
   const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
   const float* q = reinterpret_cast<const float*>(a.q) + (int64_t)(s.q0 + i0) * a.q_stride + head * HD;
   const float* k = reinterpret_cast<const float*>(a.k) + (int64_t)s.k0 * a.k_stride + (head / a.group) * HD;
   const float* v = reinterpret_cast<const float*>(a.v) + (int64_t)s.k0 * a.v_stride + (head / a.group) * HD;
-  for (int x = tid; x < kWfRows * HD; x += kWfThreads) {
-    const int r = x / HD, d = x % HD;
-    qs[r * Cfg::kPad + d] = r < rows ? q[(int64_t)r * a.q_stride + d] : 0.f;
-  }
-  constexpr int kC = HD / 16;  // output columns of a thread: tx * 4 + 64 * (c / 4) + c % 4
-  float o[4][kC] = {}, m[4], l[4] = {};
-  WaRange rr[4];
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    m[e] = -INFINITY;
-    rr[e] = wa_range(a, s, i0 + min(ty * 4 + e, rows - 1));
+  for (int x = tid; x < kRows * kVecs; x += kWfThreads) {
+    const int r = x / kVecs, d = x % kVecs * 4;
+    cp_async16(smem_u32(qs + r * Cfg::kPad + d), q + (int64_t)min(r, rows - 1) * a.q_stride + d, r < rows ? 16 : 0);
   }
   // keys some row of the tile sees: the sinks, then from the first row's lo to the last row's hi
   const WaRange top = wa_range(a, s, i0), bottom = wa_range(a, s, i0 + rows - 1);
   const int front = min(a.sinks, min(top.lo, bottom.hi + 1));
-  int j0 = front > 0 ? 0 : top.lo / kWfKeys * kWfKeys;
-  while (j0 <= bottom.hi) {
-    __syncthreads();
-    for (int x = tid; x < kWfKeys * HD; x += kWfThreads) {
-      const int r = x / HD, d = x % HD;
-      const bool in = j0 + r < s.nk;
-      ks[r * Cfg::kPad + d] = in ? k[(int64_t)(j0 + r) * a.k_stride + d] : 0.f;
-      vs[r * HD + d] = in ? v[(int64_t)(j0 + r) * a.v_stride + d] : 0.f;
+  auto load = [&](int j0, int buf) {  // keys behind the sequence's end: zeros
+    float* ks = wf_sm + Cfg::kOffKv + buf * Cfg::kStage;
+#pragma unroll
+    for (int x = tid; x < kWfKeys * kVecs; x += kWfThreads) {
+      const int r = x / kVecs, d = x % kVecs * 4, j = min(j0 + r, s.nk - 1), bytes = j0 + r < s.nk ? 16 : 0;
+      cp_async16(smem_u32(ks + r * Cfg::kPad + d), k + (int64_t)j * a.k_stride + d, bytes);
+      cp_async16(smem_u32(ks + kWfKeys * Cfg::kPad + r * HD + d), v + (int64_t)j * a.v_stride + d, bytes);
     }
+  };
+  auto behind = [&](int j0) {  // the tile after j0's: behind the sinks, on to the window
+    const int j = j0 + kWfKeys;
+    return j >= front && j < top.lo ? max(j, top.lo / kWfKeys * kWfKeys) : j;
+  };
+  constexpr int kC = HD / 16;  // output columns of a thread: tx * 4 + 64 * (c / 4) + c % 4, as pairs
+  uint64_t o[kE][kC / 2] = {};
+  float m[kE], l[kE] = {};
+  WaRange rr[kE];
+#pragma unroll
+  for (int e = 0; e < kE; ++e) {
+    m[e] = -INFINITY;
+    rr[e] = wa_range(a, s, i0 + min(ty * kE + e, rows - 1));
+  }
+  int j0 = front > 0 ? 0 : top.lo / kWfKeys * kWfKeys;
+  if (j0 <= bottom.hi) load(j0, 0);
+  cp_async_commit();
+  for (int buf = 0; j0 <= bottom.hi; buf ^= 1) {
+    const int jn = behind(j0);
+    __syncthreads();  // the other buffer has been read
+    if (jn <= bottom.hi) load(jn, buf ^ 1);
+    cp_async_commit();
+    cp_async_wait<1>();
     __syncthreads();
-    float sc[4][2] = {};
+    const float* ks = wf_sm + Cfg::kOffKv + buf * Cfg::kStage;
+    const float* vs = ks + kWfKeys * Cfg::kPad;
+    uint64_t sc2[kE][2] = {};  // sums over the even and the odd dimensions
 #pragma unroll 4
     for (int d = 0; d < HD; d += 4) {
-      float4 kk[2];
+      ulonglong2 kk[2];
 #pragma unroll
-      for (int u = 0; u < 2; ++u) kk[u] = *reinterpret_cast<const float4*>(ks + (tx + 16 * u) * Cfg::kPad + d);
+      for (int u = 0; u < 2; ++u) kk[u] = *reinterpret_cast<const ulonglong2*>(ks + (tx + 16 * u) * Cfg::kPad + d);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float4 qq = *reinterpret_cast<const float4*>(qs + (ty * 4 + e) * Cfg::kPad + d);
+      for (int e = 0; e < kE; ++e) {
+        const ulonglong2 qq = *reinterpret_cast<const ulonglong2*>(qs + (ty * kE + e) * Cfg::kPad + d);
 #pragma unroll
-        for (int u = 0; u < 2; ++u)
-          sc[e][u] = fmaf(qq.x, kk[u].x, fmaf(qq.y, kk[u].y, fmaf(qq.z, kk[u].z, fmaf(qq.w, kk[u].w, sc[e][u]))));
+        for (int u = 0; u < 2; ++u) sc2[e][u] = fma2(qq.x, kk[u].x, fma2(qq.y, kk[u].y, sc2[e][u]));
       }
     }
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      float mx = -INFINITY;
+    for (int e = 0; e < kE; ++e) {
+      float mx = -INFINITY, sc[2];
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
-        sc[e][u] = wa_sees(rr[e], a.sinks, j0 + tx + 16 * u) ? sc[e][u] * a.scale_log2 : -INFINITY;
-        mx = fmaxf(mx, sc[e][u]);
+        float even, odd;
+        f32x2_parts(sc2[e][u], even, odd);
+        sc[u] = wa_sees(rr[e], a.sinks, j0 + tx + 16 * u) ? (even + odd) * a.scale_log2 : -INFINITY;
+        mx = fmaxf(mx, sc[u]);
       }
 #pragma unroll
       for (int d = 8; d > 0; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
@@ -246,60 +299,70 @@ __global__ void __launch_bounds__(kWfThreads) window_f32_kernel(const __grid_con
       l[e] *= alpha;
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
-        const float p = ex2_approx(sc[e][u] - nm);
+        const float p = ex2_approx(sc[u] - nm);
         l[e] += p;
-        ps[(ty * 4 + e) * (kWfKeys + 1) + tx + 16 * u] = p;
+        ps[(ty * kE + e) * Cfg::kPitchP + tx + 16 * u] = p;
       }
+      const uint64_t alpha2 = f32x2(__float_as_uint(alpha), __float_as_uint(alpha));
 #pragma unroll
-      for (int c = 0; c < kC; ++c) o[e][c] *= alpha;
+      for (int c = 0; c < kC / 2; ++c) o[e][c] = mul2(o[e][c], alpha2);
     }
     __syncwarp();  // a row's 16 threads are half a warp
-#pragma unroll 4
-    for (int j = 0; j < kWfKeys; ++j) {
-      float vv[kC];
+#pragma unroll 2
+    for (int j = 0; j < kWfKeys; j += 4) {
+      float pj[kE][4];
 #pragma unroll
-      for (int c = 0; c < kC; c += 4)
-        *reinterpret_cast<float4*>(vv + c) = *reinterpret_cast<const float4*>(vs + j * HD + tx * 4 + 16 * c);
+      for (int e = 0; e < kE; ++e)
+        *reinterpret_cast<float4*>(pj[e]) = *reinterpret_cast<const float4*>(ps + (ty * kE + e) * Cfg::kPitchP + j);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float p = ps[(ty * 4 + e) * (kWfKeys + 1) + j];
+      for (int jj = 0; jj < 4; ++jj) {
+        uint64_t vv[kC / 2];
 #pragma unroll
-        for (int c = 0; c < kC; ++c) o[e][c] = fmaf(p, vv[c], o[e][c]);
+        for (int c = 0; c < kC / 2; c += 2)
+          *reinterpret_cast<ulonglong2*>(vv + c) = *reinterpret_cast<const ulonglong2*>(vs + (j + jj) * HD + tx * 4 + 32 * c);
+#pragma unroll
+        for (int e = 0; e < kE; ++e) {
+          const uint64_t p2 = f32x2(__float_as_uint(pj[e][jj]), __float_as_uint(pj[e][jj]));
+#pragma unroll
+          for (int c = 0; c < kC / 2; ++c) o[e][c] = fma2(p2, vv[c], o[e][c]);
+        }
       }
     }
-    j0 += kWfKeys;
-    if (j0 >= front && j0 < top.lo) j0 = max(j0, top.lo / kWfKeys * kWfKeys);  // behind the sinks: on to the window
+    j0 = jn;
   }
+  cp_async_wait<0>();
   // sums over the 16 threads of a row, and whether all of it is finite
   uint32_t redo = 0;
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    float sum = l[e], worst = 0.f;
+  for (int e = 0; e < kE; ++e) {
+    float sum = l[e], worst = 0.f, out[kC];
 #pragma unroll
-    for (int c = 0; c < kC; ++c) worst = fmaxf(worst, fabsf(o[e][c]) <= 3.0e38f ? 0.f : 1.f);
+    for (int c = 0; c < kC; ++c) {
+      if (c % 2 == 0) f32x2_parts(o[e][c / 2], out[c], out[c + 1]);
+      worst = fmaxf(worst, fabsf(out[c]) <= 3.0e38f ? 0.f : 1.f);
+    }
 #pragma unroll
     for (int d = 8; d > 0; d >>= 1) {
       sum += __shfl_xor_sync(0xffffffffu, sum, d);
       worst = fmaxf(worst, __shfl_xor_sync(0xffffffffu, worst, d));
     }
-    const int r = ty * 4 + e;
+    const int r = ty * kE + e;
     const bool bad = worst != 0.f || !(sum <= 3.0e38f);
     const uint32_t bads = __ballot_sync(0xffffffffu, bad && r < rows);
     redo |= ((bads & 0xffffu) ? 1u << e : 0u) | ((bads >> 16) ? 16u << e : 0u);
     if (r < rows) {
       const float inv = sum == 0.f ? 0.f : 1.f / sum;
-      float* out = reinterpret_cast<float*>(a.o) + (int64_t)(s.q0 + i0 + r) * a.o_stride + head * HD;
+      float* to = reinterpret_cast<float*>(a.o) + (int64_t)(s.q0 + i0 + r) * a.o_stride + head * HD;
 #pragma unroll
       for (int c = 0; c < kC; c += 4)
-        ka_store4(out + tx * 4 + 16 * c,
-                  make_float4(o[e][c] * inv, o[e][c + 1] * inv, o[e][c + 2] * inv, o[e][c + 3] * inv));
+        ka_store4(to + tx * 4 + 16 * c, make_float4(out[c] * inv, out[c + 1] * inv, out[c + 2] * inv, out[c + 3] * inv));
     }
   }
   __syncwarp();
   while (redo) {  // warp-uniform: bits 0-3 the rows of its lower half, 4-7 of its upper half
     const int e = __ffs(redo) - 1;
     redo &= redo - 1;
-    wa_row_exact<float, HD>(a, s, i0 + ((tid >> 5) * 2 + (e >> 2)) * 4 + (e & 3), head);
+    wa_row_exact<float, HD>(a, s, i0 + ((tid >> 5) * 2 + (e >> 2)) * kE + (e & 3), head);
   }
 }
 

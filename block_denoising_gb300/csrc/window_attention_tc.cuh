@@ -246,29 +246,6 @@ __device__ __forceinline__ int clc_taken(const uint4* answer) {
   return ok ? (int)x : -1;
 }
 
-// Two fp32 operations an instruction, on register pairs.
-__device__ __forceinline__ uint64_t f32x2(uint32_t lo, uint32_t hi) {
-  uint64_t d;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(lo), "r"(hi));
-  return d;
-}
-__device__ __forceinline__ void f32x2_parts(uint64_t d, float& lo, float& hi) {
-  uint32_t a, b;
-  asm("mov.b64 {%0, %1}, %2;" : "=r"(a), "=r"(b) : "l"(d));
-  lo = __uint_as_float(a);
-  hi = __uint_as_float(b);
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-  return d;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-  uint64_t d;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
-
 template <int HD>
 __global__ void __launch_bounds__(kWtThreads, 1)
     window_tc_kernel(const __grid_constant__ WtMaps maps, const __grid_constant__ WaArgs a, const int pair_heads,

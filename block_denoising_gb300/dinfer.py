@@ -418,9 +418,10 @@ class PagedKV:
         _require(seqs is not None or n <= self.max_seqs, "q: more rows than sequences")
         _require(ws.buf.device == self.device, "ws: a workspace on the cache's device expected")
         if out is None:
-            out = torch.empty((n, heads, hd), dtype=q.dtype, device=self.device)
-        os_ = _rows_of(out, "out", heads, hd, self.k)
-        _require(out.shape[0] == n, "out: as many rows as q expected")
+            out, os_ = q.new_empty((n, heads, hd)), heads * hd
+        else:
+            os_ = _rows_of(out, "out", heads, hd, self.k)
+            _require(out.shape[0] == n, "out: as many rows as q expected")
         self._call(lib().dinfer_kv_attention, layer, _ints(seqs, "seqs", self.device, n), n, q.data_ptr(), out.data_ptr(),
                    qs, os_, heads, window, sinks, hd ** -0.5 if scale is None else scale, ws.buf.data_ptr(), ws.nbytes)
         return out
@@ -447,9 +448,10 @@ def op_window_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, ws: O
     cq, ck = _ints(cu_q, "cu_q", dev), _ints(cu_k, "cu_k", dev, None if cu_q is None else batch + 1)
     _require(ws.buf.device == dev, "ws: a workspace on the operands' device expected")
     if out is None:
-        out = torch.empty((rows, heads, hd), dtype=q.dtype, device=dev)
-    os_ = _rows_of(out, "out", heads, hd, q)
-    _require(out.shape[0] == rows, "out: as many rows as q expected")
+        out, os_ = q.new_empty((rows, heads, hd)), heads * hd
+    else:
+        os_ = _rows_of(out, "out", heads, hd, q)
+        _require(out.shape[0] == rows, "out: as many rows as q expected")
     _run_on(dev, lib().dinfer_op_window_attention, q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), _DTYPES[q.dtype],
             batch, cq, ck, rows, k.shape[0], heads, k.shape[1], hd, qs, ks, vs, os_, left, right, sinks,
             hd ** -0.5 if scale is None else scale, ws.buf.data_ptr(), ws.nbytes)

@@ -73,6 +73,16 @@ def test_masks_over_ragged_sequences(D, ws, dtype, hd, left, right, sinks):
     run(D, ws, 7 + left + 2 * sinks, nq, nk, 2, 2, hd, dtype, left, right, sinks)
 
 
+# enough heads for the fp32 kernel's tiles of 64 rows, in either order
+@pytest.mark.parametrize("hd", [64, 128])
+@pytest.mark.parametrize("heads", [14, 30])
+@pytest.mark.parametrize("left,right,sinks", MASKS)
+def test_fp32_of_many_heads(D, ws, hd, heads, left, right, sinks):
+    nq = [1, 0, 17, 128, 300, 5, 129]
+    nk = [1, 3, 17, 128, 300, 400, 100]
+    run(D, ws, 70 + left + 2 * sinks + heads, nq, nk, heads, 2, hd, F32, left, right, sinks, rows=8)
+
+
 @pytest.mark.parametrize("dtype", [BF, F32])
 @pytest.mark.parametrize("heads,kv_heads", [(6, 2), (4, 1), (7, 7), (5, 1)])
 def test_grouped_heads(D, ws, dtype, heads, kv_heads):
@@ -110,12 +120,12 @@ def test_strided_operands_and_rows_of_nobody(D, ws):
         compare(got[3:253, :H], xq[3:253], xk[3:253], xv[3:253], [100, 150], [100, 150], 60, 60, 3, hd ** -0.5, dtype == BF)
 
 
-@pytest.mark.parametrize("dtype,hd", [(BF, 128), (BF, 64), (F32, 64)])
-def test_what_masked_keys_hold_does_not_matter(D, ws, dtype, hd):
+@pytest.mark.parametrize("dtype,hd,heads", [(BF, 128, 2), (BF, 64, 2), (F32, 64, 2), (F32, 64, 16)])
+def test_what_masked_keys_hold_does_not_matter(D, ws, dtype, hd, heads):
     # NaN and infinite keys and values touch the rows that see them and no other, tile neighbours included
     rng = np.random.default_rng(12)
     n, left, right, sinks = 500, 40, 10, 2
-    xq, q = values(rng, (n, 2, hd), dtype)
+    xq, q = values(rng, (n, heads, hd), dtype)
     xk, k = values(rng, (n, 1, hd), dtype)
     xv, v = values(rng, (n, 1, hd), dtype)
     bad = {100: "k", 230: "v", 231: "v", 499: "k"}
