@@ -207,6 +207,7 @@ dinfer_status dinfer_kv_append(const dinfer_kv_cache* kc, int32_t layer, const i
   if (!k || !v) return fail(c, DINFER_EINVAL, "NULL operand");
   if (layer < 0 || layer >= kc->n_layers) return fail(c, DINFER_EINVAL, "no layer %d", layer);
   if (n < 1 || total_rows < 1 || (!rows && total_rows != n)) return fail(c, DINFER_EINVAL, "bad number of rows or entries");
+  if (n > (seqs ? kKvMaxEntries : kc->max_seqs)) return fail(c, DINFER_EINVAL, "more entries than sequences, or than %d", kKvMaxEntries);
   const int64_t per = kc->dtype == DINFER_BF16 ? 8 : 4, row = (int64_t)kc->kv_heads * kc->head_dim;
   if (!rows_ok(k, k_stride, total_rows, row, per) || !rows_ok(v, v_stride, total_rows, row, per))
     return fail(c, DINFER_EINVAL, "k, v: 16-byte aligned rows at least a row apart are needed");

@@ -474,6 +474,14 @@ __global__ void __launch_bounds__(256) kv_append_kernel(const KvPages c, const K
       if (lane == 0) c.flag(KV_BAD_SEQ);
       continue;
     }
+    if (a.seqs) {  // two entries of one sequence would write the same slots: the first one does
+      bool named = false;
+      for (int e = lane; e < i; e += 32) named |= a.seqs[e] == s;
+      if (__any_sync(0xffffffffu, named)) {
+        if (lane == 0) c.flag(KV_BAD_SEQ);
+        continue;
+      }
+    }
     const int64_t p = (int64_t)c.lens[s] - (end - row);
     if (p < 0 || p >= (int64_t)c.max_pages * c.page_size) {
       if (lane == 0) c.flag(KV_FULL);

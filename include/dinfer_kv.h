@@ -18,7 +18,8 @@
  * Conventions (those of dinfer_ops.h, and)
  *   - All pointers are device pointers unless stated; every call is
  *     asynchronous on `stream` (a cudaStream_t, NULL = legacy default stream),
- *     allocates nothing, and can be captured into a CUDA graph.
+ *     allocates nothing, and can be captured into a CUDA graph
+ *     (dinfer_kv_status waits, and cannot).
  *   - The caller owns all memory, the cache's tables included.  Calls on one
  *     cache must be ordered on the GPU; only dinfer_kv_attention calls may
  *     overlap with one another, each with a workspace of its own.
@@ -93,7 +94,9 @@ dinfer_status dinfer_kv_extend(const dinfer_kv_cache* cache, const int32_t* seqs
  * k_stride / v_stride elements apart (multiples of 16 bytes; slices of one
  * projection's output will do), in the cache's type, 16-byte aligned.  rows
  * [n + 1] is non-decreasing; rows of k behind rows[n] are not stored.  Rows
- * that fall on a page other sequences hold are not stored (DINFER_KV_SHARED). */
+ * that fall on a page other sequences hold are not stored (DINFER_KV_SHARED).
+ * A sequence named twice takes its first entry's (DINFER_KV_BAD_SEQ).
+ * 1 <= n <= 1024, without seqs n <= max_seqs. */
 dinfer_status dinfer_kv_append(const dinfer_kv_cache* cache, int32_t layer, const int32_t* seqs, const int32_t* rows,
                                int32_t n, const void* k, const void* v, int64_t k_stride, int64_t v_stride,
                                int32_t total_rows, void* stream);
@@ -125,8 +128,9 @@ dinfer_status dinfer_kv_compact(const dinfer_kv_cache* cache, int32_t* live, voi
  * head rows packed, rows q_stride / o_stride elements apart, 16-byte aligned.
  * A sequence without tokens, or whose scores are all -inf, gives zeros.  Keys
  * on a table entry that is no page are left out (DINFER_KV_BAD_PAGE).
- * heads % kv_heads == 0, 1 <= n <= 1024, scale > 0.  The keys are split over the GPU and
- * joined in a fixed order: the same call gives the same bits. */
+ * A sequence may be named more than once, and o may be q.  heads % kv_heads == 0,
+ * 1 <= n <= 1024, scale > 0.  The keys are split over the GPU and joined in a
+ * fixed order: the same call gives the same bits. */
 dinfer_status dinfer_kv_attention(const dinfer_kv_cache* cache, int32_t layer, const int32_t* seqs, int32_t n,
                                   const void* q, void* o, int64_t q_stride, int64_t o_stride, int32_t heads,
                                   int32_t window, int32_t sinks, float scale, void* workspace, size_t workspace_bytes,
@@ -143,8 +147,8 @@ dinfer_status dinfer_kv_attention(const dinfer_kv_cache* cache, int32_t layer, c
  * DINFER_BF16 or DINFER_FP32, head rows packed, rows x_stride elements apart
  * (multiples of 16 bytes), 16-byte aligned.  cu_q, cu_k: int32 [batch + 1],
  * non-decreasing, or both NULL with batch 1 (all rows).  Rows of o outside
- * every sequence stay as they were.  1 <= batch <= 1024, head_dim 64 or 128,
- * scale > 0; o must not overlap q, k or v.
+ * every sequence stay as they were.  1 <= batch <= 1024, 1 <= total_q, total_k
+ * <= 2^30, head_dim 64 or 128, scale > 0; o must not overlap q, k or v.
  * bf16 runs on the tensor cores: probabilities are rounded to bf16 and summed
  * in fp32.  fp32 is computed in fp32.  Keys that a row does not see do not
  * touch it, whatever they hold.  The workspace may be NULL; when given, a wait

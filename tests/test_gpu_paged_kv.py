@@ -132,6 +132,7 @@ def test_skipped_entries_are_flagged_and_left_alone(D):
         (lambda c: c.extend(ints([30, 30, 20]), ints([4, 5, 0])), 2),  # the pages run out: 4 + 4 + 3 of 7
         (lambda c: c.append(0, *[torch.zeros(40, 1, 64, dtype=torch.bfloat16, device=dev)] * 2, rows=ints([0, 40]),
                             seqs=ints([1])), 16),                    # more rows than tokens: the last ones are stored
+        (lambda c: c.append(0, *[torch.zeros(2, 1, 64, dtype=torch.bfloat16, device=dev)] * 2, seqs=ints([3, 3])), 1),
     ):
         call(cache)
         assert status(D, cache) == bit
@@ -348,6 +349,66 @@ def test_calls_on_another_stream_and_in_a_graph(D, ws):
         graph.replay()
         follow()
     assert status(D, cache) == 0
+
+
+def test_a_thousand_sequences(D, ws):
+    rng = np.random.default_rng(21)
+    cache, model = make(D, rng, 1, 4500, 4, 1, 64, 1024, 6)
+    add = [int(x) for x in rng.integers(0, 21, 700)]
+    model.extend(range(700), add)
+    cache.extend(ints(add))
+    xk, k = values(rng, (sum(add) + 3, 1, 64), torch.bfloat16)
+    xv, v = values(rng, (sum(add) + 3, 1, 64), torch.bfloat16)
+    rows = ints(np.cumsum([0] + add))
+    cache.append(0, k, v, rows=rows)
+    model.append(0, range(700), add, xk, xv)
+    src, dst = [int(x) for x in rng.integers(0, 700, 324)], list(range(700, 1024))
+    for share in (True, False):
+        cache.fork(ints(src), ints(dst), share=share)
+        model.fork(src, dst, share)
+        same(cache, model)
+        gone = dst if share else [int(x) for x in rng.permutation(1024)[:500]]
+        cache.free(ints(gone))
+        model.free(gone)
+    cache.compact()
+    model.compact()
+    same(cache, model)
+    xq, q = values(rng, (1024, 2, 64), torch.bfloat16)
+    out = cache.attention(0, q, ws).double().cpu().numpy()
+    assert status(D, cache) == 0
+    for s in range(0, 1024, 9):
+        mk, mv = model.sequence(0, s)
+        A.check(out[s:s + 1], xq[s:s + 1], mk, mv, np.ones((1, len(mk)), bool), 0.125, True)
+
+
+def test_a_sequence_twice_many_heads_and_in_place(D, ws):
+    rng = np.random.default_rng(22)
+    for dtype, hd in ((torch.bfloat16, 128), (torch.float32, 64)):
+        cache, seqs = filled(D, rng, [700, 5, 3000, 0], 16, 1, hd, dtype)
+        order = [2, 0, 2, 2, 3, 1, 2]
+        x, q = values(rng, (len(order), 300, hd), dtype)  # 300 query heads on one key head
+        out = cache.attention(0, q, ws, seqs=ints(order))
+        for i in (0, 1, 3, 6):
+            k, v = (c[0] for c in seqs[order[i]])
+            A.check(out[i:i + 1].double().cpu().numpy(), x[i:i + 1], k, v, np.ones((1, len(k)), bool), hd ** -0.5,
+                    dtype == torch.bfloat16)
+        assert cache.attention(0, q, ws, seqs=ints(order), out=q) is q
+        assert torch.equal(q, out)
+
+
+def test_two_calls_at_once(D, ws):
+    rng = np.random.default_rng(23)
+    cache, _ = filled(D, rng, [5000, 1, 900, 40], 16, 2, 128, torch.bfloat16)
+    _, q = values(rng, (4, 8, 128), torch.bfloat16)
+    other, side = D.OpWorkspace(), torch.cuda.Stream()
+    want = [cache.attention(0, q, ws), cache.attention(0, q, ws, window=700, sinks=3)]
+    torch.cuda.synchronize()
+    for _ in range(30):
+        a = cache.attention(0, q, ws)
+        with torch.cuda.stream(side):
+            b = cache.attention(0, q, other, window=700, sinks=3)
+        torch.cuda.synchronize()
+        assert torch.equal(a, want[0]) and torch.equal(b, want[1])
 
 
 def test_forks_and_compaction_captured_in_a_graph(D):

@@ -70,6 +70,10 @@ def test_bad_call_arguments_are_refused(L):
         a = list(ok)
         a[i] = v
         assert L.dinfer_kv_append(*a) == dinfer.EINVAL, (i, v)
+    many = [c, 0, P, P, 1025, P, P, 1024, 1024, 4, None]  # more entries than a call may name
+    assert L.dinfer_kv_append(*many) == dinfer.EINVAL
+    many[2], many[4] = None, cache().max_seqs + 1
+    assert L.dinfer_kv_append(*many) == dinfer.EINVAL
     ok = [c, 0, None, 4, P, P, 4096, 4096, 32, -1, 0, 0.1, P, 1 << 30, None]
     for i, v in ((1, 2), (3, 0), (3, 1025), (4, P + 4), (5, P + 4), (6, 4000), (7, 4095), (8, 0), (8, 31), (10, -1),
                  (11, float("nan")), (11, float("inf")), (11, 0.0), (11, -0.1), (12, None), (12, P + 8), (13, 1000)):
