@@ -301,7 +301,7 @@ def _rows_of(t: torch.Tensor, name: str, heads: Optional[int], head_dim: int, li
     """Checks [rows, heads, head_dim] with packed head rows, of like's type and device; returns the row stride."""
     shape, s = t.shape, t.stride()
     if (len(shape) == 3 and shape[2] == head_dim and (heads is None or shape[1] == heads) and t.dtype is like.dtype
-            and t.device == like.device and s[2] == 1 and (s[1] == head_dim or shape[1] == 1)):
+            and t.get_device() == like.get_device() and s[2] == 1 and (s[1] == head_dim or shape[1] == 1)):
         return s[0]
     raise ValueError(f"{name}: [rows, {'heads' if heads is None else heads}, {head_dim}] {like.dtype} on {like.device} with "
                      f"the heads of a row packed expected, got {list(shape)} {t.dtype} on {t.device} with strides {s}")
@@ -311,8 +311,9 @@ def _ints(t: Optional[torch.Tensor], name: str, device, n: Optional[int] = None)
     """Address of a contiguous int32 vector on device (None: NULL)."""
     if t is None:
         return None
-    if (t.dtype is torch.int32 and t.dim() == 1 and t.device == device and t.is_contiguous()
-            and (n is None or t.shape[0] == n)):
+    shape = t.shape
+    if (t.dtype is torch.int32 and len(shape) == 1 and t.get_device() == device.index and t.is_contiguous()
+            and (n is None or shape[0] == n)):
         return t.data_ptr()
     raise ValueError(f"{name}: a contiguous int32 vector {'' if n is None else f'of {n} '}on {device} expected, got "
                      f"{list(t.shape)} {t.dtype} on {t.device}")
@@ -321,7 +322,7 @@ def _ints(t: Optional[torch.Tensor], name: str, device, n: Optional[int] = None)
 def _run_on(device, fn, *args):
     """One library call on torch's current stream of the operands' device, which becomes the current one for it."""
     i = device.index
-    if i == torch.cuda.current_device():
+    if i == torch._C._cuda_getDevice():
         st = fn(*args, torch._C._cuda_getCurrentRawStream(i))
     else:
         with torch.cuda.device(i):
@@ -367,9 +368,6 @@ class PagedKV:
                    torch.zeros(max_seqs, dtype=torch.int32, device=device),
                    torch.zeros(pages, dtype=torch.int32, device=device))
 
-    def _call(self, fn, *args):
-        _run_on(self.device, fn, self._desc, *args)
-
     def set_tables(self, table: torch.Tensor, lens: torch.Tensor, refs: torch.Tensor):
         """Takes over another set of tables of the same sizes (a snapshot, a scheduler's own plan)."""
         _require(table.shape == self.table.shape and lens.shape == self.lens.shape and refs.shape == self.refs.shape,
@@ -383,7 +381,8 @@ class PagedKV:
         """Sequences seqs (default: the first ones, one per entry of add; all) grow by add tokens (default: one each)."""
         n = seqs.shape[0] if seqs is not None else add.shape[0] if add is not None else self.max_seqs
         _require(seqs is not None or n <= self.max_seqs, "add: more entries than sequences")
-        self._call(lib().dinfer_kv_extend, _ints(seqs, "seqs", self.device), _ints(add, "add", self.device, n), n)
+        dev = self.device
+        _run_on(dev, lib().dinfer_kv_extend, self._desc, _ints(seqs, "seqs", dev), _ints(add, "add", dev, n), n)
 
     def append(self, layer: int, k: torch.Tensor, v: torch.Tensor, rows: Optional[torch.Tensor] = None,
                seqs: Optional[torch.Tensor] = None):
@@ -394,41 +393,45 @@ class PagedKV:
         _require(k.shape[0] == v.shape[0], "k, v: as many rows expected")
         n = rows.shape[0] - 1 if rows is not None else k.shape[0]
         _require(seqs is not None or n <= self.max_seqs, "more entries than sequences")
-        self._call(lib().dinfer_kv_append, layer, _ints(seqs, "seqs", self.device, n), _ints(rows, "rows", self.device), n,
-                   k.data_ptr(), v.data_ptr(), ks, vs, k.shape[0])
+        dev = self.device
+        _run_on(dev, lib().dinfer_kv_append, self._desc, layer, _ints(seqs, "seqs", dev, n), _ints(rows, "rows", dev), n,
+                k.data_ptr(), v.data_ptr(), ks, vs, k.shape[0])
 
     def fork(self, src: torch.Tensor, dst: torch.Tensor, share: bool = True):
         """Sequences dst (not in use) become copies of src, sharing the full pages or copying all of them."""
         n = src.shape[0]
-        self._call(lib().dinfer_kv_fork, _ints(src, "src", self.device), _ints(dst, "dst", self.device, n), n, int(share))
+        dev = self.device
+        _run_on(dev, lib().dinfer_kv_fork, self._desc, _ints(src, "src", dev), _ints(dst, "dst", dev, n), n, int(share))
 
     def free(self, seqs: torch.Tensor):
-        self._call(lib().dinfer_kv_free, _ints(seqs, "seqs", self.device), seqs.shape[0])
+        _run_on(self.device, lib().dinfer_kv_free, self._desc, _ints(seqs, "seqs", self.device), seqs.shape[0])
 
     def compact(self, live: Optional[torch.Tensor] = None):
         """Packs the pages in use to the front; live (optional, int32 [1]) receives how many there are."""
-        self._call(lib().dinfer_kv_compact, _ints(live, "live", self.device, 1))
+        _run_on(self.device, lib().dinfer_kv_compact, self._desc, _ints(live, "live", self.device, 1))
 
     def attention(self, layer: int, q: torch.Tensor, ws: OpWorkspace, window: int = -1, sinks: int = 0,
                   scale: Optional[float] = None, seqs: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None):
-        """Attention of each sequence's last token: q [n, heads, head_dim] -> [n, heads, head_dim]."""
+        """Attention of each sequence's last token: q [n, heads, head_dim] -> [n, heads, head_dim] (out may be q)."""
         hd = self.head_dim
         qs = _rows_of(q, "q", None, hd, self.k)
         n, heads, _ = q.shape
         _require(seqs is not None or n <= self.max_seqs, "q: more rows than sequences")
-        _require(ws.buf.device == self.device, "ws: a workspace on the cache's device expected")
+        _require(ws.buf.get_device() == self.device.index, "ws: a workspace on the cache's device expected")
         if out is None:
-            out, os_ = q.new_empty((n, heads, hd)), heads * hd
+            out, os_ = torch.empty_like(q, memory_format=torch.contiguous_format), heads * hd
         else:
             os_ = _rows_of(out, "out", heads, hd, self.k)
             _require(out.shape[0] == n, "out: as many rows as q expected")
-        self._call(lib().dinfer_kv_attention, layer, _ints(seqs, "seqs", self.device, n), n, q.data_ptr(), out.data_ptr(),
-                   qs, os_, heads, window, sinks, hd ** -0.5 if scale is None else scale, ws.buf.data_ptr(), ws.nbytes)
+        dev = self.device
+        _run_on(dev, lib().dinfer_kv_attention, self._desc, layer, _ints(seqs, "seqs", dev, n), n, q.data_ptr(),
+                out.data_ptr(), qs, os_, heads, window, sinks, hd ** -0.5 if scale is None else scale,
+                ws.buf.data_ptr(), ws.nbytes)
         return out
 
     def check(self):
         """Raise if an entry of an earlier call was skipped (DinferError names why); clears the status."""
-        self._call(lib().dinfer_kv_status, None)
+        _run_on(self.device, lib().dinfer_kv_status, self._desc, None)
 
 
 def op_window_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, ws: OpWorkspace,
@@ -446,9 +449,9 @@ def op_window_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, ws: O
     dev = q.device
     batch = 1 if cu_q is None else cu_q.shape[0] - 1
     cq, ck = _ints(cu_q, "cu_q", dev), _ints(cu_k, "cu_k", dev, None if cu_q is None else batch + 1)
-    _require(ws.buf.device == dev, "ws: a workspace on the operands' device expected")
+    _require(ws.buf.get_device() == dev.index, "ws: a workspace on the operands' device expected")
     if out is None:
-        out, os_ = q.new_empty((rows, heads, hd)), heads * hd
+        out, os_ = torch.empty_like(q, memory_format=torch.contiguous_format), heads * hd
     else:
         os_ = _rows_of(out, "out", heads, hd, q)
         _require(out.shape[0] == rows, "out: as many rows as q expected")

@@ -207,6 +207,25 @@ def test_many_sequences(D, ws):
     run(D, ws, 17, nq, nq, 1, 1, 64, BF, -1, 0, 0, rows=1)
 
 
+def test_two_calls_at_once(D, ws):
+    rng = np.random.default_rng(24)
+    other, side = D.OpWorkspace(), torch.cuda.Stream()
+    for dtype in (BF, F32):
+        _, q = values(rng, (1500, 4, 64), dtype)
+        _, k = values(rng, (1500, 2, 64), dtype)
+        call = lambda w, left, right: D.op_window_attention(q, k, k, w, left=left, right=right, sinks=3)  # noqa: E731
+        want = [call(ws, -1, 0), call(ws, 100, 7)]
+        torch.cuda.synchronize()
+        for _ in range(20):
+            a = call(ws, -1, 0)
+            with torch.cuda.stream(side):
+                b = call(other, 100, 7)
+            torch.cuda.synchronize()
+            assert torch.equal(a, want[0]) and torch.equal(b, want[1])
+    ws.check()
+    other.check()
+
+
 def test_another_stream_and_a_graph(D, ws):
     rng = np.random.default_rng(18)
     xq, q = values(rng, (300, 2, 128), BF)
