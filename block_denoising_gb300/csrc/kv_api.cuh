@@ -92,8 +92,8 @@ template <int HD>
 bool kv_setup_hd() {
   return kv_setup_attention<__nv_bfloat16, HD, 8>() && kv_setup_attention<__nv_bfloat16, HD, 16>() &&
          kv_setup_attention<float, HD, 1>() && kv_setup_attention<float, HD, 2>() && kv_setup_attention<float, HD, 4>() &&
-         kv_setup_attention<float, HD, 8>() && max_smem(window_f32_kernel<HD, 1>, WfCfg<HD, 1>::kSmem) &&
-         max_smem(window_f32_kernel<HD, 4>, WfCfg<HD, 4>::kSmem) &&
+         kv_setup_attention<float, HD, 8>() && max_smem(window_f32_kernel<HD, 4>, WfCfg<HD, 4>::kSmem) &&
+         max_smem(window_f32_kernel<HD, 16>, WfCfg<HD, 16>::kSmem) &&
          max_smem(window_tc_kernel<HD>, WtCfg<HD>::kSmem);
 }
 
@@ -112,9 +112,10 @@ cudaError_t launch_kv_attention_r(const KaArgs& a, cudaStream_t s) {
   using Cfg = KaCfg<T, HD, R>;
   return launchk(kv_attention_kernel<T, HD, R>, dim3(num_sms()), dim3(Cfg::kThreads), Cfg::kSmem, s, 1, a);
 }
-template <int HD, int kE>
+template <int HD, int kTy>
 cudaError_t launch_window_f32(const WaArgs& a, dim3 grid, cudaStream_t s) {
-  return launchk(window_f32_kernel<HD, kE>, grid, dim3(kWfThreads), WfCfg<HD, kE>::kSmem, s, 1, a);
+  using Cfg = WfCfg<HD, kTy>;
+  return launchk(window_f32_kernel<HD, kTy>, grid, dim3(Cfg::kThreads), Cfg::kSmem, s, 1, a);
 }
 // rows: the query heads a CTA takes at once (kv_rows)
 template <int HD>
@@ -362,21 +363,26 @@ dinfer_status dinfer_op_window_attention(const void* q, const void* k, const voi
   a.status = w.st;
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   // every sequence adds at most one partly filled tile
-  const int pair = a.group % 2 == 0;
-  // fp32: tiles of 64 rows once they give three SMs in four one, else of 16 (4 heads of 64, causal, 16 against
-  // 64: 1024 rows, 68 tiles of 64, 71 against 79 us; 2048 rows, 132 tiles, 199 against 164 us)
-  const bool small = dtype == DINFER_FP32 && (int64_t)(total_q / 64 + 1) * heads < num_sms() * 3 / 4;
-  const int block_rows = dtype == DINFER_FP32 ? (small ? 16 : 64) : pair ? kWtRows : 2 * kWtRows;
+  // fp32: tiles of 64 rows once there are more of them than run at once (two an SM), else of 16 (causal, heads of 128:
+  // 1024 rows, 4 heads, 68 tiles of 64: 124 us, 85 with 16 rows; 4096 rows, 4 heads, 260 tiles: 745 and 638 us;
+  // 4096 rows, 16 heads, 1040 tiles: 1.69 and 2.37 ms)
+  const bool small = dtype == DINFER_FP32 && (int64_t)(total_q / 64 + 1) * heads <= 2 * num_sms();
+  // bf16: two tiles a CTA, or one while there is an SM for each (1024 causal rows, 16 heads of 128, 144 tiles: 15.2 us
+  // alone, 18.3 in pairs; 18 heads, 162 tiles: pairs 19.1)
+  const int form = (int64_t)(total_q / kWtRows + batch) * heads <= num_sms() ? kWtSingle
+                   : a.group % 2 == 0                                        ? kWtPairHeads
+                                                                             : kWtPairRows;
+  const int block_rows = dtype == DINFER_FP32 ? (small ? 16 : 64) : form == kWtPairRows ? 2 * kWtRows : kWtRows;
   const int blocks = total_q / block_rows + batch;
-  const int64_t ctas = (int64_t)blocks * (dtype == DINFER_BF16 && pair ? heads / 2 : heads);
+  const int64_t ctas = (int64_t)blocks * (dtype == DINFER_BF16 && form == kWtPairHeads ? heads / 2 : heads);
   if (ctas >= (1ll << 31)) return fail(c, DINFER_EINVAL, "too many rows");
   const dim3 grid((unsigned)ctas);
   if (dtype == DINFER_FP32) {
-    // Causal rows see the more keys the later they come: where the CTAs (two an SM) do not all start at once, the
-    // last ones go first (16 heads of 64, 4096 rows: 940 us, else 1077; 1024 rows, 272 CTAs: 129, else 108).
+    // Causal rows see the more keys the later they come: where the CTAs do not all start at once, the last ones go
+    // first (16 heads of 64, 4096 rows: 940 us, else 1077).
     a.last_first = ctas > 2 * num_sms();
-    CK(head_dim == 128 ? (small ? launch_window_f32<128, 1>(a, grid, s) : launch_window_f32<128, 4>(a, grid, s))
-                       : (small ? launch_window_f32<64, 1>(a, grid, s) : launch_window_f32<64, 4>(a, grid, s)));
+    CK(head_dim == 128 ? (small ? launch_window_f32<128, 4>(a, grid, s) : launch_window_f32<128, 16>(a, grid, s))
+                       : (small ? launch_window_f32<64, 4>(a, grid, s) : launch_window_f32<64, 16>(a, grid, s)));
     return DINFER_OK;
   }
   WtMaps maps;
@@ -384,8 +390,8 @@ dinfer_status dinfer_op_window_attention(const void* q, const void* k, const voi
       !make_map_rows(&maps.k, k, total_k, kv_heads, head_dim, k_stride) ||
       !make_map_rows(&maps.v, v, total_k, kv_heads, head_dim, v_stride))
     return fail(c, DINFER_EINVAL, "tensor map encoding failed");
-  CK(head_dim == 128 ? launchk(window_tc_kernel<128>, grid, dim3(kWtThreads), WtCfg<128>::kSmem, s, 1, maps, a, pair, blocks)
-                     : launchk(window_tc_kernel<64>, grid, dim3(kWtThreads), WtCfg<64>::kSmem, s, 1, maps, a, pair, blocks));
+  CK(head_dim == 128 ? launchk(window_tc_kernel<128>, grid, dim3(kWtThreads), WtCfg<128>::kSmem, s, 1, maps, a, form, blocks)
+                     : launchk(window_tc_kernel<64>, grid, dim3(kWtThreads), WtCfg<64>::kSmem, s, 1, maps, a, form, blocks));
   return DINFER_OK;
 }
 

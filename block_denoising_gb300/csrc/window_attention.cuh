@@ -185,22 +185,24 @@ __device__ __noinline__ void wa_row_exact(const WaArgs& a, const WaSeq s, int i,
 // ---------------------------------------------------------------------------
 // fp32
 // ---------------------------------------------------------------------------
-// One CTA = 16 kE rows of one head, 256 threads; K and V in tiles of 32 keys, two
-// of them in shared memory, the next one copied in while the current one is
-// worked on.  Thread (ty, tx) of 16 x 16 computes the scores of rows kE ty ..
-// + kE - 1 and keys tx, tx + 16, and owns kE rows x HD / 16 columns of the
-// output; two FMAs an instruction.  Bound by the fp32 FMA rate (there is no
-// fp32 tensor product that keeps 24 bits).
+// One CTA = 4 kTy rows of one head, 16 kTy threads; K and V in tiles of 32 keys,
+// two of them in shared memory, the next one copied in while the current one is
+// worked on.  Thread (ty, tx) of kTy x 16 computes the scores of rows 4 ty .. + 3
+// and keys tx, tx + 16, and owns 4 rows x HD / 16 columns of the output; two FMAs
+// an instruction.  Bound by the fp32 FMA rate (there is no fp32 tensor product
+// that keeps 24 bits) and the shared-memory reads that feed it, which is why a
+// thread has four rows in the short tiles too.
 //
-// kE = 4 (64 rows) does the most products per shared-memory read: 41 TFLOP/s
-// (16 heads of 128, 4096 causal rows; peak 80).  kE = 1 gives short calls four
-// times the CTAs, each half as long: 96 rows, 4 heads of 64, a window of 31 on
-// both sides: 6.4 us, 9.7 with kE = 4; 16 rows: 3.2 us, 4.8 with kE = 4.
-constexpr int kWfThreads = 256;
+// kTy = 16 (64 rows): 41 TFLOP/s (16 heads of 128, 4096 causal rows; peak 80).
+// kTy = 4 (16 rows) for short calls, two or more CTAs an SM: 62 rows in five
+// sequences behind 975 keys each, 32 heads of 64: 52 us; 16 x 16 threads with a
+// row each read every key tile eight times: 86 us.
 constexpr int kWfKeys = 32;
-template <int HD, int kE>
+constexpr int kWfE = 4;  // rows of a thread
+template <int HD, int kTy>
 struct WfCfg {
-  static constexpr int kRows = 16 * kE;
+  static constexpr int kThreads = 16 * kTy;
+  static constexpr int kRows = kWfE * kTy;
   static constexpr int kPad = HD + 4;              // rows of Q and K start 4 banks apart
   static constexpr int kPitchP = kWfKeys + 4;
   static constexpr int kStage = kWfKeys * (kPad + HD);  // floats: K, then V
@@ -209,10 +211,10 @@ struct WfCfg {
   static constexpr int kSmem = (kOffP + kRows * kPitchP) * 4;
 };
 
-template <int HD, int kE>
-__global__ void __launch_bounds__(kWfThreads, 2) window_f32_kernel(const __grid_constant__ WaArgs a) {
-  using Cfg = WfCfg<HD, kE>;
-  constexpr int kRows = Cfg::kRows, kVecs = HD / 4;
+template <int HD, int kTy>
+__global__ void __launch_bounds__(16 * kTy, kTy == 16 ? 2 : 4) window_f32_kernel(const __grid_constant__ WaArgs a) {
+  using Cfg = WfCfg<HD, kTy>;
+  constexpr int kRows = Cfg::kRows, kVecs = HD / 4, kE = kWfE, kThreads = Cfg::kThreads;
   extern __shared__ __align__(16) float wf_sm[];
   float* qs = wf_sm;
   float* ps = wf_sm + Cfg::kOffP;
@@ -226,7 +228,7 @@ __global__ void __launch_bounds__(kWfThreads, 2) window_f32_kernel(const __grid_
   const float* q = reinterpret_cast<const float*>(a.q) + (int64_t)(s.q0 + i0) * a.q_stride + head * HD;
   const float* k = reinterpret_cast<const float*>(a.k) + (int64_t)s.k0 * a.k_stride + (head / a.group) * HD;
   const float* v = reinterpret_cast<const float*>(a.v) + (int64_t)s.k0 * a.v_stride + (head / a.group) * HD;
-  for (int x = tid; x < kRows * kVecs; x += kWfThreads) {
+  for (int x = tid; x < kRows * kVecs; x += kThreads) {
     const int r = x / kVecs, d = x % kVecs * 4;
     cp_async16(smem_u32(qs + r * Cfg::kPad + d), q + (int64_t)min(r, rows - 1) * a.q_stride + d, r < rows ? 16 : 0);
   }
@@ -236,7 +238,7 @@ __global__ void __launch_bounds__(kWfThreads, 2) window_f32_kernel(const __grid_
   auto load = [&](int j0, int buf) {  // keys behind the sequence's end: zeros
     float* ks = wf_sm + Cfg::kOffKv + buf * Cfg::kStage;
 #pragma unroll
-    for (int x = tid; x < kWfKeys * kVecs; x += kWfThreads) {
+    for (int x = tid; x < kWfKeys * kVecs; x += kThreads) {
       const int r = x / kVecs, d = x % kVecs * 4, j = min(j0 + r, s.nk - 1), bytes = j0 + r < s.nk ? 16 : 0;
       cp_async16(smem_u32(ks + r * Cfg::kPad + d), k + (int64_t)j * a.k_stride + d, bytes);
       cp_async16(smem_u32(ks + kWfKeys * Cfg::kPad + r * HD + d), v + (int64_t)j * a.v_stride + d, bytes);

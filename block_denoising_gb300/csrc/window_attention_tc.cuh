@@ -3,7 +3,8 @@
 //
 // A piece of work is two tiles A and B of 128 query rows over the same key head:
 // two query heads of a group at the same rows where the group is even (both tiles
-// then want the same keys), else 256 consecutive rows of one head.  The key tiles
+// then want the same keys), else 256 consecutive rows of one head.  Short calls
+// give every tile an SM of its own (A alone).  The key tiles
 // (128 keys) that some row sees -- the sinks' tiles, then the window's -- pass
 // once through a ring of shared-memory slots and serve both.  One CTA an SM takes
 // its pieces in turn, so that a piece's output is written, and the next one's
@@ -11,7 +12,7 @@
 //   warp 0     TMA: Q of both tiles, then K_0 V_0 K_1 V_1 ... (128-byte swizzle);
 //              a slot is free once both tiles' products over it have completed
 //   warp 1     tensor memory and the single-thread MMA issue, tiles in turn:
-//              S_A, S_B, S_A', P_A V, S_B', P_B V, ...
+//              S_A, S_B, S_A', P_A V, S_B', P_B V, ...  (A alone: S, S', P V, S'', P' V, ...)
 //   warps 2-5  softmax and output of tile A, a thread per row; warps 6-9 tile B
 //   warp 10    looks the pieces up, one ahead
 //
@@ -60,6 +61,8 @@ struct WtMaps {
 constexpr int kWtThreads = 352;
 constexpr int kWtRows = 128;  // rows of a tile
 constexpr int kWtKeys = 128;  // keys of a tile
+// the tiles of a piece: two heads' rows, 256 rows of a head, one tile alone
+enum WtForm { kWtPairHeads, kWtPairRows, kWtSingle };
 
 template <int HD>
 struct WtCfg {
@@ -248,8 +251,9 @@ __device__ __forceinline__ int clc_taken(const uint4* answer) {
 
 template <int HD>
 __global__ void __launch_bounds__(kWtThreads, 1)
-    window_tc_kernel(const __grid_constant__ WtMaps maps, const __grid_constant__ WaArgs a, const int pair_heads,
+    window_tc_kernel(const __grid_constant__ WtMaps maps, const __grid_constant__ WaArgs a, const int form,
                      const int row_blocks) {
+  const bool pair_heads = form == kWtPairHeads, single = form == kWtSingle;
   using Cfg = WtCfg<HD>;
   constexpr int kSlots = Cfg::kSlots;
   extern __shared__ uint8_t smem_raw[];
@@ -337,7 +341,7 @@ __global__ void __launch_bounds__(kWtThreads, 1)
     // ------------------------------ pieces ------------------------------
     // heads fastest, so that CTAs which run together share keys; the last rows
     // (under a causal mask those with the most keys) first
-    const int per_block = pair_heads ? a.heads / 2 : a.heads, block_rows = pair_heads ? kWtRows : 2 * kWtRows;
+    const int per_block = pair_heads ? a.heads / 2 : a.heads, block_rows = form == kWtPairRows ? 2 * kWtRows : kWtRows;
     int asked = 0;
     int at = blockIdx.x;  // of the grid's pieces: this CTA's own, then one that no CTA has begun
     bool left = true, own = true;
@@ -371,7 +375,7 @@ __global__ void __launch_bounds__(kWtThreads, 1)
           p.head0 = pair_heads ? 2 * piece : piece;  // tile x: head head0 + x, or rows i0 + 128 x
           p.kvh = p.head0 / a.group;
           p.band[0] = wt_band(a, p.s, p.i0);
-          p.band[1] = pair_heads ? p.band[0] : wt_band(a, p.s, p.i0 + kWtRows);
+          p.band[1] = pair_heads ? p.band[0] : wt_band(a, p.s, single ? p.s.nq : p.i0 + kWtRows);
           // tile A holds the first row, the last row is B's or, without B, A's
           const int lo = p.band[0].lo, hi = p.band[1].rows > 0 ? p.band[1].hi : p.band[0].hi;
           p.front = (max(0, min(a.sinks, min(lo, hi + 1))) + kWtKeys - 1) / kWtKeys;
@@ -401,9 +405,10 @@ __global__ void __launch_bounds__(kWtThreads, 1)
           for (int x = 0; x < 2; ++x)
             if (ok && n[x] > 0) ok = wait(&s_full[4 * x + ((n[x] - 1) & 3)], ((n[x] - 1) >> 2) & 1);
           if (!ok) break;
-          mbar_arrive_expect_tx(q_full, 2 * Cfg::kTile);
+          const int tiles = single ? 1 : 2;
+          mbar_arrive_expect_tx(q_full, tiles * Cfg::kTile);
           ++loads_q;
-          for (int x = 0; x < 2; ++x)
+          for (int x = 0; x < tiles; ++x)
             for (int h = 0; h < HD / 64; ++h)
               tma_load_3d(sm + x * Cfg::kTile + h * Cfg::kSlab, &maps.q, q_full, h * 64, pair_heads ? p.head0 + x : p.head0,
                           p.s.q0 + p.i0 + (pair_heads ? 0 : x * kWtRows));
@@ -525,6 +530,10 @@ __global__ void __launch_bounds__(kWtThreads, 1)
                 ring.template next<kSlots>();
               }
               seek();
+            }
+            if (single) {  // P V of the turn before
+              due0 = due1;
+              due1 = -1;
             }
             if (due0 >= 0) {
               // O += P V, a half of the keys as soon as its P is there: 16 keys are 8

@@ -73,14 +73,14 @@ def test_masks_over_ragged_sequences(D, ws, dtype, hd, left, right, sinks):
     run(D, ws, 7 + left + 2 * sinks, nq, nk, 2, 2, hd, dtype, left, right, sinks)
 
 
-# enough heads for the fp32 kernel's tiles of 64 rows, in either order
+# enough heads for two tiles a CTA (of one head, of two), and for fp32 tiles of 16 rows from the last on, and of 64
 @pytest.mark.parametrize("hd", [64, 128])
-@pytest.mark.parametrize("heads", [14, 30])
+@pytest.mark.parametrize("dtype,heads", [(BF, 14), (BF, 16), (F32, 14), (F32, 40)])
 @pytest.mark.parametrize("left,right,sinks", MASKS)
-def test_fp32_of_many_heads(D, ws, hd, heads, left, right, sinks):
+def test_many_heads(D, ws, hd, dtype, heads, left, right, sinks):
     nq = [1, 0, 17, 128, 300, 5, 129]
     nk = [1, 3, 17, 128, 300, 400, 100]
-    run(D, ws, 70 + left + 2 * sinks + heads, nq, nk, heads, 2, hd, F32, left, right, sinks, rows=8)
+    run(D, ws, 70 + left + 2 * sinks + heads, nq, nk, heads, 2, hd, dtype, left, right, sinks, rows=8)
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
@@ -95,12 +95,16 @@ def test_lengths(D, ws, n):
     for dtype in (BF, F32):
         run(D, ws, n, [n], [n], 2, 1, 128, dtype, -1, 0, 0, rows=6)
         run(D, ws, n, [1], [n], 2, 1, 64, dtype, n // 2, 0, 1, rows=6)
+    run(D, ws, n, [n], [n], 160, 2, 64, BF, -1, 0, 0, rows=2)
+    run(D, ws, n, [n], [n], 153, 3, 128, BF, 100, 9, 1, rows=2)
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
 def test_long_sequence(D, ws, dtype):
     run(D, ws, 1, [3001], [3500], 2, 1, 128, dtype, 1000, 0, 4, rows=12)
     run(D, ws, 2, [2049], [2049], 1, 1, 64, dtype, -1, -1, 0, rows=12, scale=0.4)
+    run(D, ws, 3, [3001], [3500], 8, 2, 128, dtype, 1000, 0, 4, rows=8)
+    run(D, ws, 4, [3001], [3001], 7, 1, 64, dtype, -1, 0, 0, rows=8)
 
 
 def test_strided_operands_and_rows_of_nobody(D, ws):
@@ -120,7 +124,8 @@ def test_strided_operands_and_rows_of_nobody(D, ws):
         compare(got[3:253, :H], xq[3:253], xk[3:253], xv[3:253], [100, 150], [100, 150], 60, 60, 3, hd ** -0.5, dtype == BF)
 
 
-@pytest.mark.parametrize("dtype,hd,heads", [(BF, 128, 2), (BF, 64, 2), (F32, 64, 2), (F32, 64, 16)])
+@pytest.mark.parametrize("dtype,hd,heads", [(BF, 128, 2), (BF, 64, 2), (BF, 128, 40), (BF, 64, 39), (F32, 64, 2),
+                                            (F32, 64, 40)])
 def test_what_masked_keys_hold_does_not_matter(D, ws, dtype, hd, heads):
     # NaN and infinite keys and values touch the rows that see them and no other, tile neighbours included
     rng = np.random.default_rng(12)
@@ -145,8 +150,8 @@ def test_what_masked_keys_hold_does_not_matter(D, ws, dtype, hd, heads):
 
 
 def test_infinite_scores(D, ws):
-    for dtype in (BF, F32):
-        q = torch.ones(200, 1, 64, dtype=dtype, device=dev)
+    for dtype, heads in ((BF, 1), (BF, 160), (F32, 1)):
+        q = torch.ones(200, heads, 64, dtype=dtype, device=dev)
         k = torch.ones(200, 1, 64, dtype=dtype, device=dev)
         v = torch.ones(200, 1, 64, dtype=dtype, device=dev)
         k[:] = float("-inf")  # every score is -inf: zeros
@@ -161,9 +166,9 @@ def test_infinite_scores(D, ws):
 def test_growing_scores(D, ws):
     # key norms ramp up, so the running maximum grows tile after tile; every other row is damped
     rng = np.random.default_rng(14)
-    for hd in (64, 128):
+    for hd, heads in ((64, 2), (128, 2), (64, 21), (128, 20)):
         n = 900
-        xq, _ = values(rng, (n, 2, hd), BF)
+        xq, _ = values(rng, (n, heads, hd), BF)
         xk, _ = values(rng, (n, 1, hd), BF)
         xq[1::2] *= 0.0625
         xk *= np.linspace(0.25, 6.0, n)[:, None, None]
@@ -210,8 +215,8 @@ def test_many_sequences(D, ws):
 def test_two_calls_at_once(D, ws):
     rng = np.random.default_rng(24)
     other, side = D.OpWorkspace(), torch.cuda.Stream()
-    for dtype in (BF, F32):
-        _, q = values(rng, (1500, 4, 64), dtype)
+    for dtype, heads in ((BF, 4), (BF, 16), (F32, 4)):
+        _, q = values(rng, (1500, heads, 64), dtype)
         _, k = values(rng, (1500, 2, 64), dtype)
         call = lambda w, left, right: D.op_window_attention(q, k, k, w, left=left, right=right, sinks=3)  # noqa: E731
         want = [call(ws, -1, 0), call(ws, 100, 7)]
