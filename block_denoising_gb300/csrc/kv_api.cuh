@@ -94,7 +94,8 @@ bool kv_setup_hd() {
          kv_setup_attention<float, HD, 1>() && kv_setup_attention<float, HD, 2>() && kv_setup_attention<float, HD, 4>() &&
          kv_setup_attention<float, HD, 8>() && max_smem(window_f32_kernel<HD, 4>, WfCfg<HD, 4>::kSmem) &&
          max_smem(window_f32_kernel<HD, 16>, WfCfg<HD, 16>::kSmem) &&
-         max_smem(window_tc_kernel<HD>, WtCfg<HD>::kSmem);
+         max_smem(window_tc_kernel<HD, false>, WtCfg<HD>::kSmem) &&
+         max_smem(window_tc_kernel<HD, true>, WtCfg<HD>::kSmem);
 }
 
 bool kv_setup() {
@@ -116,6 +117,10 @@ template <int HD, int kTy>
 cudaError_t launch_window_f32(const WaArgs& a, dim3 grid, cudaStream_t s) {
   using Cfg = WfCfg<HD, kTy>;
   return launchk(window_f32_kernel<HD, kTy>, grid, dim3(Cfg::kThreads), Cfg::kSmem, s, 1, a);
+}
+template <int HD, bool kSplit>
+cudaError_t launch_window_tc(const WtMaps& maps, const WaArgs& a, int form, int blocks, dim3 grid, cudaStream_t s) {
+  return launchk(window_tc_kernel<HD, kSplit>, grid, dim3(kWtThreads), WtCfg<HD>::kSmem, s, 1, maps, a, form, blocks);
 }
 // rows: the query heads a CTA takes at once (kv_rows)
 template <int HD>
@@ -374,7 +379,20 @@ dinfer_status dinfer_op_window_attention(const void* q, const void* k, const voi
                                                                              : kWtPairRows;
   const int block_rows = dtype == DINFER_FP32 ? (small ? 16 : 64) : form == kWtPairRows ? 2 * kWtRows : kWtRows;
   const int blocks = total_q / block_rows + batch;
-  const int64_t ctas = (int64_t)blocks * (dtype == DINFER_BF16 && form == kWtPairHeads ? heads / 2 : heads);
+  int64_t ctas = (int64_t)blocks * (dtype == DINFER_BF16 && form == kWtPairHeads ? heads / 2 : heads);
+  a.splits = 1;
+  if (dtype == DINFER_BF16 && form == kWtSingle && workspace) {
+    // SMs to spare: a tile's keys go to several of them
+    const int64_t slot = (head_dim == 128 ? WtCfg<128>::kSlotFloats : WtCfg<64>::kSlotFloats) * 4ll;
+    const int most = (total_k + kWtKeys - 1) / kWtKeys / kWtPartTiles;
+    const int splits = std::min((int)(num_sms() / ctas), most);
+    if (splits > 1 && ctas * splits * slot <= (int64_t)w.data_bytes) {
+      a.splits = splits;
+      a.partial = reinterpret_cast<float*>(w.data);
+      a.tickets = w.tickets;
+      ctas *= splits;
+    }
+  }
   if (ctas >= (1ll << 31)) return fail(c, DINFER_EINVAL, "too many rows");
   const dim3 grid((unsigned)ctas);
   if (dtype == DINFER_FP32) {
@@ -390,8 +408,11 @@ dinfer_status dinfer_op_window_attention(const void* q, const void* k, const voi
       !make_map_rows(&maps.k, k, total_k, kv_heads, head_dim, k_stride) ||
       !make_map_rows(&maps.v, v, total_k, kv_heads, head_dim, v_stride))
     return fail(c, DINFER_EINVAL, "tensor map encoding failed");
-  CK(head_dim == 128 ? launchk(window_tc_kernel<128>, grid, dim3(kWtThreads), WtCfg<128>::kSmem, s, 1, maps, a, form, blocks)
-                     : launchk(window_tc_kernel<64>, grid, dim3(kWtThreads), WtCfg<64>::kSmem, s, 1, maps, a, form, blocks));
+  const bool split = a.splits > 1;
+  CK(head_dim == 128 ? (split ? launch_window_tc<128, true>(maps, a, form, blocks, grid, s)
+                              : launch_window_tc<128, false>(maps, a, form, blocks, grid, s))
+                     : (split ? launch_window_tc<64, true>(maps, a, form, blocks, grid, s)
+                              : launch_window_tc<64, false>(maps, a, form, blocks, grid, s)));
   return DINFER_OK;
 }
 

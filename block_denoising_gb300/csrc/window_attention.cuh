@@ -52,6 +52,9 @@ struct WaArgs {
   float scale_log2;
   int last_first;  // fp32: CTAs take the tiles from the last to the first
   DevState* status;
+  float* partial;  // bf16: the keys of a tile dealt to up to `splits` CTAs
+  int* tickets;
+  int splits;
 };
 
 // One sequence's rows and keys; out-of-order or out-of-range cu entries give an empty one.

@@ -4,7 +4,11 @@
 // A piece of work is two tiles A and B of 128 query rows over the same key head:
 // two query heads of a group at the same rows where the group is even (both tiles
 // then want the same keys), else 256 consecutive rows of one head.  Short calls
-// give every tile an SM of its own (A alone).  The key tiles
+// give every tile an SM of its own (A alone), and where SMs are left over several,
+// each with a part of the keys: the parts are joined in fp32 through the workspace,
+// by the last of their CTAs.  (One row over 4001 keys, 32 heads of 128 on 4: two
+// heads a CTA 50 us, one 41, in four parts 17; 64 rows over
+// 8704 keys, 32 heads of 128: 79 and 36.)  The key tiles
 // (128 keys) that some row sees -- the sinks' tiles, then the window's -- pass
 // once through a ring of shared-memory slots and serve both.  One CTA an SM takes
 // its pieces in turn, so that a piece's output is written, and the next one's
@@ -63,6 +67,7 @@ constexpr int kWtRows = 128;  // rows of a tile
 constexpr int kWtKeys = 128;  // keys of a tile
 // the tiles of a piece: two heads' rows, 256 rows of a head, one tile alone
 enum WtForm { kWtPairHeads, kWtPairRows, kWtSingle };
+constexpr int kWtPartTiles = 3;  // key tiles of a part at least
 
 template <int HD>
 struct WtCfg {
@@ -71,7 +76,9 @@ struct WtCfg {
   static constexpr int kSlots = HD == 128 ? 5 : 8;        // K and V tiles in flight
   static constexpr int kOffRing = 2 * kTile;
   static constexpr int kOffBar = kOffRing + kSlots * kTile;
-  static constexpr int kSmem = 1024 + kOffBar + 320;
+  static constexpr int kSmem = 1024 + kOffBar + 336;
+  // a part's rows in the workspace: (m, l) of 128, then O
+  static constexpr int kSlotFloats = 2 * 128 + 128 * HD;
   // tensor memory: S buffers, then P (64 columns) and O (HD) of each tile
   static constexpr int kBufs = HD == 128 ? 1 : 2;
   static constexpr int kColP = kBufs * 128;
@@ -129,6 +136,7 @@ struct WtPiece {
   WaSeq s;
   int i0, head0, kvh;   // first row, first query head, key head
   int front, first, n;  // key tiles: the sinks' 0 .. front - 1, then first ..; n in all (-1: no piece is left)
+  int unit, part, parts;  // kSplit: which tile, which part of its keys, of how many
   WtBand band[2];
   __device__ __forceinline__ void put(const WtPiece& p) volatile {
     s.q0 = p.s.q0;
@@ -141,6 +149,9 @@ struct WtPiece {
     front = p.front;
     first = p.first;
     n = p.n;
+    unit = p.unit;
+    part = p.part;
+    parts = p.parts;
     for (int x = 0; x < 2; ++x) {
       band[x].rows = p.band[x].rows;
       band[x].lo = p.band[x].lo;
@@ -249,11 +260,14 @@ __device__ __forceinline__ int clc_taken(const uint4* answer) {
   return ok ? (int)x : -1;
 }
 
-template <int HD>
+// kSplit: A alone, its keys dealt to up to a.splits CTAs.  A kernel of its own: with
+// the join among its code the other forms ran 3 to 5 % longer.
+template <int HD, bool kSplit>
 __global__ void __launch_bounds__(kWtThreads, 1)
     window_tc_kernel(const __grid_constant__ WtMaps maps, const __grid_constant__ WaArgs a, const int form,
                      const int row_blocks) {
-  const bool pair_heads = form == kWtPairHeads, single = form == kWtSingle;
+  const bool pair_heads = !kSplit && form == kWtPairHeads, single = kSplit || form == kWtSingle;
+  const int splits = kSplit ? a.splits : 1;
   using Cfg = WtCfg<HD>;
   constexpr int kSlots = Cfg::kSlots;
   extern __shared__ uint8_t smem_raw[];
@@ -274,12 +288,15 @@ __global__ void __launch_bounds__(kWtThreads, 1)
   uint64_t* drain = piece_empty + 2;
   uint64_t* clc_bar = drain + 1;
   uint64_t* loaded = clc_bar + 1;        // a piece's last copies are issued
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(loaded + 1);
+  uint64_t* part_out = loaded + 1;       // a part's rows are in the workspace
+  uint64_t* part_told = part_out + 1;    // whether this CTA joins the parts
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(part_told + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  static_assert((1 + kSlots + 8 + 8 + 4 + 2 + 2 + 2 + 3 + 1) * 8 <= 320, "barriers");
+  static_assert((1 + kSlots + 8 + 8 + 4 + 2 + 2 + 2 + 2 + 3 + 1) * 8 <= 336, "barriers");
   __shared__ volatile WtPiece pieces[2];
   __shared__ uint4 clc_answer[2];
   __shared__ volatile int redoing;  // warps that do rows again
+  __shared__ volatile int join_here;
   // of each slot's tile, for the TMA thread: which tiles' products read it (bits
   // 0, 1) and whether it is V (bit 2); the products' numbers
   __shared__ int slot_use[kSlots][3];
@@ -301,6 +318,10 @@ __global__ void __launch_bounds__(kWtThreads, 1)
     mbar_init(drain, 1);
     mbar_init(clc_bar, 1);
     mbar_init(loaded, 1);
+    if (kSplit) {
+      mbar_init(part_out, 4);
+      mbar_init(part_told, 1);
+    }
     *abort_flag = 0;
     redoing = 0;
     fence_mbar_init();
@@ -341,7 +362,7 @@ __global__ void __launch_bounds__(kWtThreads, 1)
     // ------------------------------ pieces ------------------------------
     // heads fastest, so that CTAs which run together share keys; the last rows
     // (under a causal mask those with the most keys) first
-    const int per_block = pair_heads ? a.heads / 2 : a.heads, block_rows = form == kWtPairRows ? 2 * kWtRows : kWtRows;
+    const int per_block = pair_heads ? a.heads / 2 : a.heads * splits, block_rows = form == kWtPairRows ? 2 * kWtRows : kWtRows;
     int asked = 0;
     int at = blockIdx.x;  // of the grid's pieces: this CTA's own, then one that no CTA has begun
     bool left = true, own = true;
@@ -369,10 +390,12 @@ __global__ void __launch_bounds__(kWtThreads, 1)
       if (lane == 0) {
         WtPiece p;
         p.n = -1;
+        p.unit = p.part = 0;
+        p.parts = 1;
         if (left) {
           p.s = wa_seq(a, b);
           p.i0 = block * block_rows;
-          p.head0 = pair_heads ? 2 * piece : piece;  // tile x: head head0 + x, or rows i0 + 128 x
+          p.head0 = pair_heads ? 2 * piece : piece / splits;  // tile x: head head0 + x, or rows i0 + 128 x
           p.kvh = p.head0 / a.group;
           p.band[0] = wt_band(a, p.s, p.i0);
           p.band[1] = pair_heads ? p.band[0] : wt_band(a, p.s, single ? p.s.nq : p.i0 + kWtRows);
@@ -381,6 +404,23 @@ __global__ void __launch_bounds__(kWtThreads, 1)
           p.front = (max(0, min(a.sinks, min(lo, hi + 1))) + kWtKeys - 1) / kWtKeys;
           p.first = max(p.front, lo / kWtKeys);
           p.n = p.front + (hi < 0 ? 0 : max(0, hi / kWtKeys - p.first + 1));
+          if constexpr (kSplit) {
+            // a part has at least three key tiles, and one more for every 16 rows to be
+            // joined (some 1 us each); the sinks go to the first part
+            const int w = p.n - p.front, parts = max(1, min(splits, w / (kWtPartTiles + p.band[0].rows / 16)));
+            p.unit = at / splits;
+            p.part = at % splits;
+            if (p.part >= parts) {  // too few keys for another part
+              p.n = 0;
+              p.band[0].rows = 0;
+            } else {
+              const int w0 = p.part * w / parts, w1 = (p.part + 1) * w / parts;
+              if (p.part > 0) p.front = 0;
+              p.first += w0;
+              p.n = p.front + w1 - w0;
+              p.parts = parts;
+            }
+          }
         }
         pieces[it & 1].put(p);
         mbar_arrive(&piece_full[it & 1]);
@@ -576,6 +616,7 @@ __global__ void __launch_bounds__(kWtThreads, 1)
     const float sc = a.scale_log2;
     bool ok = true;
     int c = 0;  // key tiles begun, over all pieces
+    int joins = 0;
     auto all_wait = [&](uint64_t* bar, uint32_t parity) -> bool {
       return __all_sync(0xffffffffu, wait(bar, parity));
     };
@@ -683,7 +724,112 @@ __global__ void __launch_bounds__(kWtThreads, 1)
         f32x2_parts(add2(rs[0], rs[1]), s0, s1);
         l += s0 + s1;
       }
-      if (live) {
+      if (kSplit && x == 0 && p.parts > 1) {
+        // A part of the keys: (m, l) and O go to the workspace; the last part's CTA to
+        // get there joins them, in the order of the parts.
+        const int rows = p.band[0].rows, parts = p.parts;
+        float* unit0 = a.partial + (int64_t)p.unit * splits * Cfg::kSlotFloats;
+        float* slot = unit0 + (int64_t)p.part * Cfg::kSlotFloats;
+        if (ok && !last_pv_done(c + 1)) ok = false;
+        if (live && ok) {
+          tc_fence_after();
+          if (r < rows) __stcg(reinterpret_cast<float2*>(slot) + r, make_float2(m_used, l));
+#pragma unroll 1
+          for (int k = 0; k < HD / 32; ++k) {
+            uint32_t o[32];
+            tmem_ld32(t_lane + Cfg::kColO + k * 32, o);
+            if (r < rows)
+#pragma unroll
+              for (int u = 0; u < 8; ++u)
+                __stcg(reinterpret_cast<uint4*>(slot + 256 + r * HD + k * 32) + u,
+                       make_uint4(o[4 * u], o[4 * u + 1], o[4 * u + 2], o[4 * u + 3]));
+          }
+          tc_fence_before();
+        }
+        __threadfence();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(part_out);
+        if (warp == 2) {
+          if (!all_wait(part_out, joins & 1)) ok = false;
+          if (lane == 0) {
+            join_here = ticket_acq_rel(a.tickets + p.unit) == parts - 1;
+            mbar_arrive(part_told);
+          }
+        }
+        if (!all_wait(part_told, joins & 1)) ok = false;
+        ++joins;
+        if (ok && join_here) {
+          if (warp == 2 && lane == 0) a.tickets[p.unit] = 0;
+          constexpr int kE = HD / 32;  // a row a warp, kE columns a lane; four rows and four parts at once
+          const WaSeq s{p.s.q0, p.s.nq, p.s.k0, p.s.nk};
+#pragma unroll 1
+          for (int r0 = (warp & 3) * 4; r0 < rows; r0 += 16) {
+            float mm[4], ll[4] = {}, acc[4][kE] = {};
+#pragma unroll
+            for (int u = 0; u < 4; ++u) mm[u] = -INFINITY;
+#pragma unroll 1
+            for (int k0 = 0; k0 < parts; k0 += 4) {
+              float2 w[4][4];
+              float v[4][4][kE];
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                  w[k][u] = make_float2(-INFINITY, 0.f);
+#pragma unroll
+                  for (int e = 0; e < kE; ++e) v[k][u][e] = 0.f;
+                  if (k0 + k < parts && r0 + u < rows) {
+                    const float* from = unit0 + (int64_t)(k0 + k) * Cfg::kSlotFloats;
+                    w[k][u] = __ldcg(reinterpret_cast<const float2*>(from) + r0 + u);
+                    from += 256 + (r0 + u) * HD + lane * kE;
+                    if constexpr (kE == 4)
+                      *reinterpret_cast<float4*>(v[k][u]) = __ldcg(reinterpret_cast<const float4*>(from));
+                    else
+                      *reinterpret_cast<float2*>(v[k][u]) = __ldcg(reinterpret_cast<const float2*>(from));
+                  }
+                }
+#pragma unroll
+              for (int u = 0; u < 4; ++u) {
+                const float mn = fmaxf(fmaxf(mm[u], fmaxf(w[0][u].x, w[1][u].x)), fmaxf(w[2][u].x, w[3][u].x));
+                const float f0 = mm[u] == -INFINITY ? 0.f : ex2_approx(mm[u] - mn);
+                mm[u] = mn;
+                ll[u] *= f0;
+#pragma unroll
+                for (int e = 0; e < kE; ++e) acc[u][e] *= f0;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                  const float f = w[k][u].x == -INFINITY ? 0.f : ex2_approx(w[k][u].x - mn);
+                  ll[u] = fmaf(f, w[k][u].y, ll[u]);
+#pragma unroll
+                  for (int e = 0; e < kE; ++e) acc[u][e] = fmaf(f, v[k][u][e], acc[u][e]);
+                }
+              }
+            }
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+              if (r0 + u >= rows) break;
+              bool fine = ll[u] <= 3.0e38f;
+              const float inv = ll[u] == 0.f ? 0.f : 1.f / ll[u];
+              uint32_t h[kE / 2];
+#pragma unroll
+              for (int e = 0; e < kE; e += 2) {
+                fine = fine && fabsf(acc[u][e]) <= 3.0e38f && fabsf(acc[u][e + 1]) <= 3.0e38f;
+                h[e / 2] = inv == 0.f ? 0u : pack_bf16x2(acc[u][e] * inv, acc[u][e + 1] * inv);
+              }
+              const int i = p.i0 + r0 + u;
+              uint32_t* out = reinterpret_cast<uint32_t*>(reinterpret_cast<__nv_bfloat16*>(a.o) +
+                                                          (int64_t)(s.q0 + i) * a.o_stride + p.head0 * HD + lane * kE);
+              if constexpr (kE == 4) *reinterpret_cast<uint2*>(out) = make_uint2(h[0], h[1]); else *out = h[0];
+              if (__any_sync(0xffffffffu, !fine)) {
+                if (lane == 0) atomicAdd(const_cast<int*>(&redoing), 1);
+                wa_row_exact<__nv_bfloat16, HD>(a, s, i, p.head0);
+                __syncwarp();
+                if (lane == 0) atomicSub(const_cast<int*>(&redoing), 1);
+              }
+            }
+          }
+        }
+      } else if (live) {
         const int rows = p.band[x].rows, i_tile = p.i0 + ((!pair_heads && x) ? kWtRows : 0);
         const int head = p.head0 + (pair_heads ? x : 0);
         const WaSeq s{p.s.q0, p.s.nq, p.s.k0, p.s.nk};

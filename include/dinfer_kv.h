@@ -151,8 +151,10 @@ dinfer_status dinfer_kv_attention(const dinfer_kv_cache* cache, int32_t layer, c
  * <= 2^30, head_dim 64 or 128, scale > 0; o must not overlap q, k or v.
  * bf16 runs on the tensor cores: probabilities are rounded to bf16 and summed
  * in fp32.  fp32 is computed in fp32.  Keys that a row does not see do not
- * touch it, whatever they hold.  The workspace may be NULL; when given, a wait
- * that timed out sets its status word. */
+ * touch it, whatever they hold.  The workspace may be NULL; when given, calls
+ * that overlap need one each, a wait that timed out sets its status word (zero
+ * it again then), and few bf16 rows over many keys are split over the keys and
+ * joined in a fixed order: the same call gives the same bits. */
 dinfer_status dinfer_op_window_attention(const void* q, const void* k, const void* v, void* o, int32_t dtype,
                                          int32_t batch, const int32_t* cu_q, const int32_t* cu_k, int32_t total_q,
                                          int32_t total_k, int32_t heads, int32_t kv_heads, int32_t head_dim,
