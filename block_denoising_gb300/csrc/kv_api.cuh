@@ -92,8 +92,9 @@ template <int HD>
 bool kv_setup_hd() {
   return kv_setup_attention<__nv_bfloat16, HD, 8>() && kv_setup_attention<__nv_bfloat16, HD, 16>() &&
          kv_setup_attention<float, HD, 1>() && kv_setup_attention<float, HD, 2>() && kv_setup_attention<float, HD, 4>() &&
-         kv_setup_attention<float, HD, 8>() && max_smem(window_f32_kernel<HD, 4>, WfCfg<HD, 4>::kSmem) &&
-         max_smem(window_f32_kernel<HD, 16>, WfCfg<HD, 16>::kSmem) &&
+         kv_setup_attention<float, HD, 8>() && max_smem(window_f32_kernel<HD, 4, false>, WfCfg<HD, 4>::kSmem) &&
+         max_smem(window_f32_kernel<HD, 4, true>, WfCfg<HD, 4>::kSmem) &&
+         max_smem(window_f32_kernel<HD, 16, false>, WfCfg<HD, 16>::kSmem) &&
          max_smem(window_tc_kernel<HD, false>, WtCfg<HD>::kSmem) &&
          max_smem(window_tc_kernel<HD, true>, WtCfg<HD>::kSmem);
 }
@@ -113,10 +114,10 @@ cudaError_t launch_kv_attention_r(const KaArgs& a, cudaStream_t s) {
   using Cfg = KaCfg<T, HD, R>;
   return launchk(kv_attention_kernel<T, HD, R>, dim3(num_sms()), dim3(Cfg::kThreads), Cfg::kSmem, s, 1, a);
 }
-template <int HD, int kTy>
+template <int HD, int kTy, bool kSplit>
 cudaError_t launch_window_f32(const WaArgs& a, dim3 grid, cudaStream_t s) {
   using Cfg = WfCfg<HD, kTy>;
-  return launchk(window_f32_kernel<HD, kTy>, grid, dim3(Cfg::kThreads), Cfg::kSmem, s, 1, a);
+  return launchk(window_f32_kernel<HD, kTy, kSplit>, grid, dim3(Cfg::kThreads), Cfg::kSmem, s, 1, a);
 }
 template <int HD, bool kSplit>
 cudaError_t launch_window_tc(const WtMaps& maps, const WaArgs& a, int form, int blocks, dim3 grid, cudaStream_t s) {
@@ -381,11 +382,13 @@ dinfer_status dinfer_op_window_attention(const void* q, const void* k, const voi
   const int blocks = total_q / block_rows + batch;
   int64_t ctas = (int64_t)blocks * (dtype == DINFER_BF16 && form == kWtPairHeads ? heads / 2 : heads);
   a.splits = 1;
-  if (dtype == DINFER_BF16 && form == kWtSingle && workspace) {
-    // SMs to spare: a tile's keys go to several of them
-    const int64_t slot = (head_dim == 128 ? WtCfg<128>::kSlotFloats : WtCfg<64>::kSlotFloats) * 4ll;
-    const int most = (total_k + kWtKeys - 1) / kWtKeys / kWtPartTiles;
-    const int splits = std::min((int)(num_sms() / ctas), most);
+  if (workspace && (dtype == DINFER_FP32 ? small : form == kWtSingle)) {
+    // SMs to spare: a tile's keys go to several of them (fp32: two CTAs an SM)
+    const bool f32 = dtype == DINFER_FP32;
+    const int64_t slot = 4ll * (f32 ? (head_dim == 128 ? WfCfg<128, 4>::kSlotFloats : WfCfg<64, 4>::kSlotFloats)
+                                    : (head_dim == 128 ? WtCfg<128>::kSlotFloats : WtCfg<64>::kSlotFloats));
+    const int most = f32 ? total_k / kWfKeys / kWfPartTiles : total_k / kWtKeys / kWtPartTiles;
+    const int splits = (int)std::min<int64_t>((f32 ? 2 : 1) * num_sms() / ctas, most);
     if (splits > 1 && ctas * splits * slot <= (int64_t)w.data_bytes) {
       a.splits = splits;
       a.partial = reinterpret_cast<float*>(w.data);
@@ -399,8 +402,13 @@ dinfer_status dinfer_op_window_attention(const void* q, const void* k, const voi
     // Causal rows see the more keys the later they come: where the CTAs do not all start at once, the last ones go
     // first (16 heads of 64, 4096 rows: 940 us, else 1077).
     a.last_first = ctas > 2 * num_sms();
-    CK(head_dim == 128 ? (small ? launch_window_f32<128, 4>(a, grid, s) : launch_window_f32<128, 16>(a, grid, s))
-                       : (small ? launch_window_f32<64, 4>(a, grid, s) : launch_window_f32<64, 16>(a, grid, s)));
+    const bool split = a.splits > 1;
+    CK(head_dim == 128 ? (split   ? launch_window_f32<128, 4, true>(a, grid, s)
+                          : small ? launch_window_f32<128, 4, false>(a, grid, s)
+                                  : launch_window_f32<128, 16, false>(a, grid, s))
+                       : (split   ? launch_window_f32<64, 4, true>(a, grid, s)
+                          : small ? launch_window_f32<64, 4, false>(a, grid, s)
+                                  : launch_window_f32<64, 16, false>(a, grid, s)));
     return DINFER_OK;
   }
   WtMaps maps;

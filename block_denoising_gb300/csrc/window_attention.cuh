@@ -52,7 +52,7 @@ struct WaArgs {
   float scale_log2;
   int last_first;  // fp32: CTAs take the tiles from the last to the first
   DevState* status;
-  float* partial;  // bf16: the keys of a tile dealt to up to `splits` CTAs
+  float* partial;  // the keys of a tile dealt to up to `splits` CTAs
   int* tickets;
   int splits;
 };
@@ -199,9 +199,12 @@ __device__ __noinline__ void wa_row_exact(const WaArgs& a, const WaSeq s, int i,
 // kTy = 16 (64 rows): 41 TFLOP/s (16 heads of 128, 4096 causal rows; peak 80).
 // kTy = 4 (16 rows) for short calls, two or more CTAs an SM: 62 rows in five
 // sequences behind 975 keys each, 32 heads of 64: 52 us; 16 x 16 threads with a
-// row each read every key tile eight times: 86 us.
+// row each read every key tile eight times: 86 us.  Where these leave SMs idle
+// the keys of a tile go to several CTAs too (one row over 4001 keys, 32 heads of
+// 64: 30 us, 188 without).
 constexpr int kWfKeys = 32;
 constexpr int kWfE = 4;  // rows of a thread
+constexpr int kWfPartTiles = 8;  // key tiles of a part at least
 template <int HD, int kTy>
 struct WfCfg {
   static constexpr int kThreads = 16 * kTy;
@@ -212,9 +215,11 @@ struct WfCfg {
   static constexpr int kOffKv = kRows * kPad;
   static constexpr int kOffP = kOffKv + 2 * kStage;
   static constexpr int kSmem = (kOffP + kRows * kPitchP) * 4;
+  static constexpr int kSlotFloats = kRows * (2 + HD);  // a part's rows in the workspace: (m, l), then O
 };
 
-template <int HD, int kTy>
+// kSplit: the keys of a tile dealt to up to a.splits CTAs.
+template <int HD, int kTy, bool kSplit>
 __global__ void __launch_bounds__(16 * kTy, kTy == 16 ? 2 : 4) window_f32_kernel(const __grid_constant__ WaArgs a) {
   using Cfg = WfCfg<HD, kTy>;
   constexpr int kRows = Cfg::kRows, kVecs = HD / 4, kE = kWfE, kThreads = Cfg::kThreads;
@@ -224,9 +229,10 @@ __global__ void __launch_bounds__(16 * kTy, kTy == 16 ? 2 : 4) window_f32_kernel
   pdl_wait();
   pdl_trigger();
   int b, tile;
-  if (!wa_find_tile(a, (a.last_first ? gridDim.x - 1 - blockIdx.x : blockIdx.x) / a.heads, kRows, &b, &tile)) return;
+  const int unit = kSplit ? blockIdx.x / a.splits : a.last_first ? gridDim.x - 1 - blockIdx.x : blockIdx.x;
+  if (!wa_find_tile(a, unit / a.heads, kRows, &b, &tile)) return;
   const WaSeq s = wa_seq(a, b);
-  const int head = blockIdx.x % a.heads, i0 = tile * kRows, rows = min(kRows, s.nq - i0);
+  const int head = unit % a.heads, i0 = tile * kRows, rows = min(kRows, s.nq - i0);
   const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
   const float* q = reinterpret_cast<const float*>(a.q) + (int64_t)(s.q0 + i0) * a.q_stride + head * HD;
   const float* k = reinterpret_cast<const float*>(a.k) + (int64_t)s.k0 * a.k_stride + (head / a.group) * HD;
@@ -237,7 +243,21 @@ __global__ void __launch_bounds__(16 * kTy, kTy == 16 ? 2 : 4) window_f32_kernel
   }
   // keys some row of the tile sees: the sinks, then from the first row's lo to the last row's hi
   const WaRange top = wa_range(a, s, i0), bottom = wa_range(a, s, i0 + rows - 1);
-  const int front = min(a.sinks, min(top.lo, bottom.hi + 1));
+  int front = min(a.sinks, min(top.lo, bottom.hi + 1)), end = bottom.hi + 1;
+  int begin = max((front + kWfKeys - 1) / kWfKeys, top.lo / kWfKeys) * kWfKeys;  // the window's tiles
+  int parts = 1, part = 0;
+  if constexpr (kSplit) {  // eight tiles a part at least; the sinks go to the first part
+    const int w = max(0, (end - begin + kWfKeys - 1) / kWfKeys);
+    parts = max(1, min(a.splits, w / kWfPartTiles));
+    part = blockIdx.x % a.splits;
+    if (part >= parts) {
+      cp_async_wait<0>();
+      return;
+    }
+    if (part > 0) front = 0;
+    end = min(end, begin + (part + 1) * w / parts * kWfKeys);
+    begin += part * w / parts * kWfKeys;
+  }
   auto load = [&](int j0, int buf) {  // keys behind the sequence's end: zeros
     float* ks = wf_sm + Cfg::kOffKv + buf * Cfg::kStage;
 #pragma unroll
@@ -249,7 +269,7 @@ __global__ void __launch_bounds__(16 * kTy, kTy == 16 ? 2 : 4) window_f32_kernel
   };
   auto behind = [&](int j0) {  // the tile after j0's: behind the sinks, on to the window
     const int j = j0 + kWfKeys;
-    return j >= front && j < top.lo ? max(j, top.lo / kWfKeys * kWfKeys) : j;
+    return j >= front ? max(j, begin) : j;
   };
   constexpr int kC = HD / 16;  // output columns of a thread: tx * 4 + 64 * (c / 4) + c % 4, as pairs
   uint64_t o[kE][kC / 2] = {};
@@ -260,13 +280,13 @@ __global__ void __launch_bounds__(16 * kTy, kTy == 16 ? 2 : 4) window_f32_kernel
     m[e] = -INFINITY;
     rr[e] = wa_range(a, s, i0 + min(ty * kE + e, rows - 1));
   }
-  int j0 = front > 0 ? 0 : top.lo / kWfKeys * kWfKeys;
-  if (j0 <= bottom.hi) load(j0, 0);
+  int j0 = front > 0 ? 0 : begin;
+  if (j0 < end) load(j0, 0);
   cp_async_commit();
-  for (int buf = 0; j0 <= bottom.hi; buf ^= 1) {
+  for (int buf = 0; j0 < end; buf ^= 1) {
     const int jn = behind(j0);
     __syncthreads();  // the other buffer has been read
-    if (jn <= bottom.hi) load(jn, buf ^ 1);
+    if (jn < end) load(jn, buf ^ 1);
     cp_async_commit();
     cp_async_wait<1>();
     __syncthreads();
@@ -336,6 +356,74 @@ __global__ void __launch_bounds__(16 * kTy, kTy == 16 ? 2 : 4) window_f32_kernel
     j0 = jn;
   }
   cp_async_wait<0>();
+  if constexpr (kSplit) {
+    if (parts > 1) {
+      // (m, l) and O of this part to the workspace; the last part's CTA to get here
+      // joins them, in the order of the parts, and goes on with the sums
+      __shared__ int join_sh;
+      float* unit0 = a.partial + (int64_t)unit * a.splits * Cfg::kSlotFloats;
+      float* slot = unit0 + (int64_t)part * Cfg::kSlotFloats;
+#pragma unroll
+      for (int e = 0; e < kE; ++e) {
+        const int r = ty * kE + e;
+#pragma unroll
+        for (int d = 8; d > 0; d >>= 1) l[e] += __shfl_xor_sync(0xffffffffu, l[e], d);
+        if (tx == 0) __stcg(reinterpret_cast<float2*>(slot) + r, make_float2(m[e], l[e]));
+#pragma unroll
+        for (int c = 0; c < kC / 2; c += 2)
+          __stcg(reinterpret_cast<ulonglong2*>(slot + 2 * kRows + r * HD + tx * 4 + 32 * c), make_ulonglong2(o[e][c], o[e][c + 1]));
+      }
+      __threadfence();
+      __syncthreads();
+      if (tid == 0) join_sh = ticket_acq_rel(a.tickets + unit) == parts - 1;
+      __syncthreads();
+      if (!join_sh) return;
+      if (tid == 0) a.tickets[unit] = 0;
+#pragma unroll
+      for (int e = 0; e < kE; ++e) {
+        const int r = ty * kE + e;
+        float mm = -INFINITY, ll = 0.f, acc[kC] = {};
+        for (int k0 = 0; k0 < parts; k0 += 4) {
+          float2 w[4];
+          float4 v[4][kC / 4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            w[k] = make_float2(-INFINITY, 0.f);
+#pragma unroll
+            for (int c = 0; c < kC / 4; ++c) v[k][c] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (k0 + k < parts) {
+              const float* from = unit0 + (int64_t)(k0 + k) * Cfg::kSlotFloats;
+              w[k] = __ldcg(reinterpret_cast<const float2*>(from) + r);
+#pragma unroll
+              for (int c = 0; c < kC / 4; ++c)
+                v[k][c] = __ldcg(reinterpret_cast<const float4*>(from + 2 * kRows + r * HD + tx * 4 + 64 * c));
+            }
+          }
+          const float mn = fmaxf(fmaxf(mm, fmaxf(w[0].x, w[1].x)), fmaxf(w[2].x, w[3].x));
+          const float f0 = mm == -INFINITY ? 0.f : ex2_approx(mm - mn);
+          mm = mn;
+          ll *= f0;
+#pragma unroll
+          for (int c = 0; c < kC; ++c) acc[c] *= f0;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float f = w[k].x == -INFINITY ? 0.f : ex2_approx(w[k].x - mn);
+            ll = fmaf(f, w[k].y, ll);
+#pragma unroll
+            for (int c = 0; c < kC / 4; ++c) {
+              acc[4 * c] = fmaf(f, v[k][c].x, acc[4 * c]);
+              acc[4 * c + 1] = fmaf(f, v[k][c].y, acc[4 * c + 1]);
+              acc[4 * c + 2] = fmaf(f, v[k][c].z, acc[4 * c + 2]);
+              acc[4 * c + 3] = fmaf(f, v[k][c].w, acc[4 * c + 3]);
+            }
+          }
+        }
+        l[e] = tx == 0 ? ll : 0.f;
+#pragma unroll
+        for (int c = 0; c < kC; c += 2) o[e][c / 2] = f32x2(__float_as_uint(acc[c]), __float_as_uint(acc[c + 1]));
+      }
+    }
+  }
   // sums over the 16 threads of a row, and whether all of it is finite
   uint32_t redo = 0;
 #pragma unroll

@@ -153,7 +153,7 @@ dinfer_status dinfer_kv_attention(const dinfer_kv_cache* cache, int32_t layer, c
  * in fp32.  fp32 is computed in fp32.  Keys that a row does not see do not
  * touch it, whatever they hold.  The workspace may be NULL; when given, calls
  * that overlap need one each, a wait that timed out sets its status word (zero
- * it again then), and few bf16 rows over many keys are split over the keys and
+ * it again then), and few rows over many keys are split over the keys and
  * joined in a fixed order: the same call gives the same bits. */
 dinfer_status dinfer_op_window_attention(const void* q, const void* k, const void* v, void* o, int32_t dtype,
                                          int32_t batch, const int32_t* cu_q, const int32_t* cu_k, int32_t total_q,

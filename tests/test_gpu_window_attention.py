@@ -212,40 +212,41 @@ def test_many_sequences(D, ws):
     run(D, ws, 17, nq, nq, 1, 1, 64, BF, -1, 0, 0, rows=1)
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
 @pytest.mark.parametrize("hd,heads,kv_heads", [(128, 3, 1), (64, 4, 2), (128, 8, 1)])
 @pytest.mark.parametrize("left,right,sinks", [(-1, 0, 0), (-1, -1, 0), (1500, 0, 130), (700, 20, 4)])
-def test_few_rows_over_many_keys(D, ws, hd, heads, kv_heads, left, right, sinks):
+def test_few_rows_over_many_keys(D, ws, dtype, hd, heads, kv_heads, left, right, sinks):
     # the keys of a tile are dealt to several SMs: long and short sequences, one without keys, rows up to a whole tile
     nq = [1, 128, 3, 40, 7]
     nk = [6000, 2500, 130, 0, 900]
-    q, k, v, o = run(D, ws, heads + left, nq, nk, heads, kv_heads, hd, BF, left, right, sinks, rows=10)
-    again = lambda: D.op_window_attention(q, k, v, ws, cu_q=cum(nq), cu_k=cum(nk), left=left, right=right, sinks=sinks)  # noqa: E731
+    q, k, v, o = run(D, ws, heads + left, nq, nk, heads, kv_heads, hd, dtype, left, right, sinks, rows=10)
     for _ in range(3):
-        assert torch.equal(again(), o)
+        assert torch.equal(o, D.op_window_attention(q, k, v, ws, cu_q=cum(nq), cu_k=cum(nk), left=left, right=right,
+                                                    sinks=sinks))
     # without a workspace the keys of a tile stay together: another order of the sums
     alone, cq, ck = torch.empty_like(o), cum(nq), cum(nk)
     st = D.lib().dinfer_op_window_attention(
-        q.data_ptr(), k.data_ptr(), v.data_ptr(), alone.data_ptr(), D.BF16, len(nq), cq.data_ptr(), ck.data_ptr(),
-        sum(nq), sum(nk), heads, kv_heads, hd, heads * hd, kv_heads * hd, kv_heads * hd, heads * hd, left, right, sinks,
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), alone.data_ptr(), D.BF16 if dtype == BF else D.FP32, len(nq),
+        cq.data_ptr(), ck.data_ptr(), sum(nq), sum(nk), heads, kv_heads, hd, heads * hd, kv_heads * hd, kv_heads * hd, heads * hd, left, right, sinks,
         hd ** -0.5, None, 0, torch.cuda.current_stream().cuda_stream)
     assert st == D.OK
     torch.cuda.synchronize()
     compare(alone.double().cpu().numpy(), *(t.double().cpu().numpy() for t in (q, k, v)), nq, nk, left, right, sinks,
-            hd ** -0.5, True, 10)
+            hd ** -0.5, dtype == BF, 10)
 
 
 def test_masked_keys_and_infinite_scores_over_many_keys(D, ws):
     rng = np.random.default_rng(25)
-    for hd in (64, 128):
+    for dtype, hd in ((BF, 64), (BF, 128), (F32, 64), (F32, 128)):
         nq, nk = 50, 3000
-        xq, q = values(rng, (nq, 2, hd), BF)
-        xk, k = values(rng, (nk, 1, hd), BF)
-        xv, v = values(rng, (nk, 1, hd), BF)
+        xq, q = values(rng, (nq, 2, hd), dtype)
+        xk, k = values(rng, (nk, 1, hd), dtype)
+        xv, v = values(rng, (nk, 1, hd), dtype)
         v[2990], k[2970] = float("nan"), float("nan")  # seen by rows 40 .., and 20 ..
         o = D.op_window_attention(q, k, v, ws, left=-1, right=0)
         seen = A.window_mask(nq, nk, -1, 0, 0)
         assert torch.isnan(o[20:]).all()
-        A.check(o[:20].double().cpu().numpy(), xq[:20], xk, xv, seen[:20], hd ** -0.5, True)
+        A.check(o[:20].double().cpu().numpy(), xq[:20], xk, xv, seen[:20], hd ** -0.5, dtype == BF)
         k[:] = float("-inf")
         k[1000:1200], v[:] = 1.0, 1.0  # one part alone holds a score above -inf
         o = D.op_window_attention(q.abs(), k, v, ws, left=-1, right=0)
