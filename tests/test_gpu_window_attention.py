@@ -194,6 +194,28 @@ def test_agrees_with_the_block_decoders_attention(D, ws):
         A.check(o.double().cpu().numpy(), xq, xk, xv, seen, 128 ** -0.5, True)
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_offsets_beyond_32_bits(D, ws, dtype):
+    # rows 2^17 elements apart: the last ones lie beyond 2^31 elements
+    rng = np.random.default_rng(26)
+    T, H, hd = 16500, 2, 128
+    t = torch.empty((T, 1 << 17), dtype=dtype, device=dev)
+    q, k, v, o = (t[:, a * hd:b * hd].unflatten(1, (b - a, hd)) for a, b in ((0, 2), (2, 3), (3, 4), (4, 6)))
+    xs = []
+    for x in (q, k, v):
+        host, there = values(rng, x.shape, dtype)
+        x.copy_(there)
+        xs.append(host)
+    D.op_window_attention(q, k, v, ws, left=50, right=0, sinks=2, out=o)
+    torch.cuda.synchronize()
+    ws.check()
+    pick = [0, 1, 128, T // 2, T - 300, T - 2, T - 1]
+    near = [sorted({0, 1, *range(max(0, i - 60), i + 1)}) for i in pick]  # keys 50 back, and some that are not seen
+    for i, keys in zip(pick, near):
+        seen = np.array([[j < 2 or j >= i - 50 for j in keys]])
+        A.check(o[i:i + 1].double().cpu().numpy(), xs[0][i:i + 1], xs[1][keys], xs[2][keys], seen, hd ** -0.5, dtype == BF, i)
+
+
 def test_bad_bounds_give_empty_sequences(D, ws):
     rng = np.random.default_rng(16)
     _, q = values(rng, (100, 1, 64), BF)
@@ -227,8 +249,8 @@ def test_few_rows_over_many_keys(D, ws, dtype, hd, heads, kv_heads, left, right,
     alone, cq, ck = torch.empty_like(o), cum(nq), cum(nk)
     st = D.lib().dinfer_op_window_attention(
         q.data_ptr(), k.data_ptr(), v.data_ptr(), alone.data_ptr(), D.BF16 if dtype == BF else D.FP32, len(nq),
-        cq.data_ptr(), ck.data_ptr(), sum(nq), sum(nk), heads, kv_heads, hd, heads * hd, kv_heads * hd, kv_heads * hd, heads * hd, left, right, sinks,
-        hd ** -0.5, None, 0, torch.cuda.current_stream().cuda_stream)
+        cq.data_ptr(), ck.data_ptr(), sum(nq), sum(nk), heads, kv_heads, hd, heads * hd, kv_heads * hd, kv_heads * hd,
+        heads * hd, left, right, sinks, hd ** -0.5, None, 0, torch.cuda.current_stream().cuda_stream)
     assert st == D.OK
     torch.cuda.synchronize()
     compare(alone.double().cpu().numpy(), *(t.double().cpu().numpy() for t in (q, k, v)), nq, nk, left, right, sinks,
