@@ -212,7 +212,7 @@ def test_offsets_beyond_32_bits(D, ws, dtype):
     pick = [0, 1, 128, T // 2, T - 300, T - 2, T - 1]
     near = [sorted({0, 1, *range(max(0, i - 60), i + 1)}) for i in pick]  # keys 50 back, and some that are not seen
     for i, keys in zip(pick, near):
-        seen = np.array([[j < 2 or j >= i - 50 for j in keys]])
+        seen = np.array([[j <= i and (j < 2 or j >= i - 50) for j in keys]])
         A.check(o[i:i + 1].double().cpu().numpy(), xs[0][i:i + 1], xs[1][keys], xs[2][keys], seen, hd ** -0.5, dtype == BF, i)
 
 
