@@ -297,36 +297,35 @@ def _require(ok, what: str):
         raise ValueError(what)
 
 
-def _rows_of(t: torch.Tensor, name: str, heads: Optional[int], head_dim: int, like: torch.Tensor):
-    """Checks [rows, heads, head_dim] with packed head rows, of like's type and device; returns the row stride."""
+def _rows_of(t: torch.Tensor, name: str, heads: Optional[int], head_dim: int, dtype, gpu: int):
+    """Checks [rows, heads, head_dim] with packed head rows; returns rows, heads and the row stride."""
     shape, s = t.shape, t.stride()
-    if (len(shape) == 3 and shape[2] == head_dim and (heads is None or shape[1] == heads) and t.dtype is like.dtype
-            and t.get_device() == like.get_device() and s[2] == 1 and (s[1] == head_dim or shape[1] == 1)):
-        return s[0]
-    raise ValueError(f"{name}: [rows, {'heads' if heads is None else heads}, {head_dim}] {like.dtype} on {like.device} with "
+    if (len(shape) == 3 and shape[2] == head_dim and (heads is None or shape[1] == heads) and t.dtype is dtype
+            and t.get_device() == gpu and s[2] == 1 and (s[1] == head_dim or shape[1] == 1)):
+        return shape[0], shape[1], s[0]
+    raise ValueError(f"{name}: [rows, {'heads' if heads is None else heads}, {head_dim}] {dtype} on cuda:{gpu} with "
                      f"the heads of a row packed expected, got {list(shape)} {t.dtype} on {t.device} with strides {s}")
 
 
-def _ints(t: Optional[torch.Tensor], name: str, device, n: Optional[int] = None):
-    """Address of a contiguous int32 vector on device (None: NULL)."""
+def _ints(t: Optional[torch.Tensor], name: str, gpu: int, n: Optional[int] = None):
+    """Address of a contiguous int32 vector on the GPU (None: NULL)."""
     if t is None:
         return None
     shape = t.shape
-    if (t.dtype is torch.int32 and len(shape) == 1 and t.get_device() == device.index and t.is_contiguous()
+    if (t.dtype is torch.int32 and len(shape) == 1 and t.get_device() == gpu and t.is_contiguous()
             and (n is None or shape[0] == n)):
         return t.data_ptr()
-    raise ValueError(f"{name}: a contiguous int32 vector {'' if n is None else f'of {n} '}on {device} expected, got "
+    raise ValueError(f"{name}: a contiguous int32 vector {'' if n is None else f'of {n} '}on cuda:{gpu} expected, got "
                      f"{list(t.shape)} {t.dtype} on {t.device}")
 
 
-def _run_on(device, fn, *args):
-    """One library call on torch's current stream of the operands' device, which becomes the current one for it."""
-    i = device.index
-    if i == torch._C._cuda_getDevice():
-        st = fn(*args, torch._C._cuda_getCurrentRawStream(i))
+def _run_on(gpu: int, fn, *args):
+    """One library call on torch's current stream of the operands' GPU, which becomes the current one for it."""
+    if gpu == torch._C._cuda_getDevice():
+        st = fn(*args, torch._C._cuda_getCurrentRawStream(gpu))
     else:
-        with torch.cuda.device(i):
-            st = fn(*args, torch._C._cuda_getCurrentRawStream(i))
+        with torch.cuda.device(gpu):
+            st = fn(*args, torch._C._cuda_getCurrentRawStream(gpu))
     if st != OK:
         _check(st)
 
@@ -348,10 +347,11 @@ class PagedKV:
                  f"table: contiguous int32 [max_seqs, max_pages] on {dev} expected")
         self.max_seqs, self.max_pages = table.shape
         layers, pages, page, heads, hd = k.shape
-        lens_p, refs_p = _ints(lens, "lens", dev, self.max_seqs), _ints(refs, "refs", dev, pages)
+        gpu = k.get_device()
+        lens_p, refs_p = _ints(lens, "lens", gpu, self.max_seqs), _ints(refs, "refs", gpu, pages)
         L = lib()
         self.k, self.v, self.table, self.lens, self.refs = k, v, table, lens, refs
-        self.device, self.kv_heads, self.head_dim = dev, heads, hd
+        self.device, self.gpu, self.dtype, self.kv_heads, self.head_dim = dev, gpu, k.dtype, heads, hd
         self.state = torch.zeros(L.dinfer_kv_state_ints(pages, self.max_seqs), dtype=torch.int32, device=dev)
         st = k.stride()
         self.desc = KvCache(k.data_ptr(), v.data_ptr(), st[0], st[1], st[2], st[3], table.data_ptr(), lens_p, refs_p,
@@ -381,57 +381,55 @@ class PagedKV:
         """Sequences seqs (default: the first ones, one per entry of add; all) grow by add tokens (default: one each)."""
         n = seqs.shape[0] if seqs is not None else add.shape[0] if add is not None else self.max_seqs
         _require(seqs is not None or n <= self.max_seqs, "add: more entries than sequences")
-        dev = self.device
-        _run_on(dev, lib().dinfer_kv_extend, self._desc, _ints(seqs, "seqs", dev), _ints(add, "add", dev, n), n)
+        gpu = self.gpu
+        _run_on(gpu, lib().dinfer_kv_extend, self._desc, _ints(seqs, "seqs", gpu), _ints(add, "add", gpu, n), n)
 
     def append(self, layer: int, k: torch.Tensor, v: torch.Tensor, rows: Optional[torch.Tensor] = None,
                seqs: Optional[torch.Tensor] = None):
         """Stores the last rows of each sequence: k, v [rows, kv_heads, head_dim]; rows [n + 1] the entries'
         first rows (default: one row per sequence)."""
-        ks = _rows_of(k, "k", self.kv_heads, self.head_dim, self.k)
-        vs = _rows_of(v, "v", self.kv_heads, self.head_dim, self.k)
-        _require(k.shape[0] == v.shape[0], "k, v: as many rows expected")
-        n = rows.shape[0] - 1 if rows is not None else k.shape[0]
+        gpu = self.gpu
+        total, _, ks = _rows_of(k, "k", self.kv_heads, self.head_dim, self.dtype, gpu)
+        also, _, vs = _rows_of(v, "v", self.kv_heads, self.head_dim, self.dtype, gpu)
+        _require(total == also, "k, v: as many rows expected")
+        n = rows.shape[0] - 1 if rows is not None else total
         _require(seqs is not None or n <= self.max_seqs, "more entries than sequences")
-        dev = self.device
-        _run_on(dev, lib().dinfer_kv_append, self._desc, layer, _ints(seqs, "seqs", dev, n), _ints(rows, "rows", dev), n,
-                k.data_ptr(), v.data_ptr(), ks, vs, k.shape[0])
+        _run_on(gpu, lib().dinfer_kv_append, self._desc, layer, _ints(seqs, "seqs", gpu, n), _ints(rows, "rows", gpu), n,
+                k.data_ptr(), v.data_ptr(), ks, vs, total)
 
     def fork(self, src: torch.Tensor, dst: torch.Tensor, share: bool = True):
         """Sequences dst (not in use) become copies of src, sharing the full pages or copying all of them."""
         n = src.shape[0]
-        dev = self.device
-        _run_on(dev, lib().dinfer_kv_fork, self._desc, _ints(src, "src", dev), _ints(dst, "dst", dev, n), n, int(share))
+        gpu = self.gpu
+        _run_on(gpu, lib().dinfer_kv_fork, self._desc, _ints(src, "src", gpu), _ints(dst, "dst", gpu, n), n, int(share))
 
     def free(self, seqs: torch.Tensor):
-        _run_on(self.device, lib().dinfer_kv_free, self._desc, _ints(seqs, "seqs", self.device), seqs.shape[0])
+        _run_on(self.gpu, lib().dinfer_kv_free, self._desc, _ints(seqs, "seqs", self.gpu), seqs.shape[0])
 
     def compact(self, live: Optional[torch.Tensor] = None):
         """Packs the pages in use to the front; live (optional, int32 [1]) receives how many there are."""
-        _run_on(self.device, lib().dinfer_kv_compact, self._desc, _ints(live, "live", self.device, 1))
+        _run_on(self.gpu, lib().dinfer_kv_compact, self._desc, _ints(live, "live", self.gpu, 1))
 
     def attention(self, layer: int, q: torch.Tensor, ws: OpWorkspace, window: int = -1, sinks: int = 0,
                   scale: Optional[float] = None, seqs: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None):
         """Attention of each sequence's last token: q [n, heads, head_dim] -> [n, heads, head_dim] (out may be q)."""
-        hd = self.head_dim
-        qs = _rows_of(q, "q", None, hd, self.k)
-        n, heads, _ = q.shape
+        hd, dtype, gpu = self.head_dim, self.dtype, self.gpu
+        n, heads, qs = _rows_of(q, "q", None, hd, dtype, gpu)
         _require(seqs is not None or n <= self.max_seqs, "q: more rows than sequences")
-        _require(ws.buf.get_device() == self.device.index, "ws: a workspace on the cache's device expected")
+        _require(ws.buf.get_device() == gpu, "ws: a workspace on the cache's device expected")
         if out is None:
             out, os_ = torch.empty_like(q, memory_format=torch.contiguous_format), heads * hd
         else:
-            os_ = _rows_of(out, "out", heads, hd, self.k)
-            _require(out.shape[0] == n, "out: as many rows as q expected")
-        dev = self.device
-        _run_on(dev, lib().dinfer_kv_attention, self._desc, layer, _ints(seqs, "seqs", dev, n), n, q.data_ptr(),
+            also, _, os_ = _rows_of(out, "out", heads, hd, dtype, gpu)
+            _require(also == n, "out: as many rows as q expected")
+        _run_on(gpu, lib().dinfer_kv_attention, self._desc, layer, _ints(seqs, "seqs", gpu, n), n, q.data_ptr(),
                 out.data_ptr(), qs, os_, heads, window, sinks, hd ** -0.5 if scale is None else scale,
                 ws.buf.data_ptr(), ws.nbytes)
         return out
 
     def check(self):
         """Raise if an entry of an earlier call was skipped (DinferError names why); clears the status."""
-        _run_on(self.device, lib().dinfer_kv_status, self._desc, None)
+        _run_on(self.gpu, lib().dinfer_kv_status, self._desc, None)
 
 
 def op_window_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, ws: OpWorkspace,
@@ -440,22 +438,22 @@ def op_window_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, ws: O
                         out: Optional[torch.Tensor] = None):
     """Attention with a sliding window and sinks: q [rows, heads, head_dim], k, v [keys, kv_heads, head_dim];
     cu_q, cu_k [batch + 1] the sequences' first rows and keys (default: one sequence of all)."""
-    _require(q.dim() == 3 and q.dtype in _DTYPES and q.is_cuda, "q: float32 or bfloat16 [rows, heads, head_dim] on a GPU expected")
-    rows, heads, hd = q.shape
-    qs = _rows_of(q, "q", None, hd, q)
-    ks = _rows_of(k, "k", None, hd, q)
-    vs = _rows_of(v, "v", k.shape[1], hd, q)
-    _require(k.shape[0] == v.shape[0], "k, v: as many keys expected")
-    dev = q.device
+    dtype, gpu = q.dtype, q.get_device()
+    _require(dtype in _DTYPES and q.is_cuda and q.dim() == 3, "q: float32 or bfloat16 [rows, heads, head_dim] on a GPU expected")
+    hd = q.shape[2]
+    rows, heads, qs = _rows_of(q, "q", None, hd, dtype, gpu)
+    keys, kv_heads, ks = _rows_of(k, "k", None, hd, dtype, gpu)
+    also, _, vs = _rows_of(v, "v", kv_heads, hd, dtype, gpu)
+    _require(keys == also, "k, v: as many keys expected")
     batch = 1 if cu_q is None else cu_q.shape[0] - 1
-    cq, ck = _ints(cu_q, "cu_q", dev), _ints(cu_k, "cu_k", dev, None if cu_q is None else batch + 1)
-    _require(ws.buf.get_device() == dev.index, "ws: a workspace on the operands' device expected")
+    cq, ck = _ints(cu_q, "cu_q", gpu), _ints(cu_k, "cu_k", gpu, None if cu_q is None else batch + 1)
+    _require(ws.buf.get_device() == gpu, "ws: a workspace on the operands' device expected")
     if out is None:
         out, os_ = torch.empty_like(q, memory_format=torch.contiguous_format), heads * hd
     else:
-        os_ = _rows_of(out, "out", heads, hd, q)
-        _require(out.shape[0] == rows, "out: as many rows as q expected")
-    _run_on(dev, lib().dinfer_op_window_attention, q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), _DTYPES[q.dtype],
-            batch, cq, ck, rows, k.shape[0], heads, k.shape[1], hd, qs, ks, vs, os_, left, right, sinks,
+        also, _, os_ = _rows_of(out, "out", heads, hd, dtype, gpu)
+        _require(also == rows, "out: as many rows as q expected")
+    _run_on(gpu, lib().dinfer_op_window_attention, q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), _DTYPES[dtype],
+            batch, cq, ck, rows, keys, heads, kv_heads, hd, qs, ks, vs, os_, left, right, sinks,
             hd ** -0.5 if scale is None else scale, ws.buf.data_ptr(), ws.nbytes)
     return out

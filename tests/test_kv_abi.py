@@ -119,16 +119,16 @@ def test_binding_refuses_what_the_library_cannot_see(L):
     q = torch.zeros(4, 2, 64)
     with pytest.raises(ValueError):
         dinfer.op_window_attention(q, q, q, None)
-    like = torch.zeros(1)
+    cpu = torch.zeros(1).get_device()
     for t in (torch.zeros(4, 128), torch.zeros(4, 2, 32), torch.zeros(4, 3, 64), torch.zeros(4, 2, 64, dtype=torch.float64),
               torch.zeros(4, 64, 2).transpose(1, 2), torch.zeros(2, 4, 64).transpose(0, 1)):
         with pytest.raises(ValueError):
-            dinfer._rows_of(t, "t", 2, 64, like)
-    assert dinfer._rows_of(torch.zeros(4, 6, 64)[:, :2], "t", 2, 64, like) == 384
+            dinfer._rows_of(t, "t", 2, 64, torch.float32, cpu)
+    assert dinfer._rows_of(torch.zeros(4, 6, 64)[:, :2], "t", 2, 64, torch.float32, cpu) == (4, 2, 384)
     for t in (torch.zeros(3), torch.zeros(3, dtype=torch.int64), torch.zeros((2, 2), dtype=torch.int32),
               torch.zeros(6, dtype=torch.int32)[::2]):
         with pytest.raises(ValueError):
-            dinfer._ints(t, "t", torch.device("cpu"))
+            dinfer._ints(t, "t", cpu)
 
 
 def test_the_test_helpers_themselves():
