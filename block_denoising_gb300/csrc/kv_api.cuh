@@ -196,6 +196,20 @@ dinfer_status dinfer_kv_status(const dinfer_kv_cache* kc, uint32_t* bits, void* 
               word & KV_SHARED ? " rows for a shared page" : "", word & KV_FULL ? " sequence too long" : "");
 }
 
+dinfer_status dinfer_kv_set(const dinfer_kv_cache* kc, const int32_t* table, const int32_t* lens, const int32_t* refs,
+                            void* stream) {
+  dinfer_ctx* c = nullptr;
+  if (const char* why = kv_bad(kc)) return fail(c, DINFER_EINVAL, "%s", why);
+  if (!table || !lens || !refs) return fail(c, DINFER_EINVAL, "NULL operand");
+  if ((reinterpret_cast<uintptr_t>(table) | reinterpret_cast<uintptr_t>(lens) | reinterpret_cast<uintptr_t>(refs)) & 3)
+    return fail(c, DINFER_EINVAL, "misaligned table, lens or refs");
+  const int64_t most = std::max<int64_t>((int64_t)kc->max_seqs * kc->max_pages, kc->num_pages);
+  const int grid = (int)std::min<int64_t>((most + 255) / 256, (int64_t)num_sms() * 8);
+  CK(launchk(kv_set_kernel, dim3(grid), dim3(256), 0, reinterpret_cast<cudaStream_t>(stream), 1, kv_pages(*kc), table,
+             lens, refs));
+  return DINFER_OK;
+}
+
 dinfer_status dinfer_kv_extend(const dinfer_kv_cache* kc, const int32_t* seqs, const int32_t* add, int32_t n,
                                void* stream) {
   dinfer_ctx* c = nullptr;

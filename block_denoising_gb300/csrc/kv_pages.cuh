@@ -162,6 +162,25 @@ __device__ __forceinline__ int kv_entry_of(const int* prefix, int n, int r) {
 }
 
 // --------------------------------------------------------------------------
+// set: another set of tables, one launch over the GPU (bound by the launch: three
+// copies and the state's zeroing as calls of their own took 8 us more)
+// --------------------------------------------------------------------------
+__global__ void __launch_bounds__(256) kv_set_kernel(const KvPages c, const int32_t* table, const int32_t* lens,
+                                                      const int32_t* refs) {
+  pdl_wait();
+  pdl_trigger();
+  const int64_t tid = (int64_t)blockIdx.x * blockDim.x + threadIdx.x, step = (int64_t)gridDim.x * blockDim.x;
+  const int64_t entries = (int64_t)c.max_seqs * c.max_pages;
+  for (int64_t e = tid; e < entries; e += step) c.table[e] = table[e];
+  for (int64_t e = tid; e < c.num_pages; e += step) c.refs[e] = refs[e];
+  for (int64_t e = tid; e < c.max_seqs; e += step) {
+    c.lens[e] = lens[e];
+    c.owner()[e] = 0;
+  }
+  if (tid < kKvHead) c.state[tid] = 0;
+}
+
+// --------------------------------------------------------------------------
 // extend: one CTA
 // --------------------------------------------------------------------------
 __global__ void __launch_bounds__(kKvPlanThreads) kv_extend_kernel(const KvPages c, const int32_t* seqs,

@@ -101,6 +101,8 @@ def lib() -> ctypes.CDLL:
     L.dinfer_kv_state_ints.restype = sz
     L.dinfer_kv_status.argtypes = [vp, ctypes.POINTER(ctypes.c_uint32), vp]
     L.dinfer_kv_status.restype = i32
+    L.dinfer_kv_set.argtypes = [vp, vp, vp, vp, vp]
+    L.dinfer_kv_set.restype = i32
     L.dinfer_kv_extend.argtypes = [vp, vp, vp, i32, vp]
     L.dinfer_kv_extend.restype = i32
     L.dinfer_kv_append.argtypes = [vp, i32, vp, vp, i32, vp, vp, i64, i64, i32, vp]
@@ -372,10 +374,9 @@ class PagedKV:
         """Takes over another set of tables of the same sizes (a snapshot, a scheduler's own plan)."""
         _require(table.shape == self.table.shape and lens.shape == self.lens.shape and refs.shape == self.refs.shape,
                  "table, lens, refs: the cache's sizes expected")
-        self.table.copy_(table)
-        self.lens.copy_(lens)
-        self.refs.copy_(refs)
-        self.state.zero_()
+        at = [t if t.dtype is torch.int32 and t.get_device() == self.gpu and t.is_contiguous()
+              else t.to(self.device, torch.int32).contiguous() for t in (table, lens, refs)]
+        _run_on(self.gpu, lib().dinfer_kv_set, self._desc, at[0].data_ptr(), at[1].data_ptr(), at[2].data_ptr())
 
     def extend(self, add: Optional[torch.Tensor] = None, seqs: Optional[torch.Tensor] = None):
         """Sequences seqs (default: the first ones, one per entry of add; all) grow by add tokens (default: one each)."""

@@ -46,7 +46,7 @@ extern "C" {
  *   lens  [max_seqs]             tokens of each sequence (0: not in use); it holds ceil(len / page_size) pages
  *   refs  [num_pages]            how many sequences hold each page (0: free)
  *   state [dinfer_kv_state_ints] the library's: zero it before the first call and
- *                                whenever table, lens or refs are written by hand
+ *                                whenever table, lens or refs are written by hand (not by dinfer_kv_set)
  * An empty cache is table all -1, the others all 0. */
 typedef struct dinfer_kv_cache {
   void* k;
@@ -76,6 +76,11 @@ enum {
  * and clears it.  DINFER_EDEVICE if any bit was set (dinfer_last_error names
  * them), else DINFER_OK. */
 dinfer_status dinfer_kv_status(const dinfer_kv_cache* cache, uint32_t* bits, void* stream);
+
+/* Takes over another set of tables of the cache's sizes (a snapshot, a plan
+ * made elsewhere), and clears the state and its status. */
+dinfer_status dinfer_kv_set(const dinfer_kv_cache* cache, const int32_t* table, const int32_t* lens,
+                            const int32_t* refs, void* stream);
 
 /* Sequence seqs[i] (NULL: i) grows by add[i] >= 0 tokens (NULL: one each):
  * its len rises and the pages this takes are handed out, lowest free page

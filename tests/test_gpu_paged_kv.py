@@ -150,6 +150,29 @@ def test_skipped_entries_are_flagged_and_left_alone(D):
     assert torch.equal(before, cache.k)
 
 
+def test_another_set_of_tables(D):
+    rng = np.random.default_rng(27)
+    cache, model = make(D, rng, 1, 4000, 4, 1, 64, 300, 50)
+    add = [int(x) for x in rng.integers(0, 60, 200)]
+    cache.extend(ints(add))
+    model.extend(range(200), add)
+    old = [t.clone() for t in (cache.table, cache.lens, cache.refs)]
+    cache.extend(ints([7, 7]), ints([250, 250]))
+    cache.free(ints([0, 3, 900]))
+    for form in (lambda t: t, lambda t: t.cpu(), lambda t: t.long(), lambda t: torch.stack([t, t], -1)[..., 0]):
+        cache.set_tables(*(form(t) for t in old))
+        assert status(D, cache) == 0
+        same(cache, model)
+        cache.extend(ints([3, 70]), ints([250, 1]))
+        cache.free(ints([2, -1]))
+    cache.set_tables(*old)
+    cache.extend(ints([5, 9]), ints([250, 299]))
+    model.extend([250, 299], [5, 9])
+    same(cache, model)
+    with pytest.raises(ValueError):
+        cache.set_tables(old[0][:5], old[1], old[2])
+
+
 def test_append_one_row_each_and_strided_rows(D):
     rng = np.random.default_rng(6)
     for page, heads, hd, dtype in ((16, 4, 128, torch.bfloat16), (5, 3, 64, torch.float32)):

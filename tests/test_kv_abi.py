@@ -33,6 +33,7 @@ def calls(L, kc, p=P):
     """Every entry point with otherwise good arguments."""
     c = ctypes.byref(kc) if kc is not None else None
     yield "extend", lambda: L.dinfer_kv_extend(c, None, None, 4, None)
+    yield "set", lambda: L.dinfer_kv_set(c, p, p, p, None)
     yield "append", lambda: L.dinfer_kv_append(c, 0, None, None, 4, p, p, 1024, 1024, 4, None)
     yield "fork", lambda: L.dinfer_kv_fork(c, p, p, 1, 1, None)
     yield "free", lambda: L.dinfer_kv_free(c, p, 1, None)
@@ -59,7 +60,7 @@ def test_null_cache_and_operands_are_refused(L):
     for name, call in calls(L, None):
         assert call() == dinfer.EINVAL, name
     for name, call in calls(L, cache(), None):
-        if name in ("append", "fork", "free", "attention"):
+        if name in ("set", "append", "fork", "free", "attention"):
             assert call() == dinfer.EINVAL, name
 
 
@@ -84,6 +85,11 @@ def test_bad_call_arguments_are_refused(L):
         assert L.dinfer_kv_extend(c, None, None, n, None) == dinfer.EINVAL
         assert L.dinfer_kv_fork(c, P, P, n, 0, None) == dinfer.EINVAL
     assert L.dinfer_kv_free(c, P, 0, None) == dinfer.EINVAL
+    for i in (1, 2, 3):
+        for bad in (None, P + 2):
+            a = [c, P, P, P, None]
+            a[i] = bad
+            assert L.dinfer_kv_set(*a) == dinfer.EINVAL
     # more units of keys than an int counts
     big = cache(max_pages=(1 << 27) - 1, max_seqs=1024)
     assert L.dinfer_kv_attention(ctypes.byref(big), 0, None, 1024, P, P, 4096, 4096, 32, -1, 0, 0.1, P, 1 << 30,
