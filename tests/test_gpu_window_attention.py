@@ -149,6 +149,20 @@ def test_what_masked_keys_hold_does_not_matter(D, ws, dtype, hd, heads):
     assert torch.isnan(o[:250]).all() and torch.isfinite(o[250:350]).all()
 
 
+def test_output_rows_that_begin_at_16_bytes(D, ws):
+    rng = np.random.default_rng(28)
+    for heads, hd in ((2, 64), (40, 128)):
+        xq, q = values(rng, (500, heads, hd), BF)
+        xk, k = values(rng, (500, 1, hd), BF)
+        want = D.op_window_attention(q, k, k, ws, left=70, right=0, sinks=2)
+        for pad, at in ((8, 0), (16, 8), (8, 8)):
+            t = torch.full((500, heads * hd + pad), 7.0, dtype=BF, device=dev)
+            o = t[:, at:at + heads * hd].unflatten(1, (heads, hd))
+            D.op_window_attention(q, k, k, ws, left=70, right=0, sinks=2, out=o)
+            assert torch.equal(o, want)
+            assert (t[:, :at] == 7).all() and (t[:, at + heads * hd:] == 7).all()
+
+
 def test_infinite_scores(D, ws):
     for dtype, heads in ((BF, 1), (BF, 160), (F32, 1)):
         q = torch.ones(200, heads, 64, dtype=dtype, device=dev)
