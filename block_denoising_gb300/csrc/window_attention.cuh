@@ -204,7 +204,9 @@ __device__ __noinline__ void wa_row_exact(const WaArgs& a, const WaSeq s, int i,
 // 64: 30 us, 188 without).
 constexpr int kWfKeys = 32;
 constexpr int kWfE = 4;  // rows of a thread
-constexpr int kWfPartTiles = 8;  // key tiles of a part at least
+// key tiles of a part at least (4 heads of 64, one row over 600 keys, and over 4001:
+// with 3 11.3 and 19.2 us, 2 10.9 and 21.9, 4 12.1 and 18.0, 8 19.2 and 20.2)
+constexpr int kWfPartTiles = 3;
 template <int HD, int kTy>
 struct WfCfg {
   static constexpr int kThreads = 16 * kTy;
@@ -246,7 +248,7 @@ __global__ void __launch_bounds__(16 * kTy, kTy == 16 ? 2 : 4) window_f32_kernel
   int front = min(a.sinks, min(top.lo, bottom.hi + 1)), end = bottom.hi + 1;
   int begin = max((front + kWfKeys - 1) / kWfKeys, top.lo / kWfKeys) * kWfKeys;  // the window's tiles
   int parts = 1, part = 0;
-  if constexpr (kSplit) {  // eight tiles a part at least; the sinks go to the first part
+  if constexpr (kSplit) {  // the sinks go to the first part
     const int w = max(0, (end - begin + kWfKeys - 1) / kWfKeys);
     parts = max(1, min(a.splits, w / kWfPartTiles));
     part = blockIdx.x % a.splits;

@@ -69,7 +69,7 @@ constexpr int kWtRows = 128;  // rows of a tile
 constexpr int kWtKeys = 128;  // keys of a tile
 // the tiles of a piece: two heads' rows, 256 rows of a head, one tile alone
 enum WtForm { kWtPairHeads, kWtPairRows, kWtSingle };
-constexpr int kWtPartTiles = 3;  // key tiles of a part at least
+constexpr int kWtPartTiles = 2;  // key tiles of a part at least
 
 template <int HD>
 struct WtCfg {
@@ -416,9 +416,11 @@ __global__ void __launch_bounds__(kWtThreads, 1)
           p.first = max(p.front, lo / kWtKeys);
           p.n = p.front + (hi < 0 ? 0 : max(0, hi / kWtKeys - p.first + 1));
           if constexpr (kSplit) {
-            // a part has at least three key tiles, and one more for every 16 rows to be
-            // joined (some 1 us each); the sinks go to the first part
-            const int w = p.n - p.front, parts = max(1, min(splits, w / (kWtPartTiles + p.band[0].rows / 16)));
+            // a part has at least two key tiles, and one more for every 32 rows to be
+            // joined (128 rows over 3000 keys, 8 heads of 128: 25.8 us; one more for every
+            // 16 rows 30.2, none 31.8; 64 rows over 1500 keys: 16.7, 18.2, 20.6); the sinks
+            // go to the first part
+            const int w = p.n - p.front, parts = max(1, min(splits, w / (kWtPartTiles + p.band[0].rows / 32)));
             p.unit = at / splits;
             p.part = at % splits;
             if (p.part >= parts) {  // too few keys for another part
