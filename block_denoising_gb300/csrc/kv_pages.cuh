@@ -63,28 +63,29 @@ struct KvPages {
 };
 
 // Exclusive sum of v over the CTA's 1024 threads; *total receives the sum.
-__device__ __forceinline__ int kv_block_scan(int v, int* total) {
-  __shared__ int warp_sums[32];
+template <typename N>
+__device__ __forceinline__ N kv_block_scan(N v, N* total) {
+  __shared__ N warp_sums[32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int inc = v;
+  N inc = v;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int u = __shfl_up_sync(0xffffffffu, inc, o);
+    const N u = __shfl_up_sync(0xffffffffu, inc, o);
     if (lane >= o) inc += u;
   }
   if (lane == 31) warp_sums[warp] = inc;
   __syncthreads();
   if (warp == 0) {
-    int w = warp_sums[lane];
+    N w = warp_sums[lane];
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int u = __shfl_up_sync(0xffffffffu, w, o);
+      const N u = __shfl_up_sync(0xffffffffu, w, o);
       if (lane >= o) w += u;
     }
     warp_sums[lane] = w;
   }
   __syncthreads();
-  const int before = warp ? warp_sums[warp - 1] : 0;
+  const N before = warp ? warp_sums[warp - 1] : 0;
   *total = warp_sums[31];
   __syncthreads();  // the sums are read before the next scan writes them
   return before + inc - v;
@@ -102,7 +103,7 @@ __device__ int kv_list_pages(const KvPages& c, int begin, int end, int want, int
     for (int k = 0; k < kKvScanItems; ++k)
       if (i0 + k < end) hit |= (uint32_t)((__ldcg(c.refs + i0 + k) > 0) == kUsed) << k;
     int total;
-    int r = found + kv_block_scan(__popc(hit), &total);
+    int r = found + kv_block_scan<int>(__popc(hit), &total);
     while (hit && r < want) {
       out[r++] = i0 + __ffs(hit) - 1;
       hit &= hit - 1;
@@ -125,23 +126,31 @@ __device__ __forceinline__ bool kv_first_mention(const KvPages& c, int s) {
   return first;
 }
 
+// A call's running sums of wanted pages take 41 bits (1024 entries of up to 2^31 - 1
+// pages).  Whether the `found` free pages reach the entry that wants `need` of them
+// behind `before` others:
+__host__ __device__ __forceinline__ bool kv_reaches(long long before, int need, int found) { return before + need <= found; }
+// and a running sum as a place in the list of pages, which ends long before 2^31 - 1.
+__host__ __device__ __forceinline__ int kv_place(long long before) { return (int)(before < 0x7fffffffll ? before : 0x7fffffffll); }
+
 // Hands out need pages to every entry (thread i: entry i), entries in order,
 // lowest free page first: the list of pages is left in c.dst().  Returns this
 // entry's first index into the list, or -1 if the free pages do not reach it;
 // *used receives how many pages were handed out.  prefix [1025] holds the
-// exclusive sums of need afterwards.
+// exclusive sums of need afterwards, those behind the list's end cut off at 2^31 - 1.
 __device__ __forceinline__ int kv_hand_out(const KvPages& c, int need, int* prefix, int* used) {
   __shared__ int served;
-  int want;
-  const int at = kv_block_scan(need, &want);
+  long long want;
+  const long long before = kv_block_scan<long long>(need, &want);
+  const int at = kv_place(before);
   prefix[threadIdx.x] = at;
   if (threadIdx.x == 0) {
-    prefix[kKvPlanThreads] = want;
+    prefix[kKvPlanThreads] = kv_place(want);
     served = 0;
   }
   const int hint = max(0, min(c.num_pages, __ldcg(c.state + 1)));
-  const int found = kv_list_pages<false>(c, hint, c.num_pages, want, c.dst());
-  const bool ok = at + need <= found;
+  const int found = kv_list_pages<false>(c, hint, c.num_pages, kv_place(want), c.dst());
+  const bool ok = kv_reaches(before, need, found);
   if (need > 0 && ok) atomicMax(&served, at + need);  // sums grow with the entry: a prefix of the entries is served
   if (need > 0 && !ok) c.flag(KV_NO_PAGES);
   __syncthreads();
@@ -291,7 +300,7 @@ __global__ void __launch_bounds__(kKvPlanThreads) kv_compact_plan_kernel(const K
     for (int k = 0; k < 4; ++k)
       if (at + k < c.num_pages) live += __ldcg(c.refs + at + k) > 0;
   int total;
-  kv_block_scan(live, &total);
+  kv_block_scan<int>(live, &total);
   live = total;
   // as many free pages below `live` as used ones at or above it
   const int moves = kv_list_pages<false>(c, 0, live, live, c.dst());

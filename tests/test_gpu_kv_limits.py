@@ -1,0 +1,52 @@
+"""The paged KV cache and windowed attention at the ends of their ranges: sums beyond 2^31, very long pieces of work,
+values near the type's largest and weights near its smallest."""
+import numpy as np
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+dev = torch.device("cuda:0")
+
+
+@pytest.fixture(scope="module")
+def D():
+    from block_denoising_gb300 import build, dinfer
+    build.build()
+    return dinfer
+
+
+@pytest.fixture(scope="module")
+def ws(D):
+    return D.OpWorkspace()
+
+
+def ints(v):
+    return torch.tensor(v, dtype=torch.int32, device=dev)
+
+
+def status(D, cache):
+    try:
+        cache.check()
+    except D.DinferError as e:
+        assert e.status == D.EDEVICE
+        return int(str(e).split("status 0x")[1].split(":")[0], 16)
+    return 0
+
+
+@pytest.mark.parametrize("most,add", [(1 << 21, [5] + [1 << 21] * 1022 + [0]), (1 << 30, [5] + [1 << 30] * 4 + [3, 2])])
+def test_wants_that_add_up_beyond_32_bits(D, most, add):
+    # the first entry alone finds pages; the sums of the others pass 2^31, and 2^32 back to small numbers
+    n = len(add)
+    cache = D.PagedKV.empty(layers=1, pages=64, page_size=1, kv_heads=1, head_dim=64, max_seqs=n, max_pages=most)
+    cache.extend(ints(add))
+    assert status(D, cache) == D.KV_NO_PAGES
+    assert cache.lens.tolist() == [5] + [0] * (n - 1)
+    assert cache.refs.tolist() == [1] * 5 + [0] * 59
+    assert cache.table[0, :6].tolist() == [0, 1, 2, 3, 4, -1]
+    assert int((cache.table[0] >= 0).sum()) == 5 and not any(int(cache.table[s].max()) >= 0 for s in range(1, n))
+    # forks of one long sequence likewise (its row names no pages behind the fifth; nobody is served, nothing is read)
+    cache.lens[0] = most
+    cache.state.zero_()
+    cache.fork(ints([0] * (n - 1)), ints(range(1, n)), share=False)
+    assert status(D, cache) == D.KV_NO_PAGES
+    assert cache.lens.tolist() == [most] + [0] * (n - 1) and int(cache.refs.sum()) == 5
