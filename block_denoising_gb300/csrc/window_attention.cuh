@@ -121,6 +121,12 @@ __device__ __forceinline__ float wa_f32(T x) {
   if constexpr (sizeof(T) == 2) return __bfloat162float(x); else return x;
 }
 
+// Key tile at which part `part` of `parts` of w key tiles begins, floor(part w / parts):
+// the product itself would pass 2^31 from 2.3e8 keys on (7.1 million tiles of 32 keys in 304 parts).
+__host__ __device__ __forceinline__ int wa_part_begin(int w, int part, int parts) {
+  return part * (w / parts) + part * (w % parts) / parts;
+}
+
 // One row by the definition, one key after the other, by a warp; a lane owns
 // HD / 32 dimensions.  Only keys that the row sees are read, so nothing a
 // masked key holds can reach the result.  The tile kernels multiply masked
@@ -257,8 +263,8 @@ __global__ void __launch_bounds__(16 * kTy, kTy == 16 ? 2 : 4) window_f32_kernel
       return;
     }
     if (part > 0) front = 0;
-    end = min(end, begin + (part + 1) * w / parts * kWfKeys);
-    begin += part * w / parts * kWfKeys;
+    end = min(end, begin + wa_part_begin(w, part + 1, parts) * kWfKeys);
+    begin += wa_part_begin(w, part, parts) * kWfKeys;
   }
   auto load = [&](int j0, int buf) {  // keys behind the sequence's end: zeros
     float* ks = wf_sm + Cfg::kOffKv + buf * Cfg::kStage;

@@ -427,7 +427,7 @@ __global__ void __launch_bounds__(kWtThreads, 1)
               p.n = 0;
               p.band[0].rows = 0;
             } else {
-              const int w0 = p.part * w / parts, w1 = (p.part + 1) * w / parts;
+              const int w0 = wa_part_begin(w, p.part, parts), w1 = wa_part_begin(w, p.part + 1, parts);
               if (p.part > 0) p.front = 0;
               p.first += w0;
               p.n = p.front + w1 - w0;

@@ -2,7 +2,10 @@
 // arithmetic: the library's own __host__ __device__ helpers, compiled by nvcc
 // and run on the CPU (no GPU is touched).  Run by tests/test_kv_index_checks.py.
 //   * the pages of a call's entries: running sums beyond 2^31 serve nobody
-//     twice and leave the search for a page's entry in order.
+//     twice and leave the search for a page's entry in order;
+//   * the parts of a tile's keys: they follow one another from the first key
+//     tile to the last, each as long as the others but for one tile, up to 2^30
+//     keys in tiles of 32 and as many parts as there are CTAs at once.
 #include <cstdio>
 #include <vector>
 
@@ -37,6 +40,18 @@ static void pages_of_a_call(const std::vector<int>& needs, int found) {
   }
 }
 
+static void parts_of_keys() {
+  for (int w : {1, 2, 3, 7, 271, 4096, 7375000, 7400000, (1 << 25) - 1, 1 << 25})
+    for (int parts = 1; parts <= 304 && parts <= w; ++parts)
+      for (int part = 0; part < parts; ++part) {
+        const int a = wa_part_begin(w, part, parts), b = wa_part_begin(w, part + 1, parts);
+        CHECK(a == (long long)part * w / parts, "part %d of %d of %d tiles: %d", part, parts, w, a);
+        CHECK(b - a == w / parts || b - a == w / parts + 1, "part %d of %d of %d tiles: %d", part, parts, w, b - a);
+        CHECK((part > 0 || a == 0) && (part + 1 < parts || b == w), "ends of %d tiles in %d parts", w, parts);
+        CHECK((long long)b * kWfKeys <= 1 << 30, "key %d beyond 2^30", b);
+      }
+}
+
 int main() {
   const int big = 0x7fffffff;
   for (int found : {0, 1, 7, 1000, 1 << 30, big - 1}) {
@@ -49,6 +64,7 @@ int main() {
     // sums that come back to a small number modulo 2^32
     pages_of_a_call({1 << 30, 1 << 30, 1 << 30, 1 << 30, 3, 2}, found);
   }
+  parts_of_keys();
   std::printf("kv index checks: %lld failures\n", g_fail);
   return g_fail ? 1 : 0;
 }

@@ -4,6 +4,8 @@ import numpy as np
 import pytest
 import torch
 
+from tests import attention64 as A
+
 pytestmark = pytest.mark.gpu
 dev = torch.device("cuda:0")
 
@@ -50,3 +52,28 @@ def test_wants_that_add_up_beyond_32_bits(D, most, add):
     cache.fork(ints([0] * (n - 1)), ints(range(1, n)), share=False)
     assert status(D, cache) == D.KV_NO_PAGES
     assert cache.lens.tolist() == [most] + [0] * (n - 1) and int(cache.refs.sum()) == 5
+
+
+def far_keys(n, dtype, hd=64):
+    """n keys of zeros of which the 40 last, 5 early and 5 middle ones hold values, and a query row that scores these
+    at 80 and more where a key of zeros scores 0: the others' weights add up to n e^-80 < 1e-25.  Keys are values too."""
+    rng = np.random.default_rng(n % 1000)
+    at = np.r_[3:8, n // 2:n // 2 + 5, n - 40:n]
+    x = rng.standard_normal((len(at), hd))
+    x[:, 0] = 8.0
+    q = np.zeros((1, hd))
+    q[0, 0], q[0, 1:] = 12.0, rng.standard_normal(hd - 1) * 0.1
+    x, q = (torch.from_numpy(t.astype(np.float32)).to(dtype) for t in (x, q))
+    k = torch.zeros((n, 1, hd), dtype=dtype, device=dev)
+    k[torch.from_numpy(at).to(dev), 0] = x.to(dev)
+    x, xq = x.double().numpy(), q.double().numpy()
+    assert (x @ xq[0]).min() > 80
+    return q.to(dev)[:, None], k, xq[:, None], x[:, None]
+
+
+def test_fp32_row_split_over_3e8_keys(D, ws):
+    # 77 GB in 304 parts: part times key tiles passes 2^31
+    q, k, xq, x = far_keys(300_000_000, torch.float32)
+    o = D.op_window_attention(q, k, k, ws, scale=1.0)
+    torch.cuda.synchronize()
+    A.check(o.double().cpu().numpy(), xq, x, x, np.ones((1, len(x)), bool), 1.0, False)
