@@ -447,6 +447,67 @@ __device__ __forceinline__ float4 ka_scaled(float4 o, float inv) {
   return inv == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
 }
 
+template <typename T>
+__device__ __forceinline__ float ka_f32(T x) {
+  if constexpr (sizeof(T) == 2) return __bfloat162float(x); else return x;
+}
+
+// One row by the definition, by a warp, eight keys at a time; a lane owns HD / 32
+// dimensions of q and o.  keys(x, k, v) gives the rows of the x-th of `seen` keys.
+// The running output is a mean, each step's weights summing to at most 1, so it stays
+// within the values' range whatever their size.  Scores of -inf alone give zeros.
+template <typename T, int HD, typename Keys>
+__device__ __forceinline__ void ka_row_exact(const T* q, int seen, float scale_log2, const Keys& keys, float (&o)[HD / 32]) {
+  constexpr int kE = HD / 32, kU = 8;
+  const int at = (threadIdx.x & 31) * kE;
+  float qq[kE], m = -INFINITY, l = 0.f;
+#pragma unroll
+  for (int e = 0; e < kE; ++e) {
+    qq[e] = ka_f32(q[at + e]);
+    o[e] = 0.f;
+  }
+  for (int x0 = 0; x0 < seen; x0 += kU) {  // kU keys' loads and sums at once
+    float d[kU], vv[kU][kE];
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+      const T *k, *v;
+      keys(min(x0 + u, seen - 1), k, v);
+      d[u] = 0.f;
+#pragma unroll
+      for (int e = 0; e < kE; ++e) {
+        d[u] = fmaf(qq[e], ka_f32(k[at + e]), d[u]);
+        vv[u][e] = ka_f32(v[at + e]);
+      }
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1)
+#pragma unroll
+      for (int u = 0; u < kU; ++u) d[u] += __shfl_xor_sync(0xffffffffu, d[u], off);
+    float mn = m;
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+      d[u] = x0 + u < seen ? d[u] * scale_log2 : -INFINITY;  // the last key again: without weight
+      mn = fmaxf(mn, d[u]);
+    }
+    const float nm = mn == -INFINITY ? 0.f : mn, before = m == -INFINITY ? 0.f : l * exp2f(m - nm);
+    m = mn;
+    l = before;
+#pragma unroll
+    for (int u = 0; u < kU; ++u) l += exp2f(d[u] - nm);
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+    for (int e = 0; e < kE; ++e) o[e] = before * inv * o[e];
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+      const float p = exp2f(d[u] - nm) * inv;
+#pragma unroll
+      for (int e = 0; e < kE; ++e) o[e] += p * vv[u][e];
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < kE; ++e) o[e] = l == 0.f ? 0.f : o[e];
+}
+
 template <typename T, int HD, int R>
 __global__ void __launch_bounds__(KaCfg<T, HD, R>::kThreads, 1) kv_attention_kernel(const __grid_constant__ KaArgs a) {
   using Cfg = KaCfg<T, HD, R>;

@@ -116,78 +116,39 @@ __device__ __forceinline__ bool wa_sees(const WaRange& r, int sinks, int j) {
   return j <= r.hi && (j >= r.lo || j < sinks);
 }
 
-template <typename T>
-__device__ __forceinline__ float wa_f32(T x) {
-  if constexpr (sizeof(T) == 2) return __bfloat162float(x); else return x;
-}
-
 // Key tile at which part `part` of `parts` of w key tiles begins, floor(part w / parts):
 // the product itself would pass 2^31 from 2.3e8 keys on (7.1 million tiles of 32 keys in 304 parts).
 __host__ __device__ __forceinline__ int wa_part_begin(int w, int part, int parts) {
   return part * (w / parts) + part * (w % parts) / parts;
 }
 
-// One row by the definition, one key after the other, by a warp; a lane owns
-// HD / 32 dimensions.  Only keys that the row sees are read, so nothing a
-// masked key holds can reach the result.  The tile kernels multiply masked
-// keys' values by a weight of 0, which is NaN for an infinite or NaN value; a
-// row that comes out not finite is done again here, and then holds what its own
-// keys give.  One warp, one key at a time: some microseconds a thousand keys,
-// paid only by such rows.
+// One row by the definition (ka_row_exact): only keys that the row sees are read,
+// so nothing a masked key holds can reach the result.  The tile kernels multiply
+// masked keys' values by a weight of 0, which is NaN for an infinite or NaN value,
+// and their sums of weights up to 2^8 overflow where the mean does not; a row that
+// comes out not finite is done again here, and then holds what its own keys give.
+// One warp, eight keys at a time: some microseconds a thousand keys, paid only by
+// such rows.
 template <typename T, int HD>
 __device__ __noinline__ void wa_row_exact(const WaArgs& a, const WaSeq s, int i, int head) {
-  constexpr int kE = HD / 32, kU = 8;
-  const int lane = threadIdx.x & 31;
+  constexpr int kE = HD / 32;
   const WaRange r = wa_range(a, s, i);
-  const T* q = reinterpret_cast<const T*>(a.q) + (int64_t)(s.q0 + i) * a.q_stride + head * HD + lane * kE;
-  const T* k = reinterpret_cast<const T*>(a.k) + (int64_t)s.k0 * a.k_stride + (head / a.group) * HD + lane * kE;
-  const T* v = reinterpret_cast<const T*>(a.v) + (int64_t)s.k0 * a.v_stride + (head / a.group) * HD + lane * kE;
-  float qq[kE], o[kE] = {}, m = -INFINITY, l = 0.f;
-#pragma unroll
-  for (int e = 0; e < kE; ++e) qq[e] = wa_f32(q[e]);
+  const T* k0 = reinterpret_cast<const T*>(a.k) + (int64_t)s.k0 * a.k_stride + (head / a.group) * HD;
+  const T* v0 = reinterpret_cast<const T*>(a.v) + (int64_t)s.k0 * a.v_stride + (head / a.group) * HD;
   const int front = min(a.sinks, min(r.lo, r.hi + 1));
-  const int seen = front + max(0, r.hi - r.lo + 1);
-  for (int x0 = 0; x0 < seen; x0 += kU) {  // kU keys' loads and sums at once
-    float d[kU], vv[kU][kE];
-#pragma unroll
-    for (int u = 0; u < kU; ++u) {
-      const int x = min(x0 + u, seen - 1), j = x < front ? x : x - front + r.lo;
-      d[u] = 0.f;
-#pragma unroll
-      for (int e = 0; e < kE; ++e) {
-        d[u] = fmaf(qq[e], wa_f32(k[(int64_t)j * a.k_stride + e]), d[u]);
-        vv[u][e] = wa_f32(v[(int64_t)j * a.v_stride + e]);
-      }
-    }
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1)
-#pragma unroll
-      for (int u = 0; u < kU; ++u) d[u] += __shfl_xor_sync(0xffffffffu, d[u], off);
-    float mn = m;
-#pragma unroll
-    for (int u = 0; u < kU; ++u) {
-      d[u] *= a.scale_log2;
-      mn = fmaxf(mn, d[u]);
-    }
-    const float nm = mn == -INFINITY ? 0.f : mn, alpha = m == -INFINITY ? 0.f : exp2f(m - nm);
-    m = mn;
-    l *= alpha;
-#pragma unroll
-    for (int e = 0; e < kE; ++e) o[e] *= alpha;
-#pragma unroll
-    for (int u = 0; u < kU; ++u)
-      if (x0 + u < seen) {
-        const float p = exp2f(d[u] - nm);
-        l += p;
-#pragma unroll
-        for (int e = 0; e < kE; ++e) o[e] += p * vv[u][e];
-      }
-  }
-  T* out = reinterpret_cast<T*>(a.o) + (int64_t)(s.q0 + i) * a.o_stride + head * HD + lane * kE;
-  const float inv = l == 0.f ? 0.f : 1.f / l;
+  float o[kE];
+  ka_row_exact<T, HD>(reinterpret_cast<const T*>(a.q) + (int64_t)(s.q0 + i) * a.q_stride + head * HD,
+                      front + max(0, r.hi - r.lo + 1), a.scale_log2,
+                      [&](int x, const T*& k, const T*& v) {
+                        const int j = x < front ? x : x - front + r.lo;
+                        k = k0 + (int64_t)j * a.k_stride;
+                        v = v0 + (int64_t)j * a.v_stride;
+                      },
+                      o);
+  T* out = reinterpret_cast<T*>(a.o) + (int64_t)(s.q0 + i) * a.o_stride + head * HD + (threadIdx.x & 31) * kE;
 #pragma unroll
   for (int e = 0; e < kE; ++e) {
-    if constexpr (sizeof(T) == 2) out[e] = __float2bfloat16(o[e] * inv); else out[e] = o[e] * inv;
+    if constexpr (sizeof(T) == 2) out[e] = __float2bfloat16(o[e]); else out[e] = o[e];
   }
 }
 

@@ -77,3 +77,23 @@ def test_fp32_row_split_over_3e8_keys(D, ws):
     o = D.op_window_attention(q, k, k, ws, scale=1.0)
     torch.cuda.synchronize()
     A.check(o.double().cpu().numpy(), xq, x, x, np.ones((1, len(x)), bool), 1.0, False)
+
+
+# many rows of one tile; few rows over many keys, split; without a workspace nothing is split
+SHAPES = [(torch.bfloat16, 128, 2, 200, 300), (torch.bfloat16, 64, 40, 130, 300), (torch.bfloat16, 128, 1, 5, 3000),
+          (torch.float32, 64, 2, 200, 300), (torch.float32, 128, 40, 70, 200), (torch.float32, 64, 1, 5, 3000)]
+
+
+@pytest.mark.parametrize("dtype,hd,heads,nq,nk", SHAPES)
+def test_prompt_means_of_values_near_the_largest(D, ws, dtype, hd, heads, nq, nk):
+    # sums of weights times values pass the type's range, the weighted means do not
+    rng = np.random.default_rng(nk + heads)
+    q, k = (torch.from_numpy(rng.standard_normal(s).astype(np.float32)).to(dtype) for s in ((nq, heads, hd), (nk, 1, hd)))
+    for low in (-3.3e38, 2.9e38):  # both signs; a mean near the largest value
+        v = torch.from_numpy(rng.uniform(low, 3.3e38, (nk, 1, hd)).astype(np.float32)).to(dtype)
+        o = D.op_window_attention(q.to(dev), k.to(dev), v.to(dev), ws, left=150, right=0, sinks=4)
+        torch.cuda.synchronize()
+        ws.check()
+        pick = [0, 1, nq // 2, nq - 1]
+        A.check(o[pick].double().cpu().numpy(), q[pick].double(), k.double(), v.double(), A.window_mask(nq, nk, 150, 0, 4)[pick],
+                hd ** -0.5, dtype == torch.bfloat16)
