@@ -452,10 +452,14 @@ __device__ __forceinline__ float ka_f32(T x) {
   if constexpr (sizeof(T) == 2) return __bfloat162float(x); else return x;
 }
 
+// w x, where an infinite x stays what it is under a weight too small for fp32
+__device__ __forceinline__ float ka_weigh(float w, float x) { return w == 0.f && isinf(x) ? x : w * x; }
+
 // One row by the definition, by a warp, eight keys at a time; a lane owns HD / 32
 // dimensions of q and o.  keys(x, k, v) gives the rows of the x-th of `seen` keys.
 // The running output is a mean, each step's weights summing to at most 1, so it stays
-// within the values' range whatever their size.  Scores of -inf alone give zeros.
+// within the values' range whatever their size; an infinite value makes its column
+// infinite however small its weight.  Scores of -inf alone give zeros.
 template <typename T, int HD, typename Keys>
 __device__ __forceinline__ void ka_row_exact(const T* q, int seen, float scale_log2, const Keys& keys, float (&o)[HD / 32]) {
   constexpr int kE = HD / 32, kU = 8;
@@ -496,12 +500,12 @@ __device__ __forceinline__ void ka_row_exact(const T* q, int seen, float scale_l
     for (int u = 0; u < kU; ++u) l += exp2f(d[u] - nm);
     const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll
-    for (int e = 0; e < kE; ++e) o[e] = before * inv * o[e];
+    for (int e = 0; e < kE; ++e) o[e] = ka_weigh(before * inv, o[e]);
 #pragma unroll
     for (int u = 0; u < kU; ++u) {
       const float p = exp2f(d[u] - nm) * inv;
 #pragma unroll
-      for (int e = 0; e < kE; ++e) o[e] += p * vv[u][e];
+      for (int e = 0; e < kE; ++e) o[e] += ka_weigh(p, vv[u][e]);
     }
   }
 #pragma unroll

@@ -97,3 +97,46 @@ def test_prompt_means_of_values_near_the_largest(D, ws, dtype, hd, heads, nq, nk
         pick = [0, 1, nq // 2, nq - 1]
         A.check(o[pick].double().cpu().numpy(), q[pick].double(), k.double(), v.double(), A.window_mask(nq, nk, 150, 0, 4)[pick],
                 hd ** -0.5, dtype == torch.bfloat16)
+
+
+@pytest.mark.parametrize("dtype,hd,heads,nq,nk", SHAPES)
+def test_prompt_infinite_values_of_tiny_weight(D, ws, dtype, hd, heads, nq, nk):
+    # a value that a row sees makes its column infinite though its weight is far below fp32's range, wherever the key
+    # lies; the other columns are what the finite values give, and rows that do not see the key stay finite
+    rng = np.random.default_rng(nk + hd)
+    xq, xk = rng.standard_normal((nq, heads, hd)), rng.standard_normal((nk, 1, hd))
+    xq[..., 0] = 8.0
+    first, last = nk - nq, nk - nq + 3  # keys seen by every row, and by all but the first three
+    xk[:, 0, 0] = 0.0
+    xk[[first, last], 0, 0] = -400.0 / (hd ** -0.5)
+    q, k, v = (torch.from_numpy(t.astype(np.float32)).to(dtype) for t in (xq, xk, rng.standard_normal((nk, 1, hd))))
+    bad = v.clone()
+    bad[first, 0, 3], bad[last, 0, 7] = float("inf"), float("-inf")
+    o = D.op_window_attention(q.to(dev), k.to(dev), bad.to(dev), ws, left=-1, right=0).double().cpu().numpy()
+    assert (o[:, :, 3] == np.inf).all()
+    assert (o[3:, :, 7] == -np.inf).all() and np.isfinite(o[:3, :, 7]).all()
+    rest = np.delete(np.arange(hd), [3, 7])
+    assert np.isfinite(o[..., rest]).all()
+    pick = [0, 2, 3, nq - 1]
+    seen = A.window_mask(nq, nk, -1, 0, 0)[pick]
+    for i, s in zip(pick, seen):
+        for h in range(0, heads, 7):
+            want, tol = A.attend(q[i, h].double().numpy(), k[:, 0].double().numpy(), v[:, 0].double().numpy(), s, hd ** -0.5,
+                                 dtype == torch.bfloat16)
+            assert (np.abs(o[i, h] - want) <= tol)[rest].all()
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_prompt_infinite_value_before_scores_that_rise(D, ws, dtype):
+    # the infinite value comes first, with all the weight there is; the keys behind it take that away
+    k = torch.zeros((64, 1, 64), dtype=dtype, device=dev)
+    k[:, 0, 0] = torch.arange(64, device=dev) * 40.0
+    v = torch.ones_like(k)
+    v[0, 0, 5] = float("inf")
+    q = torch.zeros((64, 2, 64), dtype=dtype, device=dev)
+    q[..., 0] = 4.0
+    o = D.op_window_attention(q, k, v, ws, right=0, scale=1.0)
+    assert (o[:, :, 5] == float("inf")).all() and (o[:, :, :5] == 1).all() and (o[:, :, 6:] == 1).all()
+    # scores of -inf alone give zeros, whatever the values
+    k[:, 0, 0] = float("-inf")
+    assert (D.op_window_attention(q, k, v, ws, right=0, scale=1.0) == 0).all()
