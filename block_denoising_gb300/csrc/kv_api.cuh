@@ -317,6 +317,7 @@ dinfer_status dinfer_kv_attention(const dinfer_kv_cache* kc, int32_t layer, cons
   a.window = window < 0 ? -1 : window;
   a.sinks = sinks;
   a.min_steps = 8;
+  a.in_place = o == q;
   a.scale_log2 = scale * 1.4426950408889634f;
   a.partial = reinterpret_cast<float*>(w.data);
   a.tickets = w.tickets;

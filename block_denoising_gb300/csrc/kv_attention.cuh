@@ -78,6 +78,7 @@ struct KaArgs {
   int n, group, subgroups;                // query heads per key head; pieces of at most kRows of them
   int window, sinks;
   int min_steps;  // the least a CTA is given
+  int in_place;   // o is q
   float scale_log2;
   float* partial;  // [CTA][2][kSlotFloats]
   int* tickets;    // [CTA], zero between calls
@@ -456,11 +457,12 @@ __device__ __forceinline__ float ka_f32(T x) {
 __device__ __forceinline__ float ka_weigh(float w, float x) { return w == 0.f && isinf(x) ? x : w * x; }
 
 // One row by the definition, by a warp, eight keys at a time; a lane owns HD / 32
-// dimensions of q and o.  keys(x, k, v) gives the rows of the x-th of `seen` keys.
+// dimensions of q and o.  keys(x, k, v) gives the rows of the x-th of `seen` keys;
+// with kGaps it returns whether the key is there (the rows are readable anyway).
 // The running output is a mean, each step's weights summing to at most 1, so it stays
 // within the values' range whatever their size; an infinite value makes its column
 // infinite however small its weight.  Scores of -inf alone give zeros.
-template <typename T, int HD, typename Keys>
+template <typename T, int HD, bool kGaps, typename Keys>
 __device__ __forceinline__ void ka_row_exact(const T* q, int seen, float scale_log2, const Keys& keys, float (&o)[HD / 32]) {
   constexpr int kE = HD / 32, kU = 8;
   const int at = (threadIdx.x & 31) * kE;
@@ -472,10 +474,12 @@ __device__ __forceinline__ void ka_row_exact(const T* q, int seen, float scale_l
   }
   for (int x0 = 0; x0 < seen; x0 += kU) {  // kU keys' loads and sums at once
     float d[kU], vv[kU][kE];
+    uint32_t there = 0xffffffffu;
 #pragma unroll
     for (int u = 0; u < kU; ++u) {
       const T *k, *v;
-      keys(min(x0 + u, seen - 1), k, v);
+      if constexpr (kGaps) there ^= (uint32_t)!keys(min(x0 + u, seen - 1), k, v) << u;
+      else keys(min(x0 + u, seen - 1), k, v);
       d[u] = 0.f;
 #pragma unroll
       for (int e = 0; e < kE; ++e) {
@@ -491,6 +495,11 @@ __device__ __forceinline__ void ka_row_exact(const T* q, int seen, float scale_l
 #pragma unroll
     for (int u = 0; u < kU; ++u) {
       d[u] = x0 + u < seen ? d[u] * scale_log2 : -INFINITY;  // the last key again: without weight
+      if constexpr (kGaps) {
+        d[u] = (there >> u) & 1u ? d[u] : -INFINITY;
+#pragma unroll
+        for (int e = 0; e < kE; ++e) vv[u][e] = (there >> u) & 1u ? vv[u][e] : 0.f;
+      }
       mn = fmaxf(mn, d[u]);
     }
     const float nm = mn == -INFINITY ? 0.f : mn, before = m == -INFINITY ? 0.f : l * exp2f(m - nm);
@@ -510,6 +519,35 @@ __device__ __forceinline__ void ka_row_exact(const T* q, int seen, float scale_l
   }
 #pragma unroll
   for (int e = 0; e < kE; ++e) o[e] = l == 0.f ? 0.f : o[e];
+}
+
+// Query head `head` (key head kvh) of an entry, a sequence of `len` tokens, done again
+// key by key: its sums of weights up to 2^8 overflowed where the mean does not, or it
+// sees infinities or NaN.  A warp and some microseconds a thousand keys, paid only by
+// such rows.
+template <typename T, int HD>
+__device__ __noinline__ void ka_redo(const KaArgs& a, int entry, int len, int head, int kvh) {
+  constexpr int kE = HD / 32;
+  const KvPages& c = a.c;
+  const int32_t* row = c.table + (size_t)(a.seqs ? a.seqs[entry] : entry) * c.max_pages;
+  const KaSeen s = ka_seen(len, a.window, a.sinks);
+  float o[kE];
+  ka_row_exact<T, HD, true>(
+      reinterpret_cast<const T*>(a.q) + entry * a.q_stride + head * HD, s.seen, a.scale_log2,
+      [&](int x, const T*& k, const T*& v) {
+        const int key = x < s.sink ? x : x - s.sink + s.first, j = (int)c.page_div.div((uint32_t)key), page = row[j];
+        const bool ok = page >= 0 && page < c.num_pages;
+        const int64_t off = a.layer_off + (ok ? page : 0) * c.page_stride + (key - j * c.page_size) * c.token_stride + kvh * c.head_stride;
+        k = reinterpret_cast<const T*>(c.k + off);
+        v = reinterpret_cast<const T*>(c.v + off);
+        return ok;
+      },
+      o);
+  T* out = reinterpret_cast<T*>(a.o) + entry * a.o_stride + head * HD + (threadIdx.x & 31) * kE;
+#pragma unroll
+  for (int e = 0; e < kE; ++e) {
+    if constexpr (sizeof(T) == 2) out[e] = __float2bfloat16(o[e]); else out[e] = o[e];
+  }
 }
 
 template <typename T, int HD, int R>
@@ -691,37 +729,49 @@ __global__ void __launch_bounds__(KaCfg<T, HD, R>::kThreads, 1) kv_attention_ker
       float* part = a.partial + ((int64_t)blockIdx.x * 2 + slot) * Cfg::kSlotFloats;
       state.store_ml(ml + warp * kRows * 2, lane);
       T* orow = reinterpret_cast<T*>(a.o) + use.entry * a.o_stride + head * HD;
+      // Four columns of a row, or nothing (!on); the lanes of a row are one warp's, or half of them.  Rows that are not
+      // finite are done again at the pair's end, by one call for all its rows (a call at each store: 56.4 us for 64
+      // sequences of 1 .. 8192 tokens, 32 heads on 8, this 55.4, without either 55.3).  Where o is q such a row is not
+      // stored at all, as its query is wanted still.
+      uint32_t redo = 0;
+      auto put = [&](bool on, int row, int c4, float4 acc, float ll) {
+        const bool bad = on && !(fabsf(acc.x) + fabsf(acc.y) + fabsf(acc.z) + fabsf(acc.w) + ll <= 1.0e38f);
+        if (bad) redo |= 1u << row;
+        bool store = on;
+        if (a.in_place) {
+          const uint32_t bads = __ballot_sync(0xffffffffu, bad);  // of all lanes, those that are not on too
+          store = on && !(bads & (HD == 128 ? 0xffffffffu : 0xffffu << (lane & 16)));
+        }
+        if (store) ka_store4(orow + row * HD + c4, ka_scaled(acc, ll == 0.f ? 0.f : 1.f / ll));
+      };
+      static_assert(kMergeRows * HD / 4 <= kThreads, "a round of rows is at most four columns a thread");
       for (int r0 = 0; r0 < rows; r0 += kMergeRows) {
         state.store_rows(merge + warp * (kMergeRows * HD), r0, lane);
         __syncthreads();
-        for (int x = tid; x < kMergeRows * HD / 4; x += kThreads) {
-          const int row = r0 + x / (HD / 4), c4 = (x % (HD / 4)) * 4;
-          if (row < rows) {
-            float mm = -INFINITY;
+        const int row = r0 + tid / (HD / 4), c4 = (tid % (HD / 4)) * 4;
+        const bool on = tid < kMergeRows * HD / 4 && row < rows;
+        float mm = -INFINITY, ll = 0.f;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (on) {
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, ml[(w * kRows + row) * 2]);
-            float ll = 0.f;
-            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+          for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, ml[(w * kRows + row) * 2]);
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w) {
-              const float mw = ml[(w * kRows + row) * 2];
-              const float f = mw == -INFINITY ? 0.f : ex2_approx(mw - mm);
-              const float4 v =
-                  *reinterpret_cast<const float4*>(merge + w * (kMergeRows * HD) + (row - r0) * HD + c4);
-              ll = fmaf(f, ml[(w * kRows + row) * 2 + 1], ll);
-              acc.x = fmaf(f, v.x, acc.x);
-              acc.y = fmaf(f, v.y, acc.y);
-              acc.z = fmaf(f, v.z, acc.z);
-              acc.w = fmaf(f, v.w, acc.w);
-            }
-            if (whole) {
-              const float inv = ll == 0.f ? 0.f : 1.f / ll;
-              ka_store4(orow + row * HD + c4, ka_scaled(acc, inv));
-            } else {
-              __stcg(reinterpret_cast<float4*>(part + Cfg::kSlotO + row * HD + c4), acc);
-              if (c4 == 0) __stcg(reinterpret_cast<float2*>(part + row * 2), make_float2(mm, ll));
-            }
+          for (int w = 0; w < kWarps; ++w) {
+            const float mw = ml[(w * kRows + row) * 2];
+            const float f = mw == -INFINITY ? 0.f : ex2_approx(mw - mm);
+            const float4 v = *reinterpret_cast<const float4*>(merge + w * (kMergeRows * HD) + (row - r0) * HD + c4);
+            ll = fmaf(f, ml[(w * kRows + row) * 2 + 1], ll);
+            acc.x = fmaf(f, v.x, acc.x);
+            acc.y = fmaf(f, v.y, acc.y);
+            acc.z = fmaf(f, v.z, acc.z);
+            acc.w = fmaf(f, v.w, acc.w);
           }
+        }
+        if (whole) {
+          put(on, row, c4, acc, ll);
+        } else if (on) {
+          __stcg(reinterpret_cast<float4*>(part + Cfg::kSlotO + row * HD + c4), acc);
+          if (c4 == 0) __stcg(reinterpret_cast<float2*>(part + row * 2), make_float2(mm, ll));
         }
         __syncthreads();
       }
@@ -734,11 +784,12 @@ __global__ void __launch_bounds__(KaCfg<T, HD, R>::kThreads, 1) kv_attention_ker
         __syncthreads();
         if (join_sh) {
           const int nc = c_last - c_first + 1;
-          for (int x = tid; x < rows * HD / 4; x += kThreads) {
-            const int row = x / (HD / 4), c4 = (x % (HD / 4)) * 4;
+          for (int x0 = 0; x0 < rows * HD / 4; x0 += kThreads) {
+            const int x = x0 + tid, row = x / (HD / 4), c4 = (x % (HD / 4)) * 4;
+            const bool on = row < rows;
             float mm = -INFINITY, ll = 0.f;
             float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-            for (int k0 = 0; k0 < nc; k0 += kKaJoin) {  // all loads of a round before the first use
+            for (int k0 = 0; k0 < nc && on; k0 += kKaJoin) {  // all loads of a round before the first use
               float2 w[kKaJoin];
               float4 v[kKaJoin];
 #pragma unroll
@@ -771,11 +822,14 @@ __global__ void __launch_bounds__(KaCfg<T, HD, R>::kThreads, 1) kv_attention_ker
                 acc.w = fmaf(f, v[k].w, acc.w);
               }
             }
-            const float inv = ll == 0.f ? 0.f : 1.f / ll;
-            ka_store4(orow + row * HD + c4, ka_scaled(acc, inv));
+            put(on, row, c4, acc, ll);
           }
           if (tid == 0) a.tickets[c_first] = 0;
         }
+      }
+      for (redo = __reduce_or_sync(0xffffffffu, redo); redo; redo &= redo - 1) {
+        __syncwarp();  // behind the row's first stores
+        ka_redo<T, HD>(a, use.entry, lens[use.entry], head + __ffs(redo) - 1, use.piece / a.subgroups);
       }
       if (!go) break;
       state.begin(lane, qs);

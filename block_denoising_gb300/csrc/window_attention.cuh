@@ -137,7 +137,7 @@ __device__ __noinline__ void wa_row_exact(const WaArgs& a, const WaSeq s, int i,
   const T* v0 = reinterpret_cast<const T*>(a.v) + (int64_t)s.k0 * a.v_stride + (head / a.group) * HD;
   const int front = min(a.sinks, min(r.lo, r.hi + 1));
   float o[kE];
-  ka_row_exact<T, HD>(reinterpret_cast<const T*>(a.q) + (int64_t)(s.q0 + i) * a.q_stride + head * HD,
+  ka_row_exact<T, HD, false>(reinterpret_cast<const T*>(a.q) + (int64_t)(s.q0 + i) * a.q_stride + head * HD,
                       front + max(0, r.hi - r.lo + 1), a.scale_log2,
                       [&](int x, const T*& k, const T*& v) {
                         const int j = x < front ? x : x - front + r.lo;

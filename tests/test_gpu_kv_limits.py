@@ -140,3 +140,75 @@ def test_prompt_infinite_value_before_scores_that_rise(D, ws, dtype):
     # scores of -inf alone give zeros, whatever the values
     k[:, 0, 0] = float("-inf")
     assert (D.op_window_attention(q, k, v, ws, right=0, scale=1.0) == 0).all()
+
+
+def paged(D, keys, values, page=16, seed=0):
+    """A cache of one layer that holds keys[s], values[s] [n, kv_heads, hd] on scattered pages; other slots hold NaN."""
+    rng = np.random.default_rng(seed)
+    held = [-(-len(k) // page) for k in keys]
+    at = rng.permutation(sum(held) + 2)
+    table, refs = torch.full((len(keys), max(held)), -1, dtype=torch.int32), torch.zeros(len(at), dtype=torch.int32)
+    k, v = (torch.full((1, len(at), page, *keys[0].shape[1:]), float("nan"), dtype=keys[0].dtype) for _ in range(2))
+    for s, h in enumerate(held):
+        mine = torch.from_numpy(at[sum(held[:s]):sum(held[:s + 1])])
+        table[s, :h], refs[mine] = mine.int(), 1
+        p = torch.arange(len(keys[s]))
+        k[0, mine[p // page], p % page], v[0, mine[p // page], p % page] = keys[s], values[s]
+    return D.PagedKV(k.to(dev), v.to(dev), table.to(dev), ints([len(x) for x in keys]), refs.to(dev))
+
+
+# one round of rows and several, whole pairs and ones joined over many CTAs
+TOKENS = [(torch.bfloat16, 128, 3), (torch.bfloat16, 64, 8), (torch.bfloat16, 128, 17), (torch.bfloat16, 64, 11),
+          (torch.float32, 64, 1), (torch.float32, 128, 2), (torch.float32, 64, 5), (torch.float32, 128, 12)]
+
+
+@pytest.mark.parametrize("dtype,hd,group", TOKENS)
+def test_token_means_of_values_near_the_largest(D, ws, dtype, hd, group):
+    # as for prompts; in place, and with a page that is none among the keys
+    rng = np.random.default_rng(hd + group)
+    lens, kvh = [1, 40, 700, 6000], 2
+    put = lambda x: torch.from_numpy(x.astype(np.float32)).to(dtype)  # noqa: E731
+    q = put(rng.standard_normal((4, kvh * group, hd)))
+    keys = [put(rng.standard_normal((n, kvh, hd))) for n in lens]
+    for low in (-3.3e38, 2.9e38):
+        vals = [put(rng.uniform(low, 3.3e38, (n, kvh, hd))) for n in lens]
+        cache = paged(D, keys, vals)
+        cache.table[1, 1] = 1 << 20
+        for window, sinks in ((-1, 0), (300, 5)):
+            seen = [A.window_mask(1, n, window, 0, sinks) for n in lens]
+            seen[1][:, 16:32] = False
+            o = cache.attention(0, q.to(dev), ws, window=window, sinks=sinks)
+            assert status(D, cache) == D.KV_BAD_PAGE
+            for s, n in enumerate(lens):
+                A.check(o[s:s + 1].double().cpu().numpy(), q[s:s + 1].double(), keys[s].double(), vals[s].double(), seen[s],
+                        hd ** -0.5, dtype == torch.bfloat16, (low, window, n))
+            x = q.to(dev)
+            assert torch.equal(cache.attention(0, x, ws, window=window, sinks=sinks, out=x), o)
+            assert status(D, cache) == D.KV_BAD_PAGE
+
+
+@pytest.mark.parametrize("dtype,hd,group", TOKENS)
+def test_token_infinite_values_of_tiny_weight(D, ws, dtype, hd, group):
+    rng = np.random.default_rng(hd + group)
+    lens = [50, 5000]
+    q = torch.from_numpy(rng.standard_normal((2, group, hd)).astype(np.float32)).to(dtype)
+    q[..., 0] = 8.0
+    keys = [torch.from_numpy(rng.standard_normal((n, 1, hd)).astype(np.float32)).to(dtype) for n in lens]
+    clean = [torch.from_numpy(rng.standard_normal((n, 1, hd)).astype(np.float32)).to(dtype) for n in lens]
+    vals = [v.clone() for v in clean]
+    for k, v in zip(keys, vals):
+        k[:, 0, 0] = 0.0
+        k[[3, len(k) // 2], 0, 0] = -400.0 / (hd ** -0.5)
+        v[3, 0, 3], v[len(k) // 2, 0, 7] = float("inf"), float("-inf")
+    cache = paged(D, keys, vals)
+    o = cache.attention(0, q.to(dev), ws).double().cpu().numpy()
+    assert status(D, cache) == 0
+    assert (o[:, :, 3] == np.inf).all() and (o[:, :, 7] == -np.inf).all()
+    rest = np.delete(np.arange(hd), [3, 7])
+    for s, n in enumerate(lens):
+        for h in range(group):
+            want, tol = A.attend(q[s, h].double().numpy(), keys[s][:, 0].double().numpy(), clean[s][:, 0].double().numpy(),
+                                 np.ones(n, bool), hd ** -0.5, dtype == torch.bfloat16)
+            assert (np.abs(o[s, h] - want) <= tol)[rest].all()
+    # outside the window they touch nothing
+    assert np.isfinite(cache.attention(0, q.to(dev), ws, window=20, sinks=3).double().cpu().numpy()).all()
