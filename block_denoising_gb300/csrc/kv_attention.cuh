@@ -26,7 +26,7 @@
 // bf16: S = Q K^T and O += P V on mma.sync m16n8k16 with the query heads of
 // the group as the 16 rows (one token has too few rows for a tcgen05 tile of
 // 128, and the products are far from the bound either way).  P goes through its
-// product as two bf16 (rounded down, and the rounded rest, 16 bits together):
+// product as two bf16 (the number below it cut off, and the rounded rest, 16 bits together):
 // the products have the room, and the output's own rounding is then all that is
 // left.  Everything else is fp32.  fp32: plain FMAs.
 #pragma once
@@ -288,12 +288,12 @@ struct KaStateBf16 {
 #pragma unroll
       for (int e = 0; e < 8; e += 2) {
         const float p0 = ex2_approx(x[e] - nm), p1 = ex2_approx(x[e + 1] - nm);
-        const uint32_t u0 = __float_as_uint(p0), u1 = __float_as_uint(p1);
+        // the upper half of the bits of the number just below p, and the rest, which is thus more than 0 wherever p is:
+        // an infinite value does not meet 0 there, and a weight of 0 (0 and 0) adds nothing
+        const uint32_t u0 = max(__float_as_uint(p0), 1u) - 1u, u1 = max(__float_as_uint(p1), 1u) - 1u;
         const int at = ((e >> 1) & 1) * 2 + h;  // a0 / a1: keys 2t, 2t + 1; a2 / a3: keys 2t + 8, 2t + 9
-        p[e >> 2][at] = __byte_perm(u0, u1, 0x7632);  // the upper halves: p rounded down
-        // the rest, never 0 (2^-126 at least): an infinite value must not meet 0
-        const uint32_t rest = pack_bf16x2(fmaxf(p0 - __uint_as_float(u0 & 0xffff0000u), 1.17549435e-38f),
-                                          fmaxf(p1 - __uint_as_float(u1 & 0xffff0000u), 1.17549435e-38f));
+        p[e >> 2][at] = __byte_perm(u0, u1, 0x7632);
+        const uint32_t rest = pack_bf16x2(p0 - __uint_as_float(u0 & 0xffff0000u), p1 - __uint_as_float(u1 & 0xffff0000u));
         if constexpr (R == 8) p[e >> 2][at + 1] = rest; else pl[e >> 2][at] = rest;
         l[h] += p0 + p1;  // this lane's keys; the lanes of a row are summed at the end
       }

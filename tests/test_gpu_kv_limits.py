@@ -212,3 +212,24 @@ def test_token_infinite_values_of_tiny_weight(D, ws, dtype, hd, group):
             assert (np.abs(o[s, h] - want) <= tol)[rest].all()
     # outside the window they touch nothing
     assert np.isfinite(cache.attention(0, q.to(dev), ws, window=20, sinks=3).double().cpu().numpy()).all()
+
+
+@pytest.mark.parametrize("dtype,hd,group", TOKENS)
+def test_token_large_value_without_weight(D, ws, dtype, hd, group):
+    # keys whose weight is far below the smallest number add nothing, however large their (finite) values
+    rng = np.random.default_rng(hd + group)
+    lens = [50, 5000]
+    put = lambda x: torch.from_numpy(x.astype(np.float32)).to(dtype)  # noqa: E731
+    q = put(rng.standard_normal((2, group, hd)))
+    q[..., 0] = 8.0
+    keys = [put(rng.standard_normal((n, 1, hd))) for n in lens]
+    vals = [put(rng.standard_normal((n, 1, hd))) for n in lens]
+    for k, v in zip(keys, vals):
+        k[:, 0, 0] = 0.0
+        far = [1, 3, len(k) // 2, len(k) - 1]
+        k[far, 0, 0] = -40.0 / (hd ** -0.5)
+        v[far] = 3e38
+    o = paged(D, keys, vals).attention(0, q.to(dev), ws).double().cpu().numpy()
+    for s, n in enumerate(lens):
+        A.check(o[s:s + 1], q[s:s + 1].double(), keys[s].double(), vals[s].double(), np.ones((1, n), bool), hd ** -0.5,
+                dtype == torch.bfloat16)
