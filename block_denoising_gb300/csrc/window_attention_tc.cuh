@@ -308,7 +308,7 @@ __global__ void __launch_bounds__(kWtThreads, 1)
   __shared__ volatile int redoing;  // warps that do rows again
   __shared__ volatile int join_here;
   // of each slot's tile, for the TMA thread: which tiles' products read it (bits
-  // 0, 1) and whether it is V (bit 2); the products' numbers
+  // 0, 1) and whether it is V (bit 2); the products' numbers (the long waits look at slot 0's)
   __shared__ int slot_use[kSlots][3];
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -364,9 +364,27 @@ __global__ void __launch_bounds__(kWtThreads, 1)
     }
     return true;
   };
+  // A wait that may last as long as a piece (warp 10's for its last copies, and that of
+  // warps without a part in it for the next one: the limit's second is reached at some
+  // 1e8 keys): it runs out when slot 0 got no tile since it last looked.
+  auto wait_long = [&](uint64_t* bar, uint32_t parity) -> bool {
+    if (mbar_try_wait(bar, parity)) return true;
+    long long t0 = clock64();
+    int before = -1;
+    while (!mbar_try_wait(bar, parity)) {
+      if (*abort_flag) return false;
+      if (clock64() - t0 > kWaitCycles) {
+        const int now = *(volatile int*)&slot_use[0][1] + *(volatile int*)&slot_use[0][2];
+        if (now == before && redoing == 0) *abort_flag = 1;
+        before = now;
+        t0 = clock64();
+      }
+    }
+    return true;
+  };
   // piece number it of this CTA lies in pieces[it & 1] (named as an array, so that
   // its fields are loads from shared memory and not through a generic address)
-  auto have_piece = [&](int it) -> bool { return wait(&piece_full[it & 1], (it >> 1) & 1); };
+  auto have_piece = [&](int it) -> bool { return wait_long(&piece_full[it & 1], (it >> 1) & 1); };
 
   if (warp == 10) {
     // ------------------------------ pieces ------------------------------
@@ -379,7 +397,7 @@ __global__ void __launch_bounds__(kWtThreads, 1)
     for (int it = 0; left; ++it) {
       // asked for once the last piece's copies are issued, some three key tiles
       // before its end: no CTA holds pieces that another could have begun
-      if (it > 0 && !__all_sync(0xffffffffu, wait(loaded, (it - 1) & 1))) break;
+      if (it > 0 && !__all_sync(0xffffffffu, wait_long(loaded, (it - 1) & 1))) break;
       int b = 0, block = 0, piece = 0;
       left = false;
       while (!left) {

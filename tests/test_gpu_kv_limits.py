@@ -233,3 +233,16 @@ def test_token_large_value_without_weight(D, ws, dtype, hd, group):
     for s, n in enumerate(lens):
         A.check(o[s:s + 1], q[s:s + 1].double(), keys[s].double(), vals[s].double(), np.ones((1, n), bool), hd ** -0.5,
                 dtype == torch.bfloat16)
+
+
+def test_bf16_piece_that_lasts_seconds(D):
+    # 3.6e8 keys of one row that no workspace lets split, some 3 s: the waits for its end outlast the limit of a wait
+    # without progress (about a second)
+    q, k, xq, x = far_keys(360_000_000, torch.bfloat16)
+    o = torch.full_like(q, 7.0)
+    st = D.lib().dinfer_op_window_attention(q.data_ptr(), k.data_ptr(), k.data_ptr(), o.data_ptr(), D.BF16, 1, None, None, 1, k.shape[0],
+                                            1, 1, 64, 64, 64, 64, 64, -1, -1, 0, 1.0, None, 0,
+                                            torch.cuda.current_stream().cuda_stream)
+    assert st == D.OK
+    torch.cuda.synchronize()
+    A.check(o.double().cpu().numpy(), xq, x, x, np.ones((1, len(x)), bool), 1.0, True)
