@@ -1,5 +1,6 @@
 """The paged KV cache and windowed attention at the ends of their ranges: sums beyond 2^31, very long pieces of work,
-values near the type's largest and weights near its smallest."""
+values near the type's largest, weights near its smallest,
+and what is kept of a weight."""
 import numpy as np
 import pytest
 import torch
@@ -246,3 +247,21 @@ def test_bf16_piece_that_lasts_seconds(D):
     assert st == D.OK
     torch.cuda.synchronize()
     A.check(o.double().cpu().numpy(), xq, x, x, np.ones((1, len(x)), bool), 1.0, True)
+
+
+@pytest.mark.parametrize("hd,group", [(64, 3), (128, 8), (64, 11), (128, 16), (64, 1), (128, 19)])
+def test_token_weights_in_two_bf16(D, ws, hd, group):
+    # sums that nearly cancel, and plain ones: 2^-16 of a weight is lost, no more (tests/test_attention64.py: one part alone
+    # is beyond this bound)
+    rng = np.random.default_rng(hd + group)
+    rounded = lambda x: torch.from_numpy(np.asarray(x, np.float32)).to(torch.bfloat16).double().numpy()  # noqa: E731
+    cases = [A.cancelling(rng, n, hd, group, rounded) for n in (5, 40, 130, 300)]
+    cases += [tuple(rounded(rng.standard_normal(s)) for s in ((group, hd), (n, hd), (n, hd))) for n in (2, 33, 1500)]
+    put = lambda x: torch.from_numpy(x.astype(np.float32)).to(torch.bfloat16)  # noqa: E731
+    cache = paged(D, [put(k)[:, None] for _, k, _ in cases], [put(v)[:, None] for _, _, v in cases])
+    q = put(np.stack([q for q, _, _ in cases]))
+    o = cache.attention(0, q.to(dev), ws, scale=1.0)
+    torch.cuda.synchronize()
+    for s, (x, k, v) in enumerate(cases):
+        A.check(o[s:s + 1].double().cpu().numpy(), x[None], k[:, None], v[:, None], np.ones((1, len(k)), bool), 1.0, True,
+                (len(k),), 2.0 ** -16)
