@@ -157,6 +157,11 @@ bool rows_ok(const void* p, int64_t stride, int64_t rows, int64_t row, int64_t p
   return rows <= 1 || (stride % per == 0 && stride >= row && stride < (1ll << 36));
 }
 
+// int32 operands (NULL where that is allowed): aligned
+bool ints_ok(const void* a, const void* b = nullptr) {
+  return ((reinterpret_cast<uintptr_t>(a) | reinterpret_cast<uintptr_t>(b)) & 3) == 0;
+}
+
 // bf16 rows [rows][heads][hd], `stride` elements apart: boxes of 128 rows x one
 // head x 64 elements with the 128-byte swizzle; rows behind the last read as zeros.
 bool make_map_rows(CUtensorMap* m, const void* base, int64_t rows, int64_t heads, int64_t hd, int64_t stride) {
@@ -201,7 +206,7 @@ dinfer_status dinfer_kv_set(const dinfer_kv_cache* kc, const int32_t* table, con
   dinfer_ctx* c = nullptr;
   if (const char* why = kv_bad(kc)) return fail(c, DINFER_EINVAL, "%s", why);
   if (!table || !lens || !refs) return fail(c, DINFER_EINVAL, "NULL operand");
-  if ((reinterpret_cast<uintptr_t>(table) | reinterpret_cast<uintptr_t>(lens) | reinterpret_cast<uintptr_t>(refs)) & 3)
+  if (!ints_ok(table, lens) || !ints_ok(refs))
     return fail(c, DINFER_EINVAL, "misaligned table, lens or refs");
   const int64_t most = std::max<int64_t>((int64_t)kc->max_seqs * kc->max_pages, kc->num_pages);
   const int grid = (int)std::min<int64_t>((most + 255) / 256, (int64_t)num_sms() * 8);
@@ -215,6 +220,7 @@ dinfer_status dinfer_kv_extend(const dinfer_kv_cache* kc, const int32_t* seqs, c
   dinfer_ctx* c = nullptr;
   if (const char* why = kv_bad(kc)) return fail(c, DINFER_EINVAL, "%s", why);
   if (n < 1 || n > kKvMaxEntries) return fail(c, DINFER_EINVAL, "n must be 1 .. %d", kKvMaxEntries);
+  if (!ints_ok(seqs, add)) return fail(c, DINFER_EINVAL, "misaligned seqs or add");
   CK(launchk(kv_extend_kernel, dim3(1), dim3(kKvPlanThreads), 0, reinterpret_cast<cudaStream_t>(stream), 1,
              kv_pages(*kc), seqs, add, (int)n));
   return DINFER_OK;
@@ -232,6 +238,7 @@ dinfer_status dinfer_kv_append(const dinfer_kv_cache* kc, int32_t layer, const i
   const int64_t per = kc->dtype == DINFER_BF16 ? 8 : 4, row = (int64_t)kc->kv_heads * kc->head_dim;
   if (!rows_ok(k, k_stride, total_rows, row, per) || !rows_ok(v, v_stride, total_rows, row, per))
     return fail(c, DINFER_EINVAL, "k, v: 16-byte aligned rows at least a row apart are needed");
+  if (!ints_ok(seqs, rows)) return fail(c, DINFER_EINVAL, "misaligned seqs or rows");
   const KvPages p = kv_pages(*kc);
   KvAppend a{};
   a.seqs = seqs;
@@ -255,6 +262,7 @@ dinfer_status dinfer_kv_fork(const dinfer_kv_cache* kc, const int32_t* src, cons
   dinfer_ctx* c = nullptr;
   if (const char* why = kv_bad(kc)) return fail(c, DINFER_EINVAL, "%s", why);
   if (!src || !dst) return fail(c, DINFER_EINVAL, "NULL operand");
+  if (!ints_ok(src, dst)) return fail(c, DINFER_EINVAL, "misaligned src or dst");
   if (n < 1 || n > kKvMaxEntries) return fail(c, DINFER_EINVAL, "n must be 1 .. %d", kKvMaxEntries);
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const KvPages p = kv_pages(*kc);
@@ -272,6 +280,7 @@ dinfer_status dinfer_kv_free(const dinfer_kv_cache* kc, const int32_t* seqs, int
   dinfer_ctx* c = nullptr;
   if (const char* why = kv_bad(kc)) return fail(c, DINFER_EINVAL, "%s", why);
   if (!seqs) return fail(c, DINFER_EINVAL, "NULL operand");
+  if (!ints_ok(seqs)) return fail(c, DINFER_EINVAL, "misaligned seqs");
   if (n < 1) return fail(c, DINFER_EINVAL, "n must be positive");
   CK(launchk(kv_free_kernel, dim3(n), dim3(128), 0, reinterpret_cast<cudaStream_t>(stream), 1, kv_pages(*kc), seqs));
   return DINFER_OK;
@@ -280,6 +289,7 @@ dinfer_status dinfer_kv_free(const dinfer_kv_cache* kc, const int32_t* seqs, int
 dinfer_status dinfer_kv_compact(const dinfer_kv_cache* kc, int32_t* live, void* stream) {
   dinfer_ctx* c = nullptr;
   if (const char* why = kv_bad(kc)) return fail(c, DINFER_EINVAL, "%s", why);
+  if (!ints_ok(live)) return fail(c, DINFER_EINVAL, "misaligned live");
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const KvPages p = kv_pages(*kc);
   CK(launchk(kv_compact_plan_kernel, dim3(1), dim3(kKvPlanThreads), 0, s, 1, p, live));
@@ -301,6 +311,7 @@ dinfer_status dinfer_kv_attention(const dinfer_kv_cache* kc, int32_t layer, cons
   const int64_t per = kc->dtype == DINFER_BF16 ? 8 : 4, row = (int64_t)heads * kc->head_dim;
   if (!rows_ok(q, q_stride, n, row, per) || !rows_ok(o, o_stride, n, row, per))
     return fail(c, DINFER_EINVAL, "q, o: 16-byte aligned rows at least a row apart are needed");
+  if (!ints_ok(seqs)) return fail(c, DINFER_EINVAL, "misaligned seqs");
   OpWs w;
   if (!op_ws(workspace, workspace_bytes, w)) return fail(c, DINFER_EINVAL, "workspace too small");
   if (reinterpret_cast<uintptr_t>(workspace) & 15) return fail(c, DINFER_EINVAL, "workspace must be 16-byte aligned");
@@ -356,6 +367,7 @@ dinfer_status dinfer_op_window_attention(const void* q, const void* k, const voi
   if (!rows_ok(q, q_stride, total_q, qr, per) || !rows_ok(o, o_stride, total_q, qr, per) ||
       !rows_ok(k, k_stride, total_k, kr, per) || !rows_ok(v, v_stride, total_k, kr, per))
     return fail(c, DINFER_EINVAL, "16-byte aligned rows at least a row apart are needed");
+  if (!ints_ok(cu_q, cu_k)) return fail(c, DINFER_EINVAL, "misaligned cu_q or cu_k");
   OpWs w{};
   if (workspace && !op_ws(workspace, workspace_bytes, w)) return fail(c, DINFER_EINVAL, "workspace too small");
   if (reinterpret_cast<uintptr_t>(workspace) & 15) return fail(c, DINFER_EINVAL, "workspace must be 16-byte aligned");

@@ -25,7 +25,8 @@
  *     overlap with one another, each with a workspace of its own.
  *   - What the host cannot see (sequence numbers, page numbers, free pages) is
  *     checked on the device: the entry is skipped, and a bit is set in the
- *     cache's status word (dinfer_kv_status).
+ *     cache's status word (dinfer_kv_status).  int32 operands (sequence numbers,
+ *     row bounds, tables) are 4-byte aligned, or the call is refused.
  */
 #ifndef DINFER_KV_H
 #define DINFER_KV_H

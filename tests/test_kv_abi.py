@@ -162,3 +162,20 @@ def test_the_test_helpers_themselves():
     assert np.array_equal(m.sequence(0, 1)[0], before)
     m.extend([0, 2], [21, 16])
     assert m.status == 16 and m.lens.tolist() == [0, 9, 16] and m.table[2].tolist() == [3, 4, 5, 6]
+
+
+def test_misaligned_index_operands_are_refused(L):
+    c = ctypes.byref(cache())
+    for bad in (P + 1, P + 2, P + 3):
+        for call in (lambda: L.dinfer_kv_extend(c, bad, P, 4, None), lambda: L.dinfer_kv_extend(c, P, bad, 4, None),
+                     lambda: L.dinfer_kv_append(c, 0, bad, None, 4, P, P, 1024, 1024, 4, None),
+                     lambda: L.dinfer_kv_append(c, 0, None, bad, 4, P, P, 1024, 1024, 4, None),
+                     lambda: L.dinfer_kv_fork(c, bad, P, 1, 1, None), lambda: L.dinfer_kv_fork(c, P, bad, 1, 1, None),
+                     lambda: L.dinfer_kv_free(c, bad, 1, None), lambda: L.dinfer_kv_compact(c, bad, None),
+                     lambda: L.dinfer_kv_attention(c, 0, bad, 4, P, P, 4096, 4096, 32, -1, 0, 0.1, P, 1 << 30, None),
+                     lambda: L.dinfer_op_window_attention(P, P, P, P, dinfer.BF16, 2, bad, P, 100, 100, 32, 8, 128, 4096, 1024, 1024,
+                                                          4096, -1, 0, 0, 0.1, None, 0, None),
+                     lambda: L.dinfer_op_window_attention(P, P, P, P, dinfer.BF16, 2, P, bad, 100, 100, 32, 8, 128, 4096, 1024, 1024,
+                                                          4096, -1, 0, 0, 0.1, None, 0, None)):
+            assert call() == dinfer.EINVAL
+            assert "misaligned" in L.dinfer_last_error(None).decode()
