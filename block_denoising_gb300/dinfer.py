@@ -321,6 +321,11 @@ def _ints(t: Optional[torch.Tensor], name: str, gpu: int, n: Optional[int] = Non
                      f"{list(t.shape)} {t.dtype} on {t.device}")
 
 
+def _i32(x: int) -> int:
+    """x, or int32's end next to it: ctypes would take the lower 32 bits of a larger one (a window of 2^32 as 0)."""
+    return x if -0x80000000 <= x <= 0x7fffffff else 0x7fffffff if x > 0 else -0x80000000
+
+
 def _run_on(gpu: int, fn, *args):
     """One library call on torch's current stream of the operands' GPU, which becomes the current one for it."""
     if gpu == torch._C._cuda_getDevice():
@@ -395,7 +400,7 @@ class PagedKV:
         _require(total == also, "k, v: as many rows expected")
         n = rows.shape[0] - 1 if rows is not None else total
         _require(seqs is not None or n <= self.max_seqs, "more entries than sequences")
-        _run_on(gpu, lib().dinfer_kv_append, self._desc, layer, _ints(seqs, "seqs", gpu, n), _ints(rows, "rows", gpu), n,
+        _run_on(gpu, lib().dinfer_kv_append, self._desc, _i32(layer), _ints(seqs, "seqs", gpu, n), _ints(rows, "rows", gpu), n,
                 k.data_ptr(), v.data_ptr(), ks, vs, total)
 
     def fork(self, src: torch.Tensor, dst: torch.Tensor, share: bool = True):
@@ -423,8 +428,8 @@ class PagedKV:
         else:
             also, _, os_ = _rows_of(out, "out", heads, hd, dtype, gpu)
             _require(also == n, "out: as many rows as q expected")
-        _run_on(gpu, lib().dinfer_kv_attention, self._desc, layer, _ints(seqs, "seqs", gpu, n), n, q.data_ptr(),
-                out.data_ptr(), qs, os_, heads, window, sinks, hd ** -0.5 if scale is None else scale,
+        _run_on(gpu, lib().dinfer_kv_attention, self._desc, _i32(layer), _ints(seqs, "seqs", gpu, n), n, q.data_ptr(),
+                out.data_ptr(), qs, os_, heads, _i32(window), _i32(sinks), hd ** -0.5 if scale is None else scale,
                 ws.buf.data_ptr(), ws.nbytes)
         return out
 
@@ -455,6 +460,6 @@ def op_window_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, ws: O
         also, _, os_ = _rows_of(out, "out", heads, hd, dtype, gpu)
         _require(also == rows, "out: as many rows as q expected")
     _run_on(gpu, lib().dinfer_op_window_attention, q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), _DTYPES[dtype],
-            batch, cq, ck, rows, keys, heads, kv_heads, hd, qs, ks, vs, os_, left, right, sinks,
+            batch, cq, ck, rows, keys, heads, kv_heads, hd, qs, ks, vs, os_, _i32(left), _i32(right), _i32(sinks),
             hd ** -0.5 if scale is None else scale, ws.buf.data_ptr(), ws.nbytes)
     return out

@@ -179,3 +179,27 @@ def test_misaligned_index_operands_are_refused(L):
                                                           4096, -1, 0, 0, 0.1, None, 0, None)):
             assert call() == dinfer.EINVAL
             assert "misaligned" in L.dinfer_last_error(None).decode()
+
+
+def test_binding_keeps_numbers_beyond_32_bits_at_their_end(L, monkeypatch):
+    # a window or a side beyond int32 is an open one, not its lower 32 bits; a layer beyond it is refused
+    assert [dinfer._i32(x) for x in (0, -1, 2 ** 31 - 1, 2 ** 31, 2 ** 32, 10 ** 30, -2 ** 31, -2 ** 31 - 1, -2 ** 32)] == \
+        [0, -1, 2 ** 31 - 1, 2 ** 31 - 1, 2 ** 31 - 1, 2 ** 31 - 1, -2 ** 31, -2 ** 31, -2 ** 31]
+    seen = {}
+    monkeypatch.setattr(dinfer, "_run_on", lambda gpu, fn, *args: seen.update({fn.__name__: args}))
+    monkeypatch.setattr(dinfer, "_require", lambda ok, what: None)
+    far, t = 2 ** 32, torch.zeros(4, 2, 64)
+
+    class Ws:
+        buf, nbytes = torch.zeros(8), 32
+
+    kv = object.__new__(dinfer.PagedKV)
+    kv.gpu, kv.head_dim, kv.dtype, kv.kv_heads, kv.max_seqs, kv._desc = t.get_device(), 64, torch.float32, 2, 4, None
+    kv.append(far, t, t)
+    kv.attention(far, t, Ws, window=far, sinks=far)
+    dinfer.op_window_attention(t, t, t, Ws, left=far, right=-far, sinks=far)
+    end = 2 ** 31 - 1
+    assert seen["dinfer_kv_append"][1] == end
+    a = seen["dinfer_kv_attention"]
+    assert (a[1], a[9], a[10]) == (end, end, end)
+    assert seen["dinfer_op_window_attention"][17:20] == (end, -2 ** 31, end)
