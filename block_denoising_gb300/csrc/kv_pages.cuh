@@ -539,6 +539,10 @@ __global__ void __launch_bounds__(256) kv_append_kernel(const KvPages c, const K
       }
     }
   }
+  // what no row shows: bounds out of order, or more rows than there are
+  if (a.rows && blockIdx.x == 0)
+    for (int i = threadIdx.x; i < a.n; i += blockDim.x)
+      if (a.rows[i] < 0 || a.rows[i + 1] < a.rows[i] || a.rows[i + 1] > a.total_rows) c.flag(KV_FULL);
 }
 
 }  // namespace dinfer

@@ -70,7 +70,7 @@ enum {
   DINFER_KV_NO_PAGES = 2, /* not enough free pages */
   DINFER_KV_BAD_PAGE = 4, /* a table entry inside a sequence's length is no page of the cache */
   DINFER_KV_SHARED = 8,   /* rows appended to a page that other sequences hold too */
-  DINFER_KV_FULL = 16     /* a sequence beyond max_pages pages, or more rows than tokens */
+  DINFER_KV_FULL = 16     /* a sequence beyond max_pages pages, more rows than tokens, or row bounds out of order or beyond k's last row */
 };
 
 /* Waits for `stream`, reads the status word into *bits (host, may be NULL)
@@ -99,7 +99,8 @@ dinfer_status dinfer_kv_extend(const dinfer_kv_cache* cache, const int32_t* seqs
  * k, v [total_rows][kv_heads][head_dim], head rows packed, consecutive rows
  * k_stride / v_stride elements apart (multiples of 16 bytes; slices of one
  * projection's output will do), in the cache's type, 16-byte aligned.  rows
- * [n + 1] is non-decreasing; rows of k behind rows[n] are not stored.  Rows
+ * [n + 1] is non-decreasing, from 0 or more to at most total_rows (else
+ * DINFER_KV_FULL); rows of k before rows[0] or behind rows[n] are not stored.  Rows
  * that fall on a page other sequences hold are not stored (DINFER_KV_SHARED).
  * A sequence named twice takes its first entry's (DINFER_KV_BAD_SEQ).
  * 1 <= n <= 1024, without seqs n <= max_seqs. */

@@ -265,3 +265,23 @@ def test_token_weights_in_two_bf16(D, ws, hd, group):
     for s, (x, k, v) in enumerate(cases):
         A.check(o[s:s + 1].double().cpu().numpy(), x[None], k[:, None], v[:, None], np.ones((1, len(k)), bool), 1.0, True,
                 (len(k),), 2.0 ** -16)
+
+
+@pytest.mark.parametrize("rows,stored", [([0, 5, 7], [5, 2]), ([0, 5, 5], [5, 0]), ([2, 4, 7], [2, 3]), ([0, 5, 8], [5, 2]),
+                                         ([0, 9, 9], None), ([0, 5, 3], None), ([-1, 2, 7], None), ([0, 5, 1 << 30], None)])
+def test_row_bounds_of_append(D, rows, stored):
+    # seven rows of k; bounds that name rows it does not have, or run backwards, set the status and touch no other sequence
+    rng = np.random.default_rng(1)
+    x = torch.from_numpy(rng.standard_normal((7, 1, 64)).astype(np.float32)).to(dev)
+    cache = D.PagedKV.empty(layers=1, pages=8, page_size=4, kv_heads=1, head_dim=64, max_seqs=3, max_pages=4, dtype=torch.float32)
+    cache.k.zero_()
+    cache.v.zero_()
+    cache.extend(ints([9, 6, 5]))
+    cache.append(0, x, x, rows=ints(rows), seqs=ints([0, 1]))
+    bad = rows[0] < 0 or sorted(rows) != rows or rows[2] > 7
+    assert status(D, cache) == (D.KV_FULL if bad else 0)
+    assert not cache.k[0, cache.table[2, :2].long()].any()
+    if not bad:
+        for s, n in enumerate(stored):
+            flat = cache.k[0, cache.table[s, :3 - s].long()].flatten(0, 1)[:9 - 3 * s]
+            assert torch.equal(flat[len(flat) - n:], x[rows[s]:rows[s] + n]) and not flat[:len(flat) - n].any()
