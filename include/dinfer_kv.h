@@ -41,8 +41,8 @@ extern "C" {
  * at l * layer_stride + p * page_stride + t * token_stride + h * head_stride
  * + i elements; any order of these dimensions that does not overlap will do.
  * k, v: 16-byte aligned, all strides multiples of 16 bytes.  dtype DINFER_BF16
- * or DINFER_FP32, head_dim 64 or 128, page_size 1 .. 65536,
- * max_pages * page_size < 2^31.
+ * or DINFER_FP32, head_dim 64 or 128, page_size 1 .. 65536, kv_heads 1 .. 1024,
+ * max_pages * page_size < 2^31, page_size * kv_heads * head_dim < 2^31.
  *   table [max_seqs][max_pages]  the pages of each sequence in order, -1 behind its last
  *   lens  [max_seqs]             tokens of each sequence (0: not in use); it holds ceil(len / page_size) pages
  *   refs  [num_pages]            how many sequences hold each page (0: free)
@@ -70,7 +70,7 @@ enum {
   DINFER_KV_NO_PAGES = 2, /* not enough free pages */
   DINFER_KV_BAD_PAGE = 4, /* a table entry inside a sequence's length is no page of the cache */
   DINFER_KV_SHARED = 8,   /* rows appended to a page that other sequences hold too */
-  DINFER_KV_FULL = 16     /* a sequence beyond max_pages pages, more rows than tokens, or row bounds out of order or beyond k's last row */
+  DINFER_KV_FULL = 16     /* a sequence beyond max_pages pages; more rows than tokens, row bounds out of order or behind k's last row */
 };
 
 /* Waits for `stream`, reads the status word into *bits (host, may be NULL)
@@ -114,7 +114,9 @@ dinfer_status dinfer_kv_append(const dinfer_kv_cache* cache, int32_t layer, cons
  * sequences whose slots are rewritten, as block decoding does).  Copies take
  * the tokens alone; the other slots of a new page stay as they were.  Pages
  * are handed out as in dinfer_kv_extend.  One src may be forked many times;
- * a dst named twice takes its first entry.  1 <= n <= 1024. */
+ * a dst named twice takes its first entry.  All src are copied as they were
+ * before the call: a src that is also a dst of the same call is still empty,
+ * and its copy too (chains of forks take a call each).  1 <= n <= 1024. */
 dinfer_status dinfer_kv_fork(const dinfer_kv_cache* cache, const int32_t* src, const int32_t* dst, int32_t n,
                              int32_t share, void* stream);
 
@@ -136,7 +138,11 @@ dinfer_status dinfer_kv_compact(const dinfer_kv_cache* cache, int32_t* live, voi
  * A sequence without tokens, or whose scores are all -inf, gives zeros.  Keys
  * on a table entry that is no page are left out (DINFER_KV_BAD_PAGE).
  * A sequence may be named more than once, and o may be q.  heads % kv_heads == 0,
- * 1 <= n <= 1024, scale > 0.  The keys are split over the GPU and joined in a
+ * heads <= 65536, 1 <= n <= 1024, scale > 0.  The host knows no lengths, so it
+ * refuses calls whose sequences could add up to 2^31 steps of keys: none with
+ *   n * heads * (keys / 16 + 11) < 2^31,
+ * keys = max_pages * page_size or, with a window, window + 1 + sinks if that is
+ * less.  The keys are split over the GPU and joined in a
  * fixed order: the same call gives the same bits. */
 dinfer_status dinfer_kv_attention(const dinfer_kv_cache* cache, int32_t layer, const int32_t* seqs, int32_t n,
                                   const void* q, void* o, int64_t q_stride, int64_t o_stride, int32_t heads,

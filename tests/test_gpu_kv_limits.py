@@ -285,3 +285,20 @@ def test_row_bounds_of_append(D, rows, stored):
         for s, n in enumerate(stored):
             flat = cache.k[0, cache.table[s, :3 - s].long()].flatten(0, 1)[:9 - 3 * s]
             assert torch.equal(flat[len(flat) - n:], x[rows[s]:rows[s] + n]) and not flat[:len(flat) - n].any()
+
+
+@pytest.mark.parametrize("share", [True, False])
+def test_chained_forks_copy_what_was_there_before_the_call(D, share):
+    cache = D.PagedKV.empty(layers=1, pages=12, page_size=4, kv_heads=1, head_dim=64, max_seqs=6, max_pages=4)
+    cache.extend(ints([9, 3]))
+    cache.fork(ints([0, 3, 1]), ints([3, 4, 5]), share=share)  # 3 is still empty: so is 4
+    assert status(D, cache) == 0
+    assert cache.lens.tolist() == [9, 3, 0, 9, 0, 3]
+    assert (cache.table[4] == -1).all()
+    cache.fork(ints([3]), ints([4]), share=share)  # a call each
+    assert status(D, cache) == 0
+    assert cache.lens.tolist() == [9, 3, 0, 9, 9, 3]
+    held = [t[t >= 0].tolist() for t in cache.table]
+    assert [len(h) for h in held] == [3, 1, 0, 3, 3, 1]
+    assert cache.refs.tolist() == [sum(p in h for h in held) for p in range(12)]
+    assert all((held[0][:2] == held[s][:2]) == share and held[0][2] != held[s][2] for s in (3, 4))

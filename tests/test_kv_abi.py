@@ -203,3 +203,48 @@ def test_binding_keeps_numbers_beyond_32_bits_at_their_end(L, monkeypatch):
     a = seen["dinfer_kv_attention"]
     assert (a[1], a[9], a[10]) == (end, end, end)
     assert seen["dinfer_op_window_attention"][17:20] == (end, -2 ** 31, end)
+
+
+def test_limits_that_the_header_states(L):
+    hd = 128
+    c = ctypes.byref(cache(kv_heads=1025, token_stride=1025 * hd, page_stride=16 * 1025 * hd, layer_stride=100 * 16 * 1025 * hd))
+    assert L.dinfer_kv_extend(c, None, None, 4, None) == dinfer.EINVAL
+    wide = 1024 * hd  # 65536 slots of 1024 heads: a page of 2^33 elements
+    c = ctypes.byref(cache(kv_heads=1024, page_size=65536, token_stride=wide, page_stride=65536 * wide, layer_stride=100 * 65536 * wide))
+    assert L.dinfer_kv_extend(c, None, None, 4, None) == dinfer.EINVAL
+    assert "page too large" in L.dinfer_last_error(None).decode()
+    c = ctypes.byref(cache())
+    assert L.dinfer_kv_attention(c, 0, P, 4, P, P, 65544 * hd, 65544 * hd, 65544, -1, 0, 0.1, P, 1 << 30, None) == dinfer.EINVAL
+
+
+@pytest.mark.parametrize("dtype", [dinfer.BF16, dinfer.FP32])
+def test_attention_refuses_what_could_take_too_many_steps(L, dtype):
+    # by the cache's capacity or the window: below the stated bound nothing is refused for it, whatever the group
+    big = ctypes.byref(cache(max_pages=(1 << 27) - 1, max_seqs=1024))
+
+    def steps(size):  # the workspace has room for the counters: the steps are looked at
+        L.dinfer_kv_attention(big, 0, None, 1024, P, P, 4096, 4096, 32, -1, 0, 0.1, P, size, None)
+        return "steps" in L.dinfer_last_error(None).decode()
+
+    # the smallest such workspace: its rest is too small on any GPU, so that no call below gets further than the checks
+    lo, hi = 0, L.dinfer_op_workspace_bytes()
+    while hi - lo > 1:
+        lo, hi = (lo, (lo + hi) // 2) if steps((lo + hi) // 2) else ((lo + hi) // 2, hi)
+    rng = np.random.default_rng(0)
+    refused = 0
+    for _ in range(400):
+        n, kvh, group = int(2 ** rng.uniform(0, 10)), int(2 ** rng.uniform(0, 6)), int(2 ** rng.uniform(0, 6))
+        pages, window, sinks = int(2 ** rng.uniform(4, 27)), int(rng.choice([-1, 0, 4095, 1 << 28])), int(rng.choice([0, 4]))
+        kc = cache(kv_heads=kvh, token_stride=kvh * 128, page_stride=16 * kvh * 128, layer_stride=100 * 16 * kvh * 128, max_pages=pages,
+                   max_seqs=1024, dtype=dtype)
+        if pages * 16 >= 1 << 31:
+            continue
+        st = L.dinfer_kv_attention(ctypes.byref(kc), 0, None, n, P, P, kvh * group * 128, kvh * group * 128, kvh * group, window, sinks,
+                                   0.1, P, hi, None)
+        assert st != dinfer.OK
+        why = L.dinfer_last_error(None).decode()
+        keys = pages * 16 if window < 0 else min(pages * 16, window + 1 + sinks)
+        if "steps" in why:
+            refused += 1
+            assert n * kvh * group * (keys / 16 + 11) >= 1 << 31
+    assert refused > 10
