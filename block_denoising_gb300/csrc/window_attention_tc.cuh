@@ -842,7 +842,7 @@ __global__ void __launch_bounds__(kWtThreads, 1)
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
               if (r0 + u >= rows) break;
-              bool fine = ll[u] <= 3.0e38f;
+              bool fine = true;
               const float inv = ll[u] == 0.f ? 0.f : 1.f / ll[u];
               uint32_t h[kE / 2];
 #pragma unroll
@@ -854,7 +854,7 @@ __global__ void __launch_bounds__(kWtThreads, 1)
               uint32_t* out = reinterpret_cast<uint32_t*>(reinterpret_cast<__nv_bfloat16*>(a.o) +
                                                           (int64_t)(s.q0 + i) * a.o_stride + p.head0 * HD + lane * kE);
               if constexpr (kE == 4) *reinterpret_cast<uint2*>(out) = make_uint2(h[0], h[1]); else *out = h[0];
-              if (__any_sync(0xffffffffu, !fine)) {
+              if (__any_sync(0xffffffffu, !fine && ll[u] > 0.f)) {
                 if (lane == 0) atomicAdd(const_cast<int*>(&redoing), 1);
                 wa_row_exact<__nv_bfloat16, HD>(a, s, i, p.head0);
                 __syncwarp();
@@ -868,9 +868,9 @@ __global__ void __launch_bounds__(kWtThreads, 1)
         const int head = p.head0 + (pair_heads ? x : 0);
         const WaSeq s{p.s.q0, p.s.nq, p.s.k0, p.s.nk};
         if (c > c_before && ok && !last_pv_done(c + 1)) ok = false;
-        const bool some = ok && c > c_before && l != 0.f;  // l NaN: the row is done again below
+        const bool some = ok && c > c_before && l != 0.f;  // l NaN: so is the row
         const float inv = some ? 1.f / l : 0.f;
-        bool fine = ok && l <= 3.0e38f;
+        bool fine = true;
         // whole sectors a store where rows begin at 32 bytes (ragged prompts: 56 us, with 16-byte stores 60)
         const bool wide = ((reinterpret_cast<uintptr_t>(a.o) | (uintptr_t)(a.o_stride * 2)) & 31) == 0;
         __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(a.o) + (int64_t)(s.q0 + i_tile + r) * a.o_stride + head * HD;
@@ -906,7 +906,7 @@ __global__ void __launch_bounds__(kWtThreads, 1)
           }
         }
         tc_fence_before();  // before the hand-over of the next piece's first P, which lets its P V write O
-        uint32_t redo = __ballot_sync(0xffffffffu, ok && !fine && r < rows);
+        uint32_t redo = __ballot_sync(0xffffffffu, ok && !fine && l > 0.f && r < rows);
         __syncwarp();
         if (redo) {
           if (lane == 0) atomicAdd(const_cast<int*>(&redoing), 1);

@@ -302,3 +302,40 @@ def test_chained_forks_copy_what_was_there_before_the_call(D, share):
     assert [len(h) for h in held] == [3, 1, 0, 3, 3, 1]
     assert cache.refs.tolist() == [sum(p in h for h in held) for p in range(12)]
     assert all((held[0][:2] == held[s][:2]) == share and held[0][2] != held[s][2] for s in (3, 4))
+
+
+@pytest.mark.parametrize("dtype,hd,group", TOKENS)
+def test_token_bad_values_touch_their_columns_alone(D, ws, dtype, hd, group):
+    # NaN and infinities that a token sees, with and without a score; in place too.  The other columns are as before
+    rng = np.random.default_rng(hd + group)
+    lens = [1, 60, 3000, 17]
+    put = lambda x: torch.from_numpy(x.astype(np.float32)).to(dtype)  # noqa: E731
+    q = put(rng.standard_normal((4, group, hd)))
+    keys, vals = ([put(rng.standard_normal((n, 1, hd))) for n in lens] for _ in range(2))
+    clean = paged(D, keys, vals).attention(0, q.to(dev), ws)
+    inf, nan = float("inf"), float("nan")
+    for s, j, c, x in ((0, 0, 5, nan), (1, 7, 0, inf), (1, 50, 0, -inf), (1, 59, 9, -inf), (2, 0, hd - 1, nan), (2, 1500, 3, inf),
+                       (2, 1501, 3, inf)):
+        vals[s][j, 0, c] = x
+    keys[3][:, 0, :] = 0.0
+    keys[3][:, 0, 0] = -inf  # scores of -inf alone: zeros, whatever the values
+    vals[3][4:9] = inf
+    q[3, :, 0] = 1.0
+    want = clean.clone()
+    want[0, :, 5], want[1, :, 0], want[1, :, 9], want[2, :, hd - 1], want[2, :, 3], want[3] = nan, nan, -inf, nan, inf, 0.0
+    cache = paged(D, keys, vals)
+    for out in (None, q.to(dev)):
+        o = cache.attention(0, q.to(dev) if out is None else out, ws, out=out)
+        assert torch.equal(torch.isnan(o), torch.isnan(want)) and torch.equal(torch.isinf(o), torch.isinf(want))
+        assert torch.equal(o[torch.isinf(o)], want[torch.isinf(want)])
+        for s, n in enumerate(lens[:3]):
+            bad = ~torch.isfinite(vals[s]).all(0)[0]
+            v, got = vals[s].double(), o[s:s + 1].double().cpu()
+            v[:, :, bad], got[..., bad] = 0.0, 0.0
+            A.check(got.numpy(), q[s:s + 1].double(), keys[s].double(), v, np.ones((1, n), bool), hd ** -0.5,
+                    dtype == torch.bfloat16)
+        assert (o[3] == 0).all()
+    # a NaN key makes the row NaN
+    keys[1][3, 0, 2] = nan
+    o = paged(D, keys, vals).attention(0, q.to(dev), ws)
+    assert torch.isnan(o[1]).all() and torch.equal(torch.isnan(o[2]), torch.isnan(want[2])) and (o[3] == 0).all()
