@@ -395,10 +395,10 @@ dinfer_status dinfer_op_window_attention(const void* q, const void* k, const voi
   a.scale_log2 = scale * 1.4426950408889634f;
   a.status = w.st;
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  // every sequence adds at most one partly filled tile
-  // fp32: tiles of 64 rows once there are more of them than run at once (two an SM), else of 16 (causal, heads of 128:
-  // 1024 rows, 4 heads, 68 tiles of 64: 124 us, 85 with 16 rows; 4096 rows, 4 heads, 260 tiles: 745 and 638 us;
-  // 4096 rows, 16 heads, 1040 tiles: 1.69 and 2.37 ms)
+  // fp32: tiles of 64 rows once there are more full ones of them than run at once (two an SM), else of 16 (causal, heads
+  // of 128: 1024 rows, 4 heads, 68 tiles of 64: 124 us, 85 with 16 rows; 4096 rows, 4 heads, 260 tiles: 745 and 638 us;
+  // 4096 rows, 16 heads, 1040 tiles: 1.69 and 2.37 ms).  By the rows alone: the partly filled tiles that a batch adds
+  // hold few rows, and are the cheaper the fewer rows a tile has.
   const bool small = dtype == DINFER_FP32 && (int64_t)(total_q / 64 + 1) * heads <= 2 * num_sms();
   // bf16: two tiles a CTA, or one while there is an SM for each (1024 causal rows, 16 heads of 128, 144 tiles: 15.2 us
   // alone, 18.3 in pairs; 18 heads, 162 tiles: pairs 19.1)
@@ -406,7 +406,7 @@ dinfer_status dinfer_op_window_attention(const void* q, const void* k, const voi
                    : a.group % 2 == 0                                        ? kWtPairHeads
                                                                              : kWtPairRows;
   const int block_rows = dtype == DINFER_FP32 ? (small ? 16 : 64) : form == kWtPairRows ? 2 * kWtRows : kWtRows;
-  const int blocks = total_q / block_rows + batch;
+  const int blocks = total_q / block_rows + batch;  // every sequence adds at most one partly filled tile
   int64_t ctas = (int64_t)blocks * (dtype == DINFER_BF16 && form == kWtPairHeads ? heads / 2 : heads);
   a.splits = 1;
   if (workspace && (dtype == DINFER_FP32 ? small : form == kWtSingle)) {

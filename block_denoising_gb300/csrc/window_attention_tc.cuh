@@ -24,7 +24,9 @@
 // kernel show.  The links cost more than their work: a product of 128 x 128 x 128
 // (512 cycles) is seen by the next link some 840 cycles after its issue, S comes
 // out of tensor memory in 220 to 350, 64 exponentials a row take 430.  (Times:
-// 8704 causal rows, 16 heads of 128, window 4096.)
+// 8704 causal rows, 16 heads of 128, window 4096, in bursts of calls of some
+// milliseconds at 2070 MHz.  A second of them meets the power cap: 171 us where a
+// burst has 159.)
 //   - With S and P of a tile in the same columns the next S waits until P V is
 //     seen to be done (199 us).  So P has columns of its own and, at head_dim 128,
 //     S_A and S_B take turns in one buffer: S is free again as soon as its rows are
@@ -49,10 +51,13 @@
 //
 // A running maximum is raised only when a tile's maximum exceeds it by more than
 // 8 in log2 (P stays <= 2^8); O and l are rescaled then.  O / l is exact
-// whatever maximum was used.  l sums the rounded P, so O / l weights the keys
-// exactly in proportion.  Tiles that every row sees whole skip the masks; the others
-// test a bit per key (compared bounds instead: 66 us where this took 60, ragged
-// prompts with a window of 256 on both sides).
+// whatever maximum was used.  P is rounded to 8 bits, as the A operand has V's
+// type; a second part for what is lost would be another product per tile.  l sums the
+// rounded P, so O / l weights the keys exactly in proportion (8704 causal rows: off by
+// 2.0e-3 of the output's size; with 32-bit weights the output's own rounding leaves
+// 1.5e-3).  Tiles that every row sees whole skip the masks; the others test a bit per
+// key (compared bounds instead: 66 us where this took 60, ragged prompts with a window
+// of 256 on both sides).
 #pragma once
 #include "window_attention.cuh"
 
