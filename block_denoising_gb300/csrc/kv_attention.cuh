@@ -100,6 +100,9 @@ __device__ __forceinline__ KaSeen ka_seen(int len, int window, int sinks) {
   return r;
 }
 
+// Rounds of `round` keys that `seen` > 0 keys take (up to 2^31 - 1 of them: no sum passes that).
+__host__ __device__ __forceinline__ int ka_rounds(int seen, int round) { return (seen - 1) / round + 1; }
+
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
@@ -475,14 +478,15 @@ __device__ __forceinline__ void ka_row_exact(const T* q, int seen, float scale_l
     qq[e] = ka_f32(q[at + e]);
     o[e] = 0.f;
   }
-  for (int x0 = 0; x0 < seen; x0 += kU) {  // kU keys' loads and sums at once
+  // unsigned: the last step may pass 2^31
+  for (uint32_t x0 = 0; x0 < (uint32_t)seen; x0 += kU) {  // kU keys' loads and sums at once
     float d[kU], vv[kU][kE];
     uint32_t there = 0xffffffffu;
 #pragma unroll
     for (int u = 0; u < kU; ++u) {
       const T *k, *v;
-      if constexpr (kGaps) there ^= (uint32_t)!keys(min(x0 + u, seen - 1), k, v) << u;
-      else keys(min(x0 + u, seen - 1), k, v);
+      if constexpr (kGaps) there ^= (uint32_t)!keys((int)min(x0 + u, (uint32_t)seen - 1u), k, v) << u;
+      else keys((int)min(x0 + u, (uint32_t)seen - 1u), k, v);
       d[u] = 0.f;
 #pragma unroll
       for (int e = 0; e < kE; ++e) {
@@ -497,7 +501,7 @@ __device__ __forceinline__ void ka_row_exact(const T* q, int seen, float scale_l
     float mn = m;
 #pragma unroll
     for (int u = 0; u < kU; ++u) {
-      d[u] = x0 + u < seen ? d[u] * scale_log2 : -INFINITY;  // the last key again: without weight
+      d[u] = x0 + u < (uint32_t)seen ? d[u] * scale_log2 : -INFINITY;  // the last key again: without weight
       if constexpr (kGaps) {
         d[u] = (there >> u) & 1u ? d[u] : -INFINITY;
 #pragma unroll
@@ -585,7 +589,7 @@ __global__ void __launch_bounds__(KaCfg<T, HD, R>::kThreads, 1) kv_attention_ker
       }
       lens[e] = len;
       const int seen = ka_seen(len, a.window, a.sinks).seen;
-      const int x = seen ? ((seen + kKeys * kWarps - 1) / (kKeys * kWarps) * kWarps + kKaPairCost) * pieces : 0;
+      const int x = seen ? (ka_rounds(seen, kKeys * kWarps) * kWarps + kKaPairCost) * pieces : 0;
       cum[e + 1] = x;
       sum += x;
     }
@@ -644,9 +648,9 @@ __global__ void __launch_bounds__(KaCfg<T, HD, R>::kThreads, 1) kv_attention_ker
       load_row = c.table + (size_t)seq_of(load_entry) * c.max_pages;
       seen = ka_seen(lens[load_entry], a.window, a.sinks);
     }
-    const int x = (load.step + warp) * kKeys + lane % kKeys;
-    if (load.step + warp >= load.to || x >= seen.seen) return {0, -1};
-    const int key = x < seen.sink ? x : x - seen.sink + seen.first;
+    const uint32_t at = (uint32_t)(load.step + warp) * kKeys + lane % kKeys;  // unsigned: the last round may pass 2^31
+    if (load.step + warp >= load.to || at >= (uint32_t)seen.seen) return {0, -1};
+    const int x = (int)at, key = x < seen.sink ? x : x - seen.sink + seen.first;
     const int j = (int)c.page_div.div((uint32_t)key);
     return {load_row[j], a.layer_off + (key - j * c.page_size) * c.token_stride + (load.piece / a.subgroups) * c.head_stride};
   };

@@ -5,7 +5,8 @@
 //     twice and leave the search for a page's entry in order;
 //   * the parts of a tile's keys: they follow one another from the first key
 //     tile to the last, each as long as the others but for one tile, up to 2^30
-//     keys in tiles of 32 and as many parts as there are CTAs at once.
+//     keys in tiles of 32 and as many parts as there are CTAs at once;
+//   * the rounds of a token's keys, up to 2^31 - 1 of them.
 #include <cstdio>
 #include <vector>
 
@@ -52,6 +53,12 @@ static void parts_of_keys() {
       }
 }
 
+static void rounds_of_keys() {
+  for (int round : {64, 128, 256})
+    for (int seen : {1, 63, 64, 65, 128, 256, 257, 1 << 20, (1 << 30) + 1, 0x7fffffff - 256, 0x7fffffff - 254, 0x7fffffff - 1, 0x7fffffff})
+      CHECK(ka_rounds(seen, round) == ((long long)seen + round - 1) / round, "%d keys in rounds of %d", seen, round);
+}
+
 int main() {
   const int big = 0x7fffffff;
   for (int found : {0, 1, 7, 1000, 1 << 30, big - 1}) {
@@ -65,6 +72,7 @@ int main() {
     pages_of_a_call({1 << 30, 1 << 30, 1 << 30, 1 << 30, 3, 2}, found);
   }
   parts_of_keys();
+  rounds_of_keys();
   std::printf("kv index checks: %lld failures\n", g_fail);
   return g_fail ? 1 : 0;
 }

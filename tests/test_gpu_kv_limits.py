@@ -236,6 +236,24 @@ def test_token_large_value_without_weight(D, ws, dtype, hd, group):
                 dtype == torch.bfloat16)
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_token_over_2147483647_keys(D, ws, dtype):
+    # One page of one slot, held all the way along a table of 8.6 GB: every weight is the same, and the joins round weights
+    # and outputs alike, each by 2^-24.  fp32 sums in a warp are exact (powers of two).  A tensor product of bf16 may cut
+    # each of its terms off at the last place of the sum it is added to, 2^-23 of it: of N keys a warp (152 SMs, 8 warps:
+    # 1.77e6) the j-th loses up to j 2^-23 of itself, N 2^-24 = 0.106 in the mean.  Then the output's own half step.
+    n = 2 ** 31 - 1
+    k = torch.ones((1, 1, 1, 1, 64), dtype=dtype, device=dev)
+    v = (2.0 ** (torch.arange(64, device=dev) % 8) * (1 - 2 * (torch.arange(64, device=dev) % 2))).to(dtype).view(1, 1, 1, 1, 64)
+    cache = D.PagedKV(k, v, torch.zeros((1, n), dtype=torch.int32, device=dev), ints([n]), ints([1]))
+    q = torch.ones((1, 2, 64), dtype=dtype, device=dev)
+    lost = 0.106 + 2.0 ** -8 if dtype == torch.bfloat16 else 2.0 ** -18
+    for window, sinks in ((-1, 0), (n, 0), (2 ** 31 - 300, 100)):
+        o = cache.attention(0, q, ws, window=window, sinks=sinks)
+        assert status(D, cache) == 0
+        assert (o.double() / v.double().view(64) - 1).abs().max() <= lost
+
+
 def test_bf16_piece_that_lasts_seconds(D):
     # 3.6e8 keys of one row that no workspace lets split, some 3 s: the waits for its end outlast the limit of a wait
     # without progress (about a second)
