@@ -371,6 +371,7 @@ dinfer_status dinfer_op_window_attention(const void* q, const void* k, const voi
   OpWs w{};
   if (workspace && !op_ws(workspace, workspace_bytes, w)) return fail(c, DINFER_EINVAL, "workspace too small");
   if (reinterpret_cast<uintptr_t>(workspace) & 15) return fail(c, DINFER_EINVAL, "workspace must be 16-byte aligned");
+  if (o == q || o == k || o == v) return fail(c, DINFER_EINVAL, "o must not overlap q, k or v");
   if (!kv_setup()) return fail(c, DINFER_ECUDA, "kernel set-up failed");
   WaArgs a{};
   a.q = q;

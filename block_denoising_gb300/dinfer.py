@@ -443,7 +443,8 @@ def op_window_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, ws: O
                         right: int = -1, sinks: int = 0, scale: Optional[float] = None,
                         out: Optional[torch.Tensor] = None):
     """Attention with a sliding window and sinks: q [rows, heads, head_dim], k, v [keys, kv_heads, head_dim];
-    cu_q, cu_k [batch + 1] the sequences' first rows and keys (default: one sequence of all)."""
+    cu_q, cu_k [batch + 1] the sequences' first rows and keys (default: one sequence of all); out must not overlap
+    q, k or v."""
     dtype, gpu = q.dtype, q.get_device()
     _require(dtype in _DTYPES and q.is_cuda and q.dim() == 3, "q: float32 or bfloat16 [rows, heads, head_dim] on a GPU expected")
     hd = q.shape[2]

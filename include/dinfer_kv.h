@@ -155,7 +155,8 @@ dinfer_status dinfer_kv_attention(const dinfer_kv_cache* cache, int32_t layer, c
  * p = (keys - rows) + i and sees key j if
  *   (right < 0 or j <= p + right) and (left < 0 or j >= p - left or j < sinks).
  * left = -1, right = 0 is causal, -1, -1 sees everything (the block decoder's
- * attention), both >= 0 a vicinity.  A row that sees no key gives zeros.
+ * attention), both >= 0 a vicinity.  A row that sees no key, or whose scores are
+ * all -inf, gives zeros.
  * q, o [total_q][heads][head_dim], k, v [total_k][kv_heads][head_dim], dtype
  * DINFER_BF16 or DINFER_FP32, head rows packed, rows x_stride elements apart
  * (multiples of 16 bytes), 16-byte aligned.  cu_q, cu_k: int32 [batch + 1],

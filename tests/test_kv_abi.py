@@ -248,3 +248,13 @@ def test_attention_refuses_what_could_take_too_many_steps(L, dtype):
             refused += 1
             assert n * kvh * group * (keys / 16 + 11) >= 1 << 31
     assert refused > 10
+
+
+def test_window_attention_refuses_to_write_over_its_operands(L):
+    # rows that are done again still want their query
+    at = [P, P + 4096, P + 8192, P + 12288]
+    for i in range(3):
+        for dtype in (dinfer.BF16, dinfer.FP32):
+            assert L.dinfer_op_window_attention(*at[:3], at[i], dtype, 1, None, None, 1, 1, 32, 8, 128, 4096, 1024, 1024, 4096, -1, 0, 0,
+                                                0.1, None, 0, None) == dinfer.EINVAL
+            assert "overlap" in L.dinfer_last_error(None).decode()
