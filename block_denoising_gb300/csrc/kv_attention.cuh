@@ -544,7 +544,8 @@ __device__ __noinline__ void ka_redo(const KaArgs& a, int entry, int len, int he
       [&](int x, const T*& k, const T*& v) {
         const int key = x < s.sink ? x : x - s.sink + s.first, j = (int)c.page_div.div((uint32_t)key), page = row[j];
         const bool ok = page >= 0 && page < c.num_pages;
-        const int64_t off = a.layer_off + (ok ? page : 0) * c.page_stride + (key - j * c.page_size) * c.token_stride + kvh * c.head_stride;
+        const int64_t off = a.layer_off + (ok ? page : 0) * c.page_stride + (key - j * c.page_size) * c.token_stride +
+                            kvh * c.head_stride;
         k = reinterpret_cast<const T*>(c.k + off);
         v = reinterpret_cast<const T*>(c.v + off);
         return ok;

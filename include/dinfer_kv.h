@@ -70,7 +70,8 @@ enum {
   DINFER_KV_NO_PAGES = 2, /* not enough free pages */
   DINFER_KV_BAD_PAGE = 4, /* a table entry inside a sequence's length is no page of the cache */
   DINFER_KV_SHARED = 8,   /* rows appended to a page that other sequences hold too */
-  DINFER_KV_FULL = 16     /* a sequence beyond max_pages pages; more rows than tokens, row bounds out of order or behind k's last row */
+  DINFER_KV_FULL = 16     /* a sequence beyond max_pages pages; more rows than tokens, or row bounds out of order or
+                             behind k's last row */
 };
 
 /* Waits for `stream`, reads the status word into *bits (host, may be NULL)
