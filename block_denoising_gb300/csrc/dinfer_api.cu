@@ -1881,3 +1881,4 @@ extern "C" dinfer_status dinfer_op_gemm_bf16_noalloc_status(void* stream) {
 }
 
 #include "kv_api.cuh"
+#include "step_api.cuh"

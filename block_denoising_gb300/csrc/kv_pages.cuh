@@ -475,6 +475,63 @@ struct KvAppend {
   int vec_shift;
 };
 
+// Where row `row` of an append goes, as an offset within a layer, or -1: it is
+// not stored, and the status says why.  *pos receives its token's place in the
+// sequence.  All lanes of a warp call it alike.
+__device__ __forceinline__ int64_t kv_row_place(const KvPages& c, const int32_t* seqs, const int32_t* rows, int n, int row,
+                                                int* pos = nullptr) {
+  const int lane = threadIdx.x & 31;
+  // the entry: the last one that begins at or before this row
+  int i = row, begin = row, end = row + 1;
+  if (rows) {
+    int lo = 0, hi = n;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (rows[mid] <= row) lo = mid; else hi = mid;
+    }
+    i = lo;
+    begin = rows[lo];
+    end = rows[lo + 1];
+    if (row < begin || row >= end) return -1;  // before the first entry, or rows out of order
+  }
+  const int s = seqs ? seqs[i] : i;
+  if (s < 0 || s >= c.max_seqs) {
+    if (lane == 0) c.flag(KV_BAD_SEQ);
+    return -1;
+  }
+  if (seqs) {  // two entries of one sequence would write the same slots: the first one does
+    bool named = false;
+    for (int e = lane; e < i; e += 32) named |= seqs[e] == s;
+    if (__any_sync(0xffffffffu, named)) {
+      if (lane == 0) c.flag(KV_BAD_SEQ);
+      return -1;
+    }
+  }
+  const int64_t p = (int64_t)c.lens[s] - (end - row);
+  if (p < 0 || p >= (int64_t)c.max_pages * c.page_size) {
+    if (lane == 0) c.flag(KV_FULL);
+    return -1;
+  }
+  if (pos) *pos = (int)p;
+  const int j = (int)c.page_div.div((uint32_t)p), slot = (int)p - j * c.page_size;
+  const int page = c.table[(size_t)s * c.max_pages + j];
+  if (page < 0 || page >= c.num_pages) {
+    if (lane == 0) c.flag(KV_BAD_PAGE);
+    return -1;
+  }
+  if (c.refs[page] > 1) {
+    if (lane == 0) c.flag(KV_SHARED);
+    return -1;
+  }
+  return page * c.page_stride + slot * c.token_stride;
+}
+
+// What no row shows: bounds out of order, or more rows than there are (one block).
+__device__ __forceinline__ void kv_check_bounds(const KvPages& c, const int32_t* rows, int n, int total_rows) {
+  for (int i = threadIdx.x; i < n; i += blockDim.x)
+    if (rows[i] < 0 || rows[i + 1] < rows[i] || rows[i + 1] > total_rows) c.flag(KV_FULL);
+}
+
 __global__ void __launch_bounds__(256) kv_append_kernel(const KvPages c, const KvAppend a) {
   pdl_wait();
   pdl_trigger();
@@ -484,49 +541,10 @@ __global__ void __launch_bounds__(256) kv_append_kernel(const KvPages c, const K
   const int last = a.rows ? min(a.total_rows, a.rows[a.n]) : min(a.total_rows, a.n);
   for (int64_t w = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5; w < 2 * (int64_t)last; w += warps) {
     const int row = (int)(w >> 1);
-    // the entry: the last one that begins at or before this row
-    int i = row, begin = row, end = row + 1;
-    if (a.rows) {
-      int lo = 0, hi = a.n;
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (a.rows[mid] <= row) lo = mid; else hi = mid;
-      }
-      i = lo;
-      begin = a.rows[lo];
-      end = a.rows[lo + 1];
-      if (row < begin || row >= end) continue;  // before the first entry, or rows out of order
-    }
-    const int s = a.seqs ? a.seqs[i] : i;
-    if (s < 0 || s >= c.max_seqs) {
-      if (lane == 0) c.flag(KV_BAD_SEQ);
-      continue;
-    }
-    if (a.seqs) {  // two entries of one sequence would write the same slots: the first one does
-      bool named = false;
-      for (int e = lane; e < i; e += 32) named |= a.seqs[e] == s;
-      if (__any_sync(0xffffffffu, named)) {
-        if (lane == 0) c.flag(KV_BAD_SEQ);
-        continue;
-      }
-    }
-    const int64_t p = (int64_t)c.lens[s] - (end - row);
-    if (p < 0 || p >= (int64_t)c.max_pages * c.page_size) {
-      if (lane == 0) c.flag(KV_FULL);
-      continue;
-    }
-    const int j = (int)c.page_div.div((uint32_t)p), slot = (int)p - j * c.page_size;
-    const int page = c.table[(size_t)s * c.max_pages + j];
-    if (page < 0 || page >= c.num_pages) {
-      if (lane == 0) c.flag(KV_BAD_PAGE);
-      continue;
-    }
-    if (c.refs[page] > 1) {
-      if (lane == 0) c.flag(KV_SHARED);
-      continue;
-    }
+    const int64_t at = kv_row_place(c, a.seqs, a.rows, a.n, row);
+    if (at < 0) continue;
     const uint4* from = (w & 1) ? a.v + row * a.v_stride : a.k + row * a.k_stride;
-    uint4* to = ((w & 1) ? c.v : c.k) + a.layer_off + page * c.page_stride + slot * c.token_stride;
+    uint4* to = ((w & 1) ? c.v : c.k) + a.layer_off + at;
     for (int x0 = 0; x0 < row_vecs; x0 += 32 * 8) {
       uint4 x[8];
 #pragma unroll
@@ -539,10 +557,7 @@ __global__ void __launch_bounds__(256) kv_append_kernel(const KvPages c, const K
       }
     }
   }
-  // what no row shows: bounds out of order, or more rows than there are
-  if (a.rows && blockIdx.x == 0)
-    for (int i = threadIdx.x; i < a.n; i += blockDim.x)
-      if (a.rows[i] < 0 || a.rows[i + 1] < a.rows[i] || a.rows[i + 1] > a.total_rows) c.flag(KV_FULL);
+  if (a.rows && blockIdx.x == 0) kv_check_bounds(c, a.rows, a.n, a.total_rows);
 }
 
 }  // namespace dinfer

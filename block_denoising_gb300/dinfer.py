@@ -40,6 +40,26 @@ class DinferError(RuntimeError):
         self.status = status
 
 
+class Rope(ctypes.Structure):
+    """Rotary positions (dinfer_rope): the first rot_dim elements of a head turn in pairs, "half" (i, i + rot_dim / 2) or
+    "pairs" (2 i, 2 i + 1), by position * theta^(-2 i / rot_dim), scaled as "none", "linear", "base" or "bands"."""
+    _fields_ = [(n, ctypes.c_int32) for n in ("rot_dim", "layout", "scaling", "trained")] + \
+               [(n, ctypes.c_double) for n in ("theta", "factor", "slow", "fast", "magnitude")] + \
+               [("turns", ctypes.c_uint64 * 128), ("ready", ctypes.c_uint64)]
+    LAYOUTS = {"half": 0, "pairs": 1}
+    SCALINGS = {"none": 0, "linear": 1, "base": 2, "bands": 3}
+
+    def __init__(self, rot_dim: int, theta: float = 10000.0, layout: str = "half", scaling: str = "none",
+                 factor: float = 1.0, trained: int = 0, slow: float = 1.0, fast: float = 32.0, magnitude: float = 1.0):
+        for name, kinds, what in (("layout", self.LAYOUTS, layout), ("scaling", self.SCALINGS, scaling)):
+            if what not in kinds:
+                raise ValueError(f"{name}: one of {', '.join(kinds)} expected, got {what!r}")
+        super().__init__(_i32(rot_dim), self.LAYOUTS[layout], self.SCALINGS[scaling], _i32(trained), theta, factor, slow,
+                         fast, magnitude)
+        self._as_parameter_ = ctypes.addressof(self)
+        _check(lib().dinfer_rope_init(self._as_parameter_))
+
+
 class KvCache(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in ("k", "v")] + \
                [(n, ctypes.c_int64) for n in ("layer_stride", "page_stride", "token_stride", "head_stride")] + \
@@ -118,6 +138,16 @@ def lib() -> ctypes.CDLL:
     L.dinfer_op_window_attention.argtypes = [vp, vp, vp, vp, i32, i32, vp, vp, i32, i32, i32, i32, i32, i64, i64, i64,
                                              i64, i32, i32, i32, f32, vp, sz, vp]
     L.dinfer_op_window_attention.restype = i32
+    L.dinfer_rope_init.argtypes = [vp]
+    L.dinfer_rope_init.restype = i32
+    L.dinfer_op_rope.argtypes = [vp, vp, i32, vp, vp, i32, i32, i32, i32, i64, i64, vp]
+    L.dinfer_op_rope.restype = i32
+    L.dinfer_kv_append_rope.argtypes = [vp, i32, vp, vp, vp, vp, i32, vp, vp, i32, i64, i64, vp, vp, i64, i64, i32, vp]
+    L.dinfer_kv_append_rope.restype = i32
+    L.dinfer_kv_prefix_attention.argtypes = [vp, i32, vp, i32, vp, vp, i32, vp, vp, i64, i64, i32, f32, vp, sz, vp]
+    L.dinfer_kv_prefix_attention.restype = i32
+    L.dinfer_op_sample.argtypes = [vp, i32, i32, i32, i64, vp, vp, vp, vp, vp, vp, vp, vp]
+    L.dinfer_op_sample.restype = i32
     _lib = L
     return L
 
@@ -403,6 +433,35 @@ class PagedKV:
         _run_on(gpu, lib().dinfer_kv_append, self._desc, _i32(layer), _ints(seqs, "seqs", gpu, n), _ints(rows, "rows", gpu), n,
                 k.data_ptr(), v.data_ptr(), ks, vs, total)
 
+    def append_rope(self, layer: int, rope: Rope, k: torch.Tensor, v: torch.Tensor, q: Optional[torch.Tensor] = None,
+                    rows: Optional[torch.Tensor] = None, seqs: Optional[torch.Tensor] = None,
+                    positions: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None):
+        """append with the keys, and the rows' queries q [rows, heads, head_dim], rotated at their tokens' places (or at
+        positions [rows]); returns the rotated queries (out may be q)."""
+        gpu, hd, dtype = self.gpu, self.head_dim, self.dtype
+        total, _, ks = _rows_of(k, "k", self.kv_heads, hd, dtype, gpu)
+        also, _, vs = _rows_of(v, "v", self.kv_heads, hd, dtype, gpu)
+        _require(total == also, "k, v: as many rows expected")
+        n = rows.shape[0] - 1 if rows is not None else total
+        _require(seqs is not None or n <= self.max_seqs, "more entries than sequences")
+        q_p = out_p = None
+        heads = qs = os_ = 0
+        if q is not None:
+            also, heads, qs = _rows_of(q, "q", None, hd, dtype, gpu)
+            _require(also == total, "q: as many rows as k expected")
+            if out is None:
+                out, os_ = torch.empty_like(q, memory_format=torch.contiguous_format), heads * hd
+            else:
+                also, _, os_ = _rows_of(out, "out", heads, hd, dtype, gpu)
+                _require(also == total, "out: as many rows as q expected")
+            q_p, out_p = q.data_ptr(), out.data_ptr()
+        else:
+            _require(out is None, "out: without q there is nothing for it")
+        _run_on(gpu, lib().dinfer_kv_append_rope, self._desc, _i32(layer), rope, _ints(positions, "positions", gpu, total),
+                _ints(seqs, "seqs", gpu, n), _ints(rows, "rows", gpu), n, q_p, out_p, heads, qs, os_, k.data_ptr(),
+                v.data_ptr(), ks, vs, total)
+        return out
+
     def fork(self, src: torch.Tensor, dst: torch.Tensor, share: bool = True):
         """Sequences dst (not in use) become copies of src, sharing the full pages or copying all of them."""
         n = src.shape[0]
@@ -431,6 +490,26 @@ class PagedKV:
         _run_on(gpu, lib().dinfer_kv_attention, self._desc, _i32(layer), _ints(seqs, "seqs", gpu, n), n, q.data_ptr(),
                 out.data_ptr(), qs, os_, heads, _i32(window), _i32(sinks), hd ** -0.5 if scale is None else scale,
                 ws.buf.data_ptr(), ws.nbytes)
+        return out
+
+    def prefix_attention(self, layer: int, q: torch.Tensor, ws: OpWorkspace, prefix: torch.Tensor,
+                         groups: Optional[torch.Tensor] = None, scale: Optional[float] = None,
+                         seqs: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None):
+        """attention over all keys where entries groups[g] .. groups[g + 1] - 1 (default: all) hold the same pages for their
+        first prefix[g] tokens, which are read once for the group (out may be q)."""
+        hd, dtype, gpu = self.head_dim, self.dtype, self.gpu
+        n, heads, qs = _rows_of(q, "q", None, hd, dtype, gpu)
+        _require(seqs is not None or n <= self.max_seqs, "q: more rows than sequences")
+        _require(ws.buf.get_device() == gpu, "ws: a workspace on the cache's device expected")
+        n_groups = 1 if groups is None else groups.shape[0] - 1
+        if out is None:
+            out, os_ = torch.empty_like(q, memory_format=torch.contiguous_format), heads * hd
+        else:
+            also, _, os_ = _rows_of(out, "out", heads, hd, dtype, gpu)
+            _require(also == n, "out: as many rows as q expected")
+        _run_on(gpu, lib().dinfer_kv_prefix_attention, self._desc, _i32(layer), _ints(seqs, "seqs", gpu, n), n,
+                _ints(groups, "groups", gpu), _ints(prefix, "prefix", gpu, n_groups), n_groups, q.data_ptr(), out.data_ptr(), qs, os_,
+                heads, hd ** -0.5 if scale is None else scale, ws.buf.data_ptr(), ws.nbytes)
         return out
 
     def check(self):
@@ -464,3 +543,53 @@ def op_window_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, ws: O
             batch, cq, ck, rows, keys, heads, kv_heads, hd, qs, ks, vs, os_, _i32(left), _i32(right), _i32(sinks),
             hd ** -0.5 if scale is None else scale, ws.buf.data_ptr(), ws.nbytes)
     return out
+
+
+# ---------------------------------------------------------------------------
+# a serving loop's other steps (include/dinfer_ops.h)
+# ---------------------------------------------------------------------------
+def op_rope(x: torch.Tensor, rope: Rope, positions: Optional[torch.Tensor] = None, first: int = 0,
+            out: Optional[torch.Tensor] = None):
+    """x [rows, heads, head_dim] rotated at positions [rows] (default: first, first + 1, ...); out may be x."""
+    dtype, gpu = x.dtype, x.get_device()
+    _require(dtype in _DTYPES and x.is_cuda and x.dim() == 3, "x: float32 or bfloat16 [rows, heads, head_dim] on a GPU expected")
+    hd = x.shape[2]
+    rows, heads, xs = _rows_of(x, "x", None, hd, dtype, gpu)
+    if out is None:
+        out, os_ = torch.empty_like(x, memory_format=torch.contiguous_format), heads * hd
+    else:
+        also, _, os_ = _rows_of(out, "out", heads, hd, dtype, gpu)
+        _require(also == rows, "out: as many rows as x expected")
+    _run_on(gpu, lib().dinfer_op_rope, x.data_ptr(), out.data_ptr(), _DTYPES[dtype], rope, _ints(positions, "positions", gpu, rows),
+            _i32(first), rows, heads, hd, xs, os_)
+    return out
+
+
+def _per_row(t: Optional[torch.Tensor], name: str, gpu: int, n: int, dtype=torch.float32):
+    """Address of a contiguous vector of one number a row on the GPU (None: NULL)."""
+    if t is None:
+        return None
+    if t.dtype is dtype and t.dim() == 1 and t.shape[0] == n and t.get_device() == gpu and t.is_contiguous():
+        return t.data_ptr()
+    raise ValueError(f"{name}: a contiguous {dtype} vector of {n} on cuda:{gpu} expected, got {list(t.shape)} {t.dtype} on {t.device}")
+
+
+def op_sample(logits: torch.Tensor, u: torch.Tensor, temperature: Optional[torch.Tensor] = None,
+              top_k: Optional[torch.Tensor] = None, top_p: Optional[torch.Tensor] = None,
+              min_p: Optional[torch.Tensor] = None, tok: Optional[torch.Tensor] = None,
+              conf: Optional[torch.Tensor] = None):
+    """A token per row of logits [rows, vocab] by temperature, top_k (int32), top_p and min_p (each [rows] or None) from
+    u [rows] in [0, 1), and its confidence: (tok [rows] int32, conf [rows] float32)."""
+    dtype, gpu = logits.dtype, logits.get_device()
+    _require(dtype in _DTYPES and logits.is_cuda and logits.dim() == 2 and (logits.stride(1) == 1 or logits.shape[1] == 1),
+             "logits: float32 or bfloat16 [rows, vocab] with packed rows on a GPU expected")
+    rows, vocab = logits.shape
+    if tok is None:
+        tok = torch.empty(rows, dtype=torch.int32, device=logits.device)
+    if conf is None:
+        conf = torch.empty(rows, dtype=torch.float32, device=logits.device)
+    _run_on(gpu, lib().dinfer_op_sample, logits.data_ptr(), _DTYPES[dtype], rows, vocab, logits.stride(0),
+            _per_row(temperature, "temperature", gpu, rows), _per_row(top_k, "top_k", gpu, rows, torch.int32),
+            _per_row(top_p, "top_p", gpu, rows), _per_row(min_p, "min_p", gpu, rows), _per_row(u, "u", gpu, rows),
+            _per_row(tok, "tok", gpu, rows, torch.int32), _per_row(conf, "conf", gpu, rows))
+    return tok, conf

@@ -109,6 +109,19 @@ dinfer_status dinfer_kv_append(const dinfer_kv_cache* cache, int32_t layer, cons
                                int32_t n, const void* k, const void* v, int64_t k_stride, int64_t v_stride,
                                int32_t total_rows, void* stream);
 
+/* dinfer_kv_append whose keys are rotated on the way, each at its token's place in
+ * its sequence, or at positions[row] where positions [total_rows] is given.  q
+ * (optional, NULL with q_out): [total_rows][heads][head_dim], the rows' queries, go
+ * rotated alike to q_out, which is q, with the same stride, or overlaps no operand.  q,
+ * q_out: head rows packed, rows q_stride / q_out_stride elements apart, 1 <= heads <=
+ * 65536, in the cache's type and alignment.  A row that is not stored (see
+ * dinfer_kv_append) leaves its row of q_out as it was.  rope as in dinfer_op_rope. */
+dinfer_status dinfer_kv_append_rope(const dinfer_kv_cache* cache, int32_t layer, const dinfer_rope* rope,
+                                    const int32_t* positions, const int32_t* seqs, const int32_t* rows, int32_t n,
+                                    const void* q, void* q_out, int32_t heads, int64_t q_stride, int64_t q_out_stride,
+                                    const void* k, const void* v, int64_t k_stride, int64_t v_stride,
+                                    int32_t total_rows, void* stream);
+
 /* Sequence dst[i], which must not be in use, becomes a copy of sequence
  * src[i].  share != 0: the full pages are held by both, the partly filled last
  * one is copied in every layer.  share == 0: every page is copied (for
@@ -149,6 +162,24 @@ dinfer_status dinfer_kv_attention(const dinfer_kv_cache* cache, int32_t layer, c
                                   const void* q, void* o, int64_t q_stride, int64_t o_stride, int32_t heads,
                                   int32_t window, int32_t sinks, float scale, void* workspace, size_t workspace_bytes,
                                   void* stream);
+
+/* dinfer_kv_attention (all keys) where groups of entries begin alike: entries
+ * groups[g] .. groups[g + 1] - 1 (groups NULL with n_groups 1: all) hold the same pages
+ * for their first prefix[g] tokens, as dinfer_kv_fork with share leaves them; those keys
+ * and values are read once for the whole group.  Of prefix[g] the whole pages count that
+ * every sequence of the group with tokens has beyond its last token's own; 0 or less, or a
+ * group with a single such sequence, shares nothing.  The pages read are those of the
+ * group's first sequence with tokens; another that does not hold them sets
+ * DINFER_KV_BAD_SEQ.  Entries of no group are computed by themselves, bounds out of
+ * order make a group empty (DINFER_KV_FULL).  groups [n_groups + 1], prefix [n_groups],
+ * 1 <= n_groups, n + n_groups <= 1024; everything else as in dinfer_kv_attention, but that
+ * the sums of all rows have to fit the workspace:
+ *   n * heads * (8 * head_dim + 16) bytes beside 64 MiB, and
+ *   (2 n + n_groups) * heads * (max_pages * page_size / 16 + 11) < 2^31. */
+dinfer_status dinfer_kv_prefix_attention(const dinfer_kv_cache* cache, int32_t layer, const int32_t* seqs, int32_t n,
+                                         const int32_t* groups, const int32_t* prefix, int32_t n_groups, const void* q,
+                                         void* o, int64_t q_stride, int64_t o_stride, int32_t heads, float scale,
+                                         void* workspace, size_t workspace_bytes, void* stream);
 
 /* Attention of many rows with a sliding window and sinks, over `batch` ragged
  * sequences:  sequence b has the query rows cu_q[b] .. cu_q[b + 1] - 1 and the

@@ -106,6 +106,74 @@ dinfer_status dinfer_op_gemm_bf16_noalloc(const void* X, const void* W, float* Y
  * DINFER_OK that no wait timed out.  Allocates nothing. */
 dinfer_status dinfer_op_gemm_bf16_noalloc_status(void* stream);
 
+/* Rotary positions.  The first rot_dim elements of a head turn in pairs:
+ *   (a, b) -> magnitude * (a cos t - b sin t, a sin t + b cos t),  t = position * f_i,
+ * pair i < rot_dim / 2 being elements (i, i + rot_dim / 2) (DINFER_ROPE_HALF, the
+ * block decoder's) or (2 i, 2 i + 1) (DINFER_ROPE_PAIRS); the others stay as they
+ * are.  f_i = theta^(-2 i / rot_dim), for contexts longer than the trained one scaled as
+ *   DINFER_ROPE_NONE    f
+ *   DINFER_ROPE_LINEAR  f / factor (positions interpolated)
+ *   DINFER_ROPE_BASE    f factor^(-2 i / (rot_dim - 2)): theta grows so that the
+ *                       slowest pair is slowed by factor, the fastest not at all
+ *   DINFER_ROPE_BANDS   g f + (1 - g) f / factor, g = (trained f / 2 pi - slow) / (fast - slow)
+ *                       clamped to 0 .. 1: by how often a pair turns within `trained` tokens
+ * rot_dim even, 2 .. 256 and at most head_dim; theta, factor, magnitude > 0 and finite; for BANDS
+ * trained >= 1 and 0 <= slow < fast (else these are not read); f at most 2^16.  Angles are taken
+ * modulo a turn in 64 bits: positions are any int32, and -p undoes p. */
+enum { DINFER_ROPE_HALF = 0, DINFER_ROPE_PAIRS = 1 };
+enum { DINFER_ROPE_NONE = 0, DINFER_ROPE_LINEAR = 1, DINFER_ROPE_BASE = 2, DINFER_ROPE_BANDS = 3 };
+typedef struct dinfer_rope {
+  int32_t rot_dim, layout, scaling, trained;
+  double theta, factor, slow, fast, magnitude;
+  /* filled by dinfer_rope_init: turns per position of each pair, in 2^-64ths, and
+   * a mark that they are there */
+  uint64_t turns[128];
+  uint64_t ready;
+} dinfer_rope;
+
+/* Checks the fields above and fills the frequencies (host memory, once for a
+ * model's rotation: 64 powers are longer than a small call).  The calls that take a
+ * dinfer_rope copy it, and refuse one that is not filled; after a field changed it is
+ * to be filled again.  Errors: DINFER_EINVAL. */
+dinfer_status dinfer_rope_init(dinfer_rope* rope);
+
+/* y[r, h, :] = rotation of x[r, h, :] at positions[r] (NULL: first + r).
+ * x, y [rows][heads][head_dim], dtype DINFER_BF16 or DINFER_FP32, head rows packed,
+ * rows x_stride / y_stride elements apart (multiples of 16 bytes: the query and key
+ * part of one projection's output is one call), 16-byte aligned; y is x, with the
+ * same stride, or does not overlap it.  head_dim * element size a multiple of 16
+ * bytes, head_dim <= 256, 1 <= heads <= 65536, 1 <= rows <= 2^30, first + rows <= 2^31
+ * where positions is NULL.  Computed in fp32, rounded once.  Stands in front of
+ * dinfer_op_window_attention; dinfer_kv_append_rope rotates on the way to a cache. */
+dinfer_status dinfer_op_rope(const void* x, void* y, int32_t dtype, const dinfer_rope* rope, const int32_t* positions,
+                             int32_t first, int32_t rows, int32_t heads, int32_t head_dim, int64_t x_stride,
+                             int64_t y_stride, void* stream);
+
+/* A token per row of logits, drawn with a given number, and its confidence.
+ * logits [rows][vocab], dtype DINFER_BF16 or DINFER_FP32, rows `stride` elements
+ * apart (what dinfer_op_lmhead_bf16 writes, for one).  Per row, each operand [rows]
+ * or NULL (off):
+ *   temperature (NULL: 1)   w = e^((l - largest) / temperature); 0, less or NaN: the
+ *                           largest logit's token (ties: lowest index)
+ *   top_k (<= 0: off)       of the tokens in order of their logits (ties: lowest
+ *                           index first), the first top_k
+ *   top_p (>= 1, NaN: off)  of those, the first ones up to the one that reaches
+ *                           top_p of their weight
+ *   min_p (<= 0, NaN: off)  of those, the ones whose weight is at least min_p (at
+ *                           most 1) of the largest
+ *   u                       in [0, 1) (else the next such number): the token is the
+ *                           first, by index, at which the sum of the kept weights
+ *                           exceeds u of their total
+ * A weight below 2^-44 of the largest counts as 0.  Logits of -inf and NaN are not
+ * there; where one is +inf, only those that are count.  conf (NULL: not wanted) is
+ * the token's softmax probability at temperature 1, nothing left out: the decoder's
+ * confidence.  A row without a logit gives tok -1, conf 0.  Sums of weights are
+ * exact: the same call gives the same tokens.
+ * 1 <= rows <= 2^20, 1 <= vocab <= 2^19, stride >= vocab (rows > 1). */
+dinfer_status dinfer_op_sample(const void* logits, int32_t dtype, int32_t rows, int32_t vocab, int64_t stride,
+                               const float* temperature, const int32_t* top_k, const float* top_p, const float* min_p,
+                               const float* u, int32_t* tok, float* conf, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
