@@ -75,7 +75,23 @@ struct KaCfg {
 };
 static_assert(KaCfg<float, 128, 8>::kSmemShared + 256 <= 232448, "attention shared memory above 227 KB");
 
-// dinfer_kv_prefix_attention: what its kernels share (kv_prefix.cuh).
+// dinfer_kv_prefix_attention: what its kernels share (kv_prefix.cuh, kv_prefix_tc.cuh).
+constexpr int kPtCost = 2;  // a segment's beginning and end on the tensor cores, in tiles of 128 keys
+// A group as the tensor cores take it: its units lie at places place0 .. of the call's
+// (a unit: kPtCost and its key tiles), its rows' sums from row0 on.
+struct alignas(16) KpGroup {
+  int place0, row0, e0, rows;  // e0: its first entry; rows: queries per key head
+  int shared, leader, pad0, pad1;  // tokens that it shares; the sequence whose table holds them
+  __device__ __forceinline__ int tiles() const { return (shared + 127) / 128; }
+  __device__ __forceinline__ int size() const { return tiles() + kPtCost; }
+  __device__ __forceinline__ int pairs() const { return (rows + 255) / 256; }  // units per key head
+  // rows of sums per key head and CTA: a unit of at most 128 rows has two for each
+  __device__ __forceinline__ int sums() const {
+    const int last = rows - (pairs() - 1) * 256;
+    return (pairs() - 1) * 256 + (last <= 128 ? 2 * last : last);
+  }
+};
+
 struct KpArgs {
   const int32_t* bounds;  // [groups + 1] first entries; NULL: one group of all
   const int32_t* prefix;  // [groups]
@@ -83,7 +99,13 @@ struct KpArgs {
   int with_prefix;  // the prefixes' keys are this kernel's as well
   float* o_part;    // [2][entries * heads][head_dim]: sums over the prefix's keys and over the entry's own
   float2* ml_part;  // [2][entries * heads]: their (m, l)
-  int2* info;       // [entries]: keys that are read for the whole group, the entry whose table holds them
+  int4* info;       // [entries]: keys that are read for the whole group, the entry whose table holds them, the group
+  // the prefixes on the tensor cores (with_prefix 0): the groups and, behind them, the end
+  // (NULL: no such kernel); sums [rows of all units + 256 per CTA]
+  KpGroup* plan;
+  float* seg_o;
+  float2* seg_ml;
+  int seg_ctas;
 };
 
 struct KaArgs {
@@ -582,13 +604,9 @@ __device__ __noinline__ void ka_redo(const KaArgs& a, int entry, int len, int he
 // --------------------------------------------------------------------------
 // shared prefixes: what every kernel of a call works out from the tables
 // --------------------------------------------------------------------------
-// Entries of group g, as the call gives them; bounds out of order make a group empty.
+// Entries of group g, as the call gives them (in order, or no group shares anything).
 __device__ __forceinline__ int kp_first(const KaArgs& a, int g) { return a.p.bounds ? a.p.bounds[g] : 0; }
-__device__ __forceinline__ int kp_members(const KaArgs& a, int g) {
-  if (!a.p.bounds) return a.n;
-  const int x = a.p.bounds[g], y = a.p.bounds[g + 1];
-  return x >= 0 && y <= a.n && x <= y ? y - x : 0;
-}
+__device__ __forceinline__ int kp_members(const KaArgs& a, int g) { return a.p.bounds ? a.p.bounds[g + 1] - a.p.bounds[g] : a.n; }
 
 // lens, firsts, subs [groups + n].  For group g: tokens that it shares (whole pages,
 // fewer than any of its sequences has, 0 where fewer than two have any), an entry whose
@@ -598,11 +616,14 @@ template <int kThreads>
 __device__ __forceinline__ void kp_plan(const KaArgs& a, int* lens, int* firsts, int* subs, int rows) {
   const KvPages& c = a.c;
   const int groups = a.p.groups, tid = threadIdx.x;
+  bool order = true;
   for (int g = tid; g < groups; g += kThreads) {
     lens[g] = firsts[g] = 0x7fffffff;
     subs[g] = 0;
+    if (a.p.bounds) order = order && a.p.bounds[g] >= 0 && a.p.bounds[g] <= a.p.bounds[g + 1] && a.p.bounds[g + 1] <= a.n;
   }
-  __syncthreads();
+  order = __syncthreads_and(order);
+  if (!order && blockIdx.x == 0 && tid == 0) c.flag(KV_FULL);
   for (int e = tid; e < a.n; e += kThreads) {
     const int s = a.seqs ? a.seqs[e] : e;
     int len = s >= 0 && s < c.max_seqs ? c.lens[s] : -1;
@@ -618,8 +639,7 @@ __device__ __forceinline__ void kp_plan(const KaArgs& a, int* lens, int* firsts,
         if (a.p.bounds[mid] <= e) g = mid; else hi = mid;
       }
     }
-    const int x = kp_first(a, g);
-    if (e < x || e >= x + kp_members(a, g)) g = -1;
+    if (!order || e < kp_first(a, g) || e >= kp_first(a, g) + kp_members(a, g)) g = -1;
     lens[groups + e] = len;
     subs[groups + e] = g;
     if (g >= 0 && len > 0) {
@@ -630,13 +650,11 @@ __device__ __forceinline__ void kp_plan(const KaArgs& a, int* lens, int* firsts,
   }
   __syncthreads();
   for (int g = tid; g < groups; g += kThreads) {
-    const int members = kp_members(a, g);
-    if (a.p.bounds && blockIdx.x == 0 && (a.p.bounds[g] < 0 || a.p.bounds[g + 1] > a.n || a.p.bounds[g + 1] < a.p.bounds[g])) c.flag(KV_FULL);
     int shared = 0;
     if (subs[g] > 1) shared = (int)c.page_div.div((uint32_t)max(0, min(a.p.prefix[g], lens[g] - 1))) * c.page_size;
     lens[g] = shared;
     if (shared == 0) firsts[g] = 0;
-    subs[g] = (int)(((int64_t)members * a.group + rows - 1) / rows);
+    subs[g] = shared ? (int)(((int64_t)kp_members(a, g) * a.group + rows - 1) / rows) : 1;
   }
   __syncthreads();
   for (int e = tid; e < a.n; e += kThreads) {
@@ -646,6 +664,55 @@ __device__ __forceinline__ void kp_plan(const KaArgs& a, int* lens, int* firsts,
   }
   __syncthreads();
 }
+
+__device__ __forceinline__ KpGroup kp_group(const KaArgs& a, int g) {
+  KpGroup r;
+  *reinterpret_cast<int4*>(&r.place0) = __ldcg(reinterpret_cast<const int4*>(a.p.plan + g));
+  *reinterpret_cast<int4*>(&r.shared) = __ldcg(reinterpret_cast<const int4*>(a.p.plan + g) + 1);
+  return r;
+}
+
+// Writes the groups for the tensor cores: one warp.
+__device__ __forceinline__ void kp_groups(const KaArgs& a, const int* lens, const int* firsts) {
+  const int lane = threadIdx.x & 31;
+  int place = 0, row = 0;
+  for (int g0 = 0; g0 <= a.p.groups; g0 += 32) {
+    const int g = g0 + lane;
+    KpGroup r{};
+    if (g < a.p.groups && lens[g] > 0) {
+      const int e = firsts[g];
+      r.shared = lens[g];
+      r.leader = a.seqs ? a.seqs[e] : e;
+      r.e0 = kp_first(a, g);
+      r.rows = kp_members(a, g) * a.group;
+    }
+    const int places = r.shared ? a.c.kv_heads * r.pairs() * r.size() : 0, rows = r.shared ? a.c.kv_heads * r.sums() : 0;
+    int p = places, q = rows;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int u = __shfl_up_sync(0xffffffffu, p, o), v = __shfl_up_sync(0xffffffffu, q, o);
+      if (lane >= o) {
+        p += u;
+        q += v;
+      }
+    }
+    r.place0 = place + p - places;
+    r.row0 = row + q - rows;
+    if (g <= a.p.groups) a.p.plan[g] = r;
+    place += __shfl_sync(0xffffffffu, p, 31);
+    row += __shfl_sync(0xffffffffu, q, 31);
+  }
+}
+
+// How the places of all units are dealt to the CTAs; returns how many there are.
+__device__ __forceinline__ int kp_split(const KaArgs& a, KaSplit& split) {
+  const int total = __ldcg(&a.p.plan[a.p.groups].place0);
+  split.make(total, max(1, min(a.p.seg_ctas, total / (2 * kPtCost))));
+  return total;
+}
+// Where the sums of a unit's rows begin, for CTA 0 (each CTA's are 256 rows on: a unit has at most 256, and CTAs
+// share at most one).
+__device__ __forceinline__ int kp_row(const KaArgs& a, const KpGroup& g, int kvh, int row) { return g.row0 + kvh * g.sums() + row; }
 
 // kShared (dinfer_kv_prefix_attention): the groups' prefixes come before the entries
 // as entries of their own, whose rows are those of all the group's queries, and every
@@ -720,10 +787,10 @@ __global__ void __launch_bounds__(KaCfg<T, HD, R>::kThreads, 1) kv_attention_ker
   for (int e = blockIdx.x; e < a.n; e += gridDim.x) {
     if constexpr (kShared) {  // and entries without a prefix: nothing from one
       const int v = groups + e, heads = c.kv_heads * a.group;
-      if (tid == 0) a.p.info[e] = make_int2(firsts[v], firsts[v] ? firsts[subs[v]] : 0);
+      if (tid == 0) a.p.info[e] = make_int4(firsts[v], firsts[v] ? firsts[subs[v]] : 0, subs[v], 0);
       for (int h = tid; h < heads; h += kThreads) {
         if (lens[v] == 0) a.p.ml_part[(size_t)(a.n + e) * heads + h] = make_float2(-INFINITY, 0.f);
-        if (lens[v] == 0 || firsts[v] == 0) a.p.ml_part[(size_t)e * heads + h] = make_float2(-INFINITY, 0.f);
+        if (a.p.with_prefix && (lens[v] == 0 || firsts[v] == 0)) a.p.ml_part[(size_t)e * heads + h] = make_float2(-INFINITY, 0.f);
       }
       continue;
     }
@@ -732,6 +799,8 @@ __global__ void __launch_bounds__(KaCfg<T, HD, R>::kThreads, 1) kv_attention_ker
     const int vecs = c.kv_heads * a.group * Cfg::kVecs;
     for (int x = tid; x < vecs; x += kThreads) reinterpret_cast<uint4*>(orow)[x] = make_uint4(0, 0, 0, 0);
   }
+  if constexpr (kShared)
+    if (a.p.plan && blockIdx.x == gridDim.x - 1 && warp == 0) kp_groups(a, lens, firsts);
   // the host bounds the places of the call below 2^31
   const int total = cum[entries];
   KaSplit split;

@@ -24,26 +24,60 @@ __global__ void __launch_bounds__(kKjThreads) kv_join_kernel(const __grid_consta
   pdl_trigger();
   if (row >= rows) return;
   const int e = (int)(row / heads), head = (int)(row - (int64_t)e * heads);
-  float2 w[2];
-  float v[2][kE];
+  const int4 info = __ldcg(a.p.info + e);
+  float m = -INFINITY, l = 0.f, acc[kE] = {};
+  // kN sums more: all loads before the first use
+  constexpr int kN = 8;
+  auto add = [&](int n, auto ml_of, auto o_of) {
+    float2 w[kN];
+    float v[kN][kE];
 #pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    w[k] = __ldcg(a.p.ml_part + k * rows + row);
-    const float* from = a.p.o_part + (k * rows + row) * HD + lane * kE;
-    if constexpr (kE == 4)
-      *reinterpret_cast<float4*>(v[k]) = __ldcg(reinterpret_cast<const float4*>(from));
-    else
-      *reinterpret_cast<float2*>(v[k]) = __ldcg(reinterpret_cast<const float2*>(from));
-  }
-  const int2 info = __ldcg(a.p.info + e);
-  const float m = fmaxf(w[0].x, w[1].x);
-  float l = 0.f, acc[kE] = {};
+    for (int k = 0; k < kN; ++k) {
+      w[k] = make_float2(-INFINITY, 0.f);
 #pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    const float f = w[k].x == -INFINITY ? 0.f : ex2_approx(w[k].x - m);
-    l = fmaf(f, w[k].y, l);  // NaN where a score was
+      for (int i = 0; i < kE; ++i) v[k][i] = 0.f;
+      if (k >= n) continue;
+      w[k] = __ldcg(ml_of(k));
+      const float* from = o_of(k) + lane * kE;
+      if constexpr (kE == 4)
+        *reinterpret_cast<float4*>(v[k]) = __ldcg(reinterpret_cast<const float4*>(from));
+      else
+        *reinterpret_cast<float2*>(v[k]) = __ldcg(reinterpret_cast<const float2*>(from));
+    }
+    float mn = m;
 #pragma unroll
-    for (int i = 0; i < kE; ++i) acc[i] = w[k].x == -INFINITY ? acc[i] : fmaf(f, v[k][i], acc[i]);
+    for (int k = 0; k < kN; ++k) mn = fmaxf(mn, w[k].x);
+    const float f0 = m == -INFINITY ? 0.f : ex2_approx(m - mn);
+    m = mn;
+    l *= f0;
+#pragma unroll
+    for (int i = 0; i < kE; ++i) acc[i] *= f0;
+#pragma unroll
+    for (int k = 0; k < kN; ++k) {
+      const float f = w[k].x == -INFINITY ? 0.f : ex2_approx(w[k].x - m);
+      l = fmaf(f, w[k].y, l);  // NaN where a score was
+#pragma unroll
+      for (int i = 0; i < kE; ++i) acc[i] = w[k].x == -INFINITY ? acc[i] : fmaf(f, v[k][i], acc[i]);  // no sum: O is not written
+    }
+  };
+  if (a.p.with_prefix) {
+    add(2, [&](int k) { return a.p.ml_part + k * rows + row; }, [&](int k) { return a.p.o_part + (k * rows + row) * HD; });
+  } else {
+    if (info.x > 0) {  // the segments of the row's unit, CTA by CTA, stream by stream
+      const KpGroup g = kp_group(a, info.z);
+      KaSplit split;
+      kp_split(a, split);
+      const int kvh = head / a.group, x = (e - g.e0) * a.group + head - kvh * a.group, row0 = x & ~255, unit_rows = min(256, g.rows - row0);
+      const int base = g.place0 + (kvh * g.pairs() + row0 / 256) * g.size() + kPtCost;
+      const int c0 = split.owner(base), c1 = split.owner(base + g.tiles() - 1), streams = unit_rows <= 128 ? 2 : 1;
+      const int64_t at = (int64_t)kp_row(a, g, kvh, row0) + 256 * c0 + (x - row0);
+      const int parts = (c1 - c0 + 1) * streams;
+      for (int k0 = 0; k0 < parts; k0 += kN) {
+        auto at_of = [&](int k) { return streams == 1 ? at + 256 * (k0 + k) : at + 256 * ((k0 + k) >> 1) + ((k0 + k) & 1) * unit_rows; };
+        add(parts - k0, [&](int k) { return a.p.seg_ml + at_of(k); }, [&](int k) { return a.p.seg_o + at_of(k) * HD; });
+      }
+    }
+    add(1, [&](int) { return a.p.ml_part + rows + row; }, [&](int) { return a.p.o_part + (rows + row) * HD; });
   }
   const float inv = l == 0.f ? 0.f : 1.f / l;
   bool fine = true;

@@ -2,7 +2,7 @@
 // positions; include/dinfer_kv.h: rotated appends): argument checks and launches.
 // Included behind kv_api.cuh, whose helpers it uses.
 #pragma once
-#include "kv_prefix.cuh"
+#include "kv_prefix_tc.cuh"
 #include "rope.cuh"
 #include "sample.cuh"
 
@@ -60,15 +60,21 @@ cudaError_t launch_rope(RopeArgs& a, const RopeTurns& t, bool pairs, cudaStream_
   return vec ? go(rope_kernel<T, false, kVec, kPlace>) : go(rope_kernel<T, false, 1, kPlace>);
 }
 
+// Bytes of the workspace in front of the sums of dinfer_kv_prefix_attention: the token kernel's partials of each CTA
+// (at most 18 KB twice), the plan, the entries' records.
+constexpr size_t kPrefixHead = 8u << 20;
+static_assert((sizeof(KpGroup) + sizeof(int4)) * (kKvMaxEntries + 1) <= 64 * 1024, "plan and records");
+
 bool g_step_setup[kMaxDevices] = {};
 constexpr int kSmMostBytes = 232448 - 2048;
 
-// Shared-memory limits of the sampling kernel, set once per device.
+// Shared-memory limits of this file's kernels, set once per device.
 bool step_setup() {
   const int dev = current_device();
   std::lock_guard<std::mutex> lk(g_setup_mutex);
   if (!g_step_setup[dev]) {
-    g_step_setup[dev] = max_smem(sample_kernel<__nv_bfloat16>, kSmMostBytes) && max_smem(sample_kernel<float>, kSmMostBytes);
+    g_step_setup[dev] = max_smem(sample_kernel<__nv_bfloat16>, kSmMostBytes) && max_smem(sample_kernel<float>, kSmMostBytes) &&
+                        max_smem(kv_prefix_tc_kernel<64>, PtCfg<64>::kSmem) && max_smem(kv_prefix_tc_kernel<128>, PtCfg<128>::kSmem);
     if (!g_step_setup[dev]) cudaGetLastError();
   }
   return g_step_setup[dev];
@@ -193,10 +199,11 @@ dinfer_status dinfer_kv_prefix_attention(const dinfer_kv_cache* kc, int32_t laye
   if (reinterpret_cast<uintptr_t>(workspace) & 15) return fail(c, DINFER_EINVAL, "workspace must be 16-byte aligned");
   if ((kc->max_pages * (int64_t)kc->page_size / 16 + 11) * (2 * n + n_groups) >= ((1ll << 31) + heads - 1) / heads)
     return fail(c, DINFER_EINVAL, "more than 2^31 steps of keys in one call");
-  const int64_t sums = (int64_t)n * heads;
-  if ((64ll << 20) + sums * (8 * kc->head_dim + 16) + kKvMaxEntries * 8 > (int64_t)w.data_bytes)
-    return fail(c, DINFER_EINVAL, "workspace too small");
-  if (!kv_setup()) return fail(c, DINFER_ECUDA, "kernel set-up failed");
+  // of the workspace: the kernels' own partials, the plan, the sums of all rows, those of the segments
+  const int64_t sums = (int64_t)n * heads, seg_rows = 2 * sums + 256 * num_sms();
+  const int64_t row_bytes = 4 * kc->head_dim + 8;
+  if ((int64_t)kPrefixHead + (2 * sums + seg_rows) * row_bytes > (int64_t)w.data_bytes) return fail(c, DINFER_EINVAL, "workspace too small");
+  if (!kv_setup() || !step_setup()) return fail(c, DINFER_ECUDA, "kernel set-up failed");
   KaArgs a{};
   a.c = kv_pages(*kc);
   a.seqs = seqs;
@@ -213,19 +220,29 @@ dinfer_status dinfer_kv_prefix_attention(const dinfer_kv_cache* kc, int32_t laye
   a.partial = reinterpret_cast<float*>(w.data);
   a.tickets = w.tickets;
   const bool bf16 = kc->dtype == DINFER_BF16;
-  const int rows = kv_rows(bf16, (int)std::min<int64_t>((int64_t)a.group * (n / n_groups + 1), 16));
+  // the prefixes' rows: in bf16 on the tensor cores, unless one piece of 16 rows holds all that a group can have
+  const bool tc = bf16 && (int64_t)n * a.group > 16;
+  const int rows = kv_rows(bf16, (int)std::min<int64_t>(tc ? a.group : (int64_t)a.group * n, 16));
   a.subgroups = (a.group + rows - 1) / rows;
-  uint8_t* at = w.data + (64ll << 20);
+  uint8_t* at = w.data + kPrefixHead;
+  a.p.info = reinterpret_cast<int4*>(at - 64 * 1024);
+  a.p.plan = tc ? reinterpret_cast<KpGroup*>(at - 128 * 1024) : nullptr;
   a.p.o_part = reinterpret_cast<float*>(at);
-  at += sums * 8 * kc->head_dim;
-  a.p.ml_part = reinterpret_cast<float2*>(at);
-  a.p.info = reinterpret_cast<int2*>(at + sums * 16);
+  a.p.seg_o = a.p.o_part + 2 * sums * kc->head_dim;
+  a.p.ml_part = reinterpret_cast<float2*>(a.p.seg_o + seg_rows * kc->head_dim);
+  a.p.seg_ml = a.p.ml_part + 2 * sums;
+  a.p.seg_ctas = num_sms();
   a.p.bounds = groups;
   a.p.prefix = prefix;
   a.p.groups = n_groups;
-  a.p.with_prefix = 1;
+  a.p.with_prefix = !tc;
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   CK((kc->head_dim == 128 ? launch_kv_attention<128>(a, bf16, rows, s) : launch_kv_attention<64>(a, bf16, rows, s)));
+  if (tc) {
+    const PtArgs pa{a, w.st};
+    CK((kc->head_dim == 128 ? launchk(kv_prefix_tc_kernel<128>, dim3(num_sms()), dim3(kPtThreads), PtCfg<128>::kSmem, s, 1, pa)
+                            : launchk(kv_prefix_tc_kernel<64>, dim3(num_sms()), dim3(kPtThreads), PtCfg<64>::kSmem, s, 1, pa)));
+  }
   const dim3 grid((unsigned)((sums + kKjThreads / 32 - 1) / (kKjThreads / 32)));
   auto join = [&](auto* kernel) { return launchk(kernel, grid, dim3(kKjThreads), 0, s, 1, a); };
   CK((kc->head_dim == 128 ? (bf16 ? join(kv_join_kernel<__nv_bfloat16, 128>) : join(kv_join_kernel<float, 128>))

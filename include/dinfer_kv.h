@@ -170,11 +170,11 @@ dinfer_status dinfer_kv_attention(const dinfer_kv_cache* cache, int32_t layer, c
  * every sequence of the group with tokens has beyond its last token's own; 0 or less, or a
  * group with a single such sequence, shares nothing.  The pages read are those of the
  * group's first sequence with tokens; another that does not hold them sets
- * DINFER_KV_BAD_SEQ.  Entries of no group are computed by themselves, bounds out of
- * order make a group empty (DINFER_KV_FULL).  groups [n_groups + 1], prefix [n_groups],
+ * DINFER_KV_BAD_SEQ.  Entries of no group are computed by themselves; where bounds
+ * are out of order or beyond n no group shares anything (DINFER_KV_FULL).  groups [n_groups + 1], prefix [n_groups],
  * 1 <= n_groups, n + n_groups <= 1024; everything else as in dinfer_kv_attention, but that
  * the sums of all rows have to fit the workspace:
- *   n * heads * (8 * head_dim + 16) bytes beside 64 MiB, and
+ *   n * heads * (16 * head_dim + 32) bytes beside 32 MiB, and
  *   (2 n + n_groups) * heads * (max_pages * page_size / 16 + 11) < 2^31. */
 dinfer_status dinfer_kv_prefix_attention(const dinfer_kv_cache* cache, int32_t layer, const int32_t* seqs, int32_t n,
                                          const int32_t* groups, const int32_t* prefix, int32_t n_groups, const void* q,
