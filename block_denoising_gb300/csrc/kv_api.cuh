@@ -85,8 +85,7 @@ bool max_smem(K* kernel, int bytes) {
 
 template <typename T, int HD, int R>
 bool kv_setup_attention() {
-  return max_smem(kv_attention_kernel<T, HD, R, false>, KaCfg<T, HD, R>::kSmem) &&
-         max_smem(kv_attention_kernel<T, HD, R, true>, KaCfg<T, HD, R>::kSmemShared);
+  return max_smem(kv_attention_kernel<T, HD, R>, KaCfg<T, HD, R>::kSmem);
 }
 
 template <int HD>
@@ -113,8 +112,7 @@ bool kv_setup() {
 template <typename T, int HD, int R>
 cudaError_t launch_kv_attention_r(const KaArgs& a, cudaStream_t s) {
   using Cfg = KaCfg<T, HD, R>;
-  if (a.p.prefix) return launchk(kv_attention_kernel<T, HD, R, true>, dim3(num_sms()), dim3(Cfg::kThreads), Cfg::kSmemShared, s, 1, a);
-  return launchk(kv_attention_kernel<T, HD, R, false>, dim3(num_sms()), dim3(Cfg::kThreads), Cfg::kSmem, s, 1, a);
+  return launchk(kv_attention_kernel<T, HD, R>, dim3(num_sms()), dim3(Cfg::kThreads), Cfg::kSmem, s, 1, a);
 }
 template <int HD, int kTy, bool kSplit>
 cudaError_t launch_window_f32(const WaArgs& a, dim3 grid, cudaStream_t s) {

@@ -63,9 +63,6 @@ struct KaCfg {
   static constexpr int kOffLen = kOffCum + (kKvMaxEntries + 4) * 4;
   static constexpr int kOffMask = kOffLen + kKvMaxEntries * 4;  // [warp][stage]: keys present
   static constexpr int kSmem = kOffMask + kWarps * kStages * 4;
-  // shared prefixes: each entry's first key, and its group or pieces
-  static constexpr int kOffFirst = kSmem, kOffSubs = kOffFirst + kKvMaxEntries * 4;
-  static constexpr int kSmemShared = kOffSubs + kKvMaxEntries * 4;
   // a partial in the workspace: (m, l) [rows], padded so that O [rows][HD] begins at 16 bytes
   static constexpr int kSlotO = (2 * R + 3) / 4 * 4;
   static constexpr int kSlotFloats = kSlotO + R * HD;
@@ -73,40 +70,7 @@ struct KaCfg {
   static_assert(kOffMerge % 16 == 0 && kOffMl % 16 == 0 && kOffQ % 16 == 0 && kOffCum % 4 == 0, "shared-memory alignment");
   static_assert(kStageBytes == 8192 || kStageBytes == 16384, "stage size");
 };
-static_assert(KaCfg<float, 128, 8>::kSmemShared + 256 <= 232448, "attention shared memory above 227 KB");
-
-// dinfer_kv_prefix_attention: what its kernels share (kv_prefix.cuh, kv_prefix_tc.cuh).
-constexpr int kPtCost = 2;  // a segment's beginning and end on the tensor cores, in tiles of 128 keys
-// A group as the tensor cores take it: its units lie at places place0 .. of the call's
-// (a unit: kPtCost and its key tiles), its rows' sums from row0 on.
-struct alignas(16) KpGroup {
-  int place0, row0, e0, rows;  // e0: its first entry; rows: queries per key head
-  int shared, leader, pad0, pad1;  // tokens that it shares; the sequence whose table holds them
-  __device__ __forceinline__ int tiles() const { return (shared + 127) / 128; }
-  __device__ __forceinline__ int size() const { return tiles() + kPtCost; }
-  __device__ __forceinline__ int pairs() const { return (rows + 255) / 256; }  // units per key head
-  // rows of sums per key head and CTA: a unit of at most 128 rows has two for each
-  __device__ __forceinline__ int sums() const {
-    const int last = rows - (pairs() - 1) * 256;
-    return (pairs() - 1) * 256 + (last <= 128 ? 2 * last : last);
-  }
-};
-
-struct KpArgs {
-  const int32_t* bounds;  // [groups + 1] first entries; NULL: one group of all
-  const int32_t* prefix;  // [groups]
-  int groups;
-  int with_prefix;  // the prefixes' keys are this kernel's as well
-  float* o_part;    // [2][entries * heads][head_dim]: sums over the prefix's keys and over the entry's own
-  float2* ml_part;  // [2][entries * heads]: their (m, l)
-  int4* info;       // [entries]: keys that are read for the whole group, the entry whose table holds them, the group
-  // the prefixes on the tensor cores (with_prefix 0): the groups and, behind them, the end
-  // (NULL: no such kernel); sums [rows of all units + 256 per CTA]
-  KpGroup* plan;
-  float* seg_o;
-  float2* seg_ml;
-  int seg_ctas;
-};
+static_assert(KaCfg<float, 128, 8>::kSmem <= 232448, "attention shared memory above 227 KB");
 
 struct KaArgs {
   KvPages c;
@@ -121,7 +85,6 @@ struct KaArgs {
   float scale_log2;
   float* partial;  // [CTA][2][kSlotFloats]
   int* tickets;    // [CTA], zero between calls
-  KpArgs p;
 };
 
 // Visible keys of a sequence of `len` tokens: the first `sink` ones, then
@@ -197,15 +160,12 @@ struct KaSplit {
 struct KaWalk {
   int entry, piece, step;  // step: the round's first
   int steps, base, to;     // of this pair
-  // pieces(e): how many pieces entry e has
-  template <typename Pieces>
-  __device__ __forceinline__ void set_entry(int e, const int* cum, const Pieces& pieces) {
+  __device__ __forceinline__ void set_entry(int e, const int* cum, int pieces) {
     entry = e;
-    steps = (int)((unsigned)(cum[e + 1] - cum[e]) / (unsigned)pieces(e)) - kKaPairCost;
+    steps = (int)((unsigned)(cum[e + 1] - cum[e]) / (unsigned)pieces) - kKaPairCost;
   }
   // entry == n: nothing is left
-  template <typename Pieces>
-  __device__ __forceinline__ void start(int x0, int x1, const int* cum, int n, const Pieces& pieces) {
+  __device__ __forceinline__ void start(int x0, int x1, const int* cum, int n, int pieces) {
     int lo = 0, hi = n;  // cum[lo] <= x0 < cum[hi]
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
@@ -219,13 +179,13 @@ struct KaWalk {
     to = min(steps, x1 - base - kKaPairCost);
     if (to <= 0) entry = n;  // the range ends in the pair's cost
   }
-  template <int kWarps, typename Pieces>
-  __device__ __forceinline__ void next(int x1, const int* cum, int n, const Pieces& pieces) {
+  template <int kWarps>
+  __device__ __forceinline__ void next(int x1, const int* cum, int n, int pieces) {
     step += kWarps;
     if (step < to) return;
     step = 0;
     base += steps + kKaPairCost;
-    if (++piece == pieces(entry)) {
+    if (++piece == pieces) {
       piece = 0;
       int e = entry + 1;
       while (e < n && cum[e + 1] == cum[e]) ++e;  // entries without a key
@@ -601,123 +561,7 @@ __device__ __noinline__ void ka_redo(const KaArgs& a, int entry, int len, int he
   }
 }
 
-// --------------------------------------------------------------------------
-// shared prefixes: what every kernel of a call works out from the tables
-// --------------------------------------------------------------------------
-// Entries of group g, as the call gives them (in order, or no group shares anything).
-__device__ __forceinline__ int kp_first(const KaArgs& a, int g) { return a.p.bounds ? a.p.bounds[g] : 0; }
-__device__ __forceinline__ int kp_members(const KaArgs& a, int g) { return a.p.bounds ? a.p.bounds[g + 1] - a.p.bounds[g] : a.n; }
-
-// lens, firsts, subs [groups + n].  For group g: tokens that it shares (whole pages,
-// fewer than any of its sequences has, 0 where fewer than two have any), an entry whose
-// table holds them, pieces of `rows` rows.  For entry e, at groups + e: keys of its
-// own (0: a sequence without tokens), the first of them, its group (-1: none).
-template <int kThreads>
-__device__ __forceinline__ void kp_plan(const KaArgs& a, int* lens, int* firsts, int* subs, int rows) {
-  const KvPages& c = a.c;
-  const int groups = a.p.groups, tid = threadIdx.x;
-  bool order = true;
-  for (int g = tid; g < groups; g += kThreads) {
-    lens[g] = firsts[g] = 0x7fffffff;
-    subs[g] = 0;
-    if (a.p.bounds) order = order && a.p.bounds[g] >= 0 && a.p.bounds[g] <= a.p.bounds[g + 1] && a.p.bounds[g + 1] <= a.n;
-  }
-  order = __syncthreads_and(order);
-  if (!order && blockIdx.x == 0 && tid == 0) c.flag(KV_FULL);
-  for (int e = tid; e < a.n; e += kThreads) {
-    const int s = a.seqs ? a.seqs[e] : e;
-    int len = s >= 0 && s < c.max_seqs ? c.lens[s] : -1;
-    if (!c.valid_len(len)) {
-      if (blockIdx.x == 0) c.flag(KV_BAD_SEQ);
-      len = 0;
-    }
-    int g = 0;
-    if (a.p.bounds) {
-      int hi = groups;
-      while (hi - g > 1) {
-        const int mid = (g + hi) >> 1;
-        if (a.p.bounds[mid] <= e) g = mid; else hi = mid;
-      }
-    }
-    if (!order || e < kp_first(a, g) || e >= kp_first(a, g) + kp_members(a, g)) g = -1;
-    lens[groups + e] = len;
-    subs[groups + e] = g;
-    if (g >= 0 && len > 0) {
-      atomicMin(&lens[g], len);
-      atomicMin(&firsts[g], e);
-      atomicAdd(&subs[g], 1);
-    }
-  }
-  __syncthreads();
-  for (int g = tid; g < groups; g += kThreads) {
-    int shared = 0;
-    if (subs[g] > 1) shared = (int)c.page_div.div((uint32_t)max(0, min(a.p.prefix[g], lens[g] - 1))) * c.page_size;
-    lens[g] = shared;
-    if (shared == 0) firsts[g] = 0;
-    subs[g] = shared ? (int)(((int64_t)kp_members(a, g) * a.group + rows - 1) / rows) : 1;
-  }
-  __syncthreads();
-  for (int e = tid; e < a.n; e += kThreads) {
-    const int g = subs[groups + e], len = lens[groups + e], first = g >= 0 && len > 0 ? lens[g] : 0;
-    firsts[groups + e] = first;
-    lens[groups + e] = len - first;
-  }
-  __syncthreads();
-}
-
-__device__ __forceinline__ KpGroup kp_group(const KaArgs& a, int g) {
-  KpGroup r;
-  *reinterpret_cast<int4*>(&r.place0) = __ldcg(reinterpret_cast<const int4*>(a.p.plan + g));
-  *reinterpret_cast<int4*>(&r.shared) = __ldcg(reinterpret_cast<const int4*>(a.p.plan + g) + 1);
-  return r;
-}
-
-// Writes the groups for the tensor cores: one warp.
-__device__ __forceinline__ void kp_groups(const KaArgs& a, const int* lens, const int* firsts) {
-  const int lane = threadIdx.x & 31;
-  int place = 0, row = 0;
-  for (int g0 = 0; g0 <= a.p.groups; g0 += 32) {
-    const int g = g0 + lane;
-    KpGroup r{};
-    if (g < a.p.groups && lens[g] > 0) {
-      const int e = firsts[g];
-      r.shared = lens[g];
-      r.leader = a.seqs ? a.seqs[e] : e;
-      r.e0 = kp_first(a, g);
-      r.rows = kp_members(a, g) * a.group;
-    }
-    const int places = r.shared ? a.c.kv_heads * r.pairs() * r.size() : 0, rows = r.shared ? a.c.kv_heads * r.sums() : 0;
-    int p = places, q = rows;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int u = __shfl_up_sync(0xffffffffu, p, o), v = __shfl_up_sync(0xffffffffu, q, o);
-      if (lane >= o) {
-        p += u;
-        q += v;
-      }
-    }
-    r.place0 = place + p - places;
-    r.row0 = row + q - rows;
-    if (g <= a.p.groups) a.p.plan[g] = r;
-    place += __shfl_sync(0xffffffffu, p, 31);
-    row += __shfl_sync(0xffffffffu, q, 31);
-  }
-}
-
-// How the places of all units are dealt to the CTAs; returns how many there are.
-__device__ __forceinline__ int kp_split(const KaArgs& a, KaSplit& split) {
-  const int total = __ldcg(&a.p.plan[a.p.groups].place0);
-  split.make(total, max(1, min(a.p.seg_ctas, total / (2 * kPtCost))));
-  return total;
-}
-// Where the sums of a unit's rows begin, for CTA 0 (each CTA's are 256 rows on: a unit has at most 256, and CTAs
-// share at most one).
-__device__ __forceinline__ int kp_row(const KaArgs& a, const KpGroup& g, int kvh, int row) { return g.row0 + kvh * g.sums() + row; }
-
-// kShared (dinfer_kv_prefix_attention): the groups' prefixes come before the entries
-// as entries of their own, whose rows are those of all the group's queries, and every
-// pair's sums go to the workspace as they are.
-template <typename T, int HD, int R, bool kShared>
+template <typename T, int HD, int R>
 __global__ void __launch_bounds__(KaCfg<T, HD, R>::kThreads, 1) kv_attention_kernel(const __grid_constant__ KaArgs a) {
   using Cfg = KaCfg<T, HD, R>;
   constexpr int kRows = R, kMergeRows = Cfg::kMergeRows, kStages = Cfg::kStages, kKeys = Cfg::kKeys, kWarps = Cfg::kWarps, kThreads = Cfg::kThreads;
@@ -730,39 +574,26 @@ __global__ void __launch_bounds__(KaCfg<T, HD, R>::kThreads, 1) kv_attention_ker
   __shared__ int warp_places[kWarps], join_sh;
   const KvPages& c = a.c;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  int* firsts = reinterpret_cast<int*>(sm + Cfg::kOffFirst);  // kShared: see kp_plan
-  int* subs = reinterpret_cast<int*>(sm + Cfg::kOffSubs);
-  const int groups = kShared ? a.p.groups : 0, entries = a.n + groups;
-  // pieces of at most kRows query heads of a key head of entry e
-  auto subs_of = [&](int e) {
-    if constexpr (kShared) return e < groups ? subs[e] : a.subgroups; else return a.subgroups;
-  };
-  auto pieces = [&](int e) { return c.kv_heads * subs_of(e); };
+  const int pieces = c.kv_heads * a.subgroups;
   pdl_wait();
   pdl_trigger();
 
   auto seq_of = [&](int e) { return a.seqs ? a.seqs[e] : e; };
-  if constexpr (kShared) kp_plan<kThreads>(a, lens, firsts, subs, kRows);
   // places before each entry: thread i sums the entries of its own stretch
   {
-    const int per = (entries + kThreads - 1) / kThreads;
-    const int e0 = min(entries, tid * per), e1 = min(entries, e0 + per);
+    const int per = (a.n + kThreads - 1) / kThreads;
+    const int e0 = min(a.n, tid * per), e1 = min(a.n, e0 + per);
     int sum = 0;
     for (int e = e0; e < e1; ++e) {
-      int seen;
-      if constexpr (kShared) {
-        seen = e < groups && !a.p.with_prefix ? 0 : lens[e];
-      } else {
-        const int s = seq_of(e);
-        int len = s >= 0 && s < c.max_seqs ? c.lens[s] : -1;
-        if (!c.valid_len(len)) {
-          if (blockIdx.x == 0) c.flag(KV_BAD_SEQ);
-          len = 0;
-        }
-        lens[e] = len;
-        seen = ka_seen(len, a.window, a.sinks).seen;
+      const int s = seq_of(e);
+      int len = s >= 0 && s < c.max_seqs ? c.lens[s] : -1;
+      if (!c.valid_len(len)) {
+        if (blockIdx.x == 0) c.flag(KV_BAD_SEQ);
+        len = 0;
       }
-      const int x = seen ? (ka_rounds(seen, kKeys * kWarps) * kWarps + kKaPairCost) * pieces(e) : 0;
+      lens[e] = len;
+      const int seen = ka_seen(len, a.window, a.sinks).seen;
+      const int x = seen ? (ka_rounds(seen, kKeys * kWarps) * kWarps + kKaPairCost) * pieces : 0;
       cum[e + 1] = x;
       sum += x;
     }
@@ -785,31 +616,20 @@ __global__ void __launch_bounds__(KaCfg<T, HD, R>::kThreads, 1) kv_attention_ker
   }
   // entries without a key: zeros, the entries dealt round the CTAs
   for (int e = blockIdx.x; e < a.n; e += gridDim.x) {
-    if constexpr (kShared) {  // and entries without a prefix: nothing from one
-      const int v = groups + e, heads = c.kv_heads * a.group;
-      if (tid == 0) a.p.info[e] = make_int4(firsts[v], firsts[v] ? firsts[subs[v]] : 0, subs[v], 0);
-      for (int h = tid; h < heads; h += kThreads) {
-        if (lens[v] == 0) a.p.ml_part[(size_t)(a.n + e) * heads + h] = make_float2(-INFINITY, 0.f);
-        if (a.p.with_prefix && (lens[v] == 0 || firsts[v] == 0)) a.p.ml_part[(size_t)e * heads + h] = make_float2(-INFINITY, 0.f);
-      }
-      continue;
-    }
     if (cum[e + 1] != cum[e]) continue;
     T* orow = reinterpret_cast<T*>(a.o) + e * a.o_stride;
     const int vecs = c.kv_heads * a.group * Cfg::kVecs;
     for (int x = tid; x < vecs; x += kThreads) reinterpret_cast<uint4*>(orow)[x] = make_uint4(0, 0, 0, 0);
   }
-  if constexpr (kShared)
-    if (a.p.plan && blockIdx.x == gridDim.x - 1 && warp == 0) kp_groups(a, lens, firsts);
   // the host bounds the places of the call below 2^31
-  const int total = cum[entries];
+  const int total = cum[a.n];
   KaSplit split;
   split.make(total, max(1, min((int)gridDim.x, total / a.min_steps)));
   if (total == 0 || blockIdx.x >= split.ctas) return;
   const int x0 = split.begin(blockIdx.x), x1 = split.begin(blockIdx.x + 1);
   KaWalk load;
-  load.start(x0, x1, cum, entries, pieces);
-  if (load.entry >= entries) return;
+  load.start(x0, x1, cum, a.n, pieces);
+  if (load.entry >= a.n) return;
 
   uint8_t* ring = sm + warp * (kStages * Cfg::kStageBytes);
   const uint32_t ring_u32 = smem_u32(ring);
@@ -829,27 +649,21 @@ __global__ void __launch_bounds__(KaCfg<T, HD, R>::kThreads, 1) kv_attention_ker
   auto look_up = [&]() -> Where {
     if (load.entry != load_entry) {
       load_entry = load.entry;
-      if constexpr (kShared) {
-        const bool own = load_entry >= groups;
-        load_row = c.table + (size_t)seq_of(own ? load_entry - groups : firsts[load_entry]) * c.max_pages;
-        seen = {0, own ? firsts[load_entry] : 0, lens[load_entry]};
-      } else {
-        load_row = c.table + (size_t)seq_of(load_entry) * c.max_pages;
-        seen = ka_seen(lens[load_entry], a.window, a.sinks);
-      }
+      load_row = c.table + (size_t)seq_of(load_entry) * c.max_pages;
+      seen = ka_seen(lens[load_entry], a.window, a.sinks);
     }
     const uint32_t at = (uint32_t)(load.step + warp) * kKeys + lane % kKeys;  // unsigned: the last round may pass 2^31
     if (load.step + warp >= load.to || at >= (uint32_t)seen.seen) return {0, -1};
     const int x = (int)at, key = x < seen.sink ? x : x - seen.sink + seen.first;
     const int j = (int)c.page_div.div((uint32_t)key);
-    return {load_row[j], a.layer_off + (key - j * c.page_size) * c.token_stride + (load.piece / subs_of(load.entry)) * c.head_stride};
+    return {load_row[j], a.layer_off + (key - j * c.page_size) * c.token_stride + (load.piece / a.subgroups) * c.head_stride};
   };
   Where at = look_up(), at_next{0, -1};
   int ahead_rounds = 1;  // looked up and not issued yet: at, at_next
   auto advance = [&]() {
-    load.template next<kWarps>(x1, cum, entries, pieces);
-    if (load.entry < entries) {
-      if (!kShared && load.step == 0 && warp == 0) {  // a new pair: its query rows into L2 by the time they are wanted
+    load.template next<kWarps>(x1, cum, a.n, pieces);
+    if (load.entry < a.n) {
+      if (load.step == 0 && warp == 0) {  // a new pair: its query rows into L2 by the time they are wanted
         const int sub = load.piece % a.subgroups, rows = min(kRows, a.group - sub * kRows);
         const char* qp = reinterpret_cast<const char*>(reinterpret_cast<const T*>(a.q) + load.entry * a.q_stride +
                                                        ((load.piece / a.subgroups) * a.group + sub * kRows) * HD);
@@ -895,27 +709,10 @@ __global__ void __launch_bounds__(KaCfg<T, HD, R>::kThreads, 1) kv_attention_ker
     cp_async_commit();
   };
   KaState<T, HD, R> state;
-  // the rows of a pair's piece: queries of one entry, or for a prefix of its group's entries in turn
-  auto rows_of = [&](const KaWalk& w) {
-    const int sub = w.piece % subs_of(w.entry);
-    if constexpr (kShared)
-      if (w.entry < groups) return min(kRows, kp_members(a, w.entry) * a.group - sub * kRows);
-    return min(kRows, a.group - sub * kRows);
-  };
   auto load_q = [&](const KaWalk& w) {
-    const int pieces_here = subs_of(w.entry), sub = w.piece % pieces_here, kvh = w.piece / pieces_here;
-    const T* q = reinterpret_cast<const T*>(a.q);
-    if constexpr (kShared) {
-      const bool own = w.entry >= groups;
-      const int e0 = own ? w.entry - groups : kp_first(a, w.entry);
-      state.load_q([&](int r) {
-        const int x = sub * kRows + r, e = x / a.group;
-        return q + (e0 + e) * a.q_stride + (kvh * a.group + x - e * a.group) * HD;
-      }, rows_of(w), lane);
-    } else {
-      const T* qrow = q + w.entry * a.q_stride + (kvh * a.group + sub * kRows) * HD;
-      state.load_q([&](int r) { return qrow + r * HD; }, rows_of(w), lane);
-    }
+    const int sub = w.piece % a.subgroups, head = (w.piece / a.subgroups) * a.group + sub * kRows;
+    const T* qrow = reinterpret_cast<const T*>(a.q) + w.entry * a.q_stride + head * HD;
+    state.load_q([&](int r) { return qrow + r * HD; }, min(kRows, a.group - sub * kRows), lane);
   };
   load_q(use);
   for (int s = 0; s < kStages - 1; ++s) issue(s);
@@ -932,35 +729,24 @@ __global__ void __launch_bounds__(KaCfg<T, HD, R>::kThreads, 1) kv_attention_ker
     __syncwarp();  // the stage is refilled next turn
     stage = stage + 1 == kStages ? 0 : stage + 1;
     KaWalk ahead = use;
-    ahead.template next<kWarps>(x1, cum, entries, pieces);
-    const bool go = ahead.entry < entries;
+    ahead.template next<kWarps>(x1, cum, a.n, pieces);
+    const bool go = ahead.entry < a.n;
     if (!go || ahead.base != use.base) {
       // the pair's keys of this CTA are done: merge the warps
       if (go) load_q(ahead);
-      const int pieces_here = subs_of(use.entry), sub = use.piece % pieces_here, kvh = use.piece / pieces_here, rows = rows_of(use);
-      const int head = kvh * a.group + sub * kRows;
+      const int sub = use.piece % a.subgroups, rows = min(kRows, a.group - sub * kRows);
+      const int head = (use.piece / a.subgroups) * a.group + sub * kRows;
       const bool whole = use.to == use.steps && seg_step == 0;
       const int slot = seg_step == 0 ? 1 : 0;  // 0: the pair began in an earlier CTA
       float* part = a.partial + ((int64_t)blockIdx.x * 2 + slot) * Cfg::kSlotFloats;
       state.store_ml(ml + warp * kRows * 2, lane);
-      T* orow = reinterpret_cast<T*>(a.o) + use.entry * a.o_stride + head * HD;  // not kShared
+      T* orow = reinterpret_cast<T*>(a.o) + use.entry * a.o_stride + head * HD;
       // Four columns of a row, or nothing (!on); the lanes of a row are one warp's, or half of them.  Rows that are not
       // finite are done again at the pair's end, by one call for all its rows (a call at each store: 56.4 us for 64
       // sequences of 1 .. 8192 tokens, 32 heads on 8, this 55.4, without either 55.3).  Where o is q such a row is not
       // stored at all, as its query is wanted still.
       uint32_t redo = 0;
-      auto put = [&](bool on, int row, int c4, float4 acc, float mm, float ll) {
-        if constexpr (kShared) {  // the sums of an entry's row, where it is this group's and has keys
-          if (!on) return;
-          const bool own = use.entry >= groups;
-          const int x = sub * kRows + row, up = own ? 0 : x / a.group;
-          const int e = (own ? use.entry - groups : kp_first(a, use.entry)) + up;
-          if (!own && (lens[groups + e] == 0 || subs[groups + e] != use.entry)) return;
-          const size_t at = (size_t)((own ? a.n : 0) + e) * (c.kv_heads * a.group) + kvh * a.group + x - up * a.group;
-          __stcg(reinterpret_cast<float4*>(a.p.o_part + at * HD + c4), acc);
-          if (c4 == 0) __stcg(a.p.ml_part + at, make_float2(mm, ll));
-          return;
-        }
+      auto put = [&](bool on, int row, int c4, float4 acc, float ll) {
         // a row whose weights' sum is NaN or 0 is NaN or zeros: nothing else could come out
         const bool bad = on && ll > 0.f && !(fabsf(acc.x) + fabsf(acc.y) + fabsf(acc.z) + fabsf(acc.w) <= 1.0e38f);
         if (bad) redo |= 1u << row;
@@ -995,7 +781,7 @@ __global__ void __launch_bounds__(KaCfg<T, HD, R>::kThreads, 1) kv_attention_ker
           }
         }
         if (whole) {
-          put(on, row, c4, acc, mm, ll);
+          put(on, row, c4, acc, ll);
         } else if (on) {
           __stcg(reinterpret_cast<float4*>(part + Cfg::kSlotO + row * HD + c4), acc);
           if (c4 == 0) __stcg(reinterpret_cast<float2*>(part + row * 2), make_float2(mm, ll));
@@ -1049,14 +835,14 @@ __global__ void __launch_bounds__(KaCfg<T, HD, R>::kThreads, 1) kv_attention_ker
                 acc.w = fmaf(f, v[k].w, acc.w);
               }
             }
-            put(on, row, c4, acc, mm, ll);
+            put(on, row, c4, acc, ll);
           }
           if (tid == 0) a.tickets[c_first] = 0;
         }
       }
       for (redo = __reduce_or_sync(0xffffffffu, redo); redo; redo &= redo - 1) {
         __syncwarp();  // behind the row's first stores
-        ka_redo<T, HD>(a, use.entry, lens[use.entry], head + __ffs(redo) - 1, kvh);
+        ka_redo<T, HD>(a, use.entry, lens[use.entry], head + __ffs(redo) - 1, use.piece / a.subgroups);
       }
       if (!go) break;
       state.begin(lane, qs);

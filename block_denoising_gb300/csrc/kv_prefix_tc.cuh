@@ -12,11 +12,13 @@
 // tile, some 2500 cycles, so two of them run at a time (streams): the two tiles of rows
 // on the same keys, or, of a unit of at most 128 rows, one tile of rows on every other
 // key tile each, with sums of their own.  352 threads:
-//   warps 0-1   the key tiles: page numbers, then 16-byte cp.async copies to where the
-//               128-byte swizzle wants them (any page size and stride; a key that is not
-//               there is zeros, and its bit is missing from the tile's mask)
+//   warp 0      the key tiles: page numbers, a tile ahead, and a TMA box per page and 64
+//               columns, a page a lane; a page that is not there is asked for behind the
+//               last one, which reads as zeros, and its keys are missing from the tile's
+//               mask.  Pages that do not divide a tile, or it them, go by 16-byte
+//               cp.async from warps 0 and 1
 //   warp 2      tensor memory and the products, in the order S_0 S_1 S_2 P_0 V S_3 P_1 V ...
-//   warps 3-6   softmax and sums of stream 0, a thread per row; warps 7-10 stream 1
+//   warps 3-6   queries, softmax and sums of stream 0, a thread per row; warps 7-10 stream 1
 // Tensor memory, P's two halves and the lazily raised maximum are as in
 // window_attention_tc.cuh.
 #pragma once
@@ -43,14 +45,26 @@ struct PtCfg {
 };
 static_assert(PtCfg<128>::kSmem + 512 <= 232448, "prefix attention shared memory above 227 KB");
 
-struct PtArgs {
-  KaArgs a;
-  DevState* status;
+struct PtMaps {
+  CUtensorMap k, v;  // of one layer: [pages][heads][slots][hd], boxes of a page's slots (at most 128) x 64 elements
 };
+struct PtArgs {
+  KpArgs p;
+  DevState* status;
+  int tile_pages;  // pages of a tile (1: a page is whole tiles)
+};
+
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, uint64_t* bar, int x, int y, int z, int w) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(bar))
+      : "memory");
+}
 
 // The segments of a CTA's places [x0, x1), in order.
 struct PtWalk {
-  KpGroup gr;
+  KpEntry gr;
   int g, u;              // group, unit of it
   int from, to, base;    // key tiles of the segment; the unit's first place
   int x1;
@@ -59,25 +73,25 @@ struct PtWalk {
     to = min(gr.tiles(), x1 - base - kPtCost);
     return to > from;
   }
-  __device__ __forceinline__ bool start(const KaArgs& a, int x0, int end) {
+  __device__ __forceinline__ bool start(const KpArgs& p, int x0, int end) {
     x1 = end;
-    int lo = 0, hi = a.p.groups;  // place0[lo] <= x0 < place0[hi]
+    int lo = 0, hi = p.groups;  // unit0[lo] <= x0 < unit0[hi]
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
-      if (__ldcg(&a.p.plan[mid].place0) <= x0) lo = mid; else hi = mid;
+      if (__ldcg(&p.plan[mid].unit0) <= x0) lo = mid; else hi = mid;
     }
     g = lo;
-    gr = kp_group(a, g);
-    u = (int)((unsigned)(x0 - gr.place0) / (unsigned)gr.size());
-    base = gr.place0 + u * gr.size();
+    gr = kp_entry(p, g);
+    u = (int)((unsigned)(x0 - gr.unit0) / (unsigned)gr.size());
+    base = gr.unit0 + u * gr.size();
     return set(x0);
   }
-  __device__ __forceinline__ bool next(const KaArgs& a) {
+  __device__ __forceinline__ bool next(const KpArgs& p) {
     base += gr.size();
     if (base >= x1) return false;
-    if (++u == a.c.kv_heads * gr.pairs()) {
+    if (++u == p.a.c.kv_heads * gr.pairs()) {
       u = 0;
-      do gr = kp_group(a, ++g);
+      do gr = kp_entry(p, ++g);
       while (gr.shared == 0);  // there is one more: base is below the end
     }
     return set(base);
@@ -87,11 +101,13 @@ struct PtWalk {
   __device__ __forceinline__ int rows() const { return min(256, gr.rows - row0()); }
 };
 
-template <int HD>
-__global__ void __launch_bounds__(kPtThreads, 1) kv_prefix_tc_kernel(const __grid_constant__ PtArgs pa) {
+template <int HD, bool kTma>
+__global__ void __launch_bounds__(kPtThreads, 1)
+    kv_prefix_tc_kernel(const __grid_constant__ PtMaps maps, const __grid_constant__ PtArgs pa) {
   using Cfg = PtCfg<HD>;
   constexpr int kSlots = Cfg::kSlots;
-  const KaArgs& a = pa.a;
+  const KpArgs& p = pa.p;
+  const KaArgs& a = p.a;
   const KvPages& c = a.c;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -101,37 +117,44 @@ __global__ void __launch_bounds__(kPtThreads, 1) kv_prefix_tc_kernel(const __gri
   uint64_t* pv_done = s_full + 8;     // [2 streams][4]
   uint64_t* p_full = pv_done + 8;     // [2 streams][2 halves of 64 keys]
   uint64_t* s_free = p_full + 4;      // [kBufs]
-  uint64_t* drain = s_free + 2;
+  uint64_t* q_full = s_free + 2;      // a segment's queries
+  uint64_t* drain = q_full + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   uint32_t* masks = tmem_slot + 2;    // [8 key tiles][4]: keys that are there
-  static_assert((kSlots + 8 + 8 + 4 + 2 + 1) * 8 + 8 + 128 <= 512, "barriers");
+  static_assert((kSlots + 8 + 8 + 4 + 2 + 2) * 8 + 8 + 128 <= 512, "barriers");
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
-    for (int i = 0; i < kSlots; ++i) mbar_init(&full[i], kPtLoaders);
+    for (int i = 0; i < kSlots; ++i) mbar_init(&full[i], kTma ? 1 : kPtLoaders);
     for (int i = 0; i < 8; ++i) {
       mbar_init(&s_full[i], 1);
       mbar_init(&pv_done[i], 1);
     }
     for (int i = 0; i < 4; ++i) mbar_init(&p_full[i], 4);
     for (int i = 0; i < 2; ++i) mbar_init(&s_free[i], 4);
+    mbar_init(q_full, 8);
     mbar_init(drain, 1);
     *abort_flag = 0;
     fence_mbar_init();
+    if (kTma) {
+      prefetch_tmap(&maps.k);
+      prefetch_tmap(&maps.v);
+    }
   }
   if (warp == 2) tmem_alloc(tmem_slot, 512);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  pdl_wait();
+  // No wait for the own kernel, which runs beside this one: it began behind the plan, and
+  // the plan behind all that came before.
   pdl_trigger();
-
+  const int4 head = __ldcg(p.head);
   KaSplit split;
-  const int total = kp_split(a, split);
+  kp_split(p, head, split);
   PtWalk w;
-  bool any = total > 0 && blockIdx.x < split.ctas;
-  if (any) any = w.start(a, split.begin(blockIdx.x), split.begin(blockIdx.x + 1));
+  bool any = head.y > 0 && blockIdx.x < split.ctas;
+  if (any) any = w.start(p, split.begin(blockIdx.x), split.begin(blockIdx.x + 1));
 
   // Bounded; a wait that ran out sets the status at the kernel's end.
   auto wait = [&](uint64_t* bar, uint32_t parity) -> bool { return mbar_wait(bar, parity, abort_flag); };
@@ -144,125 +167,174 @@ __global__ void __launch_bounds__(kPtThreads, 1) kv_prefix_tc_kernel(const __gri
     for (int i = 0; i < kSlots; ++i) hist[i] = 0;
     int n[2] = {0, 0};   // products of each stream over the tiles loaded
     WtSlot at{0, 0}, told{0, 0};
-    int pending = 0;     // tiles asked for and not announced
-    int key_tiles = 0;
+    int key_tiles = 0, loads = 0;
     bool ok = true;
-    auto announce = [&]() {
-      fence_async_shared();
-      mbar_arrive(&full[told.slot]);
-      told.template next<kSlots>();
-      --pending;
+    auto took = [&](int kv, int streams) {
+      at.template next<kSlots>();
+      ++loads;
+#pragma unroll
+      for (int i = 0; i + 1 < kSlots; ++i) hist[i] = hist[i + 1];
+      hist[kSlots - 1] = (kv << 2) | streams | (n[0] & 7) << 3 | (n[1] & 7) << 6;
     };
-    auto flush = [&]() {
-      cp_async_wait<0>();
-      while (pending > 0) announce();
-    };
-    // The slot's last tile has been read.  What is in flight is announced before a wait that may last: the products
-    // that free the slot may need it.
-    auto wait_free = [&](int use) {
+    // The slot's last tile has been read by the products of both streams; before(): in front of a wait that may last
+    auto wait_free = [&](auto before) {
+      const int use = hist[0];
 #pragma unroll
       for (int x = 0; x < 2; ++x)
         if ((use >> x) & 1) {
           const int m = (use >> (3 + 3 * x)) & 7;
           uint64_t* bar = ((use & 4) ? pv_done : s_full) + 4 * x + (m & 3);
           if (!mbar_try_wait(bar, (m >> 2) & 1)) {
-            flush();
+            before();
             ok = ok && wait(bar, (m >> 2) & 1);
           }
         }
+      ok = __all_sync(0xffffffffu, ok);  // warp-uniform, also where a wait ran out
     };
-    const int64_t row_vecs = HD / 8;
-    do {
-      const bool pair = w.rows() > 128;
-      const int kvh = w.kvh(), row0 = w.row0(), rows = w.rows();
-      const int32_t* table = c.table + (size_t)w.gr.leader * c.max_pages;
-      // keys warp * 64 + lane and + 32 of a tile
-      auto look_up = [&](int tile, int64_t (&off)[2], int (&page)[2]) {
+    if constexpr (kTma) {
+      if (warp == 0) {
+        const int pages = pa.tile_pages, slots = 128 / pages;  // of a tile; keys of a box
+        do {
+          const bool pair = w.rows() > 128;
+          const int kvh = w.kvh();
+          const int32_t* table = c.table + (size_t)w.gr.leader * c.max_pages;
+          // a lane's page of a tile, and where in it the tile begins; page -1: no such key
+          auto look_up = [&](int tile, int& page, int& slot) {
+            const int key = tile * 128 + lane * slots;
+            page = -1;
+            slot = 0;
+            if (lane < pages && tile < w.to && key < w.gr.shared) {
+              const int j = (int)c.page_div.div((uint32_t)key);
+              page = table[j];
+              slot = key - j * c.page_size;
+              if (page < 0 || page >= c.num_pages) {
+                c.flag(KV_BAD_PAGE);
+                page = -1;
+              }
+            }
+          };
+          int page, slot, page_next, slot_next;
+          look_up(w.from, page, slot);
+          for (int j = w.from; j < w.to && ok; ++j, ++key_tiles) {
+            const uint32_t there = __ballot_sync(0xffffffffu, page >= 0);
+            const int from = page >= 0 ? page : c.num_pages, slot0 = slot;
+            look_up(j + 1, page_next, slot_next);
+            const int streams = pair ? 3 : 1 << ((j - w.from) & 1);
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const int key = tile * 128 + warp * 64 + u * 32 + lane;
-          off[u] = -1;
-          page[u] = 0;
-          if (tile < w.to && key < w.gr.shared) {
-            const int j = (int)c.page_div.div((uint32_t)key);
-            page[u] = table[j];
-            off[u] = a.layer_off + (key - j * c.page_size) * c.token_stride + kvh * c.head_stride;
+            for (int kv = 0; kv < 2; ++kv) {
+              wait_free([] {});
+              if (!ok) break;
+              uint64_t* bar = full + at.slot;
+              if (kv == 0 && lane < 4) {
+                uint32_t mask = 0;
+#pragma unroll
+                for (int b = 0; b < 4; ++b) mask |= (there >> ((lane * 32 + b * 8) / slots)) & 1u ? 0xffu << (8 * b) : 0u;
+                masks[(key_tiles & 7) * 4 + lane] = mask;
+              }
+              __syncwarp();
+              if (lane == 0) mbar_arrive_expect_tx(bar, Cfg::kTile);
+              __syncwarp();
+              if (lane < pages) {
+                const uint32_t dst = smem_u32(sm) + Cfg::kOffRing + at.slot * Cfg::kTile + lane * slots * 128;
+#pragma unroll
+                for (int h = 0; h < HD / 64; ++h)
+                  tma_load_4d(dst + h * Cfg::kSlab, kv ? &maps.v : &maps.k, bar, h * 64, slot0, kvh, from);
+              }
+              took(kv, streams);
+            }
+            n[0] += streams & 1;
+            n[1] += streams >> 1;
+            page = page_next;
+            slot = slot_next;
           }
-        }
+        } while (ok && w.next(p));
+        if (*abort_flag)  // let the copies in flight land before the CTA exits
+          for (int j = max(0, loads - kSlots); j < loads; ++j) mbar_wait_drain(&full[j % kSlots], (j / kSlots) & 1);
+      }
+    } else {
+      int pending = 0;  // tiles asked for and not announced
+      auto announce = [&]() {
+        fence_async_shared();
+        mbar_arrive(&full[told.slot]);
+        told.template next<kSlots>();
+        --pending;
       };
-      int64_t off[2], off_next[2];
-      int page[2], page_next[2];
-      look_up(w.from, off, page);
-      if (n[0] + n[1] > 0) {  // the last segment's S have all read its Q
-        flush();
+      auto flush = [&]() {
+        cp_async_wait<0>();
+        while (pending > 0) announce();
+      };
+      do {
+        const bool pair = w.rows() > 128;
+        const int kvh = w.kvh();
+        const int32_t* table = c.table + (size_t)w.gr.leader * c.max_pages;
+        // keys warp * 64 + lane and + 32 of a tile
+        auto look_up = [&](int tile, int64_t (&off)[2], int (&page)[2]) {
 #pragma unroll
-        for (int x = 0; x < 2; ++x)
-          if (ok && n[x] > 0) ok = wait(&s_full[4 * x + ((n[x] - 1) & 3)], ((n[x] - 1) >> 2) & 1);
-      }
-      if (!ok) break;
-      {  // Q: of both tiles, eight lanes on 128 bytes of a row; rows that are not there are zeros
-        const int tiles = pair ? 2 : 1;
-        for (int r = (tid >> 3); r < tiles * 128; r += kPtLoaders / 8) {
-          const int x = row0 + min(r, rows - 1), e = x / a.group;
-          const __nv_bfloat16* q = reinterpret_cast<const __nv_bfloat16*>(a.q) + (w.gr.e0 + e) * a.q_stride +
-                                   (kvh * a.group + x - e * a.group) * HD + (lane & 7) * 8;
-          const uint32_t dst = smem_u32(sm) + (r >> 7) * Cfg::kTile + (r & 127) * 128 + (((lane & 7) ^ (r & 7)) << 4);
-#pragma unroll
-          for (int h = 0; h < HD / 64; ++h) cp_async16(dst + h * Cfg::kSlab, q + h * 64, r < rows ? 16 : 0);
-        }
-      }
-      for (int j = w.from; j < w.to && ok; ++j, ++key_tiles) {
-        int64_t place[2];
-        uint32_t there[2];
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          place[u] = -1;
-          if (off[u] >= 0) {
-            if (page[u] >= 0 && page[u] < c.num_pages) place[u] = off[u] + page[u] * c.page_stride;
-            else c.flag(KV_BAD_PAGE);
+          for (int u = 0; u < 2; ++u) {
+            const int key = tile * 128 + warp * 64 + u * 32 + lane;
+            off[u] = -1;
+            page[u] = 0;
+            if (tile < w.to && key < w.gr.shared) {
+              const int j = (int)c.page_div.div((uint32_t)key);
+              page[u] = table[j];
+              off[u] = a.layer_off + (key - j * c.page_size) * c.token_stride + kvh * c.head_stride;
+            }
           }
-          there[u] = __ballot_sync(0xffffffffu, place[u] >= 0);
-        }
-        look_up(j + 1, off_next, page_next);
-        const int streams = pair ? 3 : 1 << ((j - w.from) & 1);
+        };
+        int64_t off[2], off_next[2];
+        int page[2], page_next[2];
+        look_up(w.from, off, page);
+        for (int j = w.from; j < w.to && ok; ++j, ++key_tiles) {
+          int64_t place[2];
+          uint32_t there[2];
 #pragma unroll
-        for (int kv = 0; kv < 2; ++kv) {
-          wait_free(hist[0]);
-          if (!ok) break;
-          if (kv == 0 && lane < 2) masks[(key_tiles & 7) * 4 + warp * 2 + lane] = lane ? there[1] : there[0];
-          const uint4* from = kv ? c.v : c.k;
-          const uint32_t dst0 = smem_u32(sm) + Cfg::kOffRing + at.slot * Cfg::kTile;
-#pragma unroll 4
-          for (int k = 0; k < 16; ++k) {
-            const int r = k * 4 + (lane >> 3);  // of this warp's 64 keys
-            const int64_t p = k < 8 ? __shfl_sync(0xffffffffu, place[0], r & 31) : __shfl_sync(0xffffffffu, place[1], r & 31);
-            const int row = warp * 64 + r;
-            const uint4* src = from + (p >= 0 ? p : 0) + (lane & 7);
-            const uint32_t dst = dst0 + row * 128 + (((lane & 7) ^ (row & 7)) << 4);
-#pragma unroll
-            for (int h = 0; h < HD / 64; ++h) cp_async16(dst + h * Cfg::kSlab, src + h * 8, p >= 0 ? 16 : 0);
+          for (int u = 0; u < 2; ++u) {
+            place[u] = -1;
+            if (off[u] >= 0) {
+              if (page[u] >= 0 && page[u] < c.num_pages) place[u] = off[u] + page[u] * c.page_stride;
+              else c.flag(KV_BAD_PAGE);
+            }
+            there[u] = __ballot_sync(0xffffffffu, place[u] >= 0);
           }
-          cp_async_commit();
-          ++pending;
-          at.template next<kSlots>();
+          look_up(j + 1, off_next, page_next);
+          const int streams = pair ? 3 : 1 << ((j - w.from) & 1);
 #pragma unroll
-          for (int i = 0; i + 1 < kSlots; ++i) hist[i] = hist[i + 1];
-          hist[kSlots - 1] = (kv << 2) | streams | (n[0] & 7) << 3 | (n[1] & 7) << 6;
-          if (pending > kPtAhead) {
-            cp_async_wait<kPtAhead>();
-            announce();
+          for (int kv = 0; kv < 2; ++kv) {
+            // what is in flight is announced before a wait: the products that free the slot may need it
+            wait_free(flush);
+            if (!ok) break;
+            if (kv == 0 && lane < 2) masks[(key_tiles & 7) * 4 + warp * 2 + lane] = lane ? there[1] : there[0];
+            const uint4* from = kv ? c.v : c.k;
+            const uint32_t dst0 = smem_u32(sm) + Cfg::kOffRing + at.slot * Cfg::kTile;
+#pragma unroll 8
+            for (int k = 0; k < 16; ++k) {
+              const int r = k * 4 + (lane >> 3);  // of this warp's 64 keys
+              const int64_t at_key = __shfl_sync(0xffffffffu, k < 8 ? place[0] : place[1], r & 31);
+              const int row = warp * 64 + r;
+              const uint4* src = from + (at_key >= 0 ? at_key : 0) + (lane & 7);
+              const uint32_t dst = dst0 + row * 128 + (((lane & 7) ^ (row & 7)) << 4);
+#pragma unroll
+              for (int h = 0; h < HD / 64; ++h) cp_async16(dst + h * Cfg::kSlab, src + h * 8, at_key >= 0 ? 16 : 0);
+            }
+            cp_async_commit();
+            ++pending;
+            took(kv, streams);
+            if (pending > kPtAhead) {
+              cp_async_wait<kPtAhead>();
+              announce();
+            }
+          }
+          n[0] += streams & 1;
+          n[1] += streams >> 1;
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            off[u] = off_next[u];
+            page[u] = page_next[u];
           }
         }
-        n[0] += streams & 1;
-        n[1] += streams >> 1;
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          off[u] = off_next[u];
-          page[u] = page_next[u];
-        }
-      }
-    } while (ok && w.next(a));
-    flush();
+      } while (ok && w.next(p));
+      flush();
+    }
   } else if (warp == 2) {
     // ------------------------------ products ------------------------------
     if (elect_one_sync()) {
@@ -276,8 +348,9 @@ __global__ void __launch_bounds__(kPtThreads, 1) kv_prefix_tc_kernel(const __gri
       int turns = 0;            // S of both streams
       WtSlot ring{0, 0};        // K of the key tile at hand
       bool ok = true;
-      do {
+      for (int seg = 0;; ++seg) {
         const bool pair = w.rows() > 128;
+        ok = wait(q_full, seg & 1);
         const int last = pair ? 2 * (w.to - w.from) : w.to - w.from;
         uint32_t fresh = 3;  // bit x: no P V of this segment yet
         int due0 = -1, due1 = -1;
@@ -330,7 +403,8 @@ __global__ void __launch_bounds__(kPtThreads, 1) kv_prefix_tc_kernel(const __gri
           due0 = due1;
           due1 = mine;
         }
-      } while (ok && w.next(a));
+        if (!ok || !w.next(p)) break;
+      }
       tc_commit(drain);
       mbar_wait_drain(drain, 0);
     }
@@ -342,7 +416,7 @@ __global__ void __launch_bounds__(kPtThreads, 1) kv_prefix_tc_kernel(const __gri
     const uint32_t t_lane = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const float sc = a.scale_log2;
     bool ok = true;
-    int cnt = 0, key_tiles = 0;  // turns of this stream, key tiles, over all segments
+    int cnt = 0, other = 0, key_tiles = 0;  // turns of this stream, of the other one, key tiles, over all segments
     auto all_wait = [&](uint64_t* bar, uint32_t parity) -> bool { return __all_sync(0xffffffffu, wait(bar, parity)); };
     // P V of the turn before the cnt-th has completed
     auto last_pv_done = [&](int cnt) -> bool { return cnt < 2 || all_wait(&pv_done[4 * x + ((cnt - 2) & 3)], ((cnt - 2) >> 2) & 1); };
@@ -353,6 +427,30 @@ __global__ void __launch_bounds__(kPtThreads, 1) kv_prefix_tc_kernel(const __gri
       const bool pair = w.rows() > 128;
       const int tiles = w.to - w.from, rows = pair ? (x ? w.rows() - 128 : 128) : w.rows();
       const bool live = (warp & 3) * 32 < rows;  // warp-uniform
+      {
+        // The queries, eight lanes on 128 bytes of a row; rows that are not there are zeros.  Where both streams read one
+        // tile, stream 0 fills it.  The last segment's S have all read what is written over.
+        if (ok && other > 0 && !all_wait(&s_full[4 * (x ^ 1) + ((other - 1) & 3)], ((other - 1) >> 2) & 1)) ok = false;
+        if (ok && (pair || x == 0)) {
+          const int row0 = w.row0() + x * 128, kvh = w.kvh();
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int tile_row = (warp & 3) * 32 + i * 4 + (lane >> 3), row = row0 + min(tile_row, rows - 1);
+            const int e = (int)p.group_div.div((uint32_t)row);
+            const __nv_bfloat16* q = reinterpret_cast<const __nv_bfloat16*>(a.q) + (w.gr.e0 + e) * a.q_stride +
+                                     (kvh * a.group + row - e * a.group) * HD + (lane & 7) * 8;
+            const uint32_t dst = smem_u32(sm) + x * Cfg::kTile + tile_row * 128 + (((lane & 7) ^ (tile_row & 7)) << 4);
+#pragma unroll
+            for (int h = 0; h < HD / 64; ++h) cp_async16(dst + h * Cfg::kSlab, q + h * 64, tile_row < rows ? 16 : 0);
+          }
+          cp_async_commit();
+          cp_async_wait<0>();
+          fence_async_shared();
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(q_full);
+        other += pair ? tiles : (tiles + x) / 2;
+      }
       float m_used = -INFINITY, l = 0.f;
       const int cnt_before = cnt;
       for (int j = pair ? 0 : x; j < tiles; j += pair ? 1 : 2) {
@@ -445,11 +543,11 @@ __global__ void __launch_bounds__(kPtThreads, 1) kv_prefix_tc_kernel(const __gri
       }
       key_tiles += tiles;
       // (m, l) and O of the segment; before the hand-over of the next one's first P, which lets its P V write O
-      const int64_t row = (int64_t)kp_row(a, w.gr, w.kvh(), w.row0()) + 256 * blockIdx.x + (x ? (pair ? 128 : w.rows()) : 0) + r;
+      const int64_t row = (int64_t)kp_row(w.gr, w.kvh(), w.row0()) + 256 * blockIdx.x + (x ? (pair ? 128 : w.rows()) : 0) + r;
       if (cnt > cnt_before && ok && !last_pv_done(cnt + 1)) ok = false;
       if (live && ok) {
         tc_fence_after();
-        if (r < rows) __stcg(a.p.seg_ml + row, make_float2(m_used, l));
+        if (r < rows) __stcg(p.seg_ml + row, make_float2(m_used, l));
         if (cnt > cnt_before) {
 #pragma unroll 1
           for (int k = 0; k < HD / 32; ++k) {
@@ -457,17 +555,21 @@ __global__ void __launch_bounds__(kPtThreads, 1) kv_prefix_tc_kernel(const __gri
             tmem_ld32(t_lane + Cfg::kColO + x * HD + k * 32, o);
             if (r < rows)
 #pragma unroll
-              for (int u = 0; u < 8; ++u)
-                __stcg(reinterpret_cast<uint4*>(a.p.seg_o + row * HD + k * 32) + u, make_uint4(o[4 * u], o[4 * u + 1], o[4 * u + 2], o[4 * u + 3]));
+              for (int u = 0; u < 4; ++u)  // whole sectors
+                asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p.seg_o + row * HD + k * 32 + u * 8),
+                             "r"(o[8 * u]), "r"(o[8 * u + 1]), "r"(o[8 * u + 2]), "r"(o[8 * u + 3]), "r"(o[8 * u + 4]),
+                             "r"(o[8 * u + 5]), "r"(o[8 * u + 6]), "r"(o[8 * u + 7])
+                             : "memory");
           }
         }
         tc_fence_before();
       }
       __syncwarp();
-    } while (ok && w.next(a));
+    } while (ok && w.next(p));
   }
 
   __syncthreads();
+  pdl_wait();  // the own kernel's sums: this one ends behind it
   if (tid == 0 && *abort_flag) set_status(pa.status, ST_WAIT_TIMEOUT);
   if (warp == 2) {
     tc_fence_after();

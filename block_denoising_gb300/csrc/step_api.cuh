@@ -60,10 +60,53 @@ cudaError_t launch_rope(RopeArgs& a, const RopeTurns& t, bool pairs, cudaStream_
   return vec ? go(rope_kernel<T, false, kVec, kPlace>) : go(rope_kernel<T, false, 1, kPlace>);
 }
 
-// Bytes of the workspace in front of the sums of dinfer_kv_prefix_attention: the token kernel's partials of each CTA
-// (at most 18 KB twice), the plan, the entries' records.
-constexpr size_t kPrefixHead = 8u << 20;
-static_assert((sizeof(KpGroup) + sizeof(int4)) * (kKvMaxEntries + 1) <= 64 * 1024, "plan and records");
+// Bytes of the workspace in front of the sums of dinfer_kv_prefix_attention: its plan.
+constexpr size_t kPrefixHead = 64 * 1024;
+static_assert(sizeof(int4) + sizeof(KpEntry) * (kKvMaxEntries + 1) <= kPrefixHead, "plan");
+
+// One layer of a bf16 cache as [pages][heads][slots][hd]: boxes of a page's slots, at most 128, x 64 elements with the
+// 128-byte swizzle; pages behind the last read as zeros.
+bool make_map_pages(CUtensorMap* m, const dinfer_kv_cache& kc, const void* base, int layer) {
+  EncodeTiledFn enc = get_encode_fn();
+  if (!enc) return false;
+  const int64_t row = kc.head_dim;
+  auto stride = [&](int64_t s, int64_t size) { return (cuuint64_t)(size > 1 ? s : row) * 2; };  // of one entry: never stepped over
+  cuuint64_t dims[4] = {(cuuint64_t)kc.head_dim, (cuuint64_t)kc.page_size, (cuuint64_t)kc.kv_heads, (cuuint64_t)kc.num_pages};
+  cuuint64_t strides[3] = {stride(kc.token_stride, kc.page_size), stride(kc.head_stride, kc.kv_heads), stride(kc.page_stride, kc.num_pages)};
+  for (cuuint64_t s : strides)
+    if (s >= (1ull << 40)) return false;
+  cuuint32_t box[4] = {64, (cuuint32_t)std::min(kc.page_size, 128), 1, 1};
+  cuuint32_t es[4] = {1, 1, 1, 1};
+  const uint16_t* from = reinterpret_cast<const uint16_t*>(base) + (kc.n_layers > 1 ? layer * kc.layer_stride : 0);
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<uint16_t*>(from), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <typename T, int HD, int R>
+cudaError_t launch_kv_own_r(const KpArgs& p, cudaStream_t s) {
+  using Cfg = KoCfg<T, HD, R>;
+  return launchk(kv_own_kernel<T, HD, R>, dim3(p.sms), dim3(Cfg::kThreads), Cfg::kSmem, s, 1, p);
+}
+template <int HD>
+cudaError_t launch_kv_own(const KpArgs& p, bool bf16, cudaStream_t s) {
+  if (bf16) return p.rows == 8 ? launch_kv_own_r<__nv_bfloat16, HD, 8>(p, s) : launch_kv_own_r<__nv_bfloat16, HD, 16>(p, s);
+  switch (p.rows) {
+    case 1: return launch_kv_own_r<float, HD, 1>(p, s);
+    case 2: return launch_kv_own_r<float, HD, 2>(p, s);
+    case 4: return launch_kv_own_r<float, HD, 4>(p, s);
+    default: return launch_kv_own_r<float, HD, 8>(p, s);
+  }
+}
+template <typename T, int HD, int R>
+bool step_setup_own() {
+  return max_smem(kv_own_kernel<T, HD, R>, KoCfg<T, HD, R>::kSmem);
+}
+template <int HD>
+bool step_setup_hd() {
+  return step_setup_own<__nv_bfloat16, HD, 8>() && step_setup_own<__nv_bfloat16, HD, 16>() && step_setup_own<float, HD, 1>() &&
+         step_setup_own<float, HD, 2>() && step_setup_own<float, HD, 4>() && step_setup_own<float, HD, 8>() &&
+         max_smem(kv_prefix_tc_kernel<HD, true>, PtCfg<HD>::kSmem) && max_smem(kv_prefix_tc_kernel<HD, false>, PtCfg<HD>::kSmem);
+}
 
 bool g_step_setup[kMaxDevices] = {};
 constexpr int kSmMostBytes = 232448 - 2048;
@@ -74,7 +117,7 @@ bool step_setup() {
   std::lock_guard<std::mutex> lk(g_setup_mutex);
   if (!g_step_setup[dev]) {
     g_step_setup[dev] = max_smem(sample_kernel<__nv_bfloat16>, kSmMostBytes) && max_smem(sample_kernel<float>, kSmMostBytes) &&
-                        max_smem(kv_prefix_tc_kernel<64>, PtCfg<64>::kSmem) && max_smem(kv_prefix_tc_kernel<128>, PtCfg<128>::kSmem);
+                        step_setup_hd<64>() && step_setup_hd<128>();
     if (!g_step_setup[dev]) cudaGetLastError();
   }
   return g_step_setup[dev];
@@ -199,12 +242,13 @@ dinfer_status dinfer_kv_prefix_attention(const dinfer_kv_cache* kc, int32_t laye
   if (reinterpret_cast<uintptr_t>(workspace) & 15) return fail(c, DINFER_EINVAL, "workspace must be 16-byte aligned");
   if ((kc->max_pages * (int64_t)kc->page_size / 16 + 11) * (2 * n + n_groups) >= ((1ll << 31) + heads - 1) / heads)
     return fail(c, DINFER_EINVAL, "more than 2^31 steps of keys in one call");
-  // of the workspace: the kernels' own partials, the plan, the sums of all rows, those of the segments
-  const int64_t sums = (int64_t)n * heads, seg_rows = 2 * sums + 256 * num_sms();
-  const int64_t row_bytes = 4 * kc->head_dim + 8;
-  if ((int64_t)kPrefixHead + (2 * sums + seg_rows) * row_bytes > (int64_t)w.data_bytes) return fail(c, DINFER_EINVAL, "workspace too small");
+  // of the workspace: the plan, then sums of the own keys' warps (at most 8 an SM, 16 rows) and of the prefixes' segments
+  const int64_t sums = (int64_t)n * heads, own_rows = 2 * sums + 128 * num_sms(), seg_rows = 2 * sums + 256 * num_sms();
+  if ((int64_t)kPrefixHead + (own_rows + seg_rows) * (4 * kc->head_dim + 8) > (int64_t)w.data_bytes)
+    return fail(c, DINFER_EINVAL, "workspace too small");
   if (!kv_setup() || !step_setup()) return fail(c, DINFER_ECUDA, "kernel set-up failed");
-  KaArgs a{};
+  KpArgs p{};
+  KaArgs& a = p.a;
   a.c = kv_pages(*kc);
   a.seqs = seqs;
   a.q = q;
@@ -215,38 +259,45 @@ dinfer_status dinfer_kv_prefix_attention(const dinfer_kv_cache* kc, int32_t laye
   a.n = n;
   a.group = heads / kc->kv_heads;
   a.window = -1;
-  a.min_steps = 8;
   a.scale_log2 = scale * 1.4426950408889634f;
-  a.partial = reinterpret_cast<float*>(w.data);
-  a.tickets = w.tickets;
-  const bool bf16 = kc->dtype == DINFER_BF16;
+  const bool bf16 = kc->dtype == DINFER_BF16, hd128 = kc->head_dim == 128;
   // the prefixes' rows: in bf16 on the tensor cores, unless one piece of 16 rows holds all that a group can have
   const bool tc = bf16 && (int64_t)n * a.group > 16;
   const int rows = kv_rows(bf16, (int)std::min<int64_t>(tc ? a.group : (int64_t)a.group * n, 16));
   a.subgroups = (a.group + rows - 1) / rows;
-  uint8_t* at = w.data + kPrefixHead;
-  a.p.info = reinterpret_cast<int4*>(at - 64 * 1024);
-  a.p.plan = tc ? reinterpret_cast<KpGroup*>(at - 128 * 1024) : nullptr;
-  a.p.o_part = reinterpret_cast<float*>(at);
-  a.p.seg_o = a.p.o_part + 2 * sums * kc->head_dim;
-  a.p.ml_part = reinterpret_cast<float2*>(a.p.seg_o + seg_rows * kc->head_dim);
-  a.p.seg_ml = a.p.ml_part + 2 * sums;
-  a.p.seg_ctas = num_sms();
-  a.p.bounds = groups;
-  a.p.prefix = prefix;
-  a.p.groups = n_groups;
-  a.p.with_prefix = !tc;
+  p.bounds = groups;
+  p.prefix = prefix;
+  p.groups = n_groups;
+  p.with_prefix = !tc;
+  p.sms = num_sms();
+  p.warps = hd128 ? KaCfg<float, 128, 8>::kWarps : KaCfg<float, 64, 8>::kWarps;
+  p.keys = bf16 ? KaCfg<__nv_bfloat16, 128, 8>::kKeys : KaCfg<float, 128, 8>::kKeys;
+  p.rows = rows;
+  p.group_div = FastDiv::make((uint32_t)a.group);
+  p.head = reinterpret_cast<int4*>(w.data);
+  p.plan = reinterpret_cast<KpEntry*>(p.head + 1);
+  p.own_o = reinterpret_cast<float*>(w.data + kPrefixHead);
+  p.seg_o = p.own_o + own_rows * kc->head_dim;
+  p.own_ml = reinterpret_cast<float2*>(p.seg_o + seg_rows * kc->head_dim);
+  p.seg_ml = p.own_ml + own_rows;
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  CK((kc->head_dim == 128 ? launch_kv_attention<128>(a, bf16, rows, s) : launch_kv_attention<64>(a, bf16, rows, s)));
+  PtMaps maps{};
+  // TMA boxes of whole pages or whole tiles
+  const int64_t page = kc->page_size;
+  const bool boxes = tc && ((page >= 8 && 128 % page == 0) || page % 128 == 0) && make_map_pages(&maps.k, *kc, kc->k, layer) &&
+                     make_map_pages(&maps.v, *kc, kc->v, layer);
+  CK(launchk(kv_prefix_plan_kernel, dim3(1), dim3(kKvPlanThreads), 0, s, 1, p));
+  CK((hd128 ? launch_kv_own<128>(p, bf16, s) : launch_kv_own<64>(p, bf16, s)));
   if (tc) {
-    const PtArgs pa{a, w.st};
-    CK((kc->head_dim == 128 ? launchk(kv_prefix_tc_kernel<128>, dim3(num_sms()), dim3(kPtThreads), PtCfg<128>::kSmem, s, 1, pa)
-                            : launchk(kv_prefix_tc_kernel<64>, dim3(num_sms()), dim3(kPtThreads), PtCfg<64>::kSmem, s, 1, pa)));
+    const PtArgs pa{p, w.st, (int)std::max<int64_t>(1, 128 / page)};
+    auto go = [&](auto* kernel, int smem) { return launchk(kernel, dim3(p.sms), dim3(kPtThreads), smem, s, 1, maps, pa); };
+    CK((hd128 ? go(boxes ? kv_prefix_tc_kernel<128, true> : kv_prefix_tc_kernel<128, false>, PtCfg<128>::kSmem)
+              : go(boxes ? kv_prefix_tc_kernel<64, true> : kv_prefix_tc_kernel<64, false>, PtCfg<64>::kSmem)));
   }
   const dim3 grid((unsigned)((sums + kKjThreads / 32 - 1) / (kKjThreads / 32)));
-  auto join = [&](auto* kernel) { return launchk(kernel, grid, dim3(kKjThreads), 0, s, 1, a); };
-  CK((kc->head_dim == 128 ? (bf16 ? join(kv_join_kernel<__nv_bfloat16, 128>) : join(kv_join_kernel<float, 128>))
-                          : (bf16 ? join(kv_join_kernel<__nv_bfloat16, 64>) : join(kv_join_kernel<float, 64>))));
+  auto join = [&](auto* kernel) { return launchk(kernel, grid, dim3(kKjThreads), 0, s, 1, p); };
+  CK((hd128 ? (bf16 ? join(kv_join_kernel<__nv_bfloat16, 128>) : join(kv_join_kernel<float, 128>))
+            : (bf16 ? join(kv_join_kernel<__nv_bfloat16, 64>) : join(kv_join_kernel<float, 64>))));
   return DINFER_OK;
 }
 

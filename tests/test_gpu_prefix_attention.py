@@ -98,6 +98,9 @@ CASES = [
     ([1100], [[11] * 70], 8, 2, 128, 128, BF, "head"),
     ([5000], [[1, 2, 3, 4]], 16, 16, 128, 64, BF, "token"),
     ([900], [[2, 1]], 17, 1, 128, 16, BF, "token"),
+    ([900, 600], [[2, 1] * 40, [3] * 30], 8, 2, 64, 256, BF, "token"),
+    ([1030] * 9, [[2, 1, 3]] * 9, 28, 4, 128, 40, BF, "head"),
+    ([100] * 40, [[2, 1]] * 40, 12, 4, 128, 8, BF, "token"),
     ([64, 47], [[0, 3, 0], [0, 0]], 4, 2, 128, 16, BF, "token"),  # as many tokens as are shared, and no more
 ]
 
