@@ -16,7 +16,7 @@
 //           In fp32, and where 16 rows hold all queries of a key head, the shared keys
 //           are pairs of their own here, a piece of up to 16 (8) rows at a time
 //   prefix  in bf16 the shared keys on the tensor cores (kv_prefix_tc.cuh), at the same
-//           time: the plan deals the SMs to the two by the keys they stream
+//           time: the plan deals the SMs to the two by what their work takes
 //   join    a warp per row of the output
 #pragma once
 #include "kv_attention.cuh"
@@ -57,6 +57,7 @@ struct KpArgs {
   int groups;
   int with_prefix;        // the shared keys are pairs of the own kernel
   int sms, warps, keys, rows;  // of the own kernel: warps of a CTA, keys of a step, rows of a piece
+  int step_ns, pair_ns, single_ns;  // what an SM takes for a step of the own kernel, a key tile of the prefix kernel
   FastDiv group_div;
   int4* head;     // steps of the own kernel, places of the prefix kernel, SMs of the own kernel
   KpEntry* plan;  // [groups + entries + 1]
@@ -87,6 +88,29 @@ __device__ __forceinline__ int kp_row(const KpEntry& g, int kvh, int row) { retu
 // --------------------------------------------------------------------------
 // plan
 // --------------------------------------------------------------------------
+// Exclusive sums of v's parts over the CTA's threads, whole warps; returns the totals.
+__device__ __forceinline__ int4 kp_scan(int4& v) {
+  __shared__ int4 warp_sums[32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  const int4 own = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int x = __shfl_up_sync(0xffffffffu, v.x, o), y = __shfl_up_sync(0xffffffffu, v.y, o);
+    const int z = __shfl_up_sync(0xffffffffu, v.z, o), w = __shfl_up_sync(0xffffffffu, v.w, o);
+    if (lane >= o) v = make_int4(v.x + x, v.y + y, v.z + z, v.w + w);
+  }
+  if (lane == 31) warp_sums[warp] = v;
+  __syncthreads();
+  int4 all{};
+  v = make_int4(v.x - own.x, v.y - own.y, v.z - own.z, v.w - own.w);
+  for (int i = 0; i < warps; ++i) {
+    const int4 s = warp_sums[i];
+    if (i < warp) v = make_int4(v.x + s.x, v.y + s.y, v.z + s.z, v.w + s.w);
+    all = make_int4(all.x + s.x, all.y + s.y, all.z + s.z, all.w + s.w);
+  }
+  return all;
+}
+
 __global__ void __launch_bounds__(kKvPlanThreads) kv_prefix_plan_kernel(const __grid_constant__ KpArgs p) {
   const KaArgs& a = p.a;
   const KvPages& c = a.c;
@@ -131,7 +155,7 @@ __global__ void __launch_bounds__(kKvPlanThreads) kv_prefix_plan_kernel(const __
     }
   }
   __syncthreads();
-  int places = 0, units = 0, rows = 0;
+  int places = 0, units = 0, rows = 0, weight = 0;
   if (is_group && live[t] > 1) {
     r.shared = (int)c.page_div.div((uint32_t)max(0, min(wanted, least[t] - 1))) * c.page_size;
     r.e0 = bounds[t];
@@ -143,6 +167,8 @@ __global__ void __launch_bounds__(kKvPlanThreads) kv_prefix_plan_kernel(const __
     } else if (r.shared) {
       units = a.c.kv_heads * r.pairs() * r.size();
       rows = a.c.kv_heads * r.sums();
+      // a unit of two tiles of rows, and of one: its chain, or its keys
+      weight = a.c.kv_heads * r.size() * ((r.pairs() - 1) * p.pair_ns + ((r.rows - 1) % 256 >= 128 ? p.pair_ns : p.single_ns)) / 64;
     }
   }
   if (is_group) least[t] = r.shared;
@@ -153,10 +179,11 @@ __global__ void __launch_bounds__(kKvPlanThreads) kv_prefix_plan_kernel(const __
     r.seq = s;
     places = ((r.keys - 1) / p.keys + 1 + kKpCost) * a.c.kv_heads * a.subgroups;
   }
-  int all_places, all_units, all_rows;
-  r.place0 = kv_block_scan<int>(places, &all_places);
-  r.unit0 = kv_block_scan<int>(units, &all_units);
-  r.row0 = kv_block_scan<int>(rows, &all_rows);
+  int4 sum{places, units, rows, weight};
+  const int4 all = kp_scan(sum);
+  r.place0 = sum.x;
+  r.unit0 = sum.y;
+  r.row0 = sum.z;
   if (is_group) {
     if (p.with_prefix) r.unit0 = r.place0;
     unit0[t] = r.unit0;
@@ -177,13 +204,13 @@ __global__ void __launch_bounds__(kKvPlanThreads) kv_prefix_plan_kernel(const __
   if (is_group || is_entry) p.plan[t] = r;
   if (t == 0) {
     KpEntry end{};
-    end.place0 = all_places;
-    end.unit0 = all_units;
+    end.place0 = all.x;
+    end.unit0 = all.y;
     p.plan[groups + a.n] = end;
-    // SMs by keys
-    const float own = (float)all_places * p.keys, shared = (float)all_units * 128;
-    const int sms = all_units == 0 ? p.sms : all_places == 0 ? 0 : max(1, min(p.sms - 1, (int)(p.sms * (own / (own + shared)) + 0.5f)));
-    *p.head = make_int4(all_places, all_units, sms, 0);
+    // the SMs by the time that each kernel's work takes one
+    const float own = (float)all.x * p.step_ns, shared = (float)all.w * 64;
+    const int sms = all.y == 0 ? p.sms : all.x == 0 ? 0 : max(1, min(p.sms - 1, (int)(p.sms * (own / (own + shared)) + 0.5f)));
+    *p.head = make_int4(all.x, all.y, sms, 0);
   }
 }
 
@@ -286,8 +313,16 @@ __global__ void __launch_bounds__(KoCfg<T, HD, R>::kThreads, 1) kv_own_kernel(co
   int* places = reinterpret_cast<int*>(sm + Cfg::kOffPlaces);
   int* subs = reinterpret_cast<int*>(sm + Cfg::kOffSubs);  // pieces of an entry's key head
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, groups = p.groups, entries = groups + a.n;
-  pdl_wait();
-  pdl_trigger();  // the prefix kernel may begin: what it reads is there
+  // Beside the prefix kernel, which began behind the plan, there is nothing to wait for but its end, in front of this
+  // one's: the join waits for this kernel alone.
+  if (p.with_prefix) pdl_wait();
+  pdl_trigger();
+  struct Behind {
+    bool on;
+    __device__ __forceinline__ ~Behind() {
+      if (on) pdl_wait();
+    }
+  } behind{!p.with_prefix};
   const int4 head = __ldcg(p.head);
   for (int v = tid; v <= entries; v += kThreads) {
     places[v] = __ldcg(&p.plan[v].place0);

@@ -17,7 +17,8 @@
 //               last one, which reads as zeros, and its keys are missing from the tile's
 //               mask.  Pages that do not divide a tile, or it them, go by 16-byte
 //               cp.async from warps 0 and 1
-//   warp 2      tensor memory and the products, in the order S_0 S_1 S_2 P_0 V S_3 P_1 V ...
+//   warp 2      tensor memory and the products, S_0 S_1 S_2 P_0 V S_3 P_1 V ... while the
+//               keys come in time
 //   warps 3-6   queries, softmax and sums of stream 0, a thread per row; warps 7-10 stream 1
 // Tensor memory, P's two halves and the lazily raised maximum are as in
 // window_attention_tc.cuh.
@@ -146,9 +147,8 @@ __global__ void __launch_bounds__(kPtThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  // No wait for the own kernel, which runs beside this one: it began behind the plan, and
-  // the plan behind all that came before.
-  pdl_trigger();
+  pdl_wait();
+  pdl_trigger();  // the own kernel may begin: what it reads is there
   const int4 head = __ldcg(p.head);
   KaSplit split;
   kp_split(p, head, split);
@@ -353,13 +353,26 @@ __global__ void __launch_bounds__(kPtThreads, 1)
         ok = wait(q_full, seg & 1);
         const int last = pair ? 2 * (w.to - w.from) : w.to - w.from;
         uint32_t fresh = 3;  // bit x: no P V of this segment yet
-        int due0 = -1, due1 = -1;
-        for (int t = 0; ok && (t < last || due0 >= 0 || due1 >= 0); ++t) {
-          int mine = -1;
-          if (t < last) {
-            const int x = t & 1, buf = Cfg::kBufs == 1 ? 0 : x;
-            const uint32_t n = (ns >> (8 * x)) & 7, prev = Cfg::kBufs == 1 ? (uint32_t)turns - 1 : n - 1;
+        // The turns whose P V is due, oldest first.  S of the next turn goes first where its keys are there, up to two
+        // turns ahead of P V; else P V, whose V makes room for other keys.  (In the order S_t, P_t-2 V without a look: a
+        // unit of 32 rows over 8192 keys took 1.75 us a key tile, the latency of its loads.)
+        int due[3] = {-1, -1, -1}, waiting = 0;
+        for (int t = 0; ok && (t < last || waiting > 0);) {
+          const int x = t & 1, buf = Cfg::kBufs == 1 ? 0 : x;
+          const uint32_t n_s = (ns >> (8 * x)) & 7, prev = Cfg::kBufs == 1 ? (uint32_t)turns - 1 : n_s - 1;
+          bool go = t < last && waiting == 0;
+          if (go) {
             ok = wait(full + ring.slot, ring.parity) && (!((used >> buf) & 1) || wait(s_free + buf, prev & 1));
+          } else if (t < last && waiting < 3) {  // whichever can go first
+            const int y = due[0] & 1;
+            const long long t0 = clock64();
+            while (true) {
+              go = mbar_test(full + ring.slot, ring.parity) && (!((used >> buf) & 1) || mbar_test(s_free + buf, prev & 1));
+              if (go || mbar_test(p_full + 2 * y, (np >> (8 * y)) & 1)) break;
+              if (*abort_flag || clock64() - t0 > kWaitCycles) break;  // the wait below sees to it
+            }
+          }
+          if (go) {
             if (!ok) break;
             tc_fence_after();
             const uint64_t qb = qd + (pair && x ? (uint32_t)(Cfg::kTile >> 4) : 0u), kb = kd + (uint32_t)(ring.slot * (Cfg::kTile >> 4));
@@ -368,22 +381,25 @@ __global__ void __launch_bounds__(kPtThreads, 1)
               const uint32_t off = (kk >> 2) * (Cfg::kSlab >> 4) + (kk & 3) * 2;
               tc_mma_bf16(tmem + buf * 128, qb + off, kb + off, idesc_s, kk > 0 ? 1u : 0u);
             }
-            tc_commit(s_full + 4 * x + (n & 3));
-            ns = (ns & ~(0xffu << (8 * x))) | (((n + 1) & 7) << (8 * x));
+            tc_commit(s_full + 4 * x + (n_s & 3));
+            ns = (ns & ~(0xffu << (8 * x))) | (((n_s + 1) & 7) << (8 * x));
             used |= 1u << buf;
             ++turns;
+            ++t;
             WtSlot v = ring;
             v.template next<kSlots>();
-            mine = v.slot << 2 | (int)v.parity << 1 | x;
+            const int mine = v.slot << 2 | (int)v.parity << 1 | x;
+            if (waiting == 0) due[0] = mine; else if (waiting == 1) due[1] = mine; else due[2] = mine;
+            ++waiting;
             if (!pair || x) {
               ring.template next<kSlots>();
               ring.template next<kSlots>();
             }
           }
-          if (due0 >= 0) {
-            const int y = due0 & 1, slot = due0 >> 2;
+          if (ok && (waiting == 3 || (waiting > 0 && !go))) {
+            const int y = due[0] & 1, slot = due[0] >> 2;
             const uint32_t n = (np >> (8 * y)) & 7;
-            ok = wait(full + slot, (due0 >> 1) & 1);
+            ok = wait(full + slot, (due[0] >> 1) & 1);
             const uint64_t vb = vd + (uint32_t)(slot * (Cfg::kTile >> 4));
             const uint32_t po = tmem + Cfg::kColO + y * HD, pp = tmem + Cfg::kColP + y * 64;
 #pragma unroll
@@ -399,9 +415,10 @@ __global__ void __launch_bounds__(kPtThreads, 1)
             fresh &= ~(1u << y);
             tc_commit(pv_done + 4 * y + (n & 3));
             np = (np & ~(0xffu << (8 * y))) | (((n + 1) & 7) << (8 * y));
+            due[0] = due[1];
+            due[1] = due[2];
+            --waiting;
           }
-          due0 = due1;
-          due1 = mine;
         }
         if (!ok || !w.next(p)) break;
       }
@@ -569,7 +586,6 @@ __global__ void __launch_bounds__(kPtThreads, 1)
   }
 
   __syncthreads();
-  pdl_wait();  // the own kernel's sums: this one ends behind it
   if (tid == 0 && *abort_flag) set_status(pa.status, ST_WAIT_TIMEOUT);
   if (warp == 2) {
     tc_fence_after();

@@ -273,6 +273,9 @@ dinfer_status dinfer_kv_prefix_attention(const dinfer_kv_cache* kc, int32_t laye
   p.warps = hd128 ? KaCfg<float, 128, 8>::kWarps : KaCfg<float, 64, 8>::kWarps;
   p.keys = bf16 ? KaCfg<__nv_bfloat16, 128, 8>::kKeys : KaCfg<float, 128, 8>::kKeys;
   p.rows = rows;
+  p.step_ns = hd128 ? 360 : 165;
+  p.pair_ns = hd128 ? 2100 : 1400;
+  p.single_ns = hd128 ? 1750 : 1200;
   p.group_div = FastDiv::make((uint32_t)a.group);
   p.head = reinterpret_cast<int4*>(w.data);
   p.plan = reinterpret_cast<KpEntry*>(p.head + 1);
@@ -286,14 +289,14 @@ dinfer_status dinfer_kv_prefix_attention(const dinfer_kv_cache* kc, int32_t laye
   const int64_t page = kc->page_size;
   const bool boxes = tc && ((page >= 8 && 128 % page == 0) || page % 128 == 0) && make_map_pages(&maps.k, *kc, kc->k, layer) &&
                      make_map_pages(&maps.v, *kc, kc->v, layer);
-  CK(launchk(kv_prefix_plan_kernel, dim3(1), dim3(kKvPlanThreads), 0, s, 1, p));
-  CK((hd128 ? launch_kv_own<128>(p, bf16, s) : launch_kv_own<64>(p, bf16, s)));
+  CK(launchk(kv_prefix_plan_kernel, dim3(1), dim3((n + n_groups + 31) / 32 * 32), 0, s, 1, p));
   if (tc) {
     const PtArgs pa{p, w.st, (int)std::max<int64_t>(1, 128 / page)};
     auto go = [&](auto* kernel, int smem) { return launchk(kernel, dim3(p.sms), dim3(kPtThreads), smem, s, 1, maps, pa); };
     CK((hd128 ? go(boxes ? kv_prefix_tc_kernel<128, true> : kv_prefix_tc_kernel<128, false>, PtCfg<128>::kSmem)
               : go(boxes ? kv_prefix_tc_kernel<64, true> : kv_prefix_tc_kernel<64, false>, PtCfg<64>::kSmem)));
   }
+  CK((hd128 ? launch_kv_own<128>(p, bf16, s) : launch_kv_own<64>(p, bf16, s)));
   const dim3 grid((unsigned)((sums + kKjThreads / 32 - 1) / (kKjThreads / 32)));
   auto join = [&](auto* kernel) { return launchk(kernel, grid, dim3(kKjThreads), 0, s, 1, p); };
   CK((hd128 ? (bf16 ? join(kv_join_kernel<__nv_bfloat16, 128>) : join(kv_join_kernel<float, 128>))
@@ -332,7 +335,7 @@ dinfer_status dinfer_op_sample(const void* logits, int32_t dtype, int32_t rows, 
   int ctas = 1;
   while (ctas < kSmCluster && (int64_t)ctas * 2048 < vocab) ctas *= 2;
   a.slice = (vocab + ctas - 1) / ctas;
-  const size_t smem = (sizeof(SmShared) + 15) / 16 * 16 + (size_t)a.slice * size + 16;
+  const size_t smem = (sizeof(SmShared) + 15) / 16 * 16 + (size_t)a.slice * size + 48;  // pads before and behind
   if (smem > kSmMostBytes) return fail(c, DINFER_EINVAL, "too many tokens");
   const dim3 grid(rows, 1, ctas);
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
