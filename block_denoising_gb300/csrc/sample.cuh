@@ -10,7 +10,9 @@
 // drawn hangs on where u falls among up to 157000 sums of rounded weights: with
 // fp32 exponentials one row in some ten thousand gets another token than the
 // definition's, so the exponent is carried in two floats and the power of two
-// comes from a table of 512 and a cubic, about 2^-32 of the weight in all.
+// comes from a table of 512 and a cubic, about 2^-32 of the weight in all.  Passes
+// over whole slices sum the same powers as pairs of floats, two tokens an instruction
+// (22 instructions a token where whole numbers take 50), to 2^-38 of the largest.
 //
 // top-k and top-p cut the order (larger logit first, then lower index) at one
 // place.  A floor under it is found first: for top-k the k-th largest of the
@@ -25,12 +27,13 @@
 #pragma once
 #include <cooperative_groups.h>
 
-#include "attention_tc.cuh"
+#include "window_attention.cuh"
 
 namespace dinfer {
 
 constexpr int kSmThreads = 512;
 constexpr int kSmWarps = kSmThreads / 32;
+constexpr int kSmBlocks = 3;
 constexpr int kSmCluster = 8;     // CTAs of a row at most
 constexpr int kSmBins = 1024;
 constexpr int kSmList = 1536;     // logits that the first CTA takes alone
@@ -58,7 +61,8 @@ struct SmRange {
 };
 
 struct SmShared {
-  uint32_t table[512];
+  uint32_t table[512];   // 2^(j / 512) in 2^-30ths,
+  float2 powers[512];    // as a float, and what that leaves of it, relative
   uint64_t all_mass[kSmBins];  // the row's, in the first CTA
   uint32_t all_count[kSmBins];
   union {
@@ -71,16 +75,17 @@ struct SmShared {
       uint32_t index[kSmList];  // and their tokens
     };
   };
-  uint64_t warp_sum[kSmWarps], warp_above[kSmWarps], cta_sum[kSmCluster], cta_above[kSmCluster];
-  float warp_f[kSmWarps], max_of[kSmCluster], sum_of[kSmCluster];
-  uint32_t warp_i[kSmWarps], cta_i[kSmCluster];
+  uint64_t warp_sum[kSmWarps], warp_above[kSmWarps], cta_sum[kSmCluster], cta_high[kSmCluster];
+  float warp_f[kSmWarps], max_of[kSmCluster], sum_of[kSmCluster], cta_above[kSmCluster];
+  uint32_t warp_i[kSmWarps], warp_j[kSmWarps], cta_i[kSmCluster], cta_j[kSmCluster];
   SmRange range;
-  float floor;
+  float floor, ceiling;
   int bin;
 };
 
 struct SmScale {
   float m, mh, ml, ch, cl;
+  float least;  // logits below it weigh less than 2^-60
 };
 // A logit as a multiple of 2^-10 and the rest: differences of the first parts are exact.
 __device__ __forceinline__ float sm_high(float x) { return (x + 12288.f) - 12288.f; }
@@ -101,11 +106,65 @@ __device__ __forceinline__ uint64_t sm_weight(float l, const SmScale& k, const u
   return l == k.m ? 1ull << 44 : p >= -44.f ? r : 0;  // NaN: 0
 }
 
-// Larger logits first, then lower indexes.
+__device__ __forceinline__ uint64_t both(float x) { return f32x2(__float_as_uint(x), __float_as_uint(x)); }
+
+// Weights of two tokens as x + x rest.
+struct SmPair {
+  uint64_t x, rest;
+  __device__ __forceinline__ SmPair(float l0, float l1, const SmScale& k, const float2* powers) {
+    const uint64_t one = both(-1.f);
+    l0 = fmaxf(l0, k.least);
+    l1 = fmaxf(l1, k.least);
+    const uint64_t l = f32x2(__float_as_uint(l0), __float_as_uint(l1));
+    const uint64_t lh = add2(add2(l, both(12288.f)), both(-12288.f)), dh = add2(lh, both(-k.mh)), dl = add2(fma2(lh, one, l), both(-k.ml));
+    const uint64_t p = mul2(dh, both(k.ch)), ch = both(k.ch);
+    const uint64_t t = add2(fma2(dl, ch, p), both(24576.f));
+    uint64_t s = fma2(dl, ch, fma2(dh, both(k.cl), fma2(dh, ch, mul2(dh, both(-k.ch)))));
+    s = add2(s, fma2(add2(t, both(-24576.f)), one, p));
+    const uint64_t q = mul2(s, fma2(s, fma2(s, both(0.0555041086648f), both(0.240226506959f)), both(0.693147180560f)));
+    float t0, t1;
+    f32x2_parts(t, t0, t1);
+    const int n0 = __float_as_int(t0) - __float_as_int(24576.f), n1 = __float_as_int(t1) - __float_as_int(24576.f);
+    const float2 w0 = powers[n0 & 511], w1 = powers[n1 & 511];
+    x = f32x2(__float_as_uint(w0.x) + ((n0 >> 9) << 23), __float_as_uint(w1.x) + ((n1 >> 9) << 23));
+    rest = add2(q, f32x2(__float_as_uint(w0.y), __float_as_uint(w1.y)));
+  }
+  __device__ __forceinline__ void keep(bool first, bool second) {
+    float x0, x1;
+    f32x2_parts(x, x0, x1);
+    x = f32x2(first ? __float_as_uint(x0) : 0u, second ? __float_as_uint(x1) : 0u);
+  }
+};
+// Their sums: x joins `high`, which is 64 at first and so never smaller, and what that loses of it `low`.
+struct SmSum {
+  uint64_t high = both(64.f), low = 0;
+  __device__ __forceinline__ void add(const SmPair& w) {
+    const uint64_t one = both(-1.f), h = add2(high, w.x);
+    low = fma2(w.x, w.rest, add2(low, fma2(fma2(high, one, h), one, w.x)));
+    high = h;
+  }
+  __device__ __forceinline__ uint64_t whole() const {
+    float h0, h1, l0, l1;
+    f32x2_parts(high, h0, h1);
+    f32x2_parts(low, l0, l1);
+    const long long w = __float2ll_rn((h0 - 64.f) * 0x1p44f) + __float2ll_rn((h1 - 64.f) * 0x1p44f) + __float2ll_rn(l0 * 0x1p44f) +
+                        __float2ll_rn(l1 * 0x1p44f);
+    return w > 0 ? (uint64_t)w : 0;
+  }
+};
+
+// Larger logits first, then lower indexes.  kDrop: bits of a logit that are always zero (16 of a bf16's).
+template <int kDrop>
 __device__ __forceinline__ uint64_t sm_order(float l, int index) {
   const uint32_t b = __float_as_uint(l + 0.f);  // -0 is 0
   const uint32_t up = b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
-  return ((uint64_t)~up << kSmIndexBits) | (uint32_t)index;
+  return ((uint64_t)(~up >> kDrop) << kSmIndexBits) | (uint32_t)index;
+}
+// The least logit at or before a place of the order.
+template <int kDrop>
+__device__ __forceinline__ float sm_logit(uint64_t place) {
+  const uint32_t up = ~((uint32_t)(place >> kSmIndexBits) << kDrop);
+  return __uint_as_float((up & 0x80000000u ? up ^ 0x80000000u : ~up) & ~((1u << kDrop) - 1u));
 }
 
 template <typename V, typename Op>
@@ -123,22 +182,38 @@ __device__ __forceinline__ uint64_t sm_fraction(float x) {
   return !(x > 0.f) ? 0ull : x >= 1.f ? ~0ull : (uint64_t)((double)x * 18446744073709551616.0);
 }
 
-// A slice's logits in shared memory, 16 bytes at a time: pads and NaN read as -inf.
+// A slice's logits in shared memory, 16 bytes at a time: pads and NaN read as -inf.  What needs no fp32 stays packed
+// (bf16: two of the type an instruction).
 template <typename T>
 struct SmVec;
 template <>
 struct SmVec<float> {
   static constexpr int kN = 4;
+  using Max = float;
+  static __device__ __forceinline__ Max lowest() { return -INFINITY; }
   static __device__ __forceinline__ void get(const uint4& d, float (&l)[4]) {
     l[0] = fmaxf(__uint_as_float(d.x), -INFINITY);
     l[1] = fmaxf(__uint_as_float(d.y), -INFINITY);
     l[2] = fmaxf(__uint_as_float(d.z), -INFINITY);
     l[3] = fmaxf(__uint_as_float(d.w), -INFINITY);
   }
+  static __device__ __forceinline__ void max(const uint4& d, Max& m) {
+    m = max3(m, __uint_as_float(d.x), __uint_as_float(d.y));
+    m = max3(m, __uint_as_float(d.z), __uint_as_float(d.w));
+  }
+  static __device__ __forceinline__ float largest(Max m) { return m; }
+  // bit e: logit e is `least` or more
+  static __device__ __forceinline__ uint32_t reach(const uint4& d, float least) {
+    return (uint32_t)(__uint_as_float(d.x) >= least) | (uint32_t)(__uint_as_float(d.y) >= least) << 1 |
+           (uint32_t)(__uint_as_float(d.z) >= least) << 2 | (uint32_t)(__uint_as_float(d.w) >= least) << 3;
+  }
 };
 template <>
 struct SmVec<__nv_bfloat16> {
   static constexpr int kN = 8;
+  using Max = __nv_bfloat162;
+  static __device__ __forceinline__ __nv_bfloat162 two(uint32_t w) { return *reinterpret_cast<const __nv_bfloat162*>(&w); }
+  static __device__ __forceinline__ Max lowest() { return two(0xff80ff80u); }
   static __device__ __forceinline__ void get(const uint4& d, float (&l)[8]) {
     const uint32_t w[4] = {d.x, d.y, d.z, d.w};
 #pragma unroll
@@ -147,18 +222,38 @@ struct SmVec<__nv_bfloat16> {
       l[2 * i + 1] = fmaxf(__uint_as_float(w[i] & 0xffff0000u), -INFINITY);
     }
   }
+  static __device__ __forceinline__ void max(const uint4& d, Max& m) {
+    m = __hmax2(m, __hmax2(__hmax2(two(d.x), two(d.y)), __hmax2(two(d.z), two(d.w))));
+  }
+  static __device__ __forceinline__ float largest(Max m) { return fmaxf(__low2float(m), __high2float(m)); }
+  static __device__ __forceinline__ uint32_t reach(const uint4& d, float least) {
+    const uint32_t w[4] = {d.x, d.y, d.z, d.w};
+    const __nv_bfloat162 f = __bfloat162bfloat162(__float2bfloat16_ru(least));  // no bf16 lies between
+    uint32_t hit = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t m = __hge2_mask(two(w[i]), f);
+      hit |= ((m & 1u) | (m >> 30 & 2u)) << (2 * i);
+    }
+    return hit;
+  }
 };
 
 template <typename T>
-__global__ void __launch_bounds__(kSmThreads) sample_kernel(const __grid_constant__ SmArgs a) {
+__global__ void __launch_bounds__(kSmThreads, kSmBlocks) sample_kernel(const __grid_constant__ SmArgs a) {
   namespace cg = cooperative_groups;
-  constexpr int kN = SmVec<T>::kN;
+  constexpr int kN = SmVec<T>::kN, kDrop = 32 - 8 * (int)sizeof(T);
   extern __shared__ __align__(16) uint8_t sm_raw[];
   SmShared& sh = *reinterpret_cast<SmShared*>(sm_raw);
   cg::cluster_group cluster = cg::this_cluster();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int rank = blockIdx.z, ctas = gridDim.z, row = blockIdx.x;
-  sh.table[tid] = (uint32_t)(__umul64hi(a.coarse[tid >> 5], a.fine[tid & 31]) >> 32);
+  {
+    const uint64_t w = __umul64hi(a.coarse[tid >> 5], a.fine[tid & 31]);  // 2^-62nds
+    const float f = __ull2float_rn(w);
+    sh.table[tid] = (uint32_t)(w >> 32);
+    sh.powers[tid] = make_float2(f * 0x1p-62f, __ll2float_rn((long long)(w - (uint64_t)f)) / f);
+  }
   for (int b = tid; b < kSmBins; b += kSmThreads) {
     sh.count[b] = sh.all_count[b] = 0;
     sh.mass[b] = sh.all_mass[b] = 0;
@@ -166,6 +261,10 @@ __global__ void __launch_bounds__(kSmThreads) sample_kernel(const __grid_constan
   cluster.barrier_arrive();  // waited for before the first access to another CTA's memory
   pdl_wait();
   pdl_trigger();
+  const float temperature = a.temperature ? a.temperature[row] : 1.f, top_p = a.top_p ? a.top_p[row] : 1.f;
+  const float min_p = a.min_p ? a.min_p[row] : 0.f;
+  const int top_k = a.top_k ? a.top_k[row] : 0;
+  const uint64_t u = sm_fraction(a.u[row]);
 
   // the slice, as it lies behind a boundary of 16 bytes, with -inf around it
   const int begin = rank * a.slice, n = max(0, min(a.slice, a.vocab - begin));
@@ -200,11 +299,17 @@ __global__ void __launch_bounds__(kSmThreads) sample_kernel(const __grid_constan
   // v of every CTA to every CTA's to[rank]; behind the next cluster barrier
   auto tell = [&](auto* to, auto v) { *(cluster.map_shared_rank(to, tid) + rank) = v; };
 
-  float mine = -INFINITY;  // the thread's largest
-  each([&](int, const float (&l)[kN]) {
-#pragma unroll
-    for (int e = 0; e < kN; ++e) mine = fmaxf(mine, l[e]);
-  });
+  auto each_raw = [&](auto f) {
+#pragma unroll 4
+    for (int i = v0 + lane; i < v1; i += 32) f(begin - off + i * kN, reinterpret_cast<const uint4*>(raw)[i]);
+  };
+
+  float mine;  // the thread's largest
+  {
+    typename SmVec<T>::Max most = SmVec<T>::lowest();
+    each_raw([&](int, const uint4& d) { SmVec<T>::max(d, most); });
+    mine = fmaxf(SmVec<T>::largest(most), -INFINITY);
+  }
   {
     const float m = sm_reduce(mine, [](float p, float q) { return fmaxf(p, q); });
     if (lane == 0) sh.warp_f[warp] = m;
@@ -227,19 +332,21 @@ __global__ void __launch_bounds__(kSmThreads) sample_kernel(const __grid_constan
     return;
   }
 
-  const float temperature = a.temperature ? a.temperature[row] : 1.f, top_p = a.top_p ? a.top_p[row] : 1.f;
-  const float min_p = a.min_p ? a.min_p[row] : 0.f;
-  const int top_k = a.top_k ? a.top_k[row] : 0;
   const bool greedy = !(temperature > 0.f) || top_k == 1, by_k = !greedy && top_k > 0 && top_k < a.vocab, by_p = !greedy && top_p < 1.f;
   SmScale scale;
   {
-    const double c = fmin(1.4426950408889634074 / (double)temperature, 0x1p100);
     scale.m = top;
     scale.mh = sm_high(top);
     scale.ml = top - scale.mh;
-    scale.ch = (float)c;
-    scale.cl = (float)(c - (double)scale.ch);
+    // log2(e) / temperature in two floats
+    constexpr float kLog2e = 1.44269502162933349609f, kLog2eRest = 1.92596299112661746887e-8f;
+    scale.ch = fminf(__fdiv_rn(kLog2e, temperature), 0x1p100f);
+    scale.cl = __fdiv_rn(fmaf(-scale.ch, temperature, kLog2e) + kLog2eRest, temperature);
+    if (!(fabsf(scale.cl) <= 0x1p-20f * scale.ch)) scale.cl = 0.f;  // temperatures at the ends of a float's range
+    scale.least = top - 60.f / scale.ch;
   }
+  // else the sums are of whole numbers: temperatures whose span of weights is no float, or within the logits' last places
+  const bool plain = fabsf(scale.least) < 1e30f && 60.f / scale.ch > 1e-5f * fabsf(top);
   const float bin_scale = scale.ch * ((kSmBins - 1) / kSmRange);
   auto bin_of = [&](float l) { return l == top ? 0 : (int)fminf((float)(kSmBins - 1), (top - l) * bin_scale); };
 
@@ -266,10 +373,25 @@ __global__ void __launch_bounds__(kSmThreads) sample_kernel(const __grid_constan
   // the softmax's sum at temperature 1
   if (a.conf) {
     float sum = 0.f;
-    each([&](int, const float (&l)[kN]) {
+    if (top == INFINITY) {
+      each([&](int, const float (&l)[kN]) {
 #pragma unroll
-      for (int e = 0; e < kN; ++e) sum += top == INFINITY ? (l[e] == top ? 1.f : 0.f) : ex2_approx((l[e] - top) * 1.4426950408889634f);
-    });
+        for (int e = 0; e < kN; ++e) sum += l[e] == top ? 1.f : 0.f;
+      });
+    } else {
+      uint64_t sums = 0;
+      each([&](int, const float (&l)[kN]) {
+#pragma unroll
+        for (int e = 0; e < kN; e += 2) {
+          float p, q;
+          f32x2_parts(mul2(add2(f32x2(__float_as_uint(l[e]), __float_as_uint(l[e + 1])), both(-top)), both(1.4426950408889634f)), p, q);
+          sums = add2(sums, f32x2(__float_as_uint(ex2_approx(p)), __float_as_uint(ex2_approx(q))));
+        }
+      });
+      float s1;
+      f32x2_parts(sums, sum, s1);
+      sum += s1;
+    }
     sum = sm_reduce(sum, [](float p, float q) { return p + q; });
     __syncthreads();  // the maxima are read
     if (lane == 0) sh.warp_f[warp] = sum;
@@ -286,7 +408,8 @@ __global__ void __launch_bounds__(kSmThreads) sample_kernel(const __grid_constan
     if (!a.conf) return;
     float sum = 0.f;
     for (int r = 0; r < ctas; ++r) sum += sh.sum_of[r];
-    a.conf[row] = (l == top ? 1.f : (float)exp((double)l - (double)top)) / sum;
+    const float d = l - top, back = d - l, rest = (l - (d - back)) - (top + back);  // what the difference is rounded by
+    a.conf[row] = (l == top ? 1.f : expf(d) * (1.f + (fabsf(rest) < 1.f ? rest : 0.f))) / sum;
   };
 
   if (greedy) {  // the first largest
@@ -368,11 +491,17 @@ __global__ void __launch_bounds__(kSmThreads) sample_kernel(const __grid_constan
     }
     cluster.sync();
     if (rank == 0) {
-      uint64_t part = sm_fraction(top_p + 0.25f * (1.f - top_p));
+      uint64_t part = sm_fraction(top_p + fminf(0.25f * (1.f - top_p), 0.03f));
       find_bin(!by_k, 0, by_k ? (uint64_t)top_k : 0, &part);
       // no bin: fewer maxima than top_k; weights that are all below 2^-32
       const float depth = sh.bin >= 0 ? sh.bin + 1.1f : by_k ? INFINITY : 32.f * ((kSmBins - 1) / kSmRange);
       if (tid < ctas) *cluster.map_shared_rank(&sh.floor, tid) = sh.bin == kSmBins - 1 ? -INFINITY : top - depth / bin_scale;
+      __syncthreads();
+      if (!by_k) {
+        part = sm_fraction(top_p - fminf(0.25f * top_p, 0.03f));
+        find_bin(true, 0, 0, &part);
+      }
+      if (tid < ctas) *cluster.map_shared_rank(&sh.ceiling, tid) = by_k || sh.bin <= 0 ? INFINITY : top - (sh.bin - 0.1f) / bin_scale;
       for (int b = tid; b < kSmBins; b += kSmThreads) {
         sh.all_count[b] = 0;
         sh.all_mass[b] = 0;
@@ -381,71 +510,124 @@ __global__ void __launch_bounds__(kSmThreads) sample_kernel(const __grid_constan
     cluster.sync();
     floor = sh.floor;
     if (!(floor > -INFINITY)) floor = -3.402823466e38f;  // every logit that is there
-    // how many lie above it, and for top-p all weights and theirs
-    uint32_t count = 0;
-    uint64_t above = 0;
-    each([&](int, const float (&l)[kN]) {
+    // Top-p of a flat row keeps half of it: then only what lies between the floor and a ceiling, which all have that are
+    // kept for certain, is looked at one by one.
+    float ceiling = sh.ceiling;
+    // how many lie above them, and for top-p all weights and theirs
+    uint32_t count = 0, high = 0;
+    uint64_t certain = 0;
+    float above = 0.f;  // in floats: nothing but the check below hangs on it
+    auto over = [&](float l) {
+      count += l >= floor;
+      high += l >= ceiling;
+      if (!by_k && l >= floor) above += l == top ? 1.f : ex2_approx((l - top) * scale.ch);
+    };
+    if (by_k) {
+      ceiling = INFINITY;
+      each_raw([&](int, const uint4& d) { count += __popc(SmVec<T>::reach(d, floor)); });
+    } else if (!plain) {
+      ceiling = INFINITY;
+      each([&](int, const float (&l)[kN]) {
 #pragma unroll
-      for (int e = 0; e < kN; ++e) {
-        count += l[e] >= floor;
-        if (!by_k) {
-          const uint64_t w = weight(l[e]);
-          sum += w;
-          above += l[e] >= floor ? w : 0;
+        for (int e = 0; e < kN; ++e) {
+          over(l[e]);
+          sum += weight(l[e]);
         }
-      }
-    });
+      });
+    } else {
+      SmSum all, some;
+      each([&](int, const float (&l)[kN]) {
+#pragma unroll
+        for (int e = 0; e < kN; e += 2) {
+          over(l[e]);
+          over(l[e + 1]);
+          SmPair w(l[e], l[e + 1], scale, sh.powers);
+          all.add(w);
+          w.keep(l[e] >= ceiling, l[e + 1] >= ceiling);
+          some.add(w);
+        }
+      });
+      sum = all.whole();
+      certain = some.whole();
+    }
+    high = __reduce_add_sync(0xffffffffu, high);
+    certain = sm_reduce(certain, [](uint64_t p, uint64_t q) { return p + q; });
     count = __reduce_add_sync(0xffffffffu, count);
     sum = sm_reduce(sum, [](uint64_t p, uint64_t q) { return p + q; });
-    above = sm_reduce(above, [](uint64_t p, uint64_t q) { return p + q; });
+    above = sm_reduce(above, [](float p, float q) { return p + q; });
+    __syncthreads();  // the sums for the confidence are read
     if (lane == 0) {
       sh.warp_i[warp] = count;
+      sh.warp_j[warp] = high;
       sh.warp_sum[warp] = sum;
-      sh.warp_above[warp] = above;
+      sh.warp_above[warp] = certain;
+      sh.warp_f[warp] = above;
     }
     __syncthreads();
     if (tid < ctas) {
-      count = 0;
-      sum = above = 0;
+      count = high = 0;
+      sum = certain = 0;
+      above = 0.f;
       for (int w = 0; w < kSmWarps; ++w) {
         count += sh.warp_i[w];
+        high += sh.warp_j[w];
         sum += sh.warp_sum[w];
-        above += sh.warp_above[w];
+        certain += sh.warp_above[w];
+        above += sh.warp_f[w];
       }
       tell(sh.cta_i, count);
+      tell(sh.cta_j, high);
       tell(sh.cta_sum, sum);
+      tell(sh.cta_high, certain);
       tell(sh.cta_above, above);
     }
     cluster.sync();
-    uint32_t all = 0, before = 0;
+    uint32_t all = 0, all_high = 0, before = 0, before_high = 0;
     uint64_t total = 0;
-    above = 0;
+    certain = 0;
+    above = 0.f;
     for (int r = 0; r < ctas; ++r) {
-      if (r == rank) before = all;
+      if (r == rank) {
+        before = all;
+        before_high = all_high;
+      }
       all += sh.cta_i[r];
+      all_high += sh.cta_j[r];
       total += sh.cta_sum[r];
+      certain += sh.cta_high[r];
       above += sh.cta_above[r];
     }
     uint64_t want = by_k ? (uint64_t)top_k : max((uint64_t)1, sm_part_up(sm_fraction(top_p), total));
-    if (by_k ? all < (uint32_t)top_k : above < want) {  // the floor lies too high (no cut, or a logit's last place)
+    if (by_k ? all < (uint32_t)top_k : !(above * 0x1p44f * 0.9999f > (float)want)) {  // the floor lies too high (no cut, or a logit's last place)
       floor = -3.402823466e38f;
-      all = kSmList + 1;
+      all = 0x7fffffff;
     }
-    if (all <= kSmList) {
-      // ------------------------------ the list ------------------------------
+    const bool band = all > kSmList && ceiling < INFINITY && certain < want && all_high <= all;
+    if (!band) {
+      ceiling = INFINITY;
+      certain = 0;
+    } else {
+      all -= all_high;
+      before -= before_high;
+    }
+    // ------------------------------ the list ------------------------------
+    const bool listed = all <= kSmList;
+    if (listed) {
       float* to = cluster.map_shared_rank(sh.list, 0);
       uint32_t* index = cluster.map_shared_rank(sh.index, 0);
-      for (int w = 0; w < warp; ++w) before += sh.warp_i[w];
+      for (int w = 0; w < warp; ++w) before += sh.warp_i[w] - (band ? sh.warp_j[w] : 0);
       for (int i0 = v0; i0 < v1; i0 += 32) {
         const int i = i0 + lane;
-        float l[kN];
-#pragma unroll
-        for (int e = 0; e < kN; ++e) l[e] = -INFINITY;
-        if (i < v1) SmVec<T>::get(reinterpret_cast<const uint4*>(raw)[i], l);
         uint32_t hit = 0;
-#pragma unroll
-        for (int e = 0; e < kN; ++e) hit |= (uint32_t)(l[e] >= floor) << e;
+        uint4 d{};
+        if (i < v1) {
+          d = reinterpret_cast<const uint4*>(raw)[i];
+          hit = SmVec<T>::reach(d, floor);
+          if (band) hit &= ~SmVec<T>::reach(d, ceiling);
+        }
         if (!__any_sync(0xffffffffu, hit)) continue;
+        float l[kN];
+        SmVec<T>::get(d, l);
         uint32_t inc = __popc(hit);
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -463,21 +645,28 @@ __global__ void __launch_bounds__(kSmThreads) sample_kernel(const __grid_constan
         before += __shfl_sync(0xffffffffu, inc, 31);
       }
       cluster.sync();
-      if (rank) return;
-      list = (int)all;
+      if (!band) {
+        if (rank) return;
+        list = (int)all;
+      }
     }
 
     // ------------------------------ the cut ------------------------------
     // Of the list, by the first CTA alone, or of the slices.
-    const bool alone = list >= 0;
-    auto of_all = [&](auto f) {  // f(token, logit) of everything above the floor
+    const bool alone = listed;
+    auto of_all = [&](auto f) {  // f(token, logit) of everything between the floor and the ceiling
       if (alone) {
-        for (int i = tid; i < list; i += kSmThreads) f((int)sh.index[i], sh.list[i]);
+        for (int i = tid; i < (int)all; i += kSmThreads) f((int)sh.index[i], sh.list[i]);
       } else {
-        each([&](int i, const float (&l)[kN]) {
+        each_raw([&](int i, const uint4& d) {
+          uint32_t hit = SmVec<T>::reach(d, floor);
+          if (band) hit &= ~SmVec<T>::reach(d, ceiling);
+          if (!hit) return;
+          float l[kN];
+          SmVec<T>::get(d, l);
 #pragma unroll
           for (int e = 0; e < kN; ++e)
-            if (l[e] >= floor) f(i + e, l[e]);
+            if ((hit >> e) & 1u) f(i + e, l[e]);
         });
       }
     };
@@ -488,7 +677,7 @@ __global__ void __launch_bounds__(kSmThreads) sample_kernel(const __grid_constan
     uint64_t* masses = alone ? sh.all_mass : sh.mass;
     // The place where the elements kept so far reach `want` of their number or weight.
     auto search = [&](bool by_mass, uint64_t want) {
-      SmRange at{sm_order(top, 0), min(cut, sm_order(floor, (1 << kSmIndexBits) - 1)), 0, 0};
+      SmRange at{sm_order<kDrop>(fminf(top, ceiling), 0), min(cut, sm_order<kDrop>(floor, (1 << kSmIndexBits) - 1)), certain, 0};
       while (true) {
         if (!alone) {
           for (int b = tid; b < kSmBins; b += kSmThreads) {
@@ -499,7 +688,7 @@ __global__ void __launch_bounds__(kSmThreads) sample_kernel(const __grid_constan
         }
         const int bits = max(0, 54 - __clzll((long long)(at.hi - at.lo)));  // (hi - lo) >> bits < 1024
         of_all([&](int i, float l) {
-          const uint64_t c = sm_order(l, i);
+          const uint64_t c = sm_order<kDrop>(l, i);
           if (c < at.lo || c > at.hi) return;
           const int b = (int)((c - at.lo) >> bits);
           atomicAdd(counts + b, 1u);
@@ -540,10 +729,10 @@ __global__ void __launch_bounds__(kSmThreads) sample_kernel(const __grid_constan
       }
     };
     if (by_k) search(false, (uint64_t)top_k);
-    if (by_p) {
+    if (by_p && (!listed || rank == 0)) {
       if (by_k) {  // a part of what top-k left
         sum = 0;
-        of_all([&](int i, float l) { sum += sm_order(l, i) <= cut ? weight(l) : 0; });
+        of_all([&](int i, float l) { sum += sm_order<kDrop>(l, i) <= cut ? weight(l) : 0; });
         sum = sm_reduce(sum, [](uint64_t p, uint64_t q) { return p + q; });
         __syncthreads();
         if (lane == 0) sh.warp_sum[warp] = sum;
@@ -561,11 +750,21 @@ __global__ void __launch_bounds__(kSmThreads) sample_kernel(const __grid_constan
       }
       search(true, want);
     }
+    if (listed && band) {
+      if (rank == 0 && tid < ctas) cluster.map_shared_rank(&sh.range, tid)->hi = cut;
+      cluster.sync();
+      cut = sh.range.hi;
+    }
   }
 
   // ------------------------------ the token: kept weights in index order ------------------------------
+  // the cut as a logit and, among its equals, a token
+  const float cut_l = cut == ~0ull ? -INFINITY : sm_logit<kDrop>(cut);
+  const int cut_i = cut == ~0ull ? 0x7fffffff : (int)(cut & ((1 << kSmIndexBits) - 1));
+  if (!least && floor < cut_l) floor = cut_l;
+  auto is_kept = [&](int i, float l) { return l > cut_l || (l == cut_l && i <= cut_i); };
   auto kept = [&](int i, float l) -> uint64_t {
-    if (!(l >= floor) || (cut != ~0ull && sm_order(l, i) > cut)) return 0;
+    if (!(l >= floor) || !is_kept(i, l)) return 0;
     const uint64_t w = weight(l);
     return w >= least ? w : 0;
   };
@@ -579,10 +778,33 @@ __global__ void __launch_bounds__(kSmThreads) sample_kernel(const __grid_constan
   sum = 0;
   if (list >= 0) {
     for (int i = t0 + lane; i < t1; i += 32) sum += kept((int)sh.index[i], sh.list[i]);
-  } else {
+  } else if (plain && least == 0 && cut == ~0ull) {
+    SmSum pairs;
+    each([&](int, const float (&l)[kN]) {
+#pragma unroll
+      for (int e = 0; e < kN; e += 2) pairs.add(SmPair(l[e], l[e + 1], scale, sh.powers));
+    });
+    sum = pairs.whole();
+  } else if (plain && least == 0) {
+    SmSum pairs;
     each([&](int i, const float (&l)[kN]) {
 #pragma unroll
-      for (int e = 0; e < kN; ++e) sum += kept(i + e, l[e]);
+      for (int e = 0; e < kN; e += 2) {
+        SmPair w(l[e], l[e + 1], scale, sh.powers);
+        w.keep(is_kept(i + e, l[e]), is_kept(i + e + 1, l[e + 1]));
+        pairs.add(w);
+      }
+    });
+    sum = pairs.whole();
+  } else {
+    each_raw([&](int i, const uint4& d) {
+      const uint32_t hit = SmVec<T>::reach(d, floor);
+      if (!hit) return;
+      float l[kN];
+      SmVec<T>::get(d, l);
+#pragma unroll
+      for (int e = 0; e < kN; ++e)
+        if ((hit >> e) & 1u) sum += kept(i + e, l[e]);
     });
   }
   sum = sm_reduce(sum, [](uint64_t p, uint64_t q) { return p + q; });
@@ -604,25 +826,39 @@ __global__ void __launch_bounds__(kSmThreads) sample_kernel(const __grid_constan
       total += sh.cta_sum[r];
     }
   }
-  const uint64_t target = sm_part(sm_fraction(a.u[row]), total);  // the first sum above it
+  const uint64_t target = sm_part(u, total);  // the first sum above it
   for (int w = 0; w < warp; ++w) before += sh.warp_sum[w];
   if (target < before || target >= before + sh.warp_sum[warp]) return;
+  // Where the stretch's sum in floats is a few units above that in whole numbers, its last token that counts.
+  int last = -1, any = -1;
+  float last_l = 0.f, any_l = 0.f;
   for (int i0 = t0; i0 < t1; i0 += 32) {
     int token;
     const float l = read(i0 + lane, token);
-    uint64_t inc = l > -INFINITY ? kept(token, l) : 0;
+    const uint64_t w = l > -INFINITY ? kept(token, l) : 0;
+    uint64_t inc = w;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const uint64_t y = __shfl_up_sync(0xffffffffu, inc, o);
       if (lane >= o) inc += y;
     }
-    const uint32_t over = __ballot_sync(0xffffffffu, before + inc > target);
+    const uint32_t over = __ballot_sync(0xffffffffu, before + inc > target), some = __ballot_sync(0xffffffffu, w > 0);
+    const uint32_t there = __ballot_sync(0xffffffffu, l > -INFINITY);
     if (over) {
       if (lane == __ffs(over) - 1) put(token, l);
       return;
     }
+    if (some) {
+      last = __shfl_sync(0xffffffffu, token, 31 - __clz(some));
+      last_l = __shfl_sync(0xffffffffu, l, 31 - __clz(some));
+    }
+    if (there) {
+      any = __shfl_sync(0xffffffffu, token, 31 - __clz(there));
+      any_l = __shfl_sync(0xffffffffu, l, 31 - __clz(there));
+    }
     before += __shfl_sync(0xffffffffu, inc, 31);
   }
+  if (lane == 0 && any >= 0) put(last >= 0 ? last : any, last >= 0 ? last_l : any_l);
 }
 
 }  // namespace dinfer
