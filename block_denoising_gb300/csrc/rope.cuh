@@ -14,7 +14,10 @@
 // at most pi / 4.
 //
 // The cosines of a row are the same for all its heads: a block computes those of
-// its rows into shared memory, one pair a thread, and then streams the heads.
+// its rows into shared memory, one pair a thread, and then streams the heads.  They
+// lie there in the order in which the threads of a head read them: those of the first
+// pair of every work item, then of the second (pair by pair, 64 bytes apart, four
+// threads met in a bank: 8704 rows of 32 heads of 128 31 us).
 #pragma once
 #include "attention_tc.cuh"
 #include "kv_pages.cuh"
@@ -23,7 +26,7 @@ namespace dinfer {
 
 constexpr int kRopeThreads = 256;
 constexpr int kRopePairs = 128;   // of a head of at most 256
-constexpr int kRopeRows = 4;      // rows of a block at a time, at most
+constexpr int kRopeRows = 4;      // rows of a block at a time, at most: a warp each looks its place up
 
 struct RopeTurns {
   uint64_t f[kRopePairs];  // turns per position, 2^-64ths
@@ -44,7 +47,7 @@ struct RopeArgs {
   const int32_t* positions;  // NULL: first + row, or the token's place
   int first, rows, head_dim;
   int chunk, parts;          // rows of a block at a time; blocks that share them
-  FastDiv head_items, vecs;  // work items of a rotated head; 16-byte vectors of a head
+  FastDiv head_items, copies;  // work items of a rotated head, of a copied one: two of its 16-byte vectors
   FastDiv row_items;         // of a row, all operands
   int rot_items;             // of head_items, those that are rotated
   bool in_place;             // x[0].to is x[0].from: what is not rotated stays
@@ -92,6 +95,12 @@ struct RopeVec<__nv_bfloat16, 8> {
   }
   __device__ __forceinline__ void set2(int e, float a, float b) { (&d.x)[e >> 1] = pack_bf16x2(a, b); }
 };
+template <typename Vec>
+__device__ __forceinline__ Vec rope_load(const void* p) {
+  Vec v;
+  if constexpr (sizeof(Vec) == 16) v.d = __ldcs(reinterpret_cast<const uint4*>(p)); else v = *reinterpret_cast<const Vec*>(p);
+  return v;
+}
 template <typename T>
 struct RopeVec<T, 1> {
   T d;
@@ -103,11 +112,12 @@ struct RopeVec<T, 1> {
 // bytes, or 1 where the rotated part is not made of such vectors.  An item has a
 // second vector, its pairs' other halves, unless neighbours are paired within one.
 template <typename T, bool kPairs, int V, bool kPlace>
-__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constant__ RopeArgs a, const __grid_constant__ RopeTurns turns) {
+__global__ void __launch_bounds__(kRopeThreads, 4) rope_kernel(const __grid_constant__ RopeArgs a, const __grid_constant__ RopeTurns turns) {
   using Vec = RopeVec<T, V>;
-  constexpr int kFull = 16 / (int)sizeof(T), kU = V > 1 ? 4 : 2;
+  constexpr int kFull = 16 / (int)sizeof(T), kU = V > 1 && !kPlace ? 4 : 2;
   constexpr bool kTwo = !kPairs || V == 1;
-  __shared__ float2 cs[kRopeThreads > kRopeRows * kRopePairs ? kRopeThreads : kRopeRows * kRopePairs];
+  constexpr int kEach = V == 1 ? 1 : kPairs ? V / 2 : V;  // pairs of an item
+  __shared__ float2 cs[kRopeRows * kRopePairs];
   __shared__ int64_t place[kRopeRows];  // append: where the row lies in the cache, or -1
   __shared__ int where[kRopeRows];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -132,15 +142,16 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
     __syncthreads();
     for (int i = tid; i < rows * turns.pairs; i += kRopeThreads) {
       const int r = i / turns.pairs;
-      cs[i] = rope_turn(where[r], turns.f[i - r * turns.pairs], turns.magnitude);
+      const int p = i - r * turns.pairs;
+      cs[r * turns.pairs + p % kEach * a.rot_items + p / kEach] = rope_turn(where[r], turns.f[p], turns.magnitude);
     }
     __syncthreads();
     const int all = rows * (int)a.row_items.d;
     for (int i0 = part * kRopeThreads + tid; i0 < all; i0 += a.parts * kRopeThreads * kU) {
       Vec lo[kU], hi[kU];
-      uint4 copy[kU];
+      uint4 copy[kU][2];
       T* to[kU];
-      int kind[kU], pair[kU];  // 0: nothing, 1: rotated, 2: one vector as it is, 3: 16 bytes as they are
+      int kind[kU], pair[kU];  // 0: nothing, 1: rotated, 2: one vector as it is, 3: two vectors of 16 bytes as they are
 #pragma unroll
       for (int u = 0; u < kU; ++u) {  // all loads before the first store
         const int i = i0 + u * a.parts * kRopeThreads;
@@ -163,8 +174,10 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
         T* dst = kPlace && op ? reinterpret_cast<T*>(reinterpret_cast<uint4*>(o.to) + place[r]) : reinterpret_cast<T*>(o.to) + row * o.to_stride;
         const int64_t step = kPlace && op ? a.c.head_stride * kFull : a.head_dim;
         if (kPlace && op == 2) {
-          const int h = (int)a.vecs.div((uint32_t)x), v = x - h * (int)a.vecs.d;
-          copy[u] = __ldcs(reinterpret_cast<const uint4*>(from + h * a.head_dim) + v);
+          const int h = (int)a.copies.div((uint32_t)x), v = x - h * (int)a.copies.d;
+          const uint4* row_v = reinterpret_cast<const uint4*>(from + h * a.head_dim) + v;
+          copy[u][0] = __ldcs(row_v);
+          copy[u][1] = __ldcs(row_v + a.copies.d);
           to[u] = dst + h * step + v * kFull;
           kind[u] = 3;
           continue;
@@ -174,14 +187,14 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
         dst += h * step;
         if (v < a.rot_items) {
           const int e = kPairs && V == 1 ? 2 * v : v * V;
-          pair[u] = r * turns.pairs + (kPairs && V > 1 ? e / 2 : kPairs ? v : e);
-          lo[u] = *reinterpret_cast<const Vec*>(from + e);
-          if constexpr (kTwo) hi[u] = *reinterpret_cast<const Vec*>(from + e + (kPairs ? 1 : turns.pairs));
+          pair[u] = r * turns.pairs + v;
+          lo[u] = rope_load<Vec>(from + e);
+          if constexpr (kTwo) hi[u] = rope_load<Vec>(from + e + (kPairs ? 1 : turns.pairs));
           to[u] = dst + e;
           kind[u] = 1;
         } else if (op || !a.in_place) {
           const int e = 2 * turns.pairs + (v - a.rot_items) * V;
-          lo[u] = *reinterpret_cast<const Vec*>(from + e);
+          lo[u] = rope_load<Vec>(from + e);
           to[u] = dst + e;
           kind[u] = 2;
         }
@@ -197,14 +210,14 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
           } else if constexpr (kPairs) {
 #pragma unroll
             for (int e = 0; e < V; e += 2) {
-              const float2 t = cs[pair[u] + e / 2];
+              const float2 t = cs[pair[u] + e / 2 * a.rot_items];
               const float x = lo[u].get(e), y = lo[u].get(e + 1);
               lo[u].set2(e, fmaf(x, t.x, -y * t.y), fmaf(x, t.y, y * t.x));
             }
           } else {
 #pragma unroll
             for (int e = 0; e < V; e += 2) {
-              const float2 t0 = cs[pair[u] + e], t1 = cs[pair[u] + e + 1];
+              const float2 t0 = cs[pair[u] + e * a.rot_items], t1 = cs[pair[u] + (e + 1) * a.rot_items];
               const float x0 = lo[u].get(e), y0 = hi[u].get(e), x1 = lo[u].get(e + 1), y1 = hi[u].get(e + 1);
               lo[u].set2(e, fmaf(x0, t0.x, -y0 * t0.y), fmaf(x1, t1.x, -y1 * t1.y));
               hi[u].set2(e, fmaf(x0, t0.y, y0 * t0.x), fmaf(x1, t1.y, y1 * t1.x));
@@ -215,7 +228,8 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
         } else if (kind[u] == 2) {
           *reinterpret_cast<Vec*>(to[u]) = lo[u];
         } else if (kPlace && kind[u] == 3) {
-          *reinterpret_cast<uint4*>(to[u]) = copy[u];
+          *reinterpret_cast<uint4*>(to[u]) = copy[u][0];
+          reinterpret_cast<uint4*>(to[u])[a.copies.d] = copy[u][1];
         }
       }
     }

@@ -1,7 +1,7 @@
 // A token per row of logits by temperature, top-k, top-p and min-p from a given
 // number, and its confidence (include/dinfer_ops.h, dinfer_op_sample).
 //
-// A row is read once: a cluster of up to 8 CTAs keeps it in shared memory, a slice
+// A row is read once: a cluster of up to 16 CTAs keeps it in shared memory, a slice
 // each, and everything after the load is passes over those slices, joined
 // through distributed shared memory.
 //
@@ -33,8 +33,7 @@ namespace dinfer {
 
 constexpr int kSmThreads = 512;
 constexpr int kSmWarps = kSmThreads / 32;
-constexpr int kSmBlocks = 3;
-constexpr int kSmCluster = 8;     // CTAs of a row at most
+constexpr int kSmCluster = 16;    // CTAs of a row at most
 constexpr int kSmBins = 1024;
 constexpr int kSmList = 1536;     // logits that the first CTA takes alone
 constexpr int kSmIndexBits = 19;  // of a token's index
@@ -239,8 +238,8 @@ struct SmVec<__nv_bfloat16> {
   }
 };
 
-template <typename T>
-__global__ void __launch_bounds__(kSmThreads, kSmBlocks) sample_kernel(const __grid_constant__ SmArgs a) {
+template <typename T, int kBlocks>
+__global__ void __launch_bounds__(kSmThreads, kBlocks) sample_kernel(const __grid_constant__ SmArgs a) {
   namespace cg = cooperative_groups;
   constexpr int kN = SmVec<T>::kN, kDrop = 32 - 8 * (int)sizeof(T);
   extern __shared__ __align__(16) uint8_t sm_raw[];
@@ -255,8 +254,12 @@ __global__ void __launch_bounds__(kSmThreads, kSmBlocks) sample_kernel(const __g
     sh.powers[tid] = make_float2(f * 0x1p-62f, __ll2float_rn((long long)(w - (uint64_t)f)) / f);
   }
   for (int b = tid; b < kSmBins; b += kSmThreads) {
-    sh.count[b] = sh.all_count[b] = 0;
-    sh.mass[b] = sh.all_mass[b] = 0;
+    sh.count[b] = 0;
+    sh.mass[b] = 0;
+    if (rank == 0) {
+      sh.all_count[b] = 0;
+      sh.all_mass[b] = 0;
+    }
   }
   cluster.barrier_arrive();  // waited for before the first access to another CTA's memory
   pdl_wait();

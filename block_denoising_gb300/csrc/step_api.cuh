@@ -45,10 +45,10 @@ cudaError_t launch_rope(RopeArgs& a, const RopeTurns& t, bool pairs, cudaStream_
   const int per = vec ? kVec : 1;
   a.rot_items = pairs && vec ? 2 * t.pairs / per : t.pairs / per;
   a.head_items = FastDiv::make((uint32_t)(a.rot_items + (a.head_dim - 2 * t.pairs) / per));
-  a.vecs = FastDiv::make((uint32_t)(a.head_dim / kVec));
-  const int items = (a.x[0].heads + a.x[1].heads) * (int)a.head_items.d + a.x[2].heads * (int)a.vecs.d;
+  a.copies = FastDiv::make((uint32_t)std::max(1, a.head_dim / kVec / 2));  // appended heads are 64 or 128
+  const int items = (a.x[0].heads + a.x[1].heads) * (int)a.head_items.d + a.x[2].heads * (int)a.copies.d;
   a.row_items = FastDiv::make((uint32_t)items);
-  // Four rows a block share its barriers and its cosines' threads where every SM has work all the same; else a row's
+  // Several rows a block share its barriers and its cosines' threads where every SM has work all the same; else a row's
   // items are dealt to as many blocks as there are SMs to take them.
   const int sms = num_sms();
   a.chunk = a.rows >= 16 * sms ? kRopeRows : 1;
@@ -111,12 +111,29 @@ bool step_setup_hd() {
 bool g_step_setup[kMaxDevices] = {};
 constexpr int kSmMostBytes = 232448 - 2048;
 
+template <typename T, int kBlocks>
+bool step_setup_sample_one() {
+  return max_smem(sample_kernel<T, kBlocks>, kSmMostBytes) &&
+         cudaFuncSetAttribute(sample_kernel<T, kBlocks>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess;
+}
+template <typename T>
+bool step_setup_sample() {
+  return step_setup_sample_one<T, 1>() && step_setup_sample_one<T, 2>() && step_setup_sample_one<T, 3>();
+}
+template <typename T>
+cudaError_t launch_sample(const SmArgs& a, dim3 grid, size_t smem, cudaStream_t s) {
+  // registers for as many CTAs an SM as there are, or as its shared memory takes
+  const int blocks = (int64_t)grid.x * grid.z <= num_sms() ? 1 : (int)std::min<int64_t>(3, 232448 / (smem + 1024));
+  auto go = [&](auto* kernel) { return launchk(kernel, grid, dim3(kSmThreads), smem, s, (int)grid.z, a); };
+  return blocks <= 1 ? go(sample_kernel<T, 1>) : blocks == 2 ? go(sample_kernel<T, 2>) : go(sample_kernel<T, 3>);
+}
+
 // Shared-memory limits of this file's kernels, set once per device.
 bool step_setup() {
   const int dev = current_device();
   std::lock_guard<std::mutex> lk(g_setup_mutex);
   if (!g_step_setup[dev]) {
-    g_step_setup[dev] = max_smem(sample_kernel<__nv_bfloat16>, kSmMostBytes) && max_smem(sample_kernel<float>, kSmMostBytes) &&
+    g_step_setup[dev] = step_setup_sample<__nv_bfloat16>() && step_setup_sample<float>() &&
                         step_setup_hd<64>() && step_setup_hd<128>();
     if (!g_step_setup[dev]) cudaGetLastError();
   }
@@ -331,16 +348,19 @@ dinfer_status dinfer_op_sample(const void* logits, int32_t dtype, int32_t rows, 
   a.conf = conf;
   for (int j = 0; j < 16; ++j) a.coarse[j] = (uint64_t)std::ldexp(std::exp2(j / 16.0), 63);
   for (int j = 0; j < 32; ++j) a.fine[j] = (uint64_t)std::ldexp(std::exp2(j / 512.0), 63);
-  // a CTA for every 2048 tokens, up to a cluster
+  // As few CTAs a row as two an SM can hold it with, which saves their meetings (512 rows of 126464 in bf16: 4 CTAs 278
+  // us, 8 328, 16 550; 64 rows of 157184 in fp32: 8 CTAs 49 us, 16 52); more while there are SMs to spare and 2048 tokens
+  // for each (one row of 126464: 16 CTAs 19.0 us, 8 20.6, 4 27.0).
   int ctas = 1;
-  while (ctas < kSmCluster && (int64_t)ctas * 2048 < vocab) ctas *= 2;
+  while (ctas < kSmCluster && ((int64_t)vocab * size > (int64_t)ctas * 80 * 1024 ||
+                               ((int64_t)rows * ctas * 2 <= num_sms() && (int64_t)ctas * 2048 < vocab)))
+    ctas *= 2;
   a.slice = (vocab + ctas - 1) / ctas;
   const size_t smem = (sizeof(SmShared) + 15) / 16 * 16 + (size_t)a.slice * size + 48;  // pads before and behind
   if (smem > kSmMostBytes) return fail(c, DINFER_EINVAL, "too many tokens");
   const dim3 grid(rows, 1, ctas);
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  CK((dtype == DINFER_BF16 ? launchk(sample_kernel<__nv_bfloat16>, grid, dim3(kSmThreads), smem, s, ctas, a)
-                           : launchk(sample_kernel<float>, grid, dim3(kSmThreads), smem, s, ctas, a)));
+  CK((dtype == DINFER_BF16 ? launch_sample<__nv_bfloat16>(a, grid, smem, s) : launch_sample<float>(a, grid, smem, s)));
   return DINFER_OK;
 }
 
