@@ -12,7 +12,8 @@
 // definition's, so the exponent is carried in two floats and the power of two
 // comes from a table of 512 and a cubic, about 2^-32 of the weight in all.  Passes
 // over whole slices sum the same powers as pairs of floats, two tokens an instruction
-// (22 instructions a token where whole numbers take 50), to 2^-38 of the largest.
+// (some 25 instructions a token where whole numbers take 50), from a table of 32 in
+// every lane's own banks and a quartic, to 2^-31 of a weight and 2^-38 of the largest.
 //
 // top-k and top-p cut the order (larger logit first, then lower index) at one
 // place.  A floor under it is found first: for top-k the k-th largest of the
@@ -34,7 +35,8 @@ namespace dinfer {
 constexpr int kSmThreads = 512;
 constexpr int kSmWarps = kSmThreads / 32;
 constexpr int kSmCluster = 16;    // CTAs of a row at most
-constexpr int kSmBins = 1024;
+constexpr int kSmBins = 512;      // a thread each
+static_assert(kSmBins == kSmThreads, "sm_find");
 constexpr int kSmList = 1536;     // logits that the first CTA takes alone
 constexpr int kSmIndexBits = 19;  // of a token's index
 constexpr float kSmRange = 46.f;  // weights vanish below 2^-44
@@ -50,36 +52,36 @@ struct SmArgs {
   const float* u;
   int32_t* tok;
   float* conf;
+  int cuts;  // top_k or top_p is given
   uint64_t coarse[16], fine[32];  // 2^(j / 16), 2^(j / 512) in 2^-63rds
 };
 
 // Where the cut lies: elements [lo, hi] of the order hold it, `before` (of their number or weight) lie before them.
 struct SmRange {
   uint64_t lo, hi, before;
+  uint32_t count;  // of [lo, hi]
   int state;  // 0: go on, 1: found (hi is the last kept), 2: everything is kept
 };
 
-struct SmShared {
+struct alignas(16) SmShared {
   uint32_t table[512];   // 2^(j / 512) in 2^-30ths,
-  float2 powers[512];    // as a float, and what that leaves of it, relative
-  uint64_t all_mass[kSmBins];  // the row's, in the first CTA
-  uint32_t all_count[kSmBins];
-  union {
-    struct {
-      uint64_t mass[kSmBins];
-      uint32_t count[kSmBins];
-    };
-    struct {  // in the first CTA, when all have told their counts
-      float list[kSmList];  // the logits above the floor in index order,
-      uint32_t index[kSmList];  // and their tokens
-    };
-  };
+  float2 powers[32][32];  // [j][lane], so that no two lanes meet in a bank: 2^(j / 32) as a float, and what that leaves of it
   uint64_t warp_sum[kSmWarps], warp_above[kSmWarps], cta_sum[kSmCluster], cta_high[kSmCluster];
-  float warp_f[kSmWarps], max_of[kSmCluster], sum_of[kSmCluster], cta_above[kSmCluster];
+  float warp_f[kSmWarps], max_of[kSmCluster], sum_of[kSmCluster];
   uint32_t warp_i[kSmWarps], warp_j[kSmWarps], cta_i[kSmCluster], cta_j[kSmCluster];
   SmRange range;
   float floor, ceiling;
+  uint32_t listed;
   int bin;
+};
+// Behind it, for calls with top-k or top-p.
+struct SmCut {
+  // Histograms: how many (w), and their weight in 16 bits a word, 65536 of which do not overflow.  (64-bit atomics on
+  // shared memory, and on another CTA's, are loops.)  `all` is the row's, in the first CTA, whose words the others add
+  // to with their carries done.
+  uint4 hist[kSmBins], all[kSmBins];
+  float list[kSmList];  // in the first CTA: the logits above the floor in index order,
+  uint32_t index[kSmList];  // and their tokens
 };
 
 struct SmScale {
@@ -89,7 +91,9 @@ struct SmScale {
 // A logit as a multiple of 2^-10 and the rest: differences of the first parts are exact.
 __device__ __forceinline__ float sm_high(float x) { return (x + 12288.f) - 12288.f; }
 
-__device__ __forceinline__ uint64_t sm_weight(float l, const SmScale& k, const uint32_t* table) {
+// Out of line: what runs once a row runs from a cold instruction cache, and its size is its time (one row of 126464,
+// top-p of a flat row: 39 us with every use's own copy).
+__device__ __noinline__ uint64_t sm_weight(float l, const SmScale k, const uint32_t* table) {
   const float lh = sm_high(l), dh = lh - k.mh, dl = (l - lh) - k.ml;
   const float p = __fmul_rn(dh, k.ch);  // not to be contracted with the sums below, which take its rounding off again
   float s = fmaf(dl, k.ch, fmaf(dh, k.cl, fmaf(dh, k.ch, -p)));
@@ -110,22 +114,23 @@ __device__ __forceinline__ uint64_t both(float x) { return f32x2(__float_as_uint
 // Weights of two tokens as x + x rest.
 struct SmPair {
   uint64_t x, rest;
-  __device__ __forceinline__ SmPair(float l0, float l1, const SmScale& k, const float2* powers) {
+  __device__ __forceinline__ SmPair(float l0, float l1, const SmScale& k, const float2 (*powers)[32]) {
+    constexpr float kMagic = 393216.f;  // 1.5 * 2^18: a float's last place is 1 / 32
     const uint64_t one = both(-1.f);
     l0 = fmaxf(l0, k.least);
     l1 = fmaxf(l1, k.least);
     const uint64_t l = f32x2(__float_as_uint(l0), __float_as_uint(l1));
     const uint64_t lh = add2(add2(l, both(12288.f)), both(-12288.f)), dh = add2(lh, both(-k.mh)), dl = add2(fma2(lh, one, l), both(-k.ml));
     const uint64_t p = mul2(dh, both(k.ch)), ch = both(k.ch);
-    const uint64_t t = add2(fma2(dl, ch, p), both(24576.f));
+    const uint64_t t = add2(fma2(dl, ch, p), both(kMagic));
     uint64_t s = fma2(dl, ch, fma2(dh, both(k.cl), fma2(dh, ch, mul2(dh, both(-k.ch)))));
-    s = add2(s, fma2(add2(t, both(-24576.f)), one, p));
-    const uint64_t q = mul2(s, fma2(s, fma2(s, both(0.0555041086648f), both(0.240226506959f)), both(0.693147180560f)));
+    s = add2(s, fma2(add2(t, both(-kMagic)), one, p));
+    const uint64_t q = mul2(s, fma2(s, fma2(s, fma2(s, both(0.00961812910763f), both(0.0555041086648f)), both(0.240226506959f)), both(0.693147180560f)));
     float t0, t1;
     f32x2_parts(t, t0, t1);
-    const int n0 = __float_as_int(t0) - __float_as_int(24576.f), n1 = __float_as_int(t1) - __float_as_int(24576.f);
-    const float2 w0 = powers[n0 & 511], w1 = powers[n1 & 511];
-    x = f32x2(__float_as_uint(w0.x) + ((n0 >> 9) << 23), __float_as_uint(w1.x) + ((n1 >> 9) << 23));
+    const int n0 = __float_as_int(t0) - __float_as_int(kMagic), n1 = __float_as_int(t1) - __float_as_int(kMagic);
+    const float2 w0 = powers[n0 & 31][threadIdx.x & 31], w1 = powers[n1 & 31][threadIdx.x & 31];
+    x = f32x2(__float_as_uint(w0.x) + ((n0 >> 5) << 23), __float_as_uint(w1.x) + ((n1 >> 5) << 23));
     rest = add2(q, f32x2(__float_as_uint(w0.y), __float_as_uint(w1.y)));
   }
   __device__ __forceinline__ void keep(bool first, bool second) {
@@ -165,6 +170,15 @@ __device__ __forceinline__ float sm_logit(uint64_t place) {
   const uint32_t up = ~((uint32_t)(place >> kSmIndexBits) << kDrop);
   return __uint_as_float((up & 0x80000000u ? up ^ 0x80000000u : ~up) & ~((1u << kDrop) - 1u));
 }
+
+__device__ __forceinline__ void sm_count(uint4& bin) { atomicAdd(&bin.w, 1u); }
+__device__ __forceinline__ void sm_weigh(uint4& bin, uint64_t w) {
+  const uint32_t x = (uint32_t)w & 0xffffu, y = (uint32_t)w >> 16, z = (uint32_t)(w >> 32);
+  if (x) atomicAdd(&bin.x, x);
+  if (y) atomicAdd(&bin.y, y);
+  if (z) atomicAdd(&bin.z, z);
+}
+__device__ __forceinline__ uint64_t sm_mass(const uint4& bin) { return bin.x + ((uint64_t)bin.y << 16) + ((uint64_t)bin.z << 32); }
 
 template <typename V, typename Op>
 __device__ __forceinline__ V sm_reduce(V v, Op op) {
@@ -244,23 +258,17 @@ __global__ void __launch_bounds__(kSmThreads, kBlocks) sample_kernel(const __gri
   constexpr int kN = SmVec<T>::kN, kDrop = 32 - 8 * (int)sizeof(T);
   extern __shared__ __align__(16) uint8_t sm_raw[];
   SmShared& sh = *reinterpret_cast<SmShared*>(sm_raw);
+  SmCut& sc = *reinterpret_cast<SmCut*>(sm_raw + sizeof(SmShared));  // not where a.cuts is false
   cg::cluster_group cluster = cg::this_cluster();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int rank = blockIdx.z, ctas = gridDim.z, row = blockIdx.x;
-  {
-    const uint64_t w = __umul64hi(a.coarse[tid >> 5], a.fine[tid & 31]);  // 2^-62nds
+  sh.table[tid] = (uint32_t)(__umul64hi(a.coarse[tid >> 5], a.fine[tid & 31]) >> 32);
+  for (int j = warp; j < 32; j += kSmWarps) {
+    const uint64_t w = __umul64hi(a.coarse[j >> 1], a.fine[(j & 1) * 16]);  // 2^-62nds
     const float f = __ull2float_rn(w);
-    sh.table[tid] = (uint32_t)(w >> 32);
-    sh.powers[tid] = make_float2(f * 0x1p-62f, __ll2float_rn((long long)(w - (uint64_t)f)) / f);
+    sh.powers[j][lane] = make_float2(f * 0x1p-62f, __ll2float_rn((long long)(w - (uint64_t)f)) / f);
   }
-  for (int b = tid; b < kSmBins; b += kSmThreads) {
-    sh.count[b] = 0;
-    sh.mass[b] = 0;
-    if (rank == 0) {
-      sh.all_count[b] = 0;
-      sh.all_mass[b] = 0;
-    }
-  }
+  if (a.cuts) sc.hist[tid] = sc.all[tid] = make_uint4(0, 0, 0, 0);
   cluster.barrier_arrive();  // waited for before the first access to another CTA's memory
   pdl_wait();
   pdl_trigger();
@@ -273,7 +281,7 @@ __global__ void __launch_bounds__(kSmThreads, kBlocks) sample_kernel(const __gri
   const int begin = rank * a.slice, n = max(0, min(a.slice, a.vocab - begin));
   const T* from = reinterpret_cast<const T*>(a.x) + (int64_t)row * a.stride + begin;
   const int off = (int)(reinterpret_cast<uintptr_t>(from) & 15) / (int)sizeof(T);
-  uint8_t* raw = sm_raw + (sizeof(SmShared) + 15) / 16 * 16;
+  uint8_t* raw = sm_raw + sizeof(SmShared) + (a.cuts ? sizeof(SmCut) : 0);
   T* x = reinterpret_cast<T*>(raw);  // token begin + i lies at x[off + i]
   const int vecs = (off + n + kN - 1) / kN;
   {
@@ -292,7 +300,7 @@ __global__ void __launch_bounds__(kSmThreads, kBlocks) sample_kernel(const __gri
   // each warp has a stretch of the slice; each(f) hands over the logits and the first one's token, a vector at a time
   const int per = (vecs + kSmThreads - 1) / kSmThreads * 32, v0 = min(vecs, warp * per), v1 = min(vecs, v0 + per);
   auto each = [&](auto f) {
-#pragma unroll 2
+#pragma unroll 1
     for (int i = v0 + lane; i < v1; i += 32) {
       float l[kN];
       SmVec<T>::get(reinterpret_cast<const uint4*>(raw)[i], l);
@@ -303,14 +311,24 @@ __global__ void __launch_bounds__(kSmThreads, kBlocks) sample_kernel(const __gri
   auto tell = [&](auto* to, auto v) { *(cluster.map_shared_rank(to, tid) + rank) = v; };
 
   auto each_raw = [&](auto f) {
-#pragma unroll 4
+#pragma unroll 1
     for (int i = v0 + lane; i < v1; i += 32) f(begin - off + i * kN, reinterpret_cast<const uint4*>(raw)[i]);
+  };
+  // f(token, logit) for the logits of a vector that `hit` names, one a turn: the lanes' turns are those of the one with
+  // the most, where a turn for each place in the vector would be all of them (flat rows, top-p: 20 us a pass for 7)
+  auto each_hit = [&](int token, uint32_t hit, auto f) {
+#pragma unroll 1
+    for (; hit; hit &= hit - 1) {
+      const int i = token + __ffs(hit) - 1;
+      f(i, fmaxf((float)x[i - begin + off], -INFINITY));
+    }
   };
 
   float mine;  // the thread's largest
   {
     typename SmVec<T>::Max most = SmVec<T>::lowest();
-    each_raw([&](int, const uint4& d) { SmVec<T>::max(d, most); });
+#pragma unroll 4
+    for (int i = v0 + lane; i < v1; i += 32) SmVec<T>::max(reinterpret_cast<const uint4*>(raw)[i], most);
     mine = fmaxf(SmVec<T>::largest(most), -INFINITY);
   }
   {
@@ -350,17 +368,18 @@ __global__ void __launch_bounds__(kSmThreads, kBlocks) sample_kernel(const __gri
   }
   // else the sums are of whole numbers: temperatures whose span of weights is no float, or within the logits' last places
   const bool plain = fabsf(scale.least) < 1e30f && 60.f / scale.ch > 1e-5f * fabsf(top);
-  const float bin_scale = scale.ch * ((kSmBins - 1) / kSmRange);
-  auto bin_of = [&](float l) { return l == top ? 0 : (int)fminf((float)(kSmBins - 1), (top - l) * bin_scale); };
+  constexpr int kLastBin = kSmBins - 1;  // of the exponent
+  const float bin_scale = scale.ch * (kLastBin / kSmRange);
+  auto bin_of = [&](float l) { return l == top ? 0 : (int)fminf((float)kLastBin, (top - l) * bin_scale); };
 
   // The floor: a histogram over the exponent of the threads' maxima, or of weights: of the maxima, which hold what few
   // tokens have much of, and eight times those of every eighth vector.
   if (by_k) {
-    if (mine > -INFINITY) atomicAdd(&sh.count[bin_of(mine)], 1u);
+    if (mine > -INFINITY) sm_count(sc.hist[bin_of(mine)]);
   } else if (by_p) {
     auto add = [&](float l, float scaled) {
       const float w = (l == top ? 1.f : ex2_approx((l - top) * scale.ch)) * scaled;
-      if (w >= 1.f) atomicAdd(reinterpret_cast<unsigned long long*>(&sh.mass[bin_of(l)]), (unsigned long long)w);
+      if (w >= 1.f) sm_weigh(sc.hist[bin_of(l)], (uint64_t)w);
     };
     add(mine, 0x1p32f);
     int k = 0;
@@ -441,16 +460,24 @@ __global__ void __launch_bounds__(kSmThreads, kBlocks) sample_kernel(const __gri
   auto weight = [&](float l) { return sm_weight(l, scale, sh.table); };
   const uint64_t least = min_p > 0.f ? (uint64_t)ceil(fmin((double)min_p, 1.0) * 0x1p44) : 0;
 
-  // The first CTA's threads: the bin at which the histogram's sum, on top of `before`, reaches `want`, into sh.bin (-1:
-  // none), and its sum before the bin; two bins a thread.
-  auto find_bin = [&](bool by_mass, uint64_t before, uint64_t want, uint64_t* at) {
-    uint64_t v[2], own = 0;
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      v[e] = by_mass ? sh.all_mass[tid * 2 + e] : sh.all_count[tid * 2 + e];
-      own += v[e];
-    }
-    uint64_t inc = own;
+  // The first CTA's threads: the bin at which its histogram's sum (from 1), or the row's (2), on top of `before`, reaches
+  // `want` (0: a part of the whole) into sh.bin (-1: none), its sum before the bin and its count.
+  auto push_bins = [&]() {
+    uint4 h = sc.hist[tid];
+    h.y += h.x >> 16;
+    h.z += h.y >> 16;
+    uint4* to = cluster.map_shared_rank(sc.all, 0) + tid;
+    if (h.x & 0xffffu) atomicAdd(&to->x, h.x & 0xffffu);
+    if (h.y & 0xffffu) atomicAdd(&to->y, h.y & 0xffffu);
+    if (h.z) atomicAdd(&to->z, h.z);
+    if (h.w) atomicAdd(&to->w, h.w);
+  };
+  auto find_bin = [&](bool by_mass, int from, uint64_t before, uint64_t want, uint64_t part) {
+    const uint4 h = from == 1 ? sc.hist[tid] : sc.all[tid];
+    if (from > 1) sc.all[tid] = make_uint4(0, 0, 0, 0);
+    const uint32_t count = h.w;
+    const uint64_t v = by_mass ? sm_mass(h) : h.w;
+    uint64_t inc = v;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const uint64_t y = __shfl_up_sync(0xffffffffu, inc, o);
@@ -460,25 +487,24 @@ __global__ void __launch_bounds__(kSmThreads, kBlocks) sample_kernel(const __gri
     if (tid == 0) sh.bin = -1;
     __syncthreads();
     uint64_t total = before;
-    before += inc - own;
+    before += inc - v;
     for (int w = 0; w < kSmWarps; ++w) {
       if (w < warp) before += sh.warp_sum[w];
       total += sh.warp_sum[w];
     }
-    if (want == 0) want = max((uint64_t)1, sm_part(at[0], total));  // a part of the whole
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      if (before < want && want <= before + v[e]) {
-        sh.bin = tid * 2 + e;
-        sh.range.before = before;
-      }
-      before += v[e];
+    if (want == 0) want = max((uint64_t)1, sm_part(part, total));
+    if (before < want && want <= before + v) {
+      sh.bin = tid;
+      sh.range.before = before;
+      sh.range.count = count;
     }
     __syncthreads();
   };
 
   // ------------------------------ rows without a cut ------------------------------
-  float floor = -INFINITY;  // only logits from it on count
+  constexpr float kLeast = -3.402823466e38f;  // every logit that is there reaches it
+  float floor = -INFINITY, ceiling = INFINITY;  // only logits from the floor on count; all from the ceiling on are kept
+  bool banded = false;
   uint64_t cut = ~0ull;     // the last kept place of the order
   int list = -1;            // the first CTA's: how many logits it has in its list
   uint64_t sum = 0;
@@ -488,42 +514,38 @@ __global__ void __launch_bounds__(kSmThreads, kBlocks) sample_kernel(const __gri
   } else {
     // ------------------------------ the floor ------------------------------
     __syncthreads();
-    for (int b = tid; b < kSmBins; b += kSmThreads) {
-      if (by_k && sh.count[b]) atomicAdd(cluster.map_shared_rank(sh.all_count, 0) + b, sh.count[b]);
-      if (!by_k && sh.mass[b]) atomicAdd(reinterpret_cast<unsigned long long*>(cluster.map_shared_rank(sh.all_mass, 0) + b), (unsigned long long)sh.mass[b]);
-    }
+    push_bins();
     cluster.sync();
     if (rank == 0) {
-      uint64_t part = sm_fraction(top_p + fminf(0.25f * (1.f - top_p), 0.03f));
-      find_bin(!by_k, 0, by_k ? (uint64_t)top_k : 0, &part);
+      sc.hist[tid] = sc.all[tid];  // looked at twice
+      sc.all[tid] = make_uint4(0, 0, 0, 0);
       // no bin: fewer maxima than top_k; weights that are all below 2^-32
-      const float depth = sh.bin >= 0 ? sh.bin + 1.1f : by_k ? INFINITY : 32.f * ((kSmBins - 1) / kSmRange);
-      if (tid < ctas) *cluster.map_shared_rank(&sh.floor, tid) = sh.bin == kSmBins - 1 ? -INFINITY : top - depth / bin_scale;
-      __syncthreads();
-      if (!by_k) {
-        part = sm_fraction(top_p - fminf(0.25f * top_p, 0.03f));
-        find_bin(true, 0, 0, &part);
-      }
-      if (tid < ctas) *cluster.map_shared_rank(&sh.ceiling, tid) = by_k || sh.bin <= 0 ? INFINITY : top - (sh.bin - 0.1f) / bin_scale;
-      for (int b = tid; b < kSmBins; b += kSmThreads) {
-        sh.all_count[b] = 0;
-        sh.all_mass[b] = 0;
+#pragma unroll 1
+      for (int side = 0; side < 2; ++side) {
+        const float p = side ? top_p - fminf(0.25f * top_p, 0.03f) : top_p + fminf(0.25f * (1.f - top_p), 0.03f);
+        find_bin(!by_k, 1, 0, by_k ? (uint64_t)top_k : 0, sm_fraction(p));
+        const int b = sh.bin;
+        if (tid < ctas) {
+          if (side == 0)
+            *cluster.map_shared_rank(&sh.floor, tid) = b == kLastBin ? -INFINITY : top - (b >= 0 ? b + 1.1f : by_k ? INFINITY : 32.f * (kLastBin / kSmRange)) / bin_scale;
+          if (by_k || side) *cluster.map_shared_rank(&sh.ceiling, tid) = by_k || b <= 0 ? INFINITY : top - (b - 0.1f) / bin_scale;
+        }
+        if (by_k) break;
+        __syncthreads();
       }
     }
     cluster.sync();
     floor = sh.floor;
-    if (!(floor > -INFINITY)) floor = -3.402823466e38f;  // every logit that is there
+    if (!(floor > -INFINITY)) floor = kLeast;
     // Top-p of a flat row keeps half of it: then only what lies between the floor and a ceiling, which all have that are
     // kept for certain, is looked at one by one.
-    float ceiling = sh.ceiling;
+    ceiling = sh.ceiling;
     // how many lie above them, and for top-p all weights and theirs
     uint32_t count = 0, high = 0;
     uint64_t certain = 0;
-    float above = 0.f;  // in floats: nothing but the check below hangs on it
     auto over = [&](float l) {
       count += l >= floor;
       high += l >= ceiling;
-      if (!by_k && l >= floor) above += l == top ? 1.f : ex2_approx((l - top) * scale.ch);
     };
     if (by_k) {
       ceiling = INFINITY;
@@ -557,38 +579,31 @@ __global__ void __launch_bounds__(kSmThreads, kBlocks) sample_kernel(const __gri
     certain = sm_reduce(certain, [](uint64_t p, uint64_t q) { return p + q; });
     count = __reduce_add_sync(0xffffffffu, count);
     sum = sm_reduce(sum, [](uint64_t p, uint64_t q) { return p + q; });
-    above = sm_reduce(above, [](float p, float q) { return p + q; });
-    __syncthreads();  // the sums for the confidence are read
     if (lane == 0) {
       sh.warp_i[warp] = count;
       sh.warp_j[warp] = high;
       sh.warp_sum[warp] = sum;
       sh.warp_above[warp] = certain;
-      sh.warp_f[warp] = above;
     }
     __syncthreads();
     if (tid < ctas) {
       count = high = 0;
       sum = certain = 0;
-      above = 0.f;
       for (int w = 0; w < kSmWarps; ++w) {
         count += sh.warp_i[w];
         high += sh.warp_j[w];
         sum += sh.warp_sum[w];
         certain += sh.warp_above[w];
-        above += sh.warp_f[w];
       }
       tell(sh.cta_i, count);
       tell(sh.cta_j, high);
       tell(sh.cta_sum, sum);
       tell(sh.cta_high, certain);
-      tell(sh.cta_above, above);
     }
     cluster.sync();
     uint32_t all = 0, all_high = 0, before = 0, before_high = 0;
     uint64_t total = 0;
     certain = 0;
-    above = 0.f;
     for (int r = 0; r < ctas; ++r) {
       if (r == rank) {
         before = all;
@@ -598,14 +613,13 @@ __global__ void __launch_bounds__(kSmThreads, kBlocks) sample_kernel(const __gri
       all_high += sh.cta_j[r];
       total += sh.cta_sum[r];
       certain += sh.cta_high[r];
-      above += sh.cta_above[r];
     }
     uint64_t want = by_k ? (uint64_t)top_k : max((uint64_t)1, sm_part_up(sm_fraction(top_p), total));
-    if (by_k ? all < (uint32_t)top_k : !(above * 0x1p44f * 0.9999f > (float)want)) {  // the floor lies too high (no cut, or a logit's last place)
-      floor = -3.402823466e38f;
+    if (by_k && all < (uint32_t)top_k) {  // the floor lies too high (no cut, or a logit's last place)
+      floor = kLeast;
       all = 0x7fffffff;
     }
-    const bool band = all > kSmList && ceiling < INFINITY && certain < want && all_high <= all;
+    bool band = all > kSmList && ceiling < INFINITY && certain < want;
     if (!band) {
       ceiling = INFINITY;
       certain = 0;
@@ -613,12 +627,12 @@ __global__ void __launch_bounds__(kSmThreads, kBlocks) sample_kernel(const __gri
       all -= all_high;
       before -= before_high;
     }
-    // ------------------------------ the list ------------------------------
-    const bool listed = all <= kSmList;
-    if (listed) {
-      float* to = cluster.map_shared_rank(sh.list, 0);
-      uint32_t* index = cluster.map_shared_rank(sh.index, 0);
-      for (int w = 0; w < warp; ++w) before += sh.warp_i[w] - (band ? sh.warp_j[w] : 0);
+    // Puts what lies between floor and ceiling, `all` logits, `before` of them before this warp's stretch, into the first
+    // CTA's list; returns this thread's part of its weight, if that is asked for.
+    auto gather = [&](bool weigh) -> uint64_t {
+      uint64_t w = 0;
+      float* to = cluster.map_shared_rank(sc.list, 0);
+      uint32_t* index = cluster.map_shared_rank(sc.index, 0);
       for (int i0 = v0; i0 < v1; i0 += 32) {
         const int i = i0 + lane;
         uint32_t hit = 0;
@@ -629,8 +643,6 @@ __global__ void __launch_bounds__(kSmThreads, kBlocks) sample_kernel(const __gri
           if (band) hit &= ~SmVec<T>::reach(d, ceiling);
         }
         if (!__any_sync(0xffffffffu, hit)) continue;
-        float l[kN];
-        SmVec<T>::get(d, l);
         uint32_t inc = __popc(hit);
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -638,17 +650,44 @@ __global__ void __launch_bounds__(kSmThreads, kBlocks) sample_kernel(const __gri
           if (lane >= o) inc += y;
         }
         uint32_t at = before + inc - __popc(hit);
-#pragma unroll
-        for (int e = 0; e < kN; ++e)
-          if ((hit >> e) & 1) {
-            to[at] = l[e];
-            index[at] = (uint32_t)(begin - off + i * kN + e);
-            ++at;
-          }
+        each_hit(begin - off + i * kN, hit, [&](int token, float l) {
+          to[at] = l;
+          index[at] = (uint32_t)token;
+          ++at;
+          if (weigh) w += weight(l);
+        });
         before += __shfl_sync(0xffffffffu, inc, 31);
       }
+      return w;
+    };
+    // ------------------------------ the list ------------------------------
+    bool listed = all <= kSmList;
+    if (listed) {
+      for (int w = 0; w < warp; ++w) before += sh.warp_i[w] - (band ? sh.warp_j[w] : 0);
+      uint64_t w = sm_reduce(gather(!by_k), [](uint64_t p, uint64_t q) { return p + q; });
+      if (!by_k) {  // does the floor lie low enough?
+        __syncthreads();
+        if (lane == 0) sh.warp_sum[warp] = w;
+        __syncthreads();
+        if (tid < ctas) {
+          w = 0;
+          for (int k = 0; k < kSmWarps; ++k) w += sh.warp_sum[k];
+          tell(sh.cta_sum, w);
+        }
+      }
       cluster.sync();
-      if (!band) {
+      if (!by_k) {
+        w = certain;
+        for (int r = 0; r < ctas; ++r) w += sh.cta_sum[r];
+        if (w < want) {
+          listed = band = false;
+          floor = kLeast;
+          ceiling = INFINITY;
+          certain = 0;
+          cluster.sync();  // cta_sum is read
+        }
+      }
+      if (listed && !band) {
         if (rank) return;
         list = (int)all;
       }
@@ -656,131 +695,150 @@ __global__ void __launch_bounds__(kSmThreads, kBlocks) sample_kernel(const __gri
 
     // ------------------------------ the cut ------------------------------
     // Of the list, by the first CTA alone, or of the slices.
-    const bool alone = listed;
+    bool alone = listed;
     auto of_all = [&](auto f) {  // f(token, logit) of everything between the floor and the ceiling
       if (alone) {
-        for (int i = tid; i < (int)all; i += kSmThreads) f((int)sh.index[i], sh.list[i]);
+        for (int i = tid; i < (int)all; i += kSmThreads) f((int)sc.index[i], sc.list[i]);
       } else {
         each_raw([&](int i, const uint4& d) {
           uint32_t hit = SmVec<T>::reach(d, floor);
           if (band) hit &= ~SmVec<T>::reach(d, ceiling);
-          if (!hit) return;
-          float l[kN];
-          SmVec<T>::get(d, l);
-#pragma unroll
-          for (int e = 0; e < kN; ++e)
-            if ((hit >> e) & 1u) f(i + e, l[e]);
+          each_hit(i, hit, f);
         });
       }
     };
     auto meet = [&]() {
       if (alone) __syncthreads(); else cluster.sync();
     };
-    uint32_t* counts = alone ? sh.all_count : sh.count;
-    uint64_t* masses = alone ? sh.all_mass : sh.mass;
-    // The place where the elements kept so far reach `want` of their number or weight.
-    auto search = [&](bool by_mass, uint64_t want) {
-      SmRange at{sm_order<kDrop>(fminf(top, ceiling), 0), min(cut, sm_order<kDrop>(floor, (1 << kSmIndexBits) - 1)), certain, 0};
-      while (true) {
-        if (!alone) {
-          for (int b = tid; b < kSmBins; b += kSmThreads) {
-            sh.count[b] = 0;
-            sh.mass[b] = 0;
+    // A level of the search: the bin of [lo, hi] at which what is kept so far reaches `want` in number or weight.
+    auto level = [&](bool by_mass, uint64_t want, const SmRange& at) -> SmRange {
+      sc.hist[tid] = make_uint4(0, 0, 0, 0);
+      __syncthreads();
+      const int bits = max(0, 55 - __clzll((long long)(at.hi - at.lo)));  // (hi - lo) >> bits < 512
+      of_all([&](int i, float l) {
+        const uint64_t c = sm_order<kDrop>(l, i);
+        if (c < at.lo || c > at.hi) return;
+        uint4& bin = sc.hist[(int)((c - at.lo) >> bits)];
+        sm_count(bin);
+        if (by_mass) sm_weigh(bin, weight(l));
+      });
+      __syncthreads();
+      if (!alone) {
+        push_bins();
+        cluster.sync();
+      }
+      if (rank == 0) {
+        find_bin(by_mass, alone ? 1 : 2, at.before, want, 0);
+        if (tid == 0) {
+          SmRange r = sh.range;
+          const int b = sh.bin;
+          r.lo = at.lo + ((uint64_t)max(b, 0) << bits);
+          r.hi = min(at.hi, r.lo + (((uint64_t)1 << bits) - 1));
+          r.state = b < 0 ? 2 : bits == 0 || r.count == 1 ? 1 : 0;
+          for (int k = 0; k < (alone ? 1 : ctas); ++k) *cluster.map_shared_rank(&sh.range, k) = r;
+          sh.listed = 0;
+        }
+      }
+      meet();
+      const SmRange r = sh.range;
+      __syncthreads();  // it is written again
+      return r;
+    };
+    // By number, then by weight, and that again where the floor of an eighth of the row lay too high.  One place calls
+    // level(): its code is large.
+    enum { kByNumber, kByWeight, kAgain, kDone };
+    int phase = by_k ? kByNumber : kByWeight;
+    if (listed && rank) phase = kDone;
+    bool fresh = true, solo = false, idle = false;  // solo: the first CTA takes what is left; idle: the others meanwhile
+    SmRange at{};
+    uint32_t was = all;
+    while (phase != kDone) {
+      if (fresh) {
+        if (phase == kByWeight && by_k) {  // a part of what top-k left
+          sum = 0;
+          of_all([&](int i, float l) { sum += sm_order<kDrop>(l, i) <= cut ? weight(l) : 0; });
+          sum = sm_reduce(sum, [](uint64_t p, uint64_t q) { return p + q; });
+          __syncthreads();
+          if (lane == 0) sh.warp_sum[warp] = sum;
+          __syncthreads();
+          total = 0;
+          for (int w = 0; w < kSmWarps; ++w) total += sh.warp_sum[w];
+          if (!alone) {
+            if (tid < ctas) tell(sh.cta_sum, total);
+            cluster.sync();
+            total = 0;
+            for (int r = 0; r < ctas; ++r) total += sh.cta_sum[r];
           }
+          want = max((uint64_t)1, sm_part_up(sm_fraction(top_p), total));
           __syncthreads();
         }
-        const int bits = max(0, 54 - __clzll((long long)(at.hi - at.lo)));  // (hi - lo) >> bits < 1024
+        if (phase == kAgain) {
+          band = false;
+          floor = kLeast;
+          ceiling = INFINITY;
+          certain = 0;
+        }
+        at = SmRange{sm_order<kDrop>(fminf(top, ceiling), 0), min(cut, sm_order<kDrop>(floor, (1 << kSmIndexBits) - 1)), certain, 0, 0};
+        fresh = false;
+      }
+      if (!idle) at = level(phase != kByNumber, want, at);
+      if (at.state == 0 && !alone && at.count <= kSmList) {  // the bin's logits to the list, in any order
         of_all([&](int i, float l) {
           const uint64_t c = sm_order<kDrop>(l, i);
           if (c < at.lo || c > at.hi) return;
-          const int b = (int)((c - at.lo) >> bits);
-          atomicAdd(counts + b, 1u);
-          if (by_mass) atomicAdd(reinterpret_cast<unsigned long long*>(masses + b), (unsigned long long)weight(l));
+          const uint32_t k = atomicAdd(cluster.map_shared_rank(&sh.listed, 0), 1u);
+          cluster.map_shared_rank(sc.list, 0)[k] = l;
+          cluster.map_shared_rank(sc.index, 0)[k] = (uint32_t)i;
         });
-        __syncthreads();
-        if (!alone) {
-          uint32_t* all_count = cluster.map_shared_rank(sh.all_count, 0);
-          uint64_t* all_mass = cluster.map_shared_rank(sh.all_mass, 0);
-          for (int b = tid; b < kSmBins; b += kSmThreads)
-            if (sh.count[b]) {
-              atomicAdd(all_count + b, sh.count[b]);
-              if (by_mass) atomicAdd(reinterpret_cast<unsigned long long*>(all_mass + b), (unsigned long long)sh.mass[b]);
-            }
-          cluster.sync();
-        }
+        cluster.sync();
         if (rank == 0) {
-          find_bin(by_mass, at.before, want, nullptr);
-          const int b = sh.bin;
-          if (tid == 0) {
-            SmRange r = sh.range;
-            r.lo = at.lo + ((uint64_t)max(b, 0) << bits);
-            r.hi = min(at.hi, r.lo + (((uint64_t)1 << bits) - 1));
-            r.state = b < 0 ? 2 : bits == 0 || sh.all_count[b] == 1 ? 1 : 0;
-            for (int k = 0; k < (alone ? 1 : ctas); ++k) *cluster.map_shared_rank(&sh.range, k) = r;
-          }
-          __syncthreads();
-          for (int i = tid; i < kSmBins; i += kSmThreads) {
-            sh.all_count[i] = 0;
-            sh.all_mass[i] = 0;
-          }
+          solo = alone = true;
+          all = at.count;
+          continue;
         }
-        meet();
+        idle = true;
+      }
+      if (solo && at.state) {
+        solo = alone = false;
+        all = was;
+        if (tid < ctas) *cluster.map_shared_rank(&sh.range, tid) = at;
+        idle = true;
+      }
+      if (idle) {
+        cluster.sync();
         at = sh.range;
-        if (at.state == 1) cut = at.hi;
-        if (at.state) return;
         __syncthreads();
+        idle = false;
       }
-    };
-    if (by_k) search(false, (uint64_t)top_k);
-    if (by_p && (!listed || rank == 0)) {
-      if (by_k) {  // a part of what top-k left
-        sum = 0;
-        of_all([&](int i, float l) { sum += sm_order<kDrop>(l, i) <= cut ? weight(l) : 0; });
-        sum = sm_reduce(sum, [](uint64_t p, uint64_t q) { return p + q; });
-        __syncthreads();
-        if (lane == 0) sh.warp_sum[warp] = sum;
-        __syncthreads();
-        total = 0;
-        for (int w = 0; w < kSmWarps; ++w) total += sh.warp_sum[w];
-        if (!alone) {
-          if (tid < ctas) tell(sh.cta_sum, total);
-          cluster.sync();
-          total = 0;
-          for (int r = 0; r < ctas; ++r) total += sh.cta_sum[r];
-        }
-        want = max((uint64_t)1, sm_part_up(sm_fraction(top_p), total));
-        __syncthreads();
-      }
-      search(true, want);
+      if (at.state == 0) continue;
+      if (at.state == 1) cut = at.hi;
+      fresh = true;
+      phase = phase == kByNumber ? (by_p ? kByWeight : kDone) : at.state == 2 && phase == kByWeight && !alone ? kAgain : kDone;
     }
     if (listed && band) {
       if (rank == 0 && tid < ctas) cluster.map_shared_rank(&sh.range, tid)->hi = cut;
       cluster.sync();
       cut = sh.range.hi;
     }
+    banded = band;
   }
 
   // ------------------------------ the token: kept weights in index order ------------------------------
   // the cut as a logit and, among its equals, a token
   const float cut_l = cut == ~0ull ? -INFINITY : sm_logit<kDrop>(cut);
   const int cut_i = cut == ~0ull ? 0x7fffffff : (int)(cut & ((1 << kSmIndexBits) - 1));
-  if (!least && floor < cut_l) floor = cut_l;
+  if (floor < cut_l) floor = cut_l;
   auto is_kept = [&](int i, float l) { return l > cut_l || (l == cut_l && i <= cut_i); };
   auto kept = [&](int i, float l) -> uint64_t {
     if (!(l >= floor) || !is_kept(i, l)) return 0;
     const uint64_t w = weight(l);
     return w >= least ? w : 0;
   };
-  // each warp has a stretch of the list or of the slice, a token a lane
+  // each warp has a stretch of the list or of the slice
   const int stretch = (list + kSmThreads - 1) / kSmThreads * 32;
-  const int t0 = list >= 0 ? min(list, warp * stretch) : v0 * kN, t1 = list >= 0 ? min(list, t0 + stretch) : v1 * kN;
-  auto read = [&](int i, int& token) -> float {
-    token = list >= 0 ? (int)sh.index[min(i, t1 - 1)] : begin - off + i;
-    return i >= t1 ? -INFINITY : list >= 0 ? sh.list[i] : fmaxf((float)x[i], -INFINITY);
-  };
   sum = 0;
   if (list >= 0) {
-    for (int i = t0 + lane; i < t1; i += 32) sum += kept((int)sh.index[i], sh.list[i]);
+    for (int i = warp * stretch + lane; i < min(list, (warp + 1) * stretch); i += 32) sum += kept((int)sc.index[i], sc.list[i]);
   } else if (plain && least == 0 && cut == ~0ull) {
     SmSum pairs;
     each([&](int, const float (&l)[kN]) {
@@ -788,6 +846,12 @@ __global__ void __launch_bounds__(kSmThreads, kBlocks) sample_kernel(const __gri
       for (int e = 0; e < kN; e += 2) pairs.add(SmPair(l[e], l[e + 1], scale, sh.powers));
     });
     sum = pairs.whole();
+  } else if (banded && least == 0) {  // what lies above the ceiling is summed already
+    if (lane == 0) sum = sh.warp_above[warp];
+    each_raw([&](int i, const uint4& d) {
+      const uint32_t hit = SmVec<T>::reach(d, floor) & ~SmVec<T>::reach(d, ceiling);
+      each_hit(i, hit, [&](int token, float l) { sum += kept(token, l); });
+    });
   } else if (plain && least == 0) {
     SmSum pairs;
     each([&](int i, const float (&l)[kN]) {
@@ -802,12 +866,7 @@ __global__ void __launch_bounds__(kSmThreads, kBlocks) sample_kernel(const __gri
   } else {
     each_raw([&](int i, const uint4& d) {
       const uint32_t hit = SmVec<T>::reach(d, floor);
-      if (!hit) return;
-      float l[kN];
-      SmVec<T>::get(d, l);
-#pragma unroll
-      for (int e = 0; e < kN; ++e)
-        if ((hit >> e) & 1u) sum += kept(i + e, l[e]);
+      each_hit(i, hit, [&](int token, float l) { sum += kept(token, l); });
     });
   }
   sum = sm_reduce(sum, [](uint64_t p, uint64_t q) { return p + q; });
@@ -830,9 +889,49 @@ __global__ void __launch_bounds__(kSmThreads, kBlocks) sample_kernel(const __gri
     }
   }
   const uint64_t target = sm_part(u, total);  // the first sum above it
+  // the warp whose stretch it lies in, then all warps on that stretch, then the one whose part it lies in
+  int owner = -1;
+  for (int w = 0; w < kSmWarps; ++w) {
+    if (target < before) break;
+    if (target < before + sh.warp_sum[w]) {
+      owner = w;
+      break;
+    }
+    before += sh.warp_sum[w];
+  }
+  if (owner < 0) return;  // another CTA's: all its warps
+  const int o0 = list >= 0 ? min(list, owner * stretch) : min(vecs, owner * per) * kN;
+  const int o1 = list >= 0 ? min(list, o0 + stretch) : min(vecs, min(vecs, owner * per) + per) * kN;
+  const int part = (o1 - o0 + kSmThreads - 1) / kSmThreads * 32, t0 = min(o1, o0 + warp * part), t1 = min(o1, t0 + part);
+  auto read = [&](int i, int& token) -> float {
+    token = list >= 0 ? (int)sc.index[min(i, t1 - 1)] : begin - off + i;
+    return i >= t1 ? -INFINITY : list >= 0 ? sc.list[i] : fmaxf((float)x[i], -INFINITY);
+  };
+  sum = 0;
+  bool filled = false;
+  for (int i0 = t0; i0 < t1; i0 += 32) {
+    int token;
+    const float l = read(i0 + lane, token);
+    sum += l > -INFINITY ? kept(token, l) : 0;
+    filled |= l > -INFINITY;
+  }
+  sum = sm_reduce(sum, [](uint64_t p, uint64_t q) { return p + q; });
+  filled = __any_sync(0xffffffffu, filled);
+  __syncthreads();  // the warps' sums are read
+  if (lane == 0) {
+    sh.warp_sum[warp] = sum;
+    sh.warp_i[warp] = filled;
+  }
+  __syncthreads();
+  int last_part = -1;  // the last one that holds any weight, or any logit
+  for (int w = 0; w < kSmWarps; ++w)
+    if (sh.warp_sum[w]) last_part = w;
+  for (int w = 0; w < kSmWarps && last_part < 0; ++w)
+    if (sh.warp_i[w]) last_part = w;
   for (int w = 0; w < warp; ++w) before += sh.warp_sum[w];
-  if (target < before || target >= before + sh.warp_sum[warp]) return;
-  // Where the stretch's sum in floats is a few units above that in whole numbers, its last token that counts.
+  const bool here = before <= target && target < before + sh.warp_sum[warp];
+  if (!here && !(warp == last_part && target >= before + sh.warp_sum[warp])) return;
+  // Where the stretch's sum in floats is a few units above that in whole numbers: its last token that counts.
   int last = -1, any = -1;
   float last_l = 0.f, any_l = 0.f;
   for (int i0 = t0; i0 < t1; i0 += 32) {

@@ -346,17 +346,18 @@ dinfer_status dinfer_op_sample(const void* logits, int32_t dtype, int32_t rows, 
   a.u = u;
   a.tok = tok;
   a.conf = conf;
+  a.cuts = top_k || top_p;
   for (int j = 0; j < 16; ++j) a.coarse[j] = (uint64_t)std::ldexp(std::exp2(j / 16.0), 63);
   for (int j = 0; j < 32; ++j) a.fine[j] = (uint64_t)std::ldexp(std::exp2(j / 512.0), 63);
   // As few CTAs a row as two an SM can hold it with, which saves their meetings (512 rows of 126464 in bf16: 4 CTAs 278
   // us, 8 328, 16 550; 64 rows of 157184 in fp32: 8 CTAs 49 us, 16 52); more while there are SMs to spare and 2048 tokens
   // for each (one row of 126464: 16 CTAs 19.0 us, 8 20.6, 4 27.0).
   int ctas = 1;
-  while (ctas < kSmCluster && ((int64_t)vocab * size > (int64_t)ctas * 80 * 1024 ||
+  while (ctas < kSmCluster && ((int64_t)vocab * size > (int64_t)ctas * (a.cuts ? 64 : 80) * 1024 ||
                                ((int64_t)rows * ctas * 2 <= num_sms() && (int64_t)ctas * 2048 < vocab)))
     ctas *= 2;
   a.slice = (vocab + ctas - 1) / ctas;
-  const size_t smem = (sizeof(SmShared) + 15) / 16 * 16 + (size_t)a.slice * size + 48;  // pads before and behind
+  const size_t smem = sizeof(SmShared) + (a.cuts ? sizeof(SmCut) : 0) + (size_t)a.slice * size + 48;  // pads before and behind
   if (smem > kSmMostBytes) return fail(c, DINFER_EINVAL, "too many tokens");
   const dim3 grid(rows, 1, ctas);
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
