@@ -216,7 +216,7 @@ struct KaStateBf16 {
   float o[kNt][4];
   float m[kHalves], l[kHalves];
 
-  // qrow(r): the row of query r
+  // qrow(r): the row of query r (read from L2: see kv_own_kernel)
   template <typename Row>
   __device__ __forceinline__ void load_q(const Row& qrow, int rows, int lane) {
     // A fragment: a0 (g, 2t), a1 (g + 8, 2t), a2 (g, 2t + 8), a3 (g + 8, 2t + 8); absent heads are zeros
@@ -228,7 +228,7 @@ struct KaStateBf16 {
 #pragma unroll
         for (int h = 0; h < kHalves; ++h) {
           const int row = g + h * 8, col = ks * 16 + 2 * t + e * 8;
-          qn[ks][e * kHalves + h] = row < rows ? *reinterpret_cast<const uint32_t*>(qrow(row) + col) : 0u;
+          qn[ks][e * kHalves + h] = row < rows ? __ldcg(reinterpret_cast<const uint32_t*>(qrow(row) + col)) : 0u;
         }
   }
   __device__ __forceinline__ void begin(int, float*) {
@@ -356,7 +356,7 @@ struct KaStateF32 {
   template <typename Row>
   __device__ __forceinline__ void load_q(const Row& qrow, int rows, int lane) {
 #pragma unroll
-    for (int x = 0; x < kQ; ++x) qn[x] = x * 32 < rows * HD ? qrow(x / (HD / 32))[x % (HD / 32) * 32 + lane] : 0.f;
+    for (int x = 0; x < kQ; ++x) qn[x] = x * 32 < rows * HD ? __ldcg(qrow(x / (HD / 32)) + x % (HD / 32) * 32 + lane) : 0.f;
   }
   __device__ __forceinline__ void begin(int lane, float* qs) {
     // every warp writes the same values: no barrier between the warps is needed for its own reads

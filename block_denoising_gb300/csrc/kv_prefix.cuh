@@ -168,7 +168,8 @@ __global__ void __launch_bounds__(kKvPlanThreads) kv_prefix_plan_kernel(const __
       units = a.c.kv_heads * r.pairs() * r.size();
       rows = a.c.kv_heads * r.sums();
       // a unit of two tiles of rows, and of one: its chain, or its keys
-      weight = a.c.kv_heads * r.size() * ((r.pairs() - 1) * p.pair_ns + ((r.rows - 1) % 256 >= 128 ? p.pair_ns : p.single_ns)) / 64;
+      const float unit_ns = (float)(r.pairs() - 1) * p.pair_ns + ((r.rows - 1) % 256 >= 128 ? p.pair_ns : p.single_ns);
+      weight = (int)((float)a.c.kv_heads * r.size() * unit_ns * 0x1p-12f) + 1;  // at most 2^31 places of half of it
     }
   }
   if (is_group) least[t] = r.shared;
@@ -208,7 +209,7 @@ __global__ void __launch_bounds__(kKvPlanThreads) kv_prefix_plan_kernel(const __
     end.unit0 = all.y;
     p.plan[groups + a.n] = end;
     // the SMs by the time that each kernel's work takes one
-    const float own = (float)all.x * p.step_ns, shared = (float)all.w * 64;
+    const float own = (float)all.x * p.step_ns, shared = (float)all.w * 4096.f;
     const int sms = all.y == 0 ? p.sms : all.x == 0 ? 0 : max(1, min(p.sms - 1, (int)(p.sms * (own / (own + shared)) + 0.5f)));
     *p.head = make_int4(all.x, all.y, sms, 0);
   }
@@ -314,7 +315,8 @@ __global__ void __launch_bounds__(KoCfg<T, HD, R>::kThreads, 1) kv_own_kernel(co
   int* subs = reinterpret_cast<int*>(sm + Cfg::kOffSubs);  // pieces of an entry's key head
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, groups = p.groups, entries = groups + a.n;
   // Beside the prefix kernel, which began behind the plan, there is nothing to wait for but its end, in front of this
-  // one's: the join waits for this kernel alone.
+  // one's: the join waits for this kernel alone.  Without a wait in front nothing orders what an L1 still holds, so the
+  // queries, the table and the plan are read from L2, as the keys are.
   if (p.with_prefix) pdl_wait();
   pdl_trigger();
   struct Behind {
@@ -362,7 +364,7 @@ __global__ void __launch_bounds__(KoCfg<T, HD, R>::kThreads, 1) kv_own_kernel(co
     const uint32_t at = (uint32_t)load.step * kKeys + lane % kKeys;
     if (at >= (uint32_t)keys) return {0, -1};
     const int key = first + (int)at, j = (int)c.page_div.div((uint32_t)key);
-    return {row[j], a.layer_off + (key - j * c.page_size) * c.token_stride + (load.piece / subs[load_entry]) * c.head_stride};
+    return {__ldcg(row + j), a.layer_off + (key - j * c.page_size) * c.token_stride + (load.piece / subs[load_entry]) * c.head_stride};
   };
   Where at = look_up(), at_next{0, -1};
   int ahead_steps = 1;  // looked up and not issued yet: at, at_next

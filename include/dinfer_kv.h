@@ -10,9 +10,11 @@
  * around it:
  *
  *   prompt:  dinfer_kv_extend, per layer { dinfer_op_window_attention over the
- *            prompt's own rows, dinfer_kv_append of its keys and values }
+ *            prompt's own rows (dinfer_op_rope in front), dinfer_kv_append of its
+ *            keys and values }
  *   token:   dinfer_kv_extend by one, per layer { dinfer_kv_append,
- *            dinfer_kv_attention }
+ *            dinfer_kv_attention }; with rotary positions dinfer_kv_append_rope,
+ *            for sequences that begin alike dinfer_kv_prefix_attention
  *   between: dinfer_kv_fork, dinfer_kv_free, dinfer_kv_compact
  *
  * Conventions (those of dinfer_ops.h, and)
@@ -21,8 +23,9 @@
  *     allocates nothing, and can be captured into a CUDA graph
  *     (dinfer_kv_status waits, and cannot).
  *   - The caller owns all memory, the cache's tables included.  Calls on one
- *     cache must be ordered on the GPU; only dinfer_kv_attention calls may
- *     overlap with one another, each with a workspace of its own.
+ *     cache must be ordered on the GPU; only dinfer_kv_attention and
+ *     dinfer_kv_prefix_attention calls may overlap with one another, each with
+ *     a workspace of its own.
  *   - What the host cannot see (sequence numbers, page numbers, free pages) is
  *     checked on the device: the entry is skipped, and a bit is set in the
  *     cache's status word (dinfer_kv_status).  int32 operands (sequence numbers,

@@ -85,6 +85,26 @@ def test_rotated_append_refuses_bad_arguments(L):
     assert L.dinfer_kv_append_rope(*many) == dinfer.EINVAL
 
 
+def test_prefix_attention_refuses_bad_arguments(L):
+    c = ctypes.byref(cache())
+    big = 1 << 30
+    ok = [c, 0, None, 4, None, P, 1, P, P, 4096, 4096, 32, 0.1, P, big, None]
+    refused(L, L.dinfer_kv_prefix_attention, ok, (
+        (0, None), (0, ctypes.byref(cache(page_size=0))), (1, -1), (1, 2), (2, P + 2), (3, 0), (3, 1025), (3, 1024), (4, P + 1), (5, None), (5, P + 2), (6, 0),
+        (6, 2), (7, None), (8, None), (7, P + 8), (8, P + 4), (9, 4095), (10, 4000), (11, 0), (11, 31), (11, 65544), (12, 0.0), (12, float("nan")),
+        (12, float("inf")), (13, None), (13, P + 8), (14, 1000)))
+    many = list(ok)
+    many[3], many[4], many[6] = 1000, P, 25  # together more than a call may name
+    assert L.dinfer_kv_prefix_attention(*many) == dinfer.EINVAL
+    wide = [ctypes.byref(cache(kv_heads=1024, token_stride=1024 * 128, page_stride=16 * 1024 * 128, layer_stride=100 * 16 * 1024 * 128)), 0, None, 1000, None, P,
+            1, P, P, 1024 * 128, 1024 * 128, 1024, 0.1, P, dinfer.lib().dinfer_op_workspace_bytes(), None]
+    assert L.dinfer_kv_prefix_attention(*wide) == dinfer.EINVAL  # the sums of a million rows
+    assert "workspace" in L.dinfer_last_error(None).decode()
+    long = [ctypes.byref(cache(max_pages=(1 << 27) - 1)), 0, None, 4, None, P, 1, P, P, 4096, 4096, 32, 0.1, P, big, None]
+    assert L.dinfer_kv_prefix_attention(*long) == dinfer.EINVAL
+    assert "2^31" in L.dinfer_last_error(None).decode()
+
+
 def test_sample_refuses_bad_arguments(L):
     ok = [P, dinfer.FP32, 4, 1000, 1000, None, None, None, None, P, P, P, None]
     refused(L, L.dinfer_op_sample, ok, (
