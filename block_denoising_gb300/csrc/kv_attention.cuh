@@ -197,6 +197,11 @@ struct KaWalk {
   }
 };
 
+template <bool kL2, typename V>
+__device__ __forceinline__ V ka_read(const V* p) {
+  if constexpr (kL2) return __ldcg(p); else return *p;
+}
+
 // ---------------------------------------------------------------------------
 // a warp's running state over its keys of one (sequence, head piece)
 // ---------------------------------------------------------------------------
@@ -216,8 +221,8 @@ struct KaStateBf16 {
   float o[kNt][4];
   float m[kHalves], l[kHalves];
 
-  // qrow(r): the row of query r (read from L2: see kv_own_kernel)
-  template <typename Row>
+  // qrow(r): the row of query r; kL2: read past L1 (see kv_own_kernel)
+  template <bool kL2 = false, typename Row>
   __device__ __forceinline__ void load_q(const Row& qrow, int rows, int lane) {
     // A fragment: a0 (g, 2t), a1 (g + 8, 2t), a2 (g, 2t + 8), a3 (g + 8, 2t + 8); absent heads are zeros
     const int g = lane >> 2, t = lane & 3;
@@ -228,7 +233,7 @@ struct KaStateBf16 {
 #pragma unroll
         for (int h = 0; h < kHalves; ++h) {
           const int row = g + h * 8, col = ks * 16 + 2 * t + e * 8;
-          qn[ks][e * kHalves + h] = row < rows ? __ldcg(reinterpret_cast<const uint32_t*>(qrow(row) + col)) : 0u;
+          qn[ks][e * kHalves + h] = row < rows ? ka_read<kL2>(reinterpret_cast<const uint32_t*>(qrow(row) + col)) : 0u;
         }
   }
   __device__ __forceinline__ void begin(int, float*) {
@@ -353,10 +358,10 @@ struct KaStateF32 {
   float o[kRows][kOut], qn[kQ];
   float m[kRows], l[kRows];
 
-  template <typename Row>
+  template <bool kL2 = false, typename Row>
   __device__ __forceinline__ void load_q(const Row& qrow, int rows, int lane) {
 #pragma unroll
-    for (int x = 0; x < kQ; ++x) qn[x] = x * 32 < rows * HD ? __ldcg(qrow(x / (HD / 32)) + x % (HD / 32) * 32 + lane) : 0.f;
+    for (int x = 0; x < kQ; ++x) qn[x] = x * 32 < rows * HD ? ka_read<kL2>(qrow(x / (HD / 32)) + x % (HD / 32) * 32 + lane) : 0.f;
   }
   __device__ __forceinline__ void begin(int lane, float* qs) {
     // every warp writes the same values: no barrier between the warps is needed for its own reads

@@ -420,12 +420,12 @@ __global__ void __launch_bounds__(KoCfg<T, HD, R>::kThreads, 1) kv_own_kernel(co
       next_rows = min(R, a.group - sub * R);
       next_row = (a.n + e) * heads + head0;
       const T* qrow = q + e * a.q_stride + head0 * HD;
-      state.load_q([&](int r) { return qrow + r * HD; }, next_rows, lane);
+      state.template load_q<true>([&](int r) { return qrow + r * HD; }, next_rows, lane);
     } else {  // a prefix: the queries of its group's entries in turn
       const int4 r1 = __ldcg(reinterpret_cast<const int4*>(p.plan + w.entry) + 1);  // shared, e0, rows, unit0
       next_rows = min(R, r1.z - sub * R);
       next_row = r1.y * heads + kvh * r1.z + sub * R;
-      state.load_q([&](int r) {
+      state.template load_q<true>([&](int r) {
         const int x = sub * R + r, e = (int)p.group_div.div((uint32_t)x);
         return q + (r1.y + e) * a.q_stride + (kvh * a.group + x - e * a.group) * HD;
       }, next_rows, lane);
