@@ -66,7 +66,7 @@ struct SmRange {
 struct alignas(16) SmShared {
   uint32_t table[512];   // 2^(j / 512) in 2^-30ths,
   float2 powers[32][32];  // [j][lane], so that no two lanes meet in a bank: 2^(j / 32) as a float, and what that leaves of it
-  uint64_t warp_sum[kSmWarps], warp_above[kSmWarps], cta_sum[kSmCluster], cta_high[kSmCluster];
+  uint64_t warp_sum[kSmWarps], warp_above[kSmWarps], cta_sum[kSmCluster], cta_high[kSmCluster], cta_listed[kSmCluster];
   float warp_f[kSmWarps], max_of[kSmCluster], sum_of[kSmCluster];
   uint32_t warp_i[kSmWarps], warp_j[kSmWarps], cta_i[kSmCluster], cta_j[kSmCluster];
   SmRange range;
@@ -307,7 +307,8 @@ __global__ void __launch_bounds__(kSmThreads, kBlocks) sample_kernel(const __gri
       f(begin - off + i * kN, l);
     }
   };
-  // v of every CTA to every CTA's to[rank]; behind the next cluster barrier
+  // v of every CTA to every CTA's to[rank], to be read behind the next cluster barrier.  Told again only behind another one:
+  // a CTA that is late would read the second value for the first, decide by it, and wait where the others do not.
   auto tell = [&](auto* to, auto v) { *(cluster.map_shared_rank(to, tid) + rank) = v; };
 
   auto each_raw = [&](auto f) {
@@ -672,19 +673,18 @@ __global__ void __launch_bounds__(kSmThreads, kBlocks) sample_kernel(const __gri
         if (tid < ctas) {
           w = 0;
           for (int k = 0; k < kSmWarps; ++k) w += sh.warp_sum[k];
-          tell(sh.cta_sum, w);
+          tell(sh.cta_listed, w);
         }
       }
       cluster.sync();
       if (!by_k) {
         w = certain;
-        for (int r = 0; r < ctas; ++r) w += sh.cta_sum[r];
+        for (int r = 0; r < ctas; ++r) w += sh.cta_listed[r];
         if (w < want) {
           listed = band = false;
           floor = kLeast;
           ceiling = INFINITY;
           certain = 0;
-          cluster.sync();  // cta_sum is read
         }
       }
       if (listed && !band) {

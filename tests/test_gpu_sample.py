@@ -167,3 +167,52 @@ def test_shares_follow_the_weights(D):
     share = torch.bincount(tok.long(), minlength=5).double().cpu().numpy()
     w = np.exp(x[0].double().cpu().numpy())
     assert np.abs(share - n * w / w.sum()).max() <= 2
+
+
+@pytest.mark.parametrize("rows,vocab,dtype", [(512, 126464, BF), (300, 40000, F32), (64, 157184, F32)])
+def test_many_full_rows_at_once(D, rows, vocab, dtype):
+    """More rows than are at work together, of every kind side by side, several times: what a row's CTAs tell one another
+    is told in the order in which it is read.  Some rows against the definition, all against the call before."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(rows)
+    pick = lambda values, dtype=F32: torch.tensor(values, dtype=dtype, device=dev)[torch.randint(0, len(values), (rows,), generator=g, device=dev)]
+    rng = np.random.default_rng(rows)
+    for turn in range(8):
+        x = torch.randn((rows, vocab), generator=g, device=dev) * (0.5 + 2.5 * torch.rand((rows, 1), generator=g, device=dev))
+        for _ in range(10):
+            x.scatter_add_(1, torch.randint(0, vocab, (rows, 1), generator=g, device=dev), 12 * torch.rand((rows, 1), generator=g, device=dev))
+        x = x.to(dtype)
+        u = torch.rand(rows, generator=g, device=dev)
+        s = dict(temperature=pick([0.0, 0.3, 0.7, 1.0, 1.3, 3.0]), top_k=pick([0, 0, 0, 20, 50, 1000], torch.int32), top_p=pick([1.0, 0.5, 0.9, 0.95]),
+                 min_p=pick([0.0, 0.0, 0.05, 0.1]))
+        tok, conf = D.op_sample(x, u, **s)
+        for _ in range(3):
+            again = D.op_sample(x, u, **s)
+            assert torch.equal(again[0], tok) and torch.equal(again[1], conf)
+        for r in rng.integers(0, rows, 6):
+            f = {n: v[r].item() for n, v in s.items()}
+            want, c = S.draw(x[r].double().cpu().numpy(), u[r].item(), f["temperature"], f["top_k"], f["top_p"], f["min_p"])
+            assert want is None or (int(tok[r]) == want and abs(float(conf[r]) - c) <= 2.0 ** -17 * c)
+
+
+@pytest.mark.parametrize("rows", [1, 64])
+@pytest.mark.parametrize("vocab,period", [(131072, 512), (131072, 1024), (8192, 512), (16384, 1024)])
+@pytest.mark.parametrize("inside", [True, False])
+def test_rows_whose_eighth_misleads(D, rows, vocab, period, inside):
+    """The part of a row that the first guess of top-p's cut looks at holds nothing, or nearly everything: the guess is
+    found wrong, and made good."""
+    rng = np.random.default_rng(rows + vocab + period)
+    x = -5.0 * rng.random((rows, vocab))
+    part = np.arange(vocab) % period < 128
+    x[:, part if inside else ~part] -= 60.0 if inside else 4.0
+    x = torch.from_numpy(x.astype(np.float32)).to(dev)
+    for p in (0.2, 0.5, 0.9, 0.99):
+        u = [float(np.float32(v)) for v in rng.random(rows) * 0.9999]
+        if rows == 1:
+            check(D, x, u, top_p=[p] * rows, unsure=1)
+            check(D, x, u, top_p=[p] * rows, top_k=[vocab // 2] * rows, temperature=[0.5] * rows, unsure=1)
+        else:
+            tok, conf = D.op_sample(x, col(u), top_p=col([p] * rows))
+            for r in (0, 31, 63):
+                want, c = S.draw(x[r].double().cpu().numpy(), u[r], 1.0, None, float(np.float32(p)), None)
+                assert want is None or int(tok[r]) == want
