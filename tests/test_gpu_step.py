@@ -58,7 +58,7 @@ def test_prompt_forks_and_tokens(D):
     kv.append(0, k, v, rows=ints([0, prompt]), seqs=ints([n]))
     twin = kv.k.clone()
     kv.append_rope(0, rope, qkv[:, heads:heads + kv_heads], v, rows=ints([0, prompt]), seqs=ints([n]))
-    assert torch.equal(kv.k, twin)  # the two ways into the cache
+    assert torch.equal(kv.k.view(torch.int16), twin.view(torch.int16))  # the two ways into the cache; what was never written may be NaN
     kv.fork(ints([n] * n), ints(range(n)))
 
     # six continuations
