@@ -6,10 +6,12 @@
 // unit's part in a CTA is a segment, whose sums (m, l, O) go to the workspace and are
 // joined with the others and the entry's own keys' by kv_join_kernel.
 //
-// HBM-bound up to some 280 rows: a key tile of K and V, 64 KB at head_dim 128, takes
+// By its floor HBM-bound up to some 280 rows: a key tile of K and V, 64 KB at head_dim 128, takes
 // 2800 cycles of an SM's share of the bandwidth, its four products for 256 rows 2048
 // cycles of the tensor cores.  What stands between is the chain S, softmax, P V of a
-// tile, some 2500 cycles, so two of them run at a time (streams): the two tiles of rows
+// tile, which takes longer, so two of them run at a time (streams; measured 1.95 us for 128
+// keys of 256 rows at head_dim 128, 1.3 us at 64, with the tensor cores 31% and the issue
+// slots 40% busy): the two tiles of rows
 // on the same keys, or, of a unit of at most 128 rows, one tile of rows on every other
 // key tile each, with sums of their own.  352 threads:
 //   warp 0      the key tiles: page numbers, a tile ahead, and a TMA box per page and 64
@@ -17,8 +19,8 @@
 //               last one, which reads as zeros, and its keys are missing from the tile's
 //               mask.  Pages that do not divide a tile, or it them, go by 16-byte
 //               cp.async from warps 0 and 1
-//   warp 2      tensor memory and the products, S_0 S_1 S_2 P_0 V S_3 P_1 V ... while the
-//               keys come in time
+//   warp 2      tensor memory and the products, S_0 S_1 S_2 P_0 V S_3 P_1 V ..., whichever of S
+//               and P V can go
 //   warps 3-6   queries, softmax and sums of stream 0, a thread per row; warps 7-10 stream 1
 // Tensor memory, P's two halves and the lazily raised maximum are as in
 // window_attention_tc.cuh.

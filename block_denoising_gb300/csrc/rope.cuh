@@ -17,7 +17,8 @@
 // its rows into shared memory, one pair a thread, and then streams the heads.  They
 // lie there in the order in which the threads of a head read them: those of the first
 // pair of every work item, then of the second (pair by pair, 64 bytes apart, four
-// threads met in a bank: 8704 rows of 32 heads of 128 31 us).
+// threads met in a bank: 8704 rows of 32 heads of 128 31 us).  Those rows, 143 MB, take
+// 25.0 us (5.7 TB/s); appended with their queries, 214 MB, 41.2 us (5.2 TB/s).
 #pragma once
 #include "attention_tc.cuh"
 #include "kv_pages.cuh"

@@ -19,12 +19,18 @@
 // place.  A floor under it is found first: for top-k the k-th largest of the
 // threads' own maxima, which k logits reach; for top-p from the weights of an eighth
 // of the row, checked by the exact sums.  What lies above it (some hundred logits
-// mostly) goes to the first CTA, which finds the place by histograms of 1024
+// mostly) goes to the first CTA, which finds the place by histograms of 512
 // bins over (logit, index), each over the bin of the last one that holds it, until
 // one element is left.  Where more than kSmList lie above it, all CTAs do the same on
-// their slices.  (Histograms of the whole row, one atomic a logit: 512 rows of
-// 126464, of which some 400 with top-k or top-p: 650 us.)  Rows without either take
+// their slices, until a bin holds few enough for the first one's list; for top-p only
+// between the floor and a ceiling, which the eighth gives too.  Rows without either take
 // one pass.
+//
+// 512 rows of 126464 in bf16 with settings of their own (130 MB) take 262 us in a graph, of
+// which the memory needs 19; the first form, with histograms of whole rows, one atomic a logit,
+// took 651.  64 rows of 157184 in fp32 at a temperature (40 MB) take 39 us: issue slots 43%
+// busy, DRAM 11%.  One row of 126464: 5.8 us greedy, 9.2 at a temperature, 37 by top-p where
+// it is flat.
 #pragma once
 #include <cooperative_groups.h>
 
@@ -76,8 +82,8 @@ struct alignas(16) SmShared {
 };
 // Behind it, for calls with top-k or top-p.
 struct SmCut {
-  // Histograms: how many (w), and their weight in 16 bits a word, 65536 of which do not overflow.  (64-bit atomics on
-  // shared memory, and on another CTA's, are loops.)  `all` is the row's, in the first CTA, whose words the others add
+  // Histograms: how many (w), and their weight in 16 bits a word, 65536 of which do not overflow.
+  // `all` is the row's, in the first CTA, whose words the others add
   // to with their carries done.
   uint4 hist[kSmBins], all[kSmBins];
   float list[kSmList];  // in the first CTA: the logits above the floor in index order,
@@ -91,8 +97,8 @@ struct SmScale {
 // A logit as a multiple of 2^-10 and the rest: differences of the first parts are exact.
 __device__ __forceinline__ float sm_high(float x) { return (x + 12288.f) - 12288.f; }
 
-// Out of line: what runs once a row runs from a cold instruction cache, and its size is its time (one row of 126464,
-// top-p of a flat row: 39 us with every use's own copy).
+// Out of line: the kernel's uses of it are many, and its code is large.  For time it is all but the same (one flat row of
+// 126464 with top-p: 37 us, 39 with a copy at every use).
 __device__ __noinline__ uint64_t sm_weight(float l, const SmScale k, const uint32_t* table) {
   const float lh = sm_high(l), dh = lh - k.mh, dl = (l - lh) - k.ml;
   const float p = __fmul_rn(dh, k.ch);  // not to be contracted with the sums below, which take its rounding off again
@@ -316,7 +322,7 @@ __global__ void __launch_bounds__(kSmThreads, kBlocks) sample_kernel(const __gri
     for (int i = v0 + lane; i < v1; i += 32) f(begin - off + i * kN, reinterpret_cast<const uint4*>(raw)[i]);
   };
   // f(token, logit) for the logits of a vector that `hit` names, one a turn: the lanes' turns are those of the one with
-  // the most, where a turn for each place in the vector would be all of them (flat rows, top-p: 20 us a pass for 7)
+  // the most, where a turn for each place in the vector would be all of them
   auto each_hit = [&](int token, uint32_t hit, auto f) {
 #pragma unroll 1
     for (; hit; hit &= hit - 1) {

@@ -1,5 +1,6 @@
 // Host side of a serving loop's other steps (include/dinfer_ops.h: rotary
-// positions; include/dinfer_kv.h: rotated appends): argument checks and launches.
+// positions, sampling; include/dinfer_kv.h: rotated appends, attention over shared
+// prefixes): argument checks and launches.
 // Included behind kv_api.cuh, whose helpers it uses.
 #pragma once
 #include "kv_prefix_tc.cuh"
