@@ -18,8 +18,8 @@
 //   prefix  in bf16 the shared keys on the tensor cores (kv_prefix_tc.cuh), at the same
 //           time: the plan deals the SMs to the two by what their work takes
 //   join    a warp per row of the output
-// All of it in a graph: 64 sequences behind 8192 tokens, 32 heads on 8 (66 MB) 33.2 us; 32 behind
-// 8192 with 512 of their own, 16 heads on 16 (202 MB) 47.8 us, 4.2 TB/s.
+// All of it in a graph: 64 sequences behind 8192 tokens, 32 heads on 8 (66 MB) 33.5 us; 32 behind
+// 8192 with 512 of their own, 16 heads on 16 (202 MB) 48.1 us, 4.2 TB/s.
 #pragma once
 #include "kv_attention.cuh"
 
@@ -171,7 +171,7 @@ __global__ void __launch_bounds__(kKvPlanThreads) kv_prefix_plan_kernel(const __
       rows = a.c.kv_heads * r.sums();
       // a unit of two tiles of rows, and of one: its chain, or its keys
       const float unit_ns = (float)(r.pairs() - 1) * p.pair_ns + ((r.rows - 1) % 256 >= 128 ? p.pair_ns : p.single_ns);
-      weight = (int)((float)a.c.kv_heads * r.size() * unit_ns * 0x1p-12f) + 1;  // at most 2^31 places of half of it
+      weight = (int)((float)a.c.kv_heads * r.size() * unit_ns * 0x1p-12f) + 1;  // at most 2^31 places of less than 1 each
     }
   }
   if (is_group) least[t] = r.shared;

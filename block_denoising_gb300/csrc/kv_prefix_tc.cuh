@@ -6,14 +6,14 @@
 // unit's part in a CTA is a segment, whose sums (m, l, O) go to the workspace and are
 // joined with the others and the entry's own keys' by kv_join_kernel.
 //
-// By its floor HBM-bound up to some 280 rows: a key tile of K and V, 64 KB at head_dim 128, takes
-// 2800 cycles of an SM's share of the bandwidth, its four products for 256 rows 2048
+// By its floor HBM-bound up to some 230 rows: a key tile of K and V, 64 KB at head_dim 128, takes
+// 2800 cycles of an SM's share of the bandwidth, its products for 256 rows 3072
 // cycles of the tensor cores.  What stands between is the chain S, softmax, P V of a
-// tile, which takes longer, so two of them run at a time (streams; measured 1.95 us for 128
-// keys of 256 rows at head_dim 128, 1.3 us at 64, with the tensor cores 31% and the issue
-// slots 40% busy): the two tiles of rows
+// tile, which takes longer, so two of them run at a time (streams): the two tiles of rows
 // on the same keys, or, of a unit of at most 128 rows, one tile of rows on every other
-// key tile each, with sums of their own.  352 threads:
+// key tile each, with sums of their own.  Measured 2.7 us for 128 keys of 256 rows at head_dim 128 and 1.7 us
+// at 64, 1.8 and 1.2 us of 64 rows; tensor cores 42% and issue slots 41% busy with 96 sequences in three
+// groups, 64 heads of 64 on 8.  352 threads:
 //   warp 0      the key tiles: page numbers, a tile ahead, and a TMA box per page and 64
 //               columns, a page a lane; a page that is not there is asked for behind the
 //               last one, which reads as zeros, and its keys are missing from the tile's
@@ -22,8 +22,12 @@
 //   warp 2      tensor memory and the products, S_0 S_1 S_2 P_0 V S_3 P_1 V ..., whichever of S
 //               and P V can go
 //   warps 3-6   queries, softmax and sums of stream 0, a thread per row; warps 7-10 stream 1
-// Tensor memory, P's two halves and the lazily raised maximum are as in
-// window_attention_tc.cuh.
+// A weight goes through P V as two bf16, cut off and the rest, as in kv_attention_kernel:
+// 2^-16 of it is lost (with one bf16, 2^-9: 2.1 and 1.6 us for 256 rows).  P so fills the
+// 128 columns of the S that it is made of, which has been read when it is written.  There are
+// two such places, at head_dim 64 three, which the turns of both streams take in order (with
+// two at 64 the call above 101.8 us, with three 85.5).  P's two halves and the lazily raised
+// maximum are as in window_attention_tc.cuh.
 #pragma once
 #include "kv_prefix.cuh"
 #include "window_attention_tc.cuh"
@@ -42,9 +46,8 @@ struct PtCfg {
   static constexpr int kOffRing = 2 * kTile;        // behind Q
   static constexpr int kOffBar = kOffRing + kSlots * kTile;
   static constexpr int kSmem = 1024 + kOffBar + 512;
-  static constexpr int kBufs = HD == 128 ? 1 : 2;   // S
-  static constexpr int kColP = kBufs * 128;
-  static constexpr int kColO = kColP + 128;
+  static constexpr int kBufs = HD == 128 ? 2 : 3;   // places of S and P
+  static constexpr int kColO = kBufs * 128;
 };
 static_assert(PtCfg<128>::kSmem + 512 <= 232448, "prefix attention shared memory above 227 KB");
 
@@ -119,13 +122,12 @@ __global__ void __launch_bounds__(kPtThreads, 1)
   uint64_t* s_full = full + kSlots;   // [2 streams][4]
   uint64_t* pv_done = s_full + 8;     // [2 streams][4]
   uint64_t* p_full = pv_done + 8;     // [2 streams][2 halves of 64 keys]
-  uint64_t* s_free = p_full + 4;      // [kBufs]
-  uint64_t* q_full = s_free + 2;      // a segment's queries
+  uint64_t* q_full = p_full + 4;      // a segment's queries
   uint64_t* drain = q_full + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   uint32_t* masks = tmem_slot + 2;    // [8 key tiles][4]: keys that are there
-  static_assert((kSlots + 8 + 8 + 4 + 2 + 2) * 8 + 8 + 128 <= 512, "barriers");
+  static_assert((kSlots + 8 + 8 + 4 + 2) * 8 + 8 + 128 <= 512, "barriers");
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
     for (int i = 0; i < kSlots; ++i) mbar_init(&full[i], kTma ? 1 : kPtLoaders);
@@ -134,7 +136,6 @@ __global__ void __launch_bounds__(kPtThreads, 1)
       mbar_init(&pv_done[i], 1);
     }
     for (int i = 0; i < 4; ++i) mbar_init(&p_full[i], 4);
-    for (int i = 0; i < 2; ++i) mbar_init(&s_free[i], 4);
     mbar_init(q_full, 8);
     mbar_init(drain, 1);
     *abort_flag = 0;
@@ -346,8 +347,10 @@ __global__ void __launch_bounds__(kPtThreads, 1)
       const uint64_t kd = make_sw128_desc(smem_u32(sm + Cfg::kOffRing));
       const uint64_t vd = make_sw128_desc_mn(smem_u32(sm + Cfg::kOffRing), Cfg::kSlab);
       uint32_t ns = 0, np = 0;  // products issued, 8 bits for each stream (see window_tc_kernel)
-      uint32_t used = 0;        // S buffers in use
-      int turns = 0;            // S of both streams
+      int held[Cfg::kBufs];     // the last turns, oldest first: 4 n + x, the n-th of stream x; -1: none yet
+#pragma unroll
+      for (int i = 0; i < Cfg::kBufs; ++i) held[i] = -1;
+      int buf = 0;              // place of the next S
       WtSlot ring{0, 0};        // K of the key tile at hand
       bool ok = true;
       for (int seg = 0;; ++seg) {
@@ -355,21 +358,23 @@ __global__ void __launch_bounds__(kPtThreads, 1)
         ok = wait(q_full, seg & 1);
         const int last = pair ? 2 * (w.to - w.from) : w.to - w.from;
         uint32_t fresh = 3;  // bit x: no P V of this segment yet
-        // The turns whose P V is due, oldest first.  S of the next turn goes first where its keys are there, up to two
-        // turns ahead of P V; else P V, whose V makes room for other keys.  (In the order S_t, P_t-2 V without a look: a
+        // The turns whose P V is due, oldest first.  S of the next turn goes first where its keys and a place are there, up to
+        // two turns ahead of P V; else P V, whose V makes room for other keys.  (In the order S_t, P_t-2 V without a look: a
         // unit of 32 rows over 8192 keys took 1.75 us a key tile, the latency of its loads.)
         int due[3] = {-1, -1, -1}, waiting = 0;
         for (int t = 0; ok && (t < last || waiting > 0);) {
-          const int x = t & 1, buf = Cfg::kBufs == 1 ? 0 : x;
-          const uint32_t n_s = (ns >> (8 * x)) & 7, prev = Cfg::kBufs == 1 ? (uint32_t)turns - 1 : n_s - 1;
+          const int x = t & 1;
+          const uint32_t n_s = (ns >> (8 * x)) & 7;
+          const int prev = held[0];  // its P V makes room
+          uint64_t* prev_done = pv_done + 4 * (prev & 1) + ((prev >> 2) & 3);
           bool go = t < last && waiting == 0;
           if (go) {
-            ok = wait(full + ring.slot, ring.parity) && (!((used >> buf) & 1) || wait(s_free + buf, prev & 1));
+            ok = wait(full + ring.slot, ring.parity) && (prev < 0 || wait(prev_done, (prev >> 4) & 1));
           } else if (t < last && waiting < 3) {  // whichever can go first
             const int y = due[0] & 1;
             const long long t0 = clock64();
             while (true) {
-              go = mbar_test(full + ring.slot, ring.parity) && (!((used >> buf) & 1) || mbar_test(s_free + buf, prev & 1));
+              go = mbar_test(full + ring.slot, ring.parity) && (prev < 0 || mbar_test(prev_done, (prev >> 4) & 1));
               if (go || mbar_test(p_full + 2 * y, (np >> (8 * y)) & 1)) break;
               if (*abort_flag || clock64() - t0 > kWaitCycles) break;  // the wait below sees to it
             }
@@ -385,12 +390,14 @@ __global__ void __launch_bounds__(kPtThreads, 1)
             }
             tc_commit(s_full + 4 * x + (n_s & 3));
             ns = (ns & ~(0xffu << (8 * x))) | (((n_s + 1) & 7) << (8 * x));
-            used |= 1u << buf;
-            ++turns;
+#pragma unroll
+            for (int i = 0; i + 1 < Cfg::kBufs; ++i) held[i] = held[i + 1];
+            held[Cfg::kBufs - 1] = (int)n_s << 2 | x;
             ++t;
             WtSlot v = ring;
             v.template next<kSlots>();
-            const int mine = v.slot << 2 | (int)v.parity << 1 | x;
+            const int mine = v.slot << 4 | buf << 2 | (int)v.parity << 1 | x;
+            buf = buf + 1 == Cfg::kBufs ? 0 : buf + 1;
             if (waiting == 0) due[0] = mine; else if (waiting == 1) due[1] = mine; else due[2] = mine;
             ++waiting;
             if (!pair || x) {
@@ -399,11 +406,11 @@ __global__ void __launch_bounds__(kPtThreads, 1)
             }
           }
           if (ok && (waiting == 3 || (waiting > 0 && !go))) {
-            const int y = due[0] & 1, slot = due[0] >> 2;
+            const int y = due[0] & 1, slot = due[0] >> 4;
             const uint32_t n = (np >> (8 * y)) & 7;
             ok = wait(full + slot, (due[0] >> 1) & 1);
             const uint64_t vb = vd + (uint32_t)(slot * (Cfg::kTile >> 4));
-            const uint32_t po = tmem + Cfg::kColO + y * HD, pp = tmem + Cfg::kColP + y * 64;
+            const uint32_t po = tmem + Cfg::kColO + y * HD, pp = tmem + ((due[0] >> 2) & 3) * 128;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               ok = ok && wait(p_full + 2 * y + h, n & 1);
@@ -411,7 +418,10 @@ __global__ void __launch_bounds__(kPtThreads, 1)
               tc_fence_after();
 #pragma unroll
               for (int kk = h * 4; kk < h * 4 + 4; ++kk)
-                tc_mma_bf16_ts(po, pp + kk * 8, vb + kk * (2048 >> 4), idesc_pv, kk > 0 ? 1u : (((fresh >> y) & 1) ^ 1));
+#pragma unroll
+                for (int part = 0; part < 2; ++part)  // cut off, the rest
+                  tc_mma_bf16_ts(po, pp + (h + part) * 32 + kk * 8, vb + kk * (2048 >> 4), idesc_pv,
+                                 kk + part > 0 ? 1u : (((fresh >> y) & 1) ^ 1));
             }
             if (!ok) break;
             fresh &= ~(1u << y);
@@ -435,10 +445,11 @@ __global__ void __launch_bounds__(kPtThreads, 1)
     const uint32_t t_lane = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const float sc = a.scale_log2;
     bool ok = true;
-    int cnt = 0, other = 0, key_tiles = 0;  // turns of this stream, of the other one, key tiles, over all segments
+    int cnt = 0, other = 0, turns = 0, key_tiles = 0;  // turns of this stream, of the other one, of both, key tiles, over all segments
     auto all_wait = [&](uint64_t* bar, uint32_t parity) -> bool { return __all_sync(0xffffffffu, wait(bar, parity)); };
     // P V of the turn before the cnt-th has completed
     auto last_pv_done = [&](int cnt) -> bool { return cnt < 2 || all_wait(&pv_done[4 * x + ((cnt - 2) & 3)], ((cnt - 2) >> 2) & 1); };
+    // behind the last turn's P V: a warp ahead of another one would arrive twice in a phase
     auto hand_over = [&](int half) {
       if (lane == 0) mbar_arrive(&p_full[2 * x + half]);
     };
@@ -476,8 +487,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
         const int bar = 4 * x + (cnt & 3), parity = (cnt >> 2) & 1;
         ++cnt;
         if (ok && !all_wait(&s_full[bar], parity)) ok = false;
-        if (!live || !ok) {  // keep the counts only, and no earlier than the others could
-          if (lane == 0) mbar_arrive(&s_free[Cfg::kBufs == 1 ? 0 : x]);
+        if (!live || !ok) {  // keep the counts only
           if (ok && !last_pv_done(cnt)) ok = false;
           hand_over(0);
           hand_over(1);
@@ -485,10 +495,8 @@ __global__ void __launch_bounds__(kPtThreads, 1)
         }
         uint32_t sv[128];
         tc_fence_after();
-        tmem_ld128(t_lane + (Cfg::kBufs == 1 ? 0 : x * 128), sv);
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&s_free[Cfg::kBufs == 1 ? 0 : x]);
+        const uint32_t t_sp = t_lane + (turns + (pair ? 2 * j + x : j)) % Cfg::kBufs * 128;
+        tmem_ld128(t_sp, sv);
         const volatile uint32_t* mask = masks + ((key_tiles + j) & 7) * 4;
         const uint32_t m0 = mask[0], m1 = mask[1], m2 = mask[2], m3 = mask[3];
         if ((m0 & m1 & m2 & m3) != 0xffffffffu) {
@@ -531,36 +539,39 @@ __global__ void __launch_bounds__(kPtThreads, 1)
         }
         const float nm = m_used == -INFINITY ? 0.f : -m_used;
         const uint64_t sc2 = f32x2(__float_as_uint(sc), __float_as_uint(sc)), nm2 = f32x2(__float_as_uint(nm), __float_as_uint(nm));
-        uint32_t pk[64];
+        const uint64_t minus = f32x2(__float_as_uint(-1.f), __float_as_uint(-1.f));
+        uint64_t rs[2] = {0, 0};  // of the weights as they are
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
+          uint32_t pk[32];  // cut off, the rest
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
-            float p0, p1;
+            float p0, p1, r0, r1;
             f32x2_parts(fma2(f32x2(sv[k * 32 + 2 * e], sv[k * 32 + 2 * e + 1]), sc2, nm2), p0, p1);
-            pk[k * 16 + e] = pack_bf16x2(ex2_approx(p0), ex2_approx(p1));
+            const uint32_t u0 = __float_as_uint(ex2_approx(p0)), u1 = __float_as_uint(ex2_approx(p1));
+            const uint64_t w2 = f32x2(u0, u1);
+            rs[e & 1] = add2(rs[e & 1], w2);
+            pk[e] = __byte_perm(u0, u1, 0x7632);
+            f32x2_parts(fma2(f32x2(u0 & 0xffff0000u, u1 & 0xffff0000u), minus, w2), r0, r1);
+            pk[16 + e] = pack_bf16x2(r0, r1);
           }
-          if (k == 0) {  // P is free once the last P V has completed
-            if (!last_pv_done(cnt)) ok = false;
-            tc_fence_after();
-          }
-          tmem_st16_nowait(t_lane + Cfg::kColP + x * 64 + k * 16, pk + k * 16);
+          const uint32_t at = t_sp + (k >> 1) * 64 + (k & 1) * 16;
+          tmem_st16_nowait(at, pk);
+          tmem_st16_nowait(at + 32, pk + 16);
           if (k & 1) {
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
+            if (k == 1 && !last_pv_done(cnt)) ok = false;
             hand_over(k >> 1);
           }
         }
-        // the sum of what the tensor cores multiply, while they do
-        uint64_t rs[2] = {0, 0};
-#pragma unroll
-        for (int e = 0; e < 64; ++e) rs[e & 1] = add2(rs[e & 1], f32x2(pk[e] << 16, pk[e] & 0xffff0000u));
         float s0, s1;
         f32x2_parts(add2(rs[0], rs[1]), s0, s1);
         l += s0 + s1;
       }
       key_tiles += tiles;
+      turns += pair ? 2 * tiles : tiles;
       // (m, l) and O of the segment; before the hand-over of the next one's first P, which lets its P V write O
       const int64_t row = (int64_t)kp_row(w.gr, w.kvh(), w.row0()) + 256 * blockIdx.x + (x ? (pair ? 128 : w.rows()) : 0) + r;
       if (cnt > cnt_before && ok && !last_pv_done(cnt + 1)) ok = false;

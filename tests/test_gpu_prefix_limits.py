@@ -1,0 +1,69 @@
+"""What attention over shared prefixes keeps of a weight, in every form that a call can take."""
+import numpy as np
+import pytest
+import torch
+
+from tests import attention64 as A
+from tests import test_gpu_prefix_attention as PA
+
+pytestmark = pytest.mark.gpu
+dev = torch.device("cuda:0")
+BF = torch.bfloat16
+KEPT = 2.0 ** -16  # of a bf16 weight, held as two bf16 (tests/attention64.py)
+
+
+@pytest.fixture(scope="module")
+def D():
+    from block_denoising_gb300 import build, dinfer
+    build.build()
+    return dinfer
+
+
+@pytest.fixture(scope="module")
+def ws(D):
+    return D.OpWorkspace()
+
+
+def rounded(x):
+    return torch.from_numpy(np.asarray(x, np.float32)).to(BF).double().numpy()
+
+
+def put(x):
+    return torch.from_numpy(np.asarray(x, np.float32)).to(BF).to(dev)
+
+
+# one piece of 16 rows; one tile of rows on every other key tile; two tiles; more than a unit
+@pytest.mark.parametrize("members,group", [(2, 8), (5, 8), (16, 8), (19, 8), (40, 8), (3, 19)])
+@pytest.mark.parametrize("hd,page", [(64, 16), (128, 16), (128, 24), (64, 128)])
+def test_prefix_weights_in_two_bf16(D, ws, hd, page, members, group):
+    # sums that nearly cancel: a weight that lost more shows (one bf16 alone is beyond this bound, tests/test_attention64.py)
+    for n in (140, 430, 2200):
+        rng = np.random.default_rng(hd + page + n)
+        c, seqs, bounds = PA.make(D, rng, [n - 7], [[7] * members], page, 1, hd)
+        q, k, v = A.cancelling(rng, n, hd, group, rounded)
+        for s in seqs:
+            j = torch.arange(n, device=dev)
+            at = c.table[s, j // page].long(), j % page
+            c.k[0][at[0], at[1], 0], c.v[0][at[0], at[1], 0] = put(k), put(v)
+        x = put(np.broadcast_to(q, (members, group, hd)).copy())
+        o = c.prefix_attention(0, x, ws, PA.ints([n - 7]), PA.ints(bounds), seqs=PA.ints(seqs), scale=1.0)
+        some = [0, members // 2, members - 1]
+        for i in some:
+            A.check(o[i:i + 1].double().cpu().numpy(), q[None], k[:, None], v[:, None], np.ones((1, n), bool), 1.0, True, (n, i), KEPT)
+        c.check()
+        ws.check()
+
+
+@pytest.mark.parametrize("case", [i for i, x in enumerate(PA.CASES) if x[6] is BF])
+def test_plain_sums_within_what_is_kept(D, ws, case):
+    shared, own, heads, kv_heads, hd, page, dtype, order = PA.CASES[case]
+    rng = np.random.default_rng(case + 500)
+    c, seqs, bounds = PA.make(D, rng, shared, own, page, kv_heads, hd, dtype, order)
+    q = PA.values(rng, (len(seqs), heads, hd), dtype)
+    o = c.prefix_attention(0, q, ws, PA.ints(shared), PA.ints(bounds), seqs=PA.ints(seqs))
+    qh, oh = q.double().cpu().numpy(), o.double().cpu().numpy()
+    for i in range(0, len(seqs), 1 + len(seqs) // 12):
+        if int(c.lens[seqs[i]]) == 0:
+            continue
+        k, v = PA.rows_of(c, seqs[i])
+        A.check(oh[i:i + 1], qh[i:i + 1], k, v, np.ones((1, len(k)), bool), hd ** -0.5, True, i, KEPT)
