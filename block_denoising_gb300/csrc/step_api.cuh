@@ -63,7 +63,9 @@ cudaError_t launch_rope(RopeArgs& a, const RopeTurns& t, bool pairs, cudaStream_
 
 // Bytes of the workspace in front of the sums of dinfer_kv_prefix_attention: its plan.
 constexpr size_t kPrefixHead = 64 * 1024;
-static_assert(sizeof(int4) + sizeof(KpEntry) * (kKvMaxEntries + 1) <= kPrefixHead, "plan");
+static_assert(sizeof(int4) + sizeof(KpEntry) * (kKvMaxEntries + 1) <= kPrefixHead - 16, "plan");
+// Where the sums begin: the prefix kernel stores theirs 32 bytes at a time, and the workspace may begin at 16.
+float* prefix_sums(uint8_t* data) { return reinterpret_cast<float*>(reinterpret_cast<uintptr_t>(data + kPrefixHead) & ~uintptr_t(31)); }
 
 // One layer of a bf16 cache as [pages][heads][slots][hd]: boxes of a page's slots, at most 128, x 64 elements with the
 // 128-byte swizzle; pages behind the last read as zeros.
@@ -300,7 +302,7 @@ dinfer_status dinfer_kv_prefix_attention(const dinfer_kv_cache* kc, int32_t laye
   p.group_div = FastDiv::make((uint32_t)a.group);
   p.head = reinterpret_cast<int4*>(w.data);
   p.plan = reinterpret_cast<KpEntry*>(p.head + 1);
-  p.own_o = reinterpret_cast<float*>(w.data + kPrefixHead);
+  p.own_o = prefix_sums(w.data);
   p.seg_o = p.own_o + own_rows * kc->head_dim;
   p.own_ml = reinterpret_cast<float2*>(p.seg_o + seg_rows * kc->head_dim);
   p.seg_ml = p.own_ml + own_rows;

@@ -1,4 +1,5 @@
-"""What attention over shared prefixes keeps of a weight, in every form that a call can take."""
+"""Attention over shared prefixes at its limits: what it keeps of a weight, in every form that a call can take, and the
+workspaces that it takes."""
 import numpy as np
 import pytest
 import torch
@@ -67,3 +68,22 @@ def test_plain_sums_within_what_is_kept(D, ws, case):
             continue
         k, v = PA.rows_of(c, seqs[i])
         A.check(oh[i:i + 1], qh[i:i + 1], k, v, np.ones((1, len(k)), bool), hd ** -0.5, True, i, KEPT)
+
+
+@pytest.mark.parametrize("hd,members", [(128, 40), (64, 40), (128, 5)])
+def test_a_workspace_that_begins_at_16_bytes(D, ws, hd, members):
+    rng = np.random.default_rng(hd + members)
+    c, seqs, bounds = PA.make(D, rng, [1000], [[3] * members], 16, 2, hd)
+    q = PA.values(rng, (members, 16, hd), BF)
+    args = (PA.ints([1000]), PA.ints(bounds))
+    want = c.prefix_attention(0, q, ws, *args, seqs=PA.ints(seqs))
+    whole = torch.zeros(ws.nbytes + 32 + 64, dtype=torch.uint8, device=dev)
+    off = -whole.data_ptr() % 32 + 16
+    odd = D.OpWorkspace()
+    odd.buf = whole[off:off + ws.nbytes]
+    assert odd.buf.data_ptr() % 32 == 16
+    whole[off + ws.nbytes:] = 77
+    assert torch.equal(c.prefix_attention(0, q, odd, *args, seqs=PA.ints(seqs)), want)
+    assert bool((whole[off + ws.nbytes:] == 77).all())
+    c.check()
+    odd.check()
