@@ -56,8 +56,10 @@ class Rope(ctypes.Structure):
                 raise ValueError(f"{name}: one of {', '.join(kinds)} expected, got {what!r}")
         super().__init__(_i32(rot_dim), self.LAYOUTS[layout], self.SCALINGS[scaling], _i32(trained), theta, factor, slow,
                          fast, magnitude)
-        self._as_parameter_ = ctypes.addressof(self)
-        _check(lib().dinfer_rope_init(self._as_parameter_))
+        _check(lib().dinfer_rope_init(self))
+
+    # of the object at hand: an attribute would go along into its copies and pickles
+    _as_parameter_ = property(ctypes.addressof)
 
 
 class KvCache(ctypes.Structure):
