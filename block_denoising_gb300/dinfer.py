@@ -54,7 +54,7 @@ class Rope(ctypes.Structure):
         for name, kinds, what in (("layout", self.LAYOUTS, layout), ("scaling", self.SCALINGS, scaling)):
             if what not in kinds:
                 raise ValueError(f"{name}: one of {', '.join(kinds)} expected, got {what!r}")
-        super().__init__(_i32(rot_dim), self.LAYOUTS[layout], self.SCALINGS[scaling], _i32(trained), theta, factor, slow,
+        super().__init__(_i32(rot_dim), self.LAYOUTS[layout], self.SCALINGS[scaling], _exact_i32(trained, "trained"), theta, factor, slow,
                          fast, magnitude)
         _check(lib().dinfer_rope_init(self))
 
@@ -358,6 +358,12 @@ def _i32(x: int) -> int:
     return x if -0x80000000 <= x <= 0x7fffffff else 0x7fffffff if x > 0 else -0x80000000
 
 
+def _exact_i32(x: int, name: str) -> int:
+    """x where int32 holds it: a position has no end of the range that means the same."""
+    _require(-0x80000000 <= x <= 0x7fffffff, f"{name}: an int32 expected, got {x}")
+    return x
+
+
 def _run_on(gpu: int, fn, *args):
     """One library call on torch's current stream of the operands' GPU, which becomes the current one for it."""
     if gpu == torch._C._cuda_getDevice():
@@ -553,7 +559,7 @@ def op_window_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, ws: O
 def op_rope(x: torch.Tensor, rope: Rope, positions: Optional[torch.Tensor] = None, first: int = 0,
             out: Optional[torch.Tensor] = None):
     """x [rows, heads, head_dim] rotated at positions [rows] (default: first, first + 1, ...); out may be x."""
-    dtype, gpu = x.dtype, x.get_device()
+    dtype, gpu, first = x.dtype, x.get_device(), _exact_i32(first, "first")
     _require(dtype in _DTYPES and x.is_cuda and x.dim() == 3, "x: float32 or bfloat16 [rows, heads, head_dim] on a GPU expected")
     hd = x.shape[2]
     rows, heads, xs = _rows_of(x, "x", None, hd, dtype, gpu)
@@ -563,7 +569,7 @@ def op_rope(x: torch.Tensor, rope: Rope, positions: Optional[torch.Tensor] = Non
         also, _, os_ = _rows_of(out, "out", heads, hd, dtype, gpu)
         _require(also == rows, "out: as many rows as x expected")
     _run_on(gpu, lib().dinfer_op_rope, x.data_ptr(), out.data_ptr(), _DTYPES[dtype], rope, _ints(positions, "positions", gpu, rows),
-            _i32(first), rows, heads, hd, xs, os_)
+            first, rows, heads, hd, xs, os_)
     return out
 
 

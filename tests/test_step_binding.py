@@ -5,6 +5,7 @@ import gc
 import pickle
 
 import pytest
+import torch
 
 from block_denoising_gb300 import build as B
 from block_denoising_gb300 import dinfer
@@ -45,3 +46,19 @@ def test_a_copied_rotation_is_its_own(L, how):
     assert "rows" in reason(L, twin) and list(twin.turns) == turns and len(others) == 64
     assert [getattr(twin, n) for n in ("rot_dim", "layout", "scaling", "theta", "factor")] == [128, 1, 1, 10000.0, 2.0]
     assert twin._as_parameter_ == ctypes.addressof(twin)
+
+
+@pytest.mark.parametrize("first", [1 << 31, 1 << 40, -(1 << 31) - 1, -(1 << 63), 1 << 32])
+def test_positions_beyond_int32_are_refused(first):
+    # not the end of the range in their place: a position there is another one
+    with pytest.raises(ValueError, match="first"):
+        dinfer.op_rope(torch.zeros(1, 2, 64), dinfer.Rope(64), first=first)
+    with pytest.raises(ValueError, match="trained"):
+        dinfer.Rope(64, scaling="bands", factor=2.0, trained=first)
+
+
+def test_positions_at_the_ends_of_int32_are_not():
+    for first in ((1 << 31) - 1, -(1 << 31)):
+        with pytest.raises(ValueError, match="GPU"):  # what is refused next
+            dinfer.op_rope(torch.zeros(1, 2, 64), dinfer.Rope(64), first=first)
+    assert dinfer.Rope(64, scaling="bands", factor=2.0, trained=(1 << 31) - 1).trained == (1 << 31) - 1
