@@ -91,18 +91,16 @@ struct SmCut {
 };
 
 struct SmScale {
-  float m, mh, ml, ch, cl;
+  float m, ch, cl;
   float least;  // logits below it weigh less than 2^-60
 };
-// A logit as a multiple of 2^-10 and the rest: differences of the first parts are exact.
-__device__ __forceinline__ float sm_high(float x) { return (x + 12288.f) - 12288.f; }
 
 // Out of line: the kernel's uses of it are many, and its code is large.  For time it is all but the same (one flat row of
 // 126464 with top-p: 37 us, 39 with a copy at every use).
 __device__ __noinline__ uint64_t sm_weight(float l, const SmScale k, const uint32_t* table) {
-  const float lh = sm_high(l), dh = lh - k.mh, dl = (l - lh) - k.ml;
-  const float p = __fmul_rn(dh, k.ch);  // not to be contracted with the sums below, which take its rounding off again
-  float s = fmaf(dl, k.ch, fmaf(dh, k.cl, fmaf(dh, k.ch, -p)));
+  const float d = l - k.m, back = d - l, dl = (l - (d - back)) - (k.m + back);  // the difference, and what it is rounded by
+  const float p = __fmul_rn(d, k.ch);  // not to be contracted with the sums below, which take its rounding off again
+  float s = fmaf(dl, k.ch, fmaf(d, k.cl, fmaf(d, k.ch, -p)));
   constexpr float kMagic = 24576.f;  // 1.5 * 2^14: a float's last place is 1 / 512
   const float t = fmaf(dl, k.ch, p) + kMagic;
   s += p - (t - kMagic);
@@ -126,10 +124,11 @@ struct SmPair {
     l0 = fmaxf(l0, k.least);
     l1 = fmaxf(l1, k.least);
     const uint64_t l = f32x2(__float_as_uint(l0), __float_as_uint(l1));
-    const uint64_t lh = add2(add2(l, both(12288.f)), both(-12288.f)), dh = add2(lh, both(-k.mh)), dl = add2(fma2(lh, one, l), both(-k.ml));
-    const uint64_t p = mul2(dh, both(k.ch)), ch = both(k.ch);
+    const uint64_t d = add2(l, both(-k.m)), back = fma2(l, one, d);
+    const uint64_t dl = fma2(add2(back, both(k.m)), one, fma2(fma2(back, one, d), one, l));
+    const uint64_t p = mul2(d, both(k.ch)), ch = both(k.ch);
     const uint64_t t = add2(fma2(dl, ch, p), both(kMagic));
-    uint64_t s = fma2(dl, ch, fma2(dh, both(k.cl), fma2(dh, ch, mul2(dh, both(-k.ch)))));
+    uint64_t s = fma2(dl, ch, fma2(d, both(k.cl), fma2(d, ch, mul2(d, both(-k.ch)))));
     s = add2(s, fma2(add2(t, both(-kMagic)), one, p));
     const uint64_t q = mul2(s, fma2(s, fma2(s, fma2(s, both(0.00961812910763f), both(0.0555041086648f)), both(0.240226506959f)), both(0.693147180560f)));
     float t0, t1;
@@ -364,8 +363,6 @@ __global__ void __launch_bounds__(kSmThreads, kBlocks) sample_kernel(const __gri
   SmScale scale;
   {
     scale.m = top;
-    scale.mh = sm_high(top);
-    scale.ml = top - scale.mh;
     // log2(e) / temperature in two floats
     constexpr float kLog2e = 1.44269502162933349609f, kLog2eRest = 1.92596299112661746887e-8f;
     scale.ch = fminf(__fdiv_rn(kLog2e, temperature), 0x1p100f);
