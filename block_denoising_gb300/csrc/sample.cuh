@@ -131,11 +131,13 @@ struct SmPair {
     uint64_t s = fma2(dl, ch, fma2(d, both(k.cl), fma2(d, ch, mul2(d, both(-k.ch)))));
     s = add2(s, fma2(add2(t, both(-kMagic)), one, p));
     const uint64_t q = mul2(s, fma2(s, fma2(s, fma2(s, both(0.00961812910763f), both(0.0555041086648f)), both(0.240226506959f)), both(0.693147180560f)));
-    float t0, t1;
+    float t0, t1, p0, p1;
     f32x2_parts(t, t0, t1);
+    f32x2_parts(p, p0, p1);
     const int n0 = __float_as_int(t0) - __float_as_int(kMagic), n1 = __float_as_int(t1) - __float_as_int(kMagic);
     const float2 w0 = powers[n0 & 31][threadIdx.x & 31], w1 = powers[n1 & 31][threadIdx.x & 31];
-    x = f32x2(__float_as_uint(w0.x) + ((n0 >> 5) << 23), __float_as_uint(w1.x) + ((n1 >> 5) << 23));
+    // 0 where sm_weight gives 0: what counts in these sums counts in those of whole numbers
+    x = f32x2(p0 >= -44.f ? __float_as_uint(w0.x) + ((n0 >> 5) << 23) : 0u, p1 >= -44.f ? __float_as_uint(w1.x) + ((n1 >> 5) << 23) : 0u);
     rest = add2(q, f32x2(__float_as_uint(w0.y), __float_as_uint(w1.y)));
   }
   __device__ __forceinline__ void keep(bool first, bool second) {
@@ -911,32 +913,26 @@ __global__ void __launch_bounds__(kSmThreads, kBlocks) sample_kernel(const __gri
     return i >= t1 ? -INFINITY : list >= 0 ? sc.list[i] : fmaxf((float)x[i], -INFINITY);
   };
   sum = 0;
-  bool filled = false;
   for (int i0 = t0; i0 < t1; i0 += 32) {
     int token;
     const float l = read(i0 + lane, token);
     sum += l > -INFINITY ? kept(token, l) : 0;
-    filled |= l > -INFINITY;
   }
   sum = sm_reduce(sum, [](uint64_t p, uint64_t q) { return p + q; });
-  filled = __any_sync(0xffffffffu, filled);
   __syncthreads();  // the warps' sums are read
-  if (lane == 0) {
-    sh.warp_sum[warp] = sum;
-    sh.warp_i[warp] = filled;
-  }
+  if (lane == 0) sh.warp_sum[warp] = sum;
   __syncthreads();
-  int last_part = -1;  // the last one that holds any weight, or any logit
+  // The last part that holds any weight.  There is one: the stretch's sum is above 0, in floats too only where a token counts,
+  // and one that counts weighs 1 at least in whole numbers.
+  int last_part = -1;
   for (int w = 0; w < kSmWarps; ++w)
     if (sh.warp_sum[w]) last_part = w;
-  for (int w = 0; w < kSmWarps && last_part < 0; ++w)
-    if (sh.warp_i[w]) last_part = w;
   for (int w = 0; w < warp; ++w) before += sh.warp_sum[w];
   const bool here = before <= target && target < before + sh.warp_sum[warp];
   if (!here && !(warp == last_part && target >= before + sh.warp_sum[warp])) return;
   // Where the stretch's sum in floats is a few units above that in whole numbers: its last token that counts.
-  int last = -1, any = -1;
-  float last_l = 0.f, any_l = 0.f;
+  int last = -1;
+  float last_l = 0.f;
   for (int i0 = t0; i0 < t1; i0 += 32) {
     int token;
     const float l = read(i0 + lane, token);
@@ -948,7 +944,6 @@ __global__ void __launch_bounds__(kSmThreads, kBlocks) sample_kernel(const __gri
       if (lane >= o) inc += y;
     }
     const uint32_t over = __ballot_sync(0xffffffffu, before + inc > target), some = __ballot_sync(0xffffffffu, w > 0);
-    const uint32_t there = __ballot_sync(0xffffffffu, l > -INFINITY);
     if (over) {
       if (lane == __ffs(over) - 1) put(token, l);
       return;
@@ -957,13 +952,9 @@ __global__ void __launch_bounds__(kSmThreads, kBlocks) sample_kernel(const __gri
       last = __shfl_sync(0xffffffffu, token, 31 - __clz(some));
       last_l = __shfl_sync(0xffffffffu, l, 31 - __clz(some));
     }
-    if (there) {
-      any = __shfl_sync(0xffffffffu, token, 31 - __clz(there));
-      any_l = __shfl_sync(0xffffffffu, l, 31 - __clz(there));
-    }
     before += __shfl_sync(0xffffffffu, inc, 31);
   }
-  if (lane == 0 && any >= 0) put(last >= 0 ? last : any, last >= 0 ? last_l : any_l);
+  if (lane == 0) put(last, last_l);
 }
 
 }  // namespace dinfer

@@ -1,4 +1,8 @@
-"""Sampling at the borders of its definition."""
+"""Sampling at the borders of its definition: small temperatures, weights that count as 0 between equal ones.
+
+tests/sample64.py leaves a row out where a sum lies near a border and the weights are not all equal; the rows with weights
+that count as 0 are made so that what is left is certain, and every one of them is compared.
+"""
 import numpy as np
 import pytest
 import torch
@@ -33,3 +37,42 @@ def test_small_temperatures(D, top, temperature):
             u = [float(np.float32(v)) for v in rng.random(rows) * 0.9999]
             for s in ({}, dict(top_p=[0.8] * rows), dict(top_k=[20] * rows, top_p=[0.9] * rows), dict(min_p=[0.01] * rows)):
                 T.check(D, x, u, temperature=[temperature] * rows, unsure=2, **s)
+
+
+def tied(rows, vocab, dtype, tail, tops):
+    """Logits 0 at tops, tail elsewhere."""
+    x = torch.full((rows, vocab), tail, dtype=F32)
+    x[:, tops] = 0.0
+    return x.to(dtype).to(dev)
+
+
+def draw(D, x, u, **settings):
+    """Tokens of every row for every number of u, settings the same for all rows."""
+    n = x.shape[0]
+    full = {k: torch.full((n,), v, dtype=torch.int32 if k == "top_k" else F32, device=dev) for k, v in settings.items()}
+    return [sorted(set(D.op_sample(x, torch.full((n,), v, dtype=F32, device=dev), **full)[0].tolist())) for v in u]
+
+
+# e^(tail / T): 2^-44.7 and 2^-45.7, and far less: below 2^-44 each, which counts as 0
+@pytest.mark.parametrize("dtype,tail,temperature", [(F32, -31.0, 1.0), (BF, -9.5, 0.3), (F32, -38.0, 1.0), (BF, -1000.0, 1.0), (F32, -0.031, 0.001)])
+@pytest.mark.parametrize("rows,vocab", [(1, 64), (3, 5000), (1, 126464), (64, 40000), (400, 9001)])
+def test_weights_that_count_as_zero(D, rows, vocab, dtype, tail, temperature):
+    last = vocab - 1
+    two = tied(rows, vocab, dtype, tail, [0, last])
+    below = 1.0 - 2.0 ** -24
+    t = dict(temperature=temperature)
+    # two equal weights: the first sum above half of them is the second one's
+    assert draw(D, two, [0.0, 0.5 - 2.0 ** -25, 0.5, 0.75, below, 1.0], **t) == [[0], [0], [last], [last], [last], [last]]
+    # half of their weight is the first one's; more is both's
+    assert draw(D, two, [0.0, 0.5, below, 1.0], top_p=0.5, **t) == [[0]] * 4
+    assert draw(D, two, [0.25, 0.5, below], top_p=0.5 + 2.0 ** -24, **t) == [[0], [last], [last]]
+    assert draw(D, two, [0.25, 0.5, below, 1.0], min_p=2.0 ** -43, **t) == [[0], [last], [last], [last]]
+    # of the first `vocab - 1` of the order all that weighs is the two
+    assert draw(D, two, [0.25, 0.5, below, 1.0], top_k=last, **t) == [[0], [last], [last], [last]]
+    assert draw(D, two, [0.25, below, 1.0], top_k=last, top_p=0.5, **t) == [[0]] * 3
+    one = tied(rows, vocab, dtype, tail, [0])
+    assert draw(D, one, [0.0, 0.5, below, 1.0], **t) == [[0]] * 4
+    assert draw(D, one, [0.0, 0.5, below, 1.0], top_p=below, **t) == [[0]] * 4
+    four = tied(rows, vocab, dtype, tail, [1, 2, vocab // 2, last - 1])
+    assert draw(D, four, [0.0, 0.25, 0.5, 0.75, 1.0], **t) == [[1], [2], [vocab // 2], [last - 1], [last - 1]]
+    assert draw(D, four, [0.0, 0.34, 0.67, 1.0], top_p=0.75, **t) == [[1], [2], [vocab // 2], [vocab // 2]]
