@@ -5,15 +5,17 @@
 // each, and everything after the load is passes over those slices, joined
 // through distributed shared memory.
 //
-// Weights are whole numbers, w = round(2^44 e^((l - max) / T)), so that sums are the
-// same in any order and comparisons with u and top_p are exact.  Which token is
+// Weights are whole numbers, w = round(2^44 e^((l - max) / T)), whose sums are the
+// same in any order.  Which token is
 // drawn hangs on where u falls among up to 157000 sums of rounded weights: with
 // fp32 exponentials one row in some ten thousand gets another token than the
 // definition's, so the exponent is carried in two floats and the power of two
 // comes from a table of 512 and a cubic, about 2^-32 of the weight in all.  Passes
 // over whole slices sum the same powers as pairs of floats, two tokens an instruction
 // (some 25 instructions a token where whole numbers take 50), from a table of 32 in
-// every lane's own banks and a quartic, to 2^-31 of a weight and 2^-38 of the largest.
+// every lane's own banks and a quartic, to 2^-31 of a weight and 2^-38 of the largest; a
+// thread's part of them is then rounded to a whole number, so that these sums do hang on how a
+// row is dealt to threads, in their last 2^-31.
 //
 // top-k and top-p cut the order (larger logit first, then lower index) at one
 // place.  A floor under it is found first: for top-k the k-th largest of the

@@ -168,7 +168,10 @@ dinfer_status dinfer_op_rope(const void* x, void* y, int32_t dtype, const dinfer
  * there; where one is +inf, only those that are count.  conf (NULL: not wanted) is
  * the token's softmax probability at temperature 1, nothing left out: the decoder's
  * confidence.  A row without a logit gives tok -1, conf 0.  Sums of weights are
- * exact: the same call gives the same tokens.
+ * off by some 2^-31 of themselves (none where the weights are the largest's or 0), in a
+ * way that hangs on the number of rows and the device: the same call gives the same
+ * tokens, and a row alone those that it gets among others but where u or top_p
+ * lies that near to a border.
  * 1 <= rows <= 2^20, 1 <= vocab <= 2^19, stride >= vocab (rows > 1). */
 dinfer_status dinfer_op_sample(const void* logits, int32_t dtype, int32_t rows, int32_t vocab, int64_t stride,
                                const float* temperature, const int32_t* top_k, const float* top_p, const float* min_p,

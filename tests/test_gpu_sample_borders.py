@@ -76,3 +76,23 @@ def test_weights_that_count_as_zero(D, rows, vocab, dtype, tail, temperature):
     four = tied(rows, vocab, dtype, tail, [1, 2, vocab // 2, last - 1])
     assert draw(D, four, [0.0, 0.25, 0.5, 0.75, 1.0], **t) == [[1], [2], [vocab // 2], [last - 1], [last - 1]]
     assert draw(D, four, [0.0, 0.34, 0.67, 1.0], top_p=0.75, **t) == [[1], [2], [vocab // 2], [vocab // 2]]
+
+
+@pytest.mark.parametrize("vocab,dtype", [(3001, F32), (40000, BF), (126464, F32)])
+def test_a_row_alone_and_in_batches(D, vocab, dtype):
+    """A row's token does not hang on how many rows there are, and so on how many CTAs and threads share it: no sum lies
+    within 2^-31 of its border here."""
+    rng = np.random.default_rng(vocab)
+    n = 320
+    x = T.logits(rng, n, vocab, dtype)
+    u = torch.from_numpy(rng.random(n).astype(np.float32)).to(dev).clamp(max=0.9999)
+    pick = lambda v, t=F32: torch.tensor(v, dtype=t, device=dev)[torch.from_numpy(rng.integers(0, len(v), n)).to(dev)]  # noqa: E731
+    s = dict(temperature=pick([0.0, 0.3, 1.0, 1.7]), top_k=pick([0, 0, 40, 2000], torch.int32), top_p=pick([1.0, 0.5, 0.9, 0.99]),
+             min_p=pick([0.0, 0.0, 0.02]))
+    for used in ({}, {"temperature": s["temperature"]}, {"top_p": s["top_p"]}, s):
+        tok, conf = D.op_sample(x, u, **used)
+        for size in (1, 3, 64, 160):
+            for a in range(0, n, size) if size > 3 else (0, 100, n - size):
+                got = D.op_sample(x[a:a + size], u[a:a + size], **{k: v[a:a + size] for k, v in used.items()})
+                assert torch.equal(got[0], tok[a:a + size]), (size, a, list(used))
+                assert torch.allclose(got[1], conf[a:a + size], rtol=2.0 ** -16, atol=0)  # each within 2^-17 of the definition
