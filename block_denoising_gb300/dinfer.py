@@ -445,7 +445,8 @@ class PagedKV:
                     rows: Optional[torch.Tensor] = None, seqs: Optional[torch.Tensor] = None,
                     positions: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None):
         """append with the keys, and the rows' queries q [rows, heads, head_dim], rotated at their tokens' places (or at
-        positions [rows]); returns the rotated queries (out may be q)."""
+        positions [rows]); returns the rotated queries (out may be q).  Rows that are not stored (behind the last entry's, or
+        of an entry that check() tells of) stay in out as they were; without out they hold whatever its memory held."""
         gpu, hd, dtype = self.gpu, self.head_dim, self.dtype
         total, _, ks = _rows_of(k, "k", self.kv_heads, hd, dtype, gpu)
         also, _, vs = _rows_of(v, "v", self.kv_heads, hd, dtype, gpu)
