@@ -96,3 +96,16 @@ def test_a_row_alone_and_in_batches(D, vocab, dtype):
                 got = D.op_sample(x[a:a + size], u[a:a + size], **{k: v[a:a + size] for k, v in used.items()})
                 assert torch.equal(got[0], tok[a:a + size]), (size, a, list(used))
                 assert torch.allclose(got[1], conf[a:a + size], rtol=2.0 ** -16, atol=0)  # each within 2^-17 of the definition
+
+
+def test_rows_at_the_ends_every_one_compared(D):
+    """Infinities, NaN and extreme temperatures, with numbers of which none lies near a border: no row is left out."""
+    inf, nan = np.inf, np.nan
+    rows = [[-inf] * 5, [nan] * 5, [nan, 1.0, -inf, 1.0, 0.0], [inf, 0.0, inf, nan, -inf], [3e38, -3e38, 3e38, 0.0, -inf], [1e-40, 0.0, -1e-40, -0.0, 2e-40],
+            [-1e4, -1e4 - 1, -1e4 - 2, -inf, -1e4], [5000.5, 5000.25, 5000.0, 4999.0, 0.0], [0.0, -31.0, -30.4, -30.6, -29.0]]
+    x = torch.tensor(rows, device=dev)
+    n = len(rows)
+    for u in (0.0, 0.27, 0.31, 0.62, 0.77, 0.9):
+        for s in ({}, dict(temperature=1e-30), dict(temperature=0.0), dict(temperature=-1.0), dict(temperature=1e30), dict(top_k=2), dict(top_p=0.71),
+                  dict(min_p=0.53), dict(top_k=3, top_p=0.91, min_p=0.13), dict(top_k=-1, top_p=1.5, min_p=-2.0)):
+            T.check(D, x, [float(np.float32(u))] * n, unsure=0, **{k: [v] * n for k, v in s.items()})
