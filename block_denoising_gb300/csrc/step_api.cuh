@@ -355,11 +355,13 @@ dinfer_status dinfer_op_sample(const void* logits, int32_t dtype, int32_t rows, 
   a.cuts = top_k || top_p;
   for (int j = 0; j < 16; ++j) a.coarse[j] = (uint64_t)std::ldexp(std::exp2(j / 16.0), 63);
   for (int j = 0; j < 32; ++j) a.fine[j] = (uint64_t)std::ldexp(std::exp2(j / 512.0), 63);
-  // As few CTAs a row as two an SM can hold it with, which saves their meetings (512 rows of 126464 in bf16: 4 CTAs 278
-  // us, 8 328, 16 550; 64 rows of 157184 in fp32: 8 CTAs 49 us, 16 52); more while there are SMs to spare and 2048 tokens
-  // for each (one row of 126464: 16 CTAs 19.0 us, 8 20.6, 4 27.0).
+  // As few CTAs a row as two or three an SM can hold it with, which saves their meetings (512 rows of 126464 in bf16 at a
+  // temperature: 4 CTAs 149 us, 2 174, 8 202).  With a cut, whose meetings are more, no more than four where they hold it, one
+  // an SM (300 rows of 157184 in fp32 with top-k 20, with top-p 0.9: 4 CTAs 159 and 642 us, 8 253 and 1002, 16 315 and 1170),
+  // and no fewer, whose threads' maxima give too low a floor (512 rows of 126464 in bf16 with top-k 1000: 4 CTAs 203 us, 2 366).
+  // More while there are SMs to spare and 2048 tokens for each (one row of 126464 at a temperature: 16 CTAs 9.2 us, 8 11.2, 4 15.5).
   int ctas = 1;
-  while (ctas < kSmCluster && ((int64_t)vocab * size > (int64_t)ctas * (a.cuts ? 64 : 80) * 1024 ||
+  while (ctas < kSmCluster && ((int64_t)vocab * size > (int64_t)ctas * (!a.cuts ? 80 : ctas < 4 ? 64 : 160) * 1024 ||
                                ((int64_t)rows * ctas * 2 <= num_sms() && (int64_t)ctas * 2048 < vocab)))
     ctas *= 2;
   a.slice = (vocab + ctas - 1) / ctas;
