@@ -26,7 +26,7 @@
 // 2^-16 of it is lost (with one bf16, 2^-9: 2.1 and 1.6 us for 256 rows).  P so fills the
 // 128 columns of the S that it is made of, which has been read when it is written.  There are
 // two such places, at head_dim 64 three, which the turns of both streams take in order (with
-// two at 64 the call above 101.8 us, with three 85.5).  P's two halves and the lazily raised
+// two at 64 the call above 102 us, with three 86).  P's two halves and the lazily raised
 // maximum are as in window_attention_tc.cuh.
 #pragma once
 #include "kv_prefix.cuh"

@@ -293,11 +293,11 @@ dinfer_status dinfer_kv_prefix_attention(const dinfer_kv_cache* kc, int32_t laye
   p.warps = hd128 ? KaCfg<float, 128, 8>::kWarps : KaCfg<float, 64, 8>::kWarps;
   p.keys = bf16 ? KaCfg<__nv_bfloat16, 128, 8>::kKeys : KaCfg<float, 128, 8>::kKeys;
   p.rows = rows;
-  // what an SM takes for a step of own keys and for a tile of shared ones, in the company of the others (head_dim 128: 64
-  // sequences behind 8192 tokens, 32 heads on 8, 33.5 us, with 0.7 of the tiles' 36.0, with 1.3 35.6; 32 behind 8192, 16 heads
-  // on 16, 48.1, 50.6 and 51.4; head_dim 64: three groups, 96 sequences, 64 heads on 8, 85.5, with 0.8 88.1, with 1.3 93.9)
+  // what an SM takes for a step of own keys and for a tile of shared ones, in the company of the others, keys from HBM (head_dim
+  // 128: 64 sequences behind 8192 tokens, 32 heads on 8, 35.6 us, with 0.7 of the tiles' 38.1, with 1.3 38.4; 32 behind 8192,
+  // 16 heads on 16, 48.4, 55.7 and with 1.4 52.3; head_dim 64: three groups, 96 sequences, 64 heads on 8, 86.3, 91.9 and 101.6)
   p.step_ns = hd128 ? 360 : 165;
-  p.pair_ns = hd128 ? 3750 : 1860;
+  p.pair_ns = hd128 ? 3200 : 1860;
   p.single_ns = hd128 ? 1440 : 1320;
   p.group_div = FastDiv::make((uint32_t)a.group);
   p.head = reinterpret_cast<int4*>(w.data);
