@@ -100,11 +100,13 @@ struct SmScale {
 // Out of line: the kernel's uses of it are many, and its code is large.  For time it is all but the same (one flat row of
 // 126464 with top-p: 37 us, 39 with a copy at every use).
 __device__ __noinline__ uint64_t sm_weight(float l, const SmScale k, const uint32_t* table) {
-  const float d = l - k.m, back = d - l, dl = (l - (d - back)) - (k.m + back);  // the difference, and what it is rounded by
-  const float p = __fmul_rn(d, k.ch);  // not to be contracted with the sums below, which take its rounding off again
-  float s = fmaf(dl, k.ch, fmaf(d, k.cl, fmaf(d, k.ch, -p)));
+  // half the difference, and what it is rounded by: the whole one may pass the largest float
+  const float x = 0.5f * l, m = 0.5f * k.m, ch = 2.f * k.ch;
+  const float d = x - m, back = d - x, dl = (x - (d - back)) - (m + back);
+  const float p = __fmul_rn(d, ch);  // not to be contracted with the sums below, which take its rounding off again
+  float s = fmaf(dl, ch, fmaf(d, 2.f * k.cl, fmaf(d, ch, -p)));
   constexpr float kMagic = 24576.f;  // 1.5 * 2^14: a float's last place is 1 / 512
-  const float t = fmaf(dl, k.ch, p) + kMagic;
+  const float t = fmaf(dl, ch, p) + kMagic;
   s += p - (t - kMagic);
   const float q = s * fmaf(s, fmaf(s, 0.0555041086648f, 0.240226506959f), 0.693147180560f);  // 2^s - 1
   const int n = __float_as_int(t) - __float_as_int(kMagic);

@@ -109,3 +109,17 @@ def test_rows_at_the_ends_every_one_compared(D):
         for s in ({}, dict(temperature=1e-30), dict(temperature=0.0), dict(temperature=-1.0), dict(temperature=1e30), dict(top_k=2), dict(top_p=0.71),
                   dict(min_p=0.53), dict(top_k=3, top_p=0.91, min_p=0.13), dict(top_k=-1, top_p=1.5, min_p=-2.0)):
             T.check(D, x, [float(np.float32(u))] * n, unsure=0, **{k: [v] * n for k, v in s.items()})
+
+
+@pytest.mark.parametrize("temperature", [1e37, 1e38, 3e38, float("inf")])
+def test_logits_further_apart_than_the_largest_float(D, temperature):
+    """Their differences overflow, what the temperature leaves of them does not."""
+    rows = [[3e38, -3e38, 1e38, -1e38, 0.0], [-3.4e38, 3.4e38, 2e38, -2e38, 3.4e38], [3e38, -3e38, -3e38, -3e38, -3e38]] * 2
+    x = torch.tensor(rows, device=dev)
+    for u in (0.03, 0.27, 0.41, 0.62, 0.83, 0.97):
+        for s in ({}, dict(top_k=3), dict(top_p=0.83), dict(min_p=0.013), dict(top_k=4, top_p=0.77, min_p=0.011)):
+            if temperature < 1e39:
+                T.check(D, x, [float(np.float32(u))] * 6, unsure=0, temperature=[temperature] * 6, **{k: [v] * 6 for k, v in s.items()})
+        if temperature > 1e39:  # every weight is the largest
+            tok, _ = D.op_sample(x, torch.full((6,), u, device=dev), temperature=torch.full((6,), temperature, device=dev))
+            assert tok.tolist() == [int(u * 5)] * 6
