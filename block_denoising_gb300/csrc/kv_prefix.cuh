@@ -18,8 +18,8 @@
 //   prefix  in bf16 the shared keys on the tensor cores (kv_prefix_tc.cuh), at the same
 //           time: the plan deals the SMs to the two by what their work takes
 //   join    a warp per row of the output
-// All of it in a graph: 64 sequences behind 8192 tokens, 32 heads on 8 (66 MB) 35.4 us; 32 behind
-// 8192 with 512 of their own, 16 heads on 16 (202 MB) 48.5 us, 4.2 TB/s.
+// All of it in a graph: 64 sequences behind 8192 tokens, 32 heads on 8 (66 MB) 34.8 us; 32 behind
+// 8192 with 512 of their own, 16 heads on 16 (202 MB) 48.9 us, 4.1 TB/s.
 #pragma once
 #include "kv_attention.cuh"
 

@@ -12,7 +12,7 @@
 // definition's, so the exponent is carried in two floats and the power of two
 // comes from a table of 512 and a cubic, about 2^-32 of the weight in all.  Passes
 // over whole slices sum the same powers as pairs of floats, two tokens an instruction
-// (some 25 instructions a token where whole numbers take 50), from a table of 32 in
+// (some 28 instructions a token where whole numbers take 50), from a table of 32 in
 // every lane's own banks and a quartic, to 2^-31 of a weight and 2^-38 of the largest; a
 // thread's part of them is then rounded to a whole number, so that these sums do hang on how a
 // row is dealt to threads, in their last 2^-31.
@@ -28,10 +28,10 @@
 // between the floor and a ceiling, which the eighth gives too.  Rows without either take
 // one pass.
 //
-// 512 rows of 126464 in bf16 with settings of their own (130 MB) take 262 us in a graph, of
+// 512 rows of 126464 in bf16 with settings of their own (130 MB) take 259 us in a graph, of
 // which the memory needs 19; the first form, with histograms of whole rows, one atomic a logit,
-// took 651.  64 rows of 157184 in fp32 at a temperature (40 MB) take 39 us: issue slots 43%
-// busy, DRAM 11%.  One row of 126464: 5.8 us greedy, 9.2 at a temperature, 37 by top-p where
+// took 651.  64 rows of 157184 in fp32 at a temperature (40 MB) take 39 us: issue slots 44%
+// busy, DRAM 11%.  One row of 126464: 5.5 us greedy, 9.0 at a temperature, 39 by top-p where
 // it is flat.
 #pragma once
 #include <cooperative_groups.h>
