@@ -87,3 +87,37 @@ def test_a_workspace_that_begins_at_16_bytes(D, ws, hd, members):
     assert bool((whole[off + ws.nbytes:] == 77).all())
     c.check()
     odd.check()
+
+
+@pytest.mark.parametrize("members,page,hd,dtype", [(2, 16, 128, BF), (12, 16, 128, BF), (12, 24, 64, BF), (40, 128, 128, BF), (40, 16, 64, BF), (5, 16, 64, torch.float32)])
+def test_pages_that_are_none(D, ws, members, page, hd, dtype):
+    """Table entries inside the shared and the own tokens that name no page: their keys are not there, for every member of
+    the group, and the status says so."""
+    rng = np.random.default_rng(members + page)
+    shared, own = 6 * page, page + 5
+    c, seqs, bounds = PA.make(D, rng, [shared], [[own] * members], page, 2, hd, dtype)
+    q = PA.values(rng, (members, 8, hd), dtype)
+    n, none = shared + own, {1: -1, 4: c.k.shape[1], 5: 1 << 30}
+    keys = [PA.rows_of(c, s) for s in seqs]
+    table = c.table.clone()
+    for j, v in none.items():
+        table[:, j] = v
+    table[seqs[0], 6] = -7
+    c.set_tables(table, c.lens.clone(), c.refs.clone())
+    o = c.prefix_attention(0, q, ws, PA.ints([shared]), PA.ints(bounds), seqs=PA.ints(seqs))
+    with pytest.raises(D.DinferError, match="status 0x4:"):
+        c.check()
+    for i in sorted({0, 1, members - 1}):
+        seen = np.ones((1, n), bool)
+        for j in list(none) + ([6] if i == 0 else []):
+            seen[0, j * page:(j + 1) * page] = False
+        A.check(o[i:i + 1].double().cpu().numpy(), q[i:i + 1].double().cpu().numpy(), *keys[i], seen, hd ** -0.5, dtype is BF, i,
+                KEPT if dtype is BF else None)
+    # no page at all: zeros
+    table[:] = -1
+    c.set_tables(table, c.lens.clone(), c.refs.clone())
+    o = c.prefix_attention(0, q, ws, PA.ints([shared]), PA.ints(bounds), seqs=PA.ints(seqs))
+    assert not bool(o.any())
+    with pytest.raises(D.DinferError, match="status 0x4:"):
+        c.check()
+    ws.check()
