@@ -121,3 +121,72 @@ def test_pages_that_are_none(D, ws, members, page, hd, dtype):
     with pytest.raises(D.DinferError, match="status 0x4:"):
         c.check()
     ws.check()
+
+
+# rows of a key head: one tile on every other key tile; two tiles; more than a unit
+@pytest.mark.parametrize("members,hd,page", [(12, 128, 16), (12, 64, 24), (60, 128, 16), (60, 64, 16), (110, 128, 128)])
+def test_values_that_are_not_finite_on_the_tensor_cores(D, ws, members, hd, page):
+    """Infinite and NaN values touch their columns alone, however small their weight; a NaN key its rows; sums of large values
+    whose mean is finite stay finite; slots behind the last tokens may hold anything."""
+    rng = np.random.default_rng(members + hd)
+    own = [int(x) for x in rng.integers(1, 60, members)]
+    shared, heads, kv_heads = 560, 6, 2
+    c, seqs, bounds = PA.make(D, rng, [shared], [own], page, kv_heads, hd)
+    at = lambda s, t: (int(c.table[s, t // page]), t % page)  # noqa: E731
+    used = torch.zeros(c.k.shape[1:3], dtype=torch.bool, device=dev)
+    for s in seqs:
+        j = torch.arange(int(c.lens[s]), device=dev)
+        used[c.table[s, j // page].long(), j % page] = True
+    for t in (c.k, c.v):
+        t[0][~used] = float("nan")
+    q = PA.values(rng, (members, heads, hd), BF)
+    run = lambda: c.prefix_attention(0, q, ws, PA.ints([shared]), PA.ints(bounds), seqs=PA.ints(seqs)).float()  # noqa: E731
+    some = [0, 1, members // 2, members - 1]
+    clean = run()
+    PA.check(c, [seqs[i] for i in some], q[some], clean[some].to(BF))
+    keep_k, keep_v = c.k.clone(), c.v.clone()
+    p0, t0 = at(seqs[0], 3)
+    p1, t1 = at(seqs[0], 300)
+    p2, t2 = at(seqs[1], shared + own[1] - 1)  # a token of its own of one member, or the last of the shared page it copied
+    c.v[0, p0, t0, 0, 5] = float("inf")
+    c.v[0, p1, t1, 1, 6] = float("nan")
+    c.v[0, p2, t2, 0, 7] = float("-inf")
+    c.k[0, p0, t0, 0] = -300.0 * q[0, 0].sign()  # its weight underflows for the first query
+    o = run()
+    g = heads // kv_heads
+    want = torch.ones_like(o, dtype=torch.bool)
+    want[:, :g, 5] = want[:, g:, 6] = want[1, :g, 7] = False
+    assert torch.equal(torch.isfinite(o), want)
+    assert bool((o[:, :g, 5] == float("inf")).all()) and bool((o[1, :g, 7] == float("-inf")).all())
+    for i in some:  # rows with such a column are done again in another order: within the bound, not the same bits
+        k, v = PA.rows_of(c, seqs[i])
+        got = o[i:i + 1].double().cpu().numpy()
+        v[~np.isfinite(v)] = 0.0
+        got[:, :g, [5, 7]], got[:, g:, 6], v[:, 0, [5, 7]], v[:, 1, 6] = 0.0, 0.0, 0.0, 0.0
+        A.check(got, q[i:i + 1].double().cpu().numpy(), k, v, np.ones((1, len(k)), bool), hd ** -0.5, True, i, KEPT)
+    c.v.copy_(keep_v)
+    c.k.copy_(keep_k)
+    c.v[0][used] = torch.sign(c.v[0][used]) * 3.0e38
+    o = run()
+    assert bool(torch.isfinite(o).all()) and float(o.abs().max()) <= 3.4e38
+    c.v.copy_(keep_v)
+    c.k[0, p1, t1, 0] = float("nan")
+    o = run()
+    assert bool(torch.isnan(o[:, :g]).all()) and torch.equal(o[:, g:], clean[:, g:])
+    # scores of -inf: of all shared keys, of all keys
+    c.k.copy_(keep_k)
+    first = q[..., 0].clone()
+    q[..., 0] = 1.0
+    j = torch.arange(shared // page * page, device=dev)
+    c.k[0, c.table[seqs[0], j // page].long(), j % page, :, 0] = float("-inf")
+    o = run()
+    for i in some:
+        k, v = PA.rows_of(c, seqs[i])
+        seen = np.isfinite(k[:, 0, 0])[None]
+        assert seen.sum() < shared
+        k[~seen[0]] = 0.0
+        A.check(o[i:i + 1].double().cpu().numpy(), q[i:i + 1].double().cpu().numpy(), k, v, seen, hd ** -0.5, True, i, KEPT)
+    c.k[0, ..., 0] = float("-inf")
+    assert not bool(run().any())
+    q[..., 0] = first
+    ws.check()
