@@ -9,7 +9,14 @@
 
 namespace {
 
-constexpr uint64_t kRopeReady = 0x726f7065cf0157a1;  // dinfer_rope::ready of a filled one
+// dinfer_rope::ready of one that is filled for the fields it has: all of them, mixed.
+uint64_t rope_mark(const dinfer_rope& r) {
+  static_assert(offsetof(dinfer_rope, turns) == 56, "fields without gaps");
+  uint64_t fields[7], mark = 0x726f7065cf0157a1;
+  std::memcpy(fields, &r, sizeof(fields));
+  for (uint64_t f : fields) mark = (mark ^ f) * 0x9e3779b97f4a7c15, mark ^= mark >> 29;
+  return mark;
+}
 
 // Why the rotation is unusable, or NULL.
 const char* rope_bad(const dinfer_rope* r) {
@@ -30,7 +37,7 @@ const char* rope_bad(const dinfer_rope* r) {
 // The same for a call on heads of head_dim; else the kernel's table.
 const char* rope_turns(const dinfer_rope* r, int head_dim, RopeTurns& t) {
   if (const char* why = rope_bad(r)) return why;
-  if (r->ready != kRopeReady) return "rope: dinfer_rope_init has not filled it";
+  if (r->ready != rope_mark(*r)) return "rope: dinfer_rope_init has not filled it, or not since a field changed";
   if (r->rot_dim > head_dim) return "rope: rot_dim must be even, 2 .. head_dim";
   t.pairs = r->rot_dim / 2;
   t.magnitude = (float)r->magnitude;
@@ -165,7 +172,7 @@ dinfer_status dinfer_rope_init(dinfer_rope* r) {
     const double turns = f / two_pi;
     r->turns[i] = (uint64_t)std::ldexp(turns - std::floor(turns), 64);
   }
-  r->ready = kRopeReady;
+  r->ready = rope_mark(*r);
   return DINFER_OK;
 }
 

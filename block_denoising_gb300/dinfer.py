@@ -42,7 +42,8 @@ class DinferError(RuntimeError):
 
 class Rope(ctypes.Structure):
     """Rotary positions (dinfer_rope): the first rot_dim elements of a head turn in pairs, "half" (i, i + rot_dim / 2) or
-    "pairs" (2 i, 2 i + 1), by position * theta^(-2 i / rot_dim), scaled as "none", "linear", "base" or "bands"."""
+    "pairs" (2 i, 2 i + 1), by position * theta^(-2 i / rot_dim), scaled as "none", "linear", "base" or "bands".  The
+    calls refuse one of which a field was changed afterwards: make another."""
     _fields_ = [(n, ctypes.c_int32) for n in ("rot_dim", "layout", "scaling", "trained")] + \
                [(n, ctypes.c_double) for n in ("theta", "factor", "slow", "fast", "magnitude")] + \
                [("turns", ctypes.c_uint64 * 128), ("ready", ctypes.c_uint64)]

@@ -133,8 +133,8 @@ typedef struct dinfer_rope {
 
 /* Checks the fields above and fills the frequencies (host memory, once for a
  * model's rotation: 64 powers are longer than a small call).  The calls that take a
- * dinfer_rope copy it, and refuse one that is not filled; after a field changed it is
- * to be filled again.  Errors: DINFER_EINVAL. */
+ * dinfer_rope copy it, and refuse one that is not filled, or not since a field
+ * changed.  Errors: DINFER_EINVAL. */
 dinfer_status dinfer_rope_init(dinfer_rope* rope);
 
 /* y[r, h, :] = rotation of x[r, h, :] at positions[r] (NULL: first + r).

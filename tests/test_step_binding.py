@@ -48,6 +48,22 @@ def test_a_copied_rotation_is_its_own(L, how):
     assert twin._as_parameter_ == ctypes.addressof(twin)
 
 
+CHANGES = dict(rot_dim=64, layout=0, scaling=0, trained=5, theta=500000.0, factor=3.0, slow=0.5, fast=8.0, magnitude=1.5)
+
+
+@pytest.mark.parametrize("field", CHANGES)
+def test_a_changed_rotation_is_refused_until_it_is_filled_again(L, field):
+    rope = dinfer.Rope(128, layout="pairs", scaling="bands", factor=2.0, trained=4096, slow=1.0, fast=4.0)
+    was = getattr(rope, field)
+    setattr(rope, field, CHANGES[field])
+    assert "filled" in reason(L, rope)  # its frequencies are those of the fields before
+    setattr(rope, field, was)
+    assert "rows" in reason(L, rope)
+    setattr(rope, field, CHANGES[field])
+    assert L.dinfer_rope_init(rope) == dinfer.OK
+    assert "rows" in reason(L, rope)
+
+
 @pytest.mark.parametrize("first", [1 << 31, 1 << 40, -(1 << 31) - 1, -(1 << 63), 1 << 32])
 def test_positions_beyond_int32_are_refused(first):
     # not the end of the range in their place: a position there is another one
