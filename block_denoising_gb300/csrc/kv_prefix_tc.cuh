@@ -7,7 +7,7 @@
 // joined with the others and the entry's own keys' by kv_join_kernel.
 //
 // By its floor HBM-bound up to some 230 rows: a key tile of K and V, 64 KB at head_dim 128, takes
-// 2800 cycles of an SM's share of the bandwidth, its products for 256 rows 3072
+// 2800 cycles of an SM's share of the bandwidth, its products for 256 rows some 3100
 // cycles of the tensor cores.  What stands between is the chain S, softmax, P V of a
 // tile, which takes longer, so two of them run at a time (streams): the two tiles of rows
 // on the same keys, or, of a unit of at most 128 rows, one tile of rows on every other
